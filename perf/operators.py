@@ -227,7 +227,7 @@ def _quantise(y, gsf):
     code = torch.zeros(a.shape, dtype=torch.uint8, device=DEV)
     for edge, even in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
         code += (a >= edge) if even else (a > edge)  # a tie goes to the even code
-    code = (code + 8 * torch.signbit(v)).flatten(-2)
+    code = (code + (torch.signbit(v).to(torch.uint8) << 3)).flatten(-2)
     return code[..., 0::2] | code[..., 1::2] << 4, scale.view(torch.uint8)
 
 
