@@ -470,6 +470,67 @@ int h3q_rmsnorm_adaln_nvfp4_host(const void *x_host, int64_t rows, int64_t cols,
                                  uint8_t *codes_host, uint8_t *scales_host, void *workspace,
                                  int64_t workspace_bytes, int64_t chunk_rows, void *stream);
 
+/*
+ * The paged NVFP4 key/value cache, what stands between the QKV epilogue and the
+ * attention of the tokens to come: keys and values quantized as they are written, in
+ * the block format of the producers (16 elements of one head share a scale).
+ *
+ *   codes   k_codes, v_codes  uint8 [num_pages, kv_heads, page_size, head_dim/2]: two
+ *           E2M1 codes a byte, the even element in the low nibble.  16-byte aligned.
+ *   scales  k_scales, v_scales  uint8 [num_pages, kv_heads, page_size, head_dim/16]:
+ *           one E4M3 scale per 16 elements, in order (not swizzled).  16-byte aligned.
+ *   k_global_scale, v_global_scale  device fp32, finite and > 0 (not checked): the
+ *           static per-tensor scales, one for keys and one for values.
+ *   num_pages  1 .. 2^31 - 1.    page_size  16, 32, 64 or 128.
+ *   kv_heads   >= 1.             head_dim   64, 128 or 256; kv_heads * head_dim <= 2^24.
+ *
+ * The rows of several sequences come packed, and lists on the device say where they
+ * live (read by the kernels, so they may change between the replays of a graph):
+ *
+ *   cu_rows      int32 [batch + 1], not decreasing: rows cu_rows[b] .. cu_rows[b+1]-1
+ *                belong to sequence b.  Rows before cu_rows[0] or from cu_rows[batch]
+ *                on belong to none.
+ *   kv_len       int32 [batch]: the positions of sequence b in the cache, its packed
+ *                rows included: n = cu_rows[b+1] - cu_rows[b] rows stand at its LAST n
+ *                positions, kv_len[b] - n .. kv_len[b] - 1.
+ *   block_table  int32 [batch, max_pages]: position p of sequence b is row
+ *                p % page_size of page block_table[b][p / page_size].
+ * batch >= 0, max_pages >= 1; batch * max_pages <= 2^40.  Lists are 4-byte aligned.
+ * Their entries are not checked on the host (that would need a synchronisation); no
+ * entry makes a kernel touch memory outside the buffers.
+ */
+
+/*
+ * Quantize new rows into the cache: k, v bf16 [rows, kv_heads * head_dim] (row strides
+ * ld_k, ld_v; 32-byte aligned), each block of 16 as h3q_quantize_nvfp4 does.  Nothing
+ * is written for a row of no sequence, for one whose position is negative or past the
+ * block table, or whose page is not in [0, num_pages); every other byte of the cache
+ * stays as it was.  Two rows that reach the same place in the cache (a page listed
+ * twice) leave unspecified codes and scales there.
+ */
+int h3q_kv_cache_write_nvfp4(const void *k, int64_t ld_k, const void *v, int64_t ld_v, int64_t rows,
+                             const int32_t *cu_rows, const int32_t *kv_len, const int32_t *block_table,
+                             int64_t batch, int64_t max_pages, const float *k_global_scale,
+                             const float *v_global_scale, uint8_t *k_codes, uint8_t *k_scales,
+                             uint8_t *v_codes, uint8_t *v_scales, int64_t num_pages, int64_t page_size,
+                             int64_t kv_heads, int64_t head_dim, void *stream);
+
+/*
+ * Read rows of the cache back: bf16(fl((E2M1value(c) * E4M3value(sf)) / gsf)) of the
+ * same places that h3q_kv_cache_write_nvfp4 writes with these lists (a sequence's
+ * whole prefix: n = kv_len[b]), packed.
+ *
+ *   k_out, v_out  bf16 [rows, kv_heads, head_dim] contiguous, 32-byte aligned.  Rows
+ *                 that the cache does not hold (see above) are written as zero; rows of
+ *                 no sequence stay as they were.
+ */
+int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                            const uint8_t *v_scales, int64_t num_pages, int64_t page_size,
+                            int64_t kv_heads, int64_t head_dim, const float *k_global_scale,
+                            const float *v_global_scale, int64_t rows, const int32_t *cu_rows,
+                            const int32_t *kv_len, const int32_t *block_table, int64_t batch,
+                            int64_t max_pages, void *k_out, void *v_out, void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *h3q_last_error(void);
 

@@ -27,6 +27,7 @@ __all__ = [
     "h3q_quantize_nvfp4_dynamic", "h3q_residual_rmsnorm_adaln_nvfp4", "h3q_swiglu_packed_nvfp4",
     "h3q_qkv_epilogue", "h3q_rmsnorm_adaln_nvfp4_host", "host_workspace_bytes",
     "h3q_gemm_swiglu_nvfp4", "h3q_kernel_error_flag",
+    "kv_cache_nvfp4", "h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4",
 ]
 
 H3Q_OK = 0
@@ -56,6 +57,10 @@ _SIGNATURES = {
                          _I64, ctypes.c_float, _P, _P, _P, _P],
     "h3q_gemm_swiglu_nvfp4": [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P],
     "h3q_kernel_error_flag": [_P],
+    "h3q_kv_cache_write_nvfp4": [_P, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64,
+                                 _I64, _I64, _I64, _P],
+    "h3q_kv_cache_read_nvfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P,
+                                _P, _P],
 }
 
 _lock = threading.Lock()
@@ -640,3 +645,110 @@ def h3q_kernel_error_flag() -> int:
     flag = ctypes.c_int(0)
     _check("h3q_kernel_error_flag", library().h3q_kernel_error_flag(ctypes.byref(flag)))
     return flag.value
+
+
+# --------------------------------------------------------------------------- #
+# the paged NVFP4 cache                                                        #
+# --------------------------------------------------------------------------- #
+
+def kv_cache_nvfp4(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """An empty cache: (k_codes, k_scales, v_codes, v_scales), uint8 [num_pages, kv_heads,
+    page_size, head_dim / 2] and [..., head_dim / 16], zeroed."""
+    import torch
+
+    return tuple(torch.zeros((num_pages, kv_heads, page_size, head_dim // per), dtype=torch.uint8, device=device)
+                 for per in (2, 16, 2, 16))
+
+
+def _cache(cache, device=None):
+    """Checks the four cache tensors; returns (pages, kv_heads, page_size, head_dim, device)."""
+    import torch
+
+    if len(cache) != 4:
+        raise ValueError("cache must be (k_codes, k_scales, v_codes, v_scales)")
+    _cuda_tensor("k_codes", cache[0], torch.uint8, device)
+    if cache[0].dim() != 4:
+        raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
+    pages, heads, page, half = cache[0].shape
+    for name, t, per in zip(("k_codes", "k_scales", "v_codes", "v_scales"), cache, (2, 16, 2, 16)):
+        _contiguous(name, t, torch.uint8, (pages, heads, page, 2 * half // per), cache[0].device)
+    return pages, heads, page, 2 * half, cache[0].device
+
+
+def _head_rows(name, t, device=None):
+    """bf16 [rows, heads, dim] whose rows are contiguous (any row stride); returns
+    (tensor, rows, heads, dim, ld)."""
+    import torch
+
+    _cuda_tensor(name, t, torch.bfloat16, device)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous rows")
+    rows, heads, dim = t.shape
+    return t, rows, heads, dim, t.stride(0) if rows > 1 else heads * dim
+
+
+def _row_lists(cu_rows, kv_len, block_table, device):
+    """Checks the lists of packed rows; returns (batch, max_pages)."""
+    import torch
+
+    _cuda_tensor("kv_len", kv_len, torch.int32, device)
+    if kv_len.dim() != 1 or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be contiguous [batch]")
+    batch = kv_len.shape[0]
+    _contiguous("cu_rows", cu_rows, torch.int32, (batch + 1,), device)
+    _cuda_tensor("block_table", block_table, torch.int32, device)
+    if block_table.dim() != 2 or block_table.shape[0] != batch or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous [batch, max_pages]")
+    return batch, block_table.shape[1]
+
+
+def h3q_kv_cache_write_nvfp4(k, v, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale,
+                             stream=None):
+    """Quantize new key and value rows (bf16 [rows, kv_heads, head_dim], contiguous rows of any
+    stride) into the paged NVFP4 ``cache`` (see kv_cache_nvfp4).  Rows cu_rows[b] .. cu_rows[b+1]-1
+    are the last positions of sequence b, which has kv_len[b] positions with them; position p is row
+    p % page_size of page block_table[b, p // page_size].  All lists are int32 CUDA tensors.  Returns
+    the cache."""
+    import torch
+
+    pages, heads, page, dim, dev = _cache(cache)
+    k, rows, heads_k, dim_k, ld_k = _head_rows("k", k, dev)
+    v, rows_v, heads_v, dim_v, ld_v = _head_rows("v", v, dev)
+    if (heads_k, dim_k) != (heads, dim) or (rows_v, heads_v, dim_v) != (rows, heads, dim):
+        raise ValueError("k and v must be [rows, kv_heads, head_dim] of the cache's heads")
+    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
+    with torch.cuda.device(dev):
+        rc = library().h3q_kv_cache_write_nvfp4(
+            k.data_ptr(), ld_k, v.data_ptr(), ld_v, rows, cu_rows.data_ptr(), kv_len.data_ptr(),
+            block_table.data_ptr(), batch, max_pages, kg.data_ptr(), vg.data_ptr(), cache[0].data_ptr(),
+            cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), pages, page, heads, dim,
+            _stream(stream, dev))
+    _check("h3q_kv_cache_write_nvfp4", rc)
+    return cache
+
+
+def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, *, rows=None,
+                            outs=None, stream=None):
+    """The bf16 values that the cache holds for the packed rows that the lists name (as in
+    h3q_kv_cache_write_nvfp4; a whole prefix where cu_rows[b+1] - cu_rows[b] = kv_len[b]).  Give
+    ``rows`` (the packed rows) or ``outs`` = (k_out, v_out), bf16 [rows, kv_heads, head_dim].
+    Returns (k_out, v_out)."""
+    import torch
+
+    pages, heads, page, dim, dev = _cache(cache)
+    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    if outs is None:
+        if rows is None:
+            raise ValueError("give rows or outs")
+        outs = [torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    rows = outs[0].shape[0]
+    outs = [_contiguous(n, t, torch.bfloat16, (rows, heads, dim), dev) for n, t in zip(("k_out", "v_out"), outs)]
+    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
+    with torch.cuda.device(dev):
+        rc = library().h3q_kv_cache_read_nvfp4(
+            cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), pages, page, heads,
+            dim, kg.data_ptr(), vg.data_ptr(), rows, cu_rows.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+            batch, max_pages, outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream, dev))
+    _check("h3q_kv_cache_read_nvfp4", rc)
+    return outs[0], outs[1]

@@ -700,4 +700,144 @@ int h3q_rmsnorm_adaln_nvfp4_host(const void* x_host, int64_t rows, int64_t cols,
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 
+// --- the paged NVFP4 cache ---------------------------------------------------
+
+namespace {
+
+struct CacheShape {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t num_pages, page_size, kv_heads, head_dim;
+  Span spans[4];
+};
+
+int check_cache(const char* fn, CacheShape& c) {
+  if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+    return invalid(fn, "head_dim must be 64, 128 or 256");
+  if (c.kv_heads < 1) return invalid(fn, "kv_heads must be >= 1");
+  if (c.kv_heads > kMaxCols / c.head_dim) return invalid(fn, "kv_heads * head_dim exceeds 2^24");
+  if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128)
+    return invalid(fn, "page_size must be 16, 32, 64 or 128");
+  if (c.num_pages < 1 || c.num_pages >= (int64_t(1) << 31)) return invalid(fn, "num_pages must be in [1, 2^31)");
+  return 0;
+}
+
+int check_cache_buffers(const char* fn, CacheShape& c) {
+  const uint8_t* p[4] = {c.k_codes, c.k_scales, c.v_codes, c.v_scales};
+  const int64_t rows = c.num_pages * c.page_size * c.kv_heads;
+  for (int i = 0; i < 4; ++i) {
+    if (p[i] == nullptr || !aligned(p[i], 16))
+      return invalid(fn, "k_codes, k_scales, v_codes and v_scales must be 16-byte aligned and not NULL");
+    c.spans[i] = span(p[i], rows * (c.head_dim / (i % 2 == 0 ? 2 : 16)));
+  }
+  return 0;
+}
+
+int check_lists(const char* fn, const int32_t* cu_rows, const int32_t* kv_len, const int32_t* block_table,
+                int64_t batch, int64_t max_pages) {
+  if (batch < 0 || batch >= (int64_t(1) << 31)) return invalid(fn, "batch must be in [0, 2^31)");
+  if (max_pages < 1) return invalid(fn, "max_pages must be >= 1");
+  if (batch > 0 && max_pages > (int64_t(1) << 40) / batch) return invalid(fn, "batch * max_pages exceeds 2^40");
+  if (batch == 0) return 0;
+  if (cu_rows == nullptr || kv_len == nullptr || block_table == nullptr)
+    return invalid(fn, "cu_rows, kv_len and block_table must not be NULL");
+  if (!aligned(cu_rows, 4) || !aligned(kv_len, 4) || !aligned(block_table, 4))
+    return invalid(fn, "cu_rows, kv_len and block_table must be 4-byte aligned");
+  return 0;
+}
+
+int check_scales(const char* fn, const float* k_gsf, const float* v_gsf) {
+  if (k_gsf == nullptr || v_gsf == nullptr || !aligned(k_gsf, 4) || !aligned(v_gsf, 4))
+    return invalid(fn, "k_global_scale and v_global_scale must be 4-byte aligned pointers");
+  return 0;
+}
+
+// The page of a position is found by a shift.
+int page_shift(int64_t page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
+
+h3q::PagedCache paged_cache(const CacheShape& c) {
+  h3q::PagedCache p{};
+  p.codes[0] = c.k_codes;
+  p.codes[1] = c.v_codes;
+  p.scales[0] = c.k_scales;
+  p.scales[1] = c.v_scales;
+  p.num_pages = c.num_pages;
+  p.kv_heads = static_cast<int>(c.kv_heads);
+  p.head_dim = static_cast<int>(c.head_dim);
+  p.page_shift = page_shift(c.page_size);
+  return p;
+}
+
+}  // namespace
+
+int h3q_kv_cache_write_nvfp4(const void* k, int64_t ld_k, const void* v, int64_t ld_v, int64_t rows,
+                             const int32_t* cu_rows, const int32_t* kv_len, const int32_t* block_table,
+                             int64_t batch, int64_t max_pages, const float* k_global_scale,
+                             const float* v_global_scale, uint8_t* k_codes, uint8_t* k_scales,
+                             uint8_t* v_codes, uint8_t* v_scales, int64_t num_pages, int64_t page_size,
+                             int64_t kv_heads, int64_t head_dim, void* stream) {
+  static const char* fn = "h3q_kv_cache_write_nvfp4";
+  g_last_error.clear();
+  CacheShape c{k_codes, k_scales, v_codes, v_scales, num_pages, page_size, kv_heads, head_dim, {}};
+  if (int e = check_cache(fn, c)) return e;
+  if (rows < 0) return invalid(fn, "rows must be >= 0");
+  if (rows > kMaxRows) return invalid(fn, "rows exceeds 2^40");
+  if (int e = check_lists(fn, cu_rows, kv_len, block_table, batch, max_pages)) return e;
+  if (rows == 0 || batch == 0) return H3Q_OK;
+  const int64_t d = kv_heads * head_dim;
+  if (int e = check_input(fn, "k", k, ld_k, rows, d)) return e;
+  if (int e = check_input(fn, "v", v, ld_v, rows, d)) return e;
+  if (int e = check_cache_buffers(fn, c)) return e;
+  if (int e = check_scales(fn, k_global_scale, v_global_scale)) return e;
+  const Span ins[] = {span(k, view_bytes(rows, d, ld_k)), span(v, view_bytes(rows, d, ld_v)),
+                      span(cu_rows, (batch + 1) * 4), span(kv_len, batch * 4),
+                      span(block_table, batch * max_pages * 4), span(k_global_scale, 4), span(v_global_scale, 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& in : ins)
+      if (overlap(c.spans[i], in)) return invalid(fn, "the cache overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(c.spans[i], c.spans[j])) return invalid(fn, "the cache's buffers overlap each other");
+  }
+  const uint16_t* x[2] = {static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)};
+  const int64_t ld[2] = {ld_k, ld_v};
+  const float* gsf[2] = {k_global_scale, v_global_scale};
+  const h3q::PagedRows at{cu_rows, kv_len, block_table, max_pages, static_cast<int>(batch)};
+  cudaError_t err = h3q::launch_cache_write(paged_cache(c), at, x, ld, gsf, rows, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+int h3q_kv_cache_read_nvfp4(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                            const uint8_t* v_scales, int64_t num_pages, int64_t page_size,
+                            int64_t kv_heads, int64_t head_dim, const float* k_global_scale,
+                            const float* v_global_scale, int64_t rows, const int32_t* cu_rows,
+                            const int32_t* kv_len, const int32_t* block_table, int64_t batch,
+                            int64_t max_pages, void* k_out, void* v_out, void* stream) {
+  static const char* fn = "h3q_kv_cache_read_nvfp4";
+  g_last_error.clear();
+  CacheShape c{const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_codes),
+               const_cast<uint8_t*>(v_scales), num_pages, page_size, kv_heads, head_dim, {}};
+  if (int e = check_cache(fn, c)) return e;
+  if (rows < 0) return invalid(fn, "rows must be >= 0");
+  if (rows > kMaxRows) return invalid(fn, "rows exceeds 2^40");
+  if (int e = check_lists(fn, cu_rows, kv_len, block_table, batch, max_pages)) return e;
+  if (rows == 0 || batch == 0) return H3Q_OK;
+  if (int e = check_cache_buffers(fn, c)) return e;
+  if (int e = check_scales(fn, k_global_scale, v_global_scale)) return e;
+  if (k_out == nullptr || v_out == nullptr || !aligned(k_out, 32) || !aligned(v_out, 32))
+    return invalid(fn, "k_out and v_out must be 32-byte aligned and not NULL");
+  const int64_t bytes = rows * kv_heads * head_dim * 2;
+  const Span outs[2] = {span(k_out, bytes), span(v_out, bytes)};
+  const Span ins[] = {c.spans[0], c.spans[1], c.spans[2], c.spans[3], span(cu_rows, (batch + 1) * 4),
+                      span(kv_len, batch * 4), span(block_table, batch * max_pages * 4),
+                      span(k_global_scale, 4), span(v_global_scale, 4)};
+  for (const Span& o : outs)
+    for (const Span& in : ins)
+      if (overlap(o, in)) return invalid(fn, "an output overlaps an input");
+  if (overlap(outs[0], outs[1])) return invalid(fn, "k_out and v_out overlap");
+  uint16_t* out[2] = {static_cast<uint16_t*>(k_out), static_cast<uint16_t*>(v_out)};
+  const float* gsf[2] = {k_global_scale, v_global_scale};
+  const h3q::PagedRows at{cu_rows, kv_len, block_table, max_pages, static_cast<int>(batch)};
+  cudaError_t err = h3q::launch_cache_read(paged_cache(c), at, out, gsf, rows, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
 }  // extern "C"

@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "h3q_cache.cuh"
+
 namespace h3q {
 
 // The unique id (cuCtxGetId) of the CUDA context current on the calling thread,
@@ -105,7 +107,14 @@ cudaError_t launch_gemm_swiglu(const uint8_t* a, const uint8_t* sfa, int64_t m, 
 // (synchronous); the GEMM is the library's kernel with such waits.
 cudaError_t gemm_error_flag(int* flag);
 
-// RMSNorm + AdaLN -> NVFP4 on host buffers// RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
+// New key (index 0) and value (1) rows into the paged NVFP4 cache, and rows of the
+// cache back as bf16 [rows, kv_heads, head_dim].
+cudaError_t launch_cache_write(const PagedCache& cache, const PagedRows& at, const uint16_t* const x[2],
+                               const int64_t ld[2], const float* const gsf[2], int64_t rows, cudaStream_t stream);
+cudaError_t launch_cache_read(const PagedCache& cache, const PagedRows& at, uint16_t* const out[2],
+                              const float* const gsf[2], int64_t rows, cudaStream_t stream);
+
+// RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
 // copies pipelined with the producer over chunk_rows-row chunks; `workspace`
 // holds h3q_host_workspace_bytes(chunk_rows, cols, rows, row_frame == nullptr)
 // bytes of device memory (include/h3q.h), 256-byte aligned.
