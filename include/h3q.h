@@ -531,6 +531,53 @@ int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, con
                             const int32_t *kv_len, const int32_t *block_table, int64_t batch,
                             int64_t max_pages, void *k_out, void *v_out, void *stream);
 
+/*
+ * Attention of one or a few new tokens a sequence over the paged cache that holds the
+ * sequence's context and, at its last positions, the new tokens themselves (written
+ * before by h3q_kv_cache_write_nvfp4 with the same lists): decoding (one token), several
+ * drafted tokens in a chain, or a tree of them.  For token i of sequence b and head h,
+ * with key head h / (heads / kv_heads) and the values k, v that the cache holds,
+ *   x_j = scale * (q . k_j),  o = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max x_j,
+ * over the keys j that the token sees: all positions before the sequence's new tokens,
+ * and of the new tokens those whose bit is set in its mask (bit j: token j of the same
+ * sequence; a token sees itself only if its own bit is set), or without masks itself
+ * and those before it.  lse = m + log(sum_j e^(x_j - m)), natural.  A token that sees
+ * nothing gets o = 0 and lse = -inf.  Weights are rounded to fp16, sums are fp32.
+ *
+ *   q           bf16 [rows, heads * head_dim], row stride ld_q, 32-byte aligned.
+ *   max_rows    1 .. 64: at least the new tokens of any sequence (more of a sequence are
+ *               left as they were).
+ *   tree_mask   int64 [rows] on the device, 8-byte aligned, or NULL.
+ *   heads       a multiple of kv_heads; heads * head_dim <= 2^24.
+ *   scale       finite, > 0 (e.g. head_dim^-0.5).
+ *   o           out, bf16 [rows, heads, head_dim] contiguous, 16-byte aligned.
+ *   lse         out, fp32 [heads, rows], 4-byte aligned, or NULL.
+ *               Rows of no sequence are left as they were in both.
+ *   workspace   device memory of h3q_attention_cache_workspace_bytes bytes, 256-byte
+ *               aligned, any contents; not touched by other work until the stream has
+ *               passed this call (two calls that may run at once need one each).
+ * The cache and the lists as above.  A page that is not in [0, num_pages) is read as
+ * page 0, and the outputs of its sequence are unspecified; kv_len counts at most
+ * max_pages * page_size positions.  A scale byte of all ones (which a NaN leaves in the
+ * cache) counts as 480.  Launches two kernels.  The result does not depend on what
+ * else runs.
+ */
+static inline int64_t h3q_attention_cache_workspace_bytes(int64_t max_rows, int64_t heads, int64_t kv_heads,
+                                                          int64_t head_dim)
+{
+    int64_t shared = max_rows * (heads / kv_heads);
+    int64_t tile = shared <= 8 ? 8 : shared <= 16 || head_dim == 256 ? 16 : 32;
+    return 608 * (64 + 2 * tile * (head_dim + 2) * 4);
+}
+int h3q_attention_cache_nvfp4(const void *q, int64_t ld_q, int64_t rows, int64_t heads, int64_t max_rows,
+                              const int32_t *cu_rows, const int32_t *kv_len, const int32_t *block_table,
+                              int64_t batch, int64_t max_pages, const int64_t *tree_mask,
+                              const uint8_t *k_codes, const uint8_t *k_scales, const uint8_t *v_codes,
+                              const uint8_t *v_scales, int64_t num_pages, int64_t page_size,
+                              int64_t kv_heads, int64_t head_dim, const float *k_global_scale,
+                              const float *v_global_scale, float scale, void *o, float *lse,
+                              void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *h3q_last_error(void);
 

@@ -28,6 +28,7 @@ __all__ = [
     "h3q_qkv_epilogue", "h3q_rmsnorm_adaln_nvfp4_host", "host_workspace_bytes",
     "h3q_gemm_swiglu_nvfp4", "h3q_kernel_error_flag",
     "kv_cache_nvfp4", "h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4",
+    "h3q_attention_cache_nvfp4", "attention_cache_workspace_bytes",
 ]
 
 H3Q_OK = 0
@@ -61,6 +62,8 @@ _SIGNATURES = {
                                  _I64, _I64, _I64, _P],
     "h3q_kv_cache_read_nvfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P,
                                 _P, _P],
+    "h3q_attention_cache_nvfp4": [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64,
+                                  _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64, _P],
 }
 
 _lock = threading.Lock()
@@ -752,3 +755,72 @@ def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale,
             batch, max_pages, outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream, dev))
     _check("h3q_kv_cache_read_nvfp4", rc)
     return outs[0], outs[1]
+
+
+def attention_cache_workspace_bytes(max_rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
+    """Device workspace bytes of h3q_attention_cache_nvfp4 (h3q_attention_cache_workspace_bytes in
+    include/h3q.h)."""
+    shared = max_rows * (heads // kv_heads)
+    tile = 8 if shared <= 8 else 16 if shared <= 16 or head_dim == 256 else 32
+    return 608 * (64 + 2 * tile * (head_dim + 2) * 4)
+
+
+def _workspace(workspace, nbytes, stream, device):
+    """The caller's workspace, or one of torch's allocator that outlives the work on the stream."""
+    import torch
+
+    if workspace is not None:
+        _cuda_tensor("workspace", workspace, torch.uint8, device)
+        if not workspace.is_contiguous() or workspace.numel() < nbytes:
+            raise ValueError(f"workspace must be contiguous with at least {nbytes} bytes")
+        return workspace
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        # allocated on the current stream: the kernels wait for what used the block there before,
+        # and the block is not given away before they are done
+        stream.wait_stream(torch.cuda.current_stream(device))
+        workspace.record_stream(stream)
+    return workspace
+
+
+def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, *, max_rows=1,
+                              tree_mask=None, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens over the paged NVFP4 cache that holds their context and, at its
+    end, themselves (written before with the same lists).
+
+    ``q`` is bf16 [rows, heads, head_dim] (contiguous rows of any stride), heads a multiple of the
+    cache's.  Every sequence has at most ``max_rows`` (1 .. 64) new tokens.  ``tree_mask`` (int64
+    [rows]): bit j says that the token sees token j of its sequence; without it a token sees itself
+    and those before.  ``scale`` defaults to head_dim ** -0.5.  ``lse`` (fp32 [heads, rows], optional)
+    receives the log of the sums of exponentials.  ``workspace`` (uint8, at least
+    attention_cache_workspace_bytes) is allocated when not given.  Returns out, bf16 [rows, heads,
+    head_dim]; rows of no sequence are left as they were."""
+    import torch
+
+    pages, kv_heads, page, dim, dev = _cache(cache)
+    q, rows, heads, dim_q, ld = _head_rows("q", q, dev)
+    if dim_q != dim:
+        raise ValueError(f"q has head_dim {dim_q}, the cache {dim}")
+    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
+    mask_ptr = lse_ptr = None
+    if tree_mask is not None:
+        mask_ptr = _contiguous("tree_mask", tree_mask, torch.int64, (rows,), dev).data_ptr()
+    if lse is not None:
+        lse_ptr = _contiguous("lse", lse, torch.float32, (heads, rows), dev).data_ptr()
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
+    _contiguous("out", out, torch.bfloat16, (rows, heads, dim), dev)
+    with torch.cuda.device(dev):
+        nbytes = attention_cache_workspace_bytes(int(max_rows), heads, kv_heads, dim)
+        workspace = _workspace(workspace, nbytes, stream, dev)
+        rc = library().h3q_attention_cache_nvfp4(
+            q.data_ptr(), ld, rows, heads, int(max_rows), cu_rows.data_ptr(), kv_len.data_ptr(),
+            block_table.data_ptr(), batch, max_pages, mask_ptr, cache[0].data_ptr(), cache[1].data_ptr(),
+            cache[2].data_ptr(), cache[3].data_ptr(), pages, page, kv_heads, dim, kg.data_ptr(), vg.data_ptr(),
+            float(dim ** -0.5 if scale is None else scale), out.data_ptr(), lse_ptr, workspace.data_ptr(),
+            workspace.numel(), _stream(stream, dev))
+    _check("h3q_attention_cache_nvfp4", rc)
+    return out

@@ -1,0 +1,843 @@
+// attention_cache.cu -- attention of one or a few new tokens a sequence over the paged
+// NVFP4 cache that holds their context and, at its end, the tokens themselves.
+//
+// Per row (a token and one of its heads): x_j = scale * q . k_j over the keys it sees,
+// o = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m), m = max_j x_j, in one pass with the
+// running maximum and sum.  Keys before the new tokens are seen by all of them; a new
+// token sees the new tokens of its mask (64 bits; without one, itself and those before).
+//
+// What bounds it is the cache: 2 x 72 bytes a position and head at head_dim 128.
+// The rows that share a key head (a token's group of query heads, all tokens of the
+// sequence) are taken together, so the cache is read once for up to 8 * NT rows.
+//
+// Arithmetic.  A value of the cache is E2M1 * E4M3 / gsf.  The product has at most six
+// significant bits, so it is exact in fp16 (scaled by 2^-8: 2^-18 .. 10.5), and 1 / gsf
+// goes into the softmax scale and into the output: keys and values enter the tensor
+// cores without a rounding.  A query row is scaled by the power of two that brings its
+// largest magnitude into [2^14, 2^15), where every bf16 value down to 2^-29 of it is
+// exact in fp16.  Weights e^(x - m) are scaled by 2^14 and rounded to fp16 (11 bits),
+// their sum is formed in fp32 from the unrounded ones; all accumulators are fp32.
+//
+// Products with mma.sync m16n8k16 (16 keys or 16 value columns by 8 rows): a
+// decoding step has 8 to 32 rows where a tcgen05 tile has 128.  S^T = K Q^T takes the
+// keys as the left operand, so a lane's codes (32 consecutive elements of a key) are the
+// operand as they lie in memory, one conversion instruction per two codes; O^T = V^T P^T
+// pairs the codes of two keys by two byte-wise selections per 8 + 8 codes first, and P^T
+// is the transposed accumulator (movmatrix).  Measured on this GPU: the conversion with the scaling
+// runs at 77 elements a clock and SM (the copy rate needs 42), bit-field arithmetic
+// instead at 44; mma.sync at 1,024 products a clock and SM, a third of it used at NT 1.
+//
+// Work: tiles of 32 keys of one (sequence, key head, row tile), in that order, dealt
+// out in equal contiguous ranges to the CTAs of one wave, whatever the lengths; the four
+// warps of a CTA take its tiles in turn, each with its own ring of bulk copies
+// and its own running maximum, sum and output, joined through shared memory at the end
+// of a (sequence, head).  One that a range's end cuts leaves its parts in the
+// workspace, which the second kernel joins in order of the ranges: no atomics, the same
+// result every time.
+#include <cmath>
+
+#include "h3q_async.cuh"
+#include "h3q_cache.cuh"
+#include "h3q_device.cuh"
+#include "h3q_internal.h"
+
+namespace h3q {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 32;     // keys per tile
+constexpr int kStages = 3;    // tiles in flight per warp
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kPShift = 14.0f;  // weights are held as 2^14 * e^(x - m)
+constexpr int kMergeWarps = 4;    // rows per CTA of the joining kernel
+
+__device__ int g_cache_attention_fault;
+
+struct Args {
+  PagedCache cache;
+  PagedRows at;
+  const uint16_t* q;
+  int64_t ld_q;
+  int64_t rows;
+  int heads, group;        // query heads, and per key head
+  int max_rows;
+  const int64_t* mask;     // or nullptr
+  const float* k_gsf;
+  const float* v_gsf;
+  float scale;
+  uint16_t* o;
+  float* lse;              // or nullptr
+  float* part;             // workspace: [ctas][2][tile rows][head_dim] unnormalised outputs
+  float* part_ml;          // [ctas][2][tile rows][2] maxima and sums
+  struct Cut* cut;         // [ctas]
+};
+
+// What the joining kernel needs to know of the group that the start of a CTA's range cuts:
+// written by that CTA; valid for the first range's start inside the group.
+struct Cut {
+  int64_t begin, end;      // the group's tiles
+  int64_t total;           // all tiles
+  int valid, ctas;
+  int b, kv_head, row_tile, pad;
+};
+
+// One sequence as the work is counted.
+struct Seq {
+  int64_t row0;            // its first packed row
+  int n;                   // rows that are computed
+  int ctx;                 // keys before its new tokens; negative where it has more rows than keys, and
+                           // -64 or less hides every key (a mask has 64 bits)
+  int len;                 // keys in the cache
+  int tiles, groups;       // key tiles; (key head, row tile) pairs
+  int row_tiles;
+};
+
+__device__ __forceinline__ Seq sequence(const Args& a, int b, int tile_rows) {
+  Seq s;
+  const int64_t c0 = a.at.cu[b], c1 = a.at.cu[b + 1];
+  int64_t n = c1 - c0;
+  const int64_t cap = a.at.max_pages << a.cache.page_shift;
+  int64_t len = a.at.kv_len[b];
+  s.ctx = len - n < -64 ? -64 : static_cast<int>(len - n > 0x7fffffff ? 0x7fffffff : len - n);
+  if (n > a.max_rows) n = a.max_rows;
+  if (c0 + n > a.rows) n = a.rows - c0;
+  if (c0 < 0 || n < 0) n = 0;
+  len = len < 0 ? 0 : len > cap ? cap : len;
+  s.row0 = c0;
+  s.n = static_cast<int>(n);
+  s.len = static_cast<int>(len);
+  s.tiles = s.len > kKeys ? static_cast<int>((static_cast<int64_t>(s.len) + kKeys - 1) / kKeys) : 1;
+  s.row_tiles = (s.n * a.group + tile_rows - 1) / tile_rows;
+  s.groups = s.row_tiles * a.cache.kv_heads;
+  return s;
+}
+
+__device__ __forceinline__ int64_t tiles_of(const Seq& s) { return static_cast<int64_t>(s.tiles) * s.groups; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Four bytes of two E2M1 codes -> four pairs of fp16 (exact).
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
+// The low seven bits of an E4M3 byte as fp16: its exponent and mantissa in place, which
+// is its value times 2^-8, subnormals included (and finite for all bits set).
+__device__ __forceinline__ uint32_t scale_half(uint32_t byte) { return (byte & 0x7fu) << 7; }
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) {
+  if constexpr (BYTES == 4) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  }
+}
+
+// A sum over the CTA of one value a thread, and the exclusive prefix of this thread.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* prefix) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scratch[warp] = x;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  __syncthreads();
+  *prefix = before + x - v;
+  return total;
+}
+
+template <int HD, int NT>
+struct Shape {
+  static constexpr int kRows = 8 * NT;                 // rows per tile
+  static constexpr int kCodeBytes = kKeys * HD / 2;    // a tile's codes, its scales
+  static constexpr int kScaleBytes = kKeys * HD / 16;
+  static constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
+  static constexpr int kSteps = HD / 16;               // products of 16 along the head
+  static constexpr bool kQShared = NT > 2;             // query fragments in shared memory
+  static constexpr int kPitch = HD + 4;                // floats per row of the joining buffer
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffJoin = kOffRing + kWarps * kStages * kStageBytes;
+  static constexpr int kOffMl = kOffJoin + kWarps * 8 * kPitch * 4;
+  static constexpr int kOffQ = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffMask = kOffQ + (kQShared ? NT * kSteps * 32 * 8 : 0);
+  static constexpr int kOffFactor = kOffMask + kRows * 8;
+  static constexpr int kOffBar = kOffFactor + kRows * 4;
+  static constexpr int kSmem = kOffBar + kWarps * kStages * 8;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) cache_attention_kernel(const Args a) {
+  using S = Shape<HD, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scratch[kWarps];
+  __shared__ int64_t found_base;
+  __shared__ int found_b;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + S::kOffRing + warp * kStages * S::kStageBytes;
+  const uint32_t ring_u = smem_u32(ring);
+  float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
+  float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl);
+  uint2* q_shared = reinterpret_cast<uint2*>(smem + S::kOffQ);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + S::kOffMask);
+  float* row_factor = reinterpret_cast<float*>(smem + S::kOffFactor);
+  const uint32_t bars = smem_u32(smem + S::kOffBar) + warp * kStages * 8;
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+    mbar_init_fence();
+  }
+  // ---- the plan: all tiles counted, this CTA's range found
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.at.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t prefix;
+    total += block_scan(b < a.at.batch ? tiles_of(sequence(a, b, S::kRows)) : 0, scratch, &prefix);
+  }
+  const int64_t want = (total + kWarps - 1) / kWarps;
+  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
+    return;
+  }
+  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
+  {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.at.batch && base <= t0; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, S::kRows)) : 0;
+      int64_t prefix;
+      const int64_t sum = block_scan(mine, scratch, &prefix);
+      if (base + prefix <= t0 && t0 < base + prefix + mine) {
+        found_b = b;
+        found_base = base + prefix;
+      }
+      base += sum;
+    }
+    __syncthreads();
+  }
+
+  const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
+  const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
+  const int page_shift = a.cache.page_shift;
+  const int piece_keys = page_shift == 4 ? 16 : kKeys;
+  const int pieces = page_shift == 4 ? 8 : 4;
+
+  // ---- loading: this warp's tiles t0 + warp, + kWarps, ... in order, kStages ahead
+  Seq ls = sequence(a, found_b, S::kRows);   // the sequence that the loads are in
+  int lb = found_b, l_group, l_tile;         // (key head, row tile) and key tile in it
+  int64_t l_next = t0 + warp;                // the next tile to load
+  {
+    const int64_t rel = t0 - found_base;
+    l_group = static_cast<int>(rel / ls.tiles);
+    l_tile = static_cast<int>(rel - static_cast<int64_t>(l_group) * ls.tiles) + warp;
+  }
+  auto settle = [&]() {  // carry l_tile past the ends of groups and sequences
+    while (l_tile >= ls.tiles || l_group >= ls.groups) {
+      if (l_group < ls.groups) {
+        l_tile -= ls.tiles;
+        ++l_group;
+      }
+      if (l_group >= ls.groups) {
+        ++lb;
+        ls = sequence(a, lb, S::kRows);
+        l_group = 0;  // (a sequence of no rows has no groups: the loop goes on)
+      }
+    }
+  };
+  const int piece_at = (lane >> 2) * 16;     // lanes 0..7: a copy each (two pages of 16 keys to a tile)
+  auto page_number = [&]() -> int {          // this lane's page of the tile to load, -1 for none
+    const int64_t pos = static_cast<int64_t>(l_tile) * kKeys + piece_at;
+    if (lane >= pieces || pos >= ls.len) return -1;
+    const int64_t p = a.at.table[lb * a.at.max_pages + (pos >> page_shift)];
+    return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
+  };
+  int l_page = -1;
+  if (l_next < t1) {
+    settle();
+    l_page = page_number();
+  }
+  int l_stage = 0;
+  auto issue = [&]() {
+    if (l_next >= t1) return;
+    const int what = lane & 3;
+    const int per = what & 1 ? HD / 16 : HD / 2;   // bytes a key
+    const uint32_t bytes = piece_keys * per;
+    const uint32_t live = __ballot_sync(0xffffffffu, l_page >= 0);
+    const uint32_t bar = bars + 8 * l_stage;
+    if (lane == 0) mbar_expect_tx(bar, (__popc(live) / 4) * piece_keys * 2 * (HD / 2 + HD / 16));
+    __syncwarp();
+    if (l_page >= 0) {
+      const int64_t pos = static_cast<int64_t>(l_tile) * kKeys + piece_at;
+      const int kv_head = l_group / ls.row_tiles;
+      const int64_t row = ((static_cast<int64_t>(l_page) * a.cache.kv_heads + kv_head) << page_shift) +
+                          (pos & ((1 << page_shift) - 1));
+      const uint8_t* src = (what == 0   ? a.cache.codes[0]
+                            : what == 1 ? a.cache.scales[0]
+                            : what == 2 ? a.cache.codes[1]
+                                        : a.cache.scales[1]) +
+                           row * per;
+      const uint32_t off = (what >= 2 ? S::kCodeBytes + S::kScaleBytes : 0) + (what & 1 ? S::kCodeBytes : 0) +
+                           piece_at * per;
+      bulk_load(ring_u + l_stage * S::kStageBytes + off, src, bytes, bar);
+    }
+    if (++l_stage == kStages) l_stage = 0;
+    l_next += kWarps;
+    if (l_next < t1) {
+      l_tile += kWarps;
+      settle();
+      l_page = page_number();  // used by the next issue: the load has a tile's time to arrive
+    }
+  };
+  for (int s = 0; s < kStages; ++s) issue();
+
+  // ---- the segments of the range: the part of each group that lies in it
+  int stage = 0;
+  uint32_t phase = 0;
+  bool alive = true;                 // false: a wait ran out; the rest is computed from whatever is there
+  int64_t mine = t0 + warp;          // this warp's next tile
+  int b = found_b;
+  Seq s = sequence(a, b, S::kRows);
+  int group = static_cast<int>((t0 - found_base) / s.tiles);
+  int64_t begin = found_base + static_cast<int64_t>(group) * s.tiles;   // the group's first tile
+  if (threadIdx.x == 0) {
+    Cut c;
+    c.begin = begin;
+    c.end = begin + s.tiles;
+    c.total = total;
+    c.ctas = ctas;
+    c.b = b;
+    c.kv_head = group / s.row_tiles;
+    c.row_tile = group % s.row_tiles;
+    c.valid = t0 > begin && total * (blockIdx.x - 1) / ctas <= begin;   // blockIdx.x > 0 where t0 > begin
+    c.pad = 0;
+    a.cut[blockIdx.x] = c;
+  }
+  bool first_segment = true;
+  while (begin < t1) {
+    const int64_t seg_end = begin + s.tiles < t1 ? begin + s.tiles : t1;
+    const bool whole = begin >= t0 && begin + s.tiles <= t1;
+    const int kv_head = group / s.row_tiles;
+    const int row_tile = group - kv_head * s.row_tiles;
+    const int tile_row0 = row_tile * S::kRows;
+    const int live_rows = s.n * a.group - tile_row0;   // rows of the tile that exist (may be more than it holds)
+
+    // query fragments: lane (g, t) holds elements t * HD/4 .. of row g of each 8-row tile
+    uint32_t qf[S::kQShared ? 1 : NT][S::kQShared ? 1 : S::kSteps][2];
+    const bool work = mine < seg_end;
+    if (S::kQShared || work) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (S::kQShared && nt != warp) continue;  // the warps share the work (NT == kWarps)
+        const int rho = nt * 8 + g;
+        uint32_t w[HD / 8];
+        if (rho < live_rows) {
+          const int tok = (tile_row0 + rho) / a.group;
+          const int head = kv_head * a.group + (tile_row0 + rho) - tok * a.group;
+          const uint16_t* src = a.q + (s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD + t * (HD / 4);
+#pragma unroll
+          for (int i = 0; i < HD / 32; ++i) {
+            const uint4 v = load16_reused(src + 8 * i);
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HD / 8; ++i) w[i] = 0;
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) m = absmax_bf16x2(m, w[i]) & 0x7fff7fffu;
+        m = max(m & 0xffffu, m >> 16);   // magnitudes order as their bits; NaN is the largest
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i)  // (the paired maximum skips a NaN: look for exponents of all ones)
+          if ((w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u) m = 0x7f80u;
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = m >> 7;            // biased exponent of the row's largest magnitude
+        const int fe = e == 255 || m == 0 ? 127 : 268 - e > 254 ? 254 : 268 - e;
+        const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          const float2 v = bf16x2_to_float2(w[i]);
+          const uint32_t h = half2_of(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+          if constexpr (S::kQShared) {
+            reinterpret_cast<uint32_t*>(q_shared)[((nt * S::kSteps + i / 2) * 32 + lane) * 2 + (i & 1)] = h;
+          } else {
+            qf[nt][i / 2][i & 1] = h;
+          }
+        }
+        if (t == 0) {   // (several warps may write the same values)
+          const int tok = (tile_row0 + rho) / a.group;
+          row_factor[rho] = __fdiv_rn(1.0f, f);
+          row_mask[rho] = rho >= live_rows    ? 0
+                          : a.mask != nullptr ? static_cast<uint64_t>(a.mask[s.row0 + tok])
+                                              : ~uint64_t{0} >> (63 - tok);
+        }
+      }
+    }
+    if constexpr (S::kQShared) __syncthreads(); else __syncwarp();
+
+    float cf[NT][2];    // x = cf * S of the lane's columns (rows 2t, 2t + 1 of each tile), in units of
+                        // log2; never 0, so that a hidden key's -inf stays one
+    float m_run[NT][2], l_run[NT][2];
+    float acc[NT][S::kSteps][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cf[nt][i] = work ? fmaxf(__fmul_rn(k_factor, row_factor[nt * 8 + 2 * t + i]), 0x1p-126f) : 0.0f;
+        m_run[nt][i] = -INFINITY;
+        l_run[nt][i] = 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < S::kSteps; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.0f;
+    }
+
+    for (; mine < seg_end; mine += kWarps) {
+      if (alive && !__all_sync(0xffffffffu, wait_bounded(bars + 8 * stage, phase))) {
+        alive = false;
+        if (lane == 0) atomicExch(&g_cache_attention_fault, 1);
+      }
+      const uint8_t* kc = ring + stage * S::kStageBytes;
+      const uint8_t* ks = kc + S::kCodeBytes;
+      const uint8_t* vc = ks + S::kScaleBytes;
+      const uint8_t* vs = vc + S::kCodeBytes;
+      const int64_t key0 = (mine - begin) * kKeys;
+
+      // S^T: rows of the left operand are keys 4 (g / 2) + g % 2 and that + 2, so that the
+      // values' operand below finds its four keys 4t .. 4t + 3 side by side
+      float sc[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        const int r0 = mt * 16 + 4 * (g >> 1) + (g & 1);
+        uint32_t w0[HD / 32], w1[HD / 32];
+        lds<HD / 8>(kc + r0 * (HD / 2) + t * (HD / 8), w0);
+        lds<HD / 8>(kc + (r0 + 2) * (HD / 2) + t * (HD / 8), w1);
+        uint32_t b0, b1;    // the lane's HD / 64 scale bytes of both keys
+        if constexpr (HD == 64) {
+          b0 = ks[r0 * 4 + t];
+          b1 = ks[(r0 + 2) * 4 + t];
+        } else if constexpr (HD == 128) {
+          b0 = *reinterpret_cast<const uint16_t*>(ks + r0 * 8 + t * 2);
+          b1 = *reinterpret_cast<const uint16_t*>(ks + (r0 + 2) * 8 + t * 2);
+        } else {
+          b0 = *reinterpret_cast<const uint32_t*>(ks + r0 * 16 + t * 4);
+          b1 = *reinterpret_cast<const uint32_t*>(ks + (r0 + 2) * 16 + t * 4);
+        }
+#pragma unroll
+        for (int w = 0; w < HD / 32; ++w) {   // a word: 8 codes, two steps of 4; 16 codes share a scale
+          const uint32_t f0 = scale_half(b0 >> (8 * (w >> 1))) * 0x10001u;
+          const uint32_t f1 = scale_half(b1 >> (8 * (w >> 1))) * 0x10001u;
+          uint32_t h0[4], h1[4];
+          codes_to_half(w0[w], h0);
+          codes_to_half(w1[w], h1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h0[i] = hmul2(h0[i], f0);
+            h1[i] = hmul2(h1[i], f1);
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t qb0, qb1;
+              if constexpr (S::kQShared) {
+                const uint2 v = q_shared[(nt * S::kSteps + 2 * w + half) * 32 + lane];
+                qb0 = v.x, qb1 = v.y;
+              } else {
+                qb0 = qf[nt][2 * w + half][0], qb1 = qf[nt][2 * w + half][1];
+              }
+              mma(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], qb0, qb1);
+            }
+        }
+      }
+
+      // keys that a row does not see
+      if (key0 + kKeys > s.ctx || key0 + kKeys > s.len) {
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int64_t key = key0 + mt * 16 + 4 * (g >> 1) + (g & 1) + (i & 2);
+              const int64_t draft = key - s.ctx;
+              const uint64_t bits = row_mask[nt * 8 + 2 * t + (i & 1)];
+              const bool seen = key < s.len && (draft < 0 || (draft < 64 && ((bits >> draft) & 1)));
+              if (!seen) sc[mt][nt][i] = -INFINITY;
+            }
+      }
+
+      // running maximum and sum; the weights as the right operand of the second product
+      uint32_t pf[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2], base[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float m = fmaxf(fmaxf(sc[0][nt][i], sc[0][nt][i + 2]), fmaxf(sc[1][nt][i], sc[1][nt][i + 2]));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          m = fmaxf(m_run[nt][i], m == -INFINITY ? -INFINITY : __fmul_rn(m, cf[nt][i]));
+          const float use = m == -INFINITY ? 0.0f : m;
+          alpha[i] = ex2(__fadd_rn(m_run[nt][i], -use));
+          base[i] = __fadd_rn(kPShift, -use);
+          m_run[nt][i] = m;
+        }
+        float add[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          float p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            p[i] = ex2(__fmaf_rn(sc[mt][nt][i], cf[nt][i & 1], base[i & 1]));
+            add[i & 1] = __fadd_rn(add[i & 1], p[i]);
+          }
+          pf[mt][nt][0] = transpose8x8(half2_of(p[0], p[1]));
+          pf[mt][nt][1] = transpose8x8(half2_of(p[2], p[3]));
+        }
+        l_run[nt][0] = __fmaf_rn(l_run[nt][0], alpha[0], add[0]);
+        l_run[nt][1] = __fmaf_rn(l_run[nt][1], alpha[1], add[1]);
+        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+          for (int i = 0; i < S::kSteps; ++i) {
+            acc[nt][i][0] = __fmul_rn(acc[nt][i][0], alpha[0]);
+            acc[nt][i][1] = __fmul_rn(acc[nt][i][1], alpha[1]);
+            acc[nt][i][2] = __fmul_rn(acc[nt][i][2], alpha[0]);
+            acc[nt][i][3] = __fmul_rn(acc[nt][i][3], alpha[1]);
+          }
+        }
+      }
+
+      // O^T: lane (g, t) holds columns g * HD/8 .. of keys 4t .. 4t + 3
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t w[4][HD / 64 > 0 ? HD / 64 : 1];
+        uint32_t f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = mt * 16 + 4 * t + k;
+          lds<HD / 16>(vc + key * (HD / 2) + g * (HD / 16), w[k]);
+          if constexpr (HD == 64)
+            f[k] = vs[key * 4 + (g >> 1)];
+          else if constexpr (HD == 128)
+            f[k] = vs[key * 8 + g];
+          else
+            f[k] = *reinterpret_cast<const uint16_t*>(vs + key * 16 + g * 2);
+        }
+#pragma unroll
+        for (int j = 0; j < HD / 64; ++j) {   // a word: 8 columns of each key
+          const int sh = HD == 256 ? 8 * (j >> 1) : 0;
+          const uint32_t f01 = scale_half(f[0] >> sh) | scale_half(f[1] >> sh) << 16;
+          const uint32_t f23 = scale_half(f[2] >> sh) | scale_half(f[3] >> sh) << 16;
+          // bytes of (first key's, second key's) codes of the even and of the odd columns
+          const uint32_t e01 = (w[0][j] & 0x0f0f0f0fu) | ((w[1][j] << 4) & 0xf0f0f0f0u);
+          const uint32_t o01 = ((w[0][j] >> 4) & 0x0f0f0f0fu) | (w[1][j] & 0xf0f0f0f0u);
+          const uint32_t e23 = (w[2][j] & 0x0f0f0f0fu) | ((w[3][j] << 4) & 0xf0f0f0f0u);
+          const uint32_t o23 = ((w[2][j] >> 4) & 0x0f0f0f0fu) | (w[3][j] & 0xf0f0f0f0u);
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          codes_to_half(e01, a0);
+          codes_to_half(o01, a1);
+          codes_to_half(e23, a2);
+          codes_to_half(o23, a3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a0[i] = hmul2(a0[i], f01);
+            a1[i] = hmul2(a1[i], f01);
+            a2[i] = hmul2(a2[i], f23);
+            a3[i] = hmul2(a3[i], f23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma(acc[nt][4 * j + i], a0[i], a1[i], a2[i], a3[i], pf[mt][nt][0], pf[mt][nt][1]);
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the stage before it is filled again
+      issue();
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+
+    // ---- join the warps, eight rows at a time; write the outputs or leave the part
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float l = l_run[nt][i];
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 4));
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 8));
+        l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 16));
+        if (g == 0) join_ml[warp * 8 + 2 * t + i] = make_float2(m_run[nt][i], l);
+      }
+      if (work) {
+        float* dst = join + warp * 8 * S::kPitch + g * (HD / 8);
+#pragma unroll
+        for (int i = 0; i < S::kSteps; ++i) {
+          *reinterpret_cast<float2*>(dst + (2 * t) * S::kPitch + 2 * i) = make_float2(acc[nt][i][0], acc[nt][i][2]);
+          *reinterpret_cast<float2*>(dst + (2 * t + 1) * S::kPitch + 2 * i) =
+              make_float2(acc[nt][i][1], acc[nt][i][3]);
+        }
+      }
+      __syncthreads();
+      {
+        constexpr int kPer = HD / 16;        // columns per thread, 16 threads a row
+        const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
+        const int rho = nt * 8 + row;
+        if (rho < live_rows) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_ml[w * 8 + row].x);
+          const float use = m == -INFINITY ? 0.0f : m;
+          float l = 0.0f, v[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const float2 ml = join_ml[w * 8 + row];
+            if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // no key of this warp's: its rows may hold anything
+            const float f = ex2(__fadd_rn(ml.x, -use));
+            l = __fmaf_rn(ml.y, f, l);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(join + (w * 8 + row) * S::kPitch + c0 + i);
+              v[i] = __fmaf_rn(x.x, f, v[i]);
+              v[i + 1] = __fmaf_rn(x.y, f, v[i + 1]);
+              v[i + 2] = __fmaf_rn(x.z, f, v[i + 2]);
+              v[i + 3] = __fmaf_rn(x.w, f, v[i + 3]);
+            }
+          }
+          const int tok = (tile_row0 + rho) / a.group;
+          const int head = kv_head * a.group + (tile_row0 + rho) - tok * a.group;
+          const int64_t out_row = s.row0 + tok;
+          if (whole) {
+            const float f = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
+            uint32_t w[kPer / 2];
+#pragma unroll
+            for (int i = 0; i < kPer / 2; ++i)
+              w[i] = float2_to_bf16x2(make_float2(__fmul_rn(v[2 * i], f), __fmul_rn(v[2 * i + 1], f)));
+            uint16_t* dst = a.o + (out_row * a.heads + head) * HD + c0;
+            if constexpr (kPer == 4) {
+              *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kPer / 8; ++i)
+                store16(dst + 8 * i, make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+            }
+            if (a.lse != nullptr && c0 == 0)
+              a.lse[head * a.rows + out_row] =
+                  l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, __fadd_rn(log2f(l), -kPShift)), kLn2);
+          } else {
+            const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1);
+            float* dst = a.part + (slot * S::kRows + rho) * HD + c0;
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4)
+              *reinterpret_cast<float4*>(dst + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            if (c0 == 0) reinterpret_cast<float2*>(a.part_ml)[slot * S::kRows + rho] = make_float2(m, l);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    // ---- the next group
+    first_segment = false;
+    begin += s.tiles;
+    if (begin >= t1) break;
+    if (++group >= s.groups) {
+      group = 0;
+      do {
+        s = sequence(a, ++b, S::kRows);
+      } while (s.groups == 0);
+    }
+  }
+}
+
+// Joins the parts of the groups that the ranges' starts cut: CTA (c, r) takes the group
+// that the start of range c is the first to cut, a warp each of its rows.
+template <int HD, int NT>
+__global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args a) {
+  using S = Shape<HD, NT>;
+  constexpr int kPer = HD / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are written
+  const int c = blockIdx.x + 1;
+  const Cut cut = a.cut[c];
+  if (!cut.valid) return;
+  const int lane = threadIdx.x & 31;
+  const int rho = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const Seq s = sequence(a, cut.b, S::kRows);
+  const int tile_row0 = cut.row_tile * S::kRows;
+  if (tile_row0 + rho >= s.n * a.group) return;
+  // the first range's part is its last segment: slot 0 if the range began in this group too
+  const int64_t prev0 = cut.total * (c - 1) / cut.ctas;
+  const int64_t first = static_cast<int64_t>(c - 1) * 2 + (prev0 >= cut.begin ? 0 : 1);
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+  int last = c;   // one past the last range that starts inside the group
+  while (last < cut.ctas && cut.total * last / cut.ctas < cut.end) ++last;
+  auto slot = [&](int k) { return (k == c - 1 ? first : static_cast<int64_t>(k) * 2) * S::kRows + rho; };
+  float m = -INFINITY;
+  for (int k = c - 1 + lane; k < last; k += 32) m = fmaxf(m, ml[slot(k)].x);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float use = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f, v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (int k = c - 1; k < last; ++k) {
+    const float2 x = ml[slot(k)];
+    const float f = x.x == -INFINITY ? 0.0f : ex2(__fadd_rn(x.x, -use));
+    l = __fmaf_rn(x.y, f, l);
+    const float* src = a.part + slot(k) * HD + lane * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(src + i);
+      v[i] = __fmaf_rn(y.x, f, v[i]);
+      v[i + 1] = __fmaf_rn(y.y, f, v[i + 1]);
+    }
+  }
+  const int tok = (tile_row0 + rho) / a.group;
+  const int head = cut.kv_head * a.group + (tile_row0 + rho) - tok * a.group;
+  const int64_t out_row = s.row0 + tok;
+  const float f = l == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(256.0f, *a.v_gsf), l);
+  uint16_t* dst = a.o + (out_row * a.heads + head) * HD + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2)
+    *reinterpret_cast<uint32_t*>(dst + i) =
+        float2_to_bf16x2(make_float2(__fmul_rn(v[i], f), __fmul_rn(v[i + 1], f)));
+  if (a.lse != nullptr && lane == 0)
+    a.lse[head * a.rows + out_row] =
+        l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, __fadd_rn(log2f(l), -kPShift)), kLn2);
+}
+
+template <int HD, int NT>
+cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
+  using S = Shape<HD, NT>;
+  static_assert(S::kSmem <= 227 * 1024, "shared memory");
+  static_assert(!S::kQShared || NT == kWarps, "a warp loads one 8-row tile of queries");
+  int blocks = 0;
+  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_kernel<HD, NT>), kThreads,
+                                      S::kSmem, kCacheAttentionMaxCtas, &blocks);
+  if (err != cudaSuccess) return err;
+  a.cut = reinterpret_cast<Cut*>(workspace);
+  static_assert(sizeof(Cut) <= kCacheAttentionCutBytes, "workspace");
+  a.part_ml = reinterpret_cast<float*>(workspace + kCacheAttentionCutBytes * kCacheAttentionMaxCtas);
+  a.part = a.part_ml + int64_t{kCacheAttentionMaxCtas} * 2 * S::kRows * 2;
+  cache_attention_kernel<HD, NT><<<blocks, kThreads, S::kSmem, stream>>>(a);
+  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), S::kRows / kMergeWarps, 1);
+  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD, NT>, a);
+}
+
+// Rows that share a key head are taken 8, 16 or 32 at a time: the fewest that hold them
+// all, so the cache is read once for up to 32 rows (16 at head_dim 256, where the
+// outputs of 32 would not fit the registers).
+template <int HD>
+cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group;
+  if (rows <= 8) return launch<HD, 1>(a, workspace, stream);
+  if constexpr (HD == 256) return launch<HD, 2>(a, workspace, stream);
+  else return rows <= 16 ? launch<HD, 2>(a, workspace, stream) : launch<HD, 4>(a, workspace, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attention(const PagedCache& cache, const PagedRows& at, const uint16_t* q, int64_t ld_q,
+                                   int64_t rows, int heads, int max_rows, const int64_t* mask, const float* k_gsf,
+                                   const float* v_gsf, float scale, uint16_t* o, float* lse, uint8_t* workspace,
+                                   cudaStream_t stream) {
+  Args a{};
+  a.cache = cache;
+  a.at = at;
+  a.q = q;
+  a.ld_q = ld_q;
+  a.rows = rows;
+  a.heads = heads;
+  a.group = heads / cache.kv_heads;
+  a.max_rows = max_rows;
+  a.mask = mask;
+  a.k_gsf = k_gsf;
+  a.v_gsf = v_gsf;
+  a.scale = scale;
+  a.o = o;
+  a.lse = lse;
+  switch (cache.head_dim) {
+    case 64: return dispatch<64>(a, workspace, stream);
+    case 128: return dispatch<128>(a, workspace, stream);
+    default: return dispatch<256>(a, workspace, stream);
+  }
+}
+
+cudaError_t cache_attention_error_flag(int* flag) {
+  int zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(flag, g_cache_attention_fault, sizeof(int));
+  if (err == cudaSuccess) err = cudaMemcpyToSymbol(g_cache_attention_fault, &zero, sizeof(int));
+  return err;
+}
+
+}  // namespace h3q

@@ -536,7 +536,10 @@ int h3q_kernel_error_flag(int* flag) {
   static const char* fn = "h3q_kernel_error_flag";
   g_last_error.clear();
   if (flag == nullptr) return invalid(fn, "flag must not be NULL");
-  cudaError_t err = h3q::gemm_error_flag(flag);
+  int gemm = 0, cache = 0;
+  cudaError_t err = h3q::gemm_error_flag(&gemm);
+  if (err == cudaSuccess) err = h3q::cache_attention_error_flag(&cache);
+  *flag = gemm | cache;
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 
@@ -837,6 +840,56 @@ int h3q_kv_cache_read_nvfp4(const uint8_t* k_codes, const uint8_t* k_scales, con
   const float* gsf[2] = {k_global_scale, v_global_scale};
   const h3q::PagedRows at{cu_rows, kv_len, block_table, max_pages, static_cast<int>(batch)};
   cudaError_t err = h3q::launch_cache_read(paged_cache(c), at, out, gsf, rows, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+int h3q_attention_cache_nvfp4(const void* q, int64_t ld_q, int64_t rows, int64_t heads, int64_t max_rows,
+                              const int32_t* cu_rows, const int32_t* kv_len, const int32_t* block_table,
+                              int64_t batch, int64_t max_pages, const int64_t* tree_mask, const uint8_t* k_codes,
+                              const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales,
+                              int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t head_dim,
+                              const float* k_global_scale, const float* v_global_scale, float scale, void* o,
+                              float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  static const char* fn = "h3q_attention_cache_nvfp4";
+  g_last_error.clear();
+  CacheShape c{const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(k_scales), const_cast<uint8_t*>(v_codes),
+               const_cast<uint8_t*>(v_scales), num_pages, page_size, kv_heads, head_dim, {}};
+  if (int e = check_cache(fn, c)) return e;
+  if (rows < 0) return invalid(fn, "rows must be >= 0");
+  if (rows > kMaxRows) return invalid(fn, "rows exceeds 2^40");
+  if (heads < 1 || heads % kv_heads != 0) return invalid(fn, "heads must be a positive multiple of kv_heads");
+  if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
+  if (max_rows < 1 || max_rows > 64) return invalid(fn, "max_rows must be in [1, 64]");
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
+  if (int e = check_lists(fn, cu_rows, kv_len, block_table, batch, max_pages)) return e;
+  if (rows == 0 || batch == 0) return H3Q_OK;
+  const int64_t d = heads * head_dim;
+  if (int e = check_input(fn, "q", q, ld_q, rows, d)) return e;
+  if (int e = check_cache_buffers(fn, c)) return e;
+  if (int e = check_scales(fn, k_global_scale, v_global_scale)) return e;
+  if (tree_mask != nullptr && !aligned(tree_mask, 8)) return invalid(fn, "tree_mask must be 8-byte aligned");
+  if (o == nullptr || !aligned(o, 16)) return invalid(fn, "o must be 16-byte aligned and not NULL");
+  if (lse != nullptr && !aligned(lse, 4)) return invalid(fn, "lse must be 4-byte aligned");
+  if (workspace == nullptr || !aligned(workspace, 256)) return invalid(fn, "workspace must be 256-byte aligned");
+  if (workspace_bytes < h3q_attention_cache_workspace_bytes(max_rows, heads, kv_heads, head_dim))
+    return invalid(fn, "workspace_bytes is below h3q_attention_cache_workspace_bytes");
+  const Span outs[3] = {span(o, rows * d * 2), lse ? span(lse, heads * rows * 4) : Span{0, 0},
+                        span(workspace, workspace_bytes)};
+  const Span ins[] = {span(q, view_bytes(rows, d, ld_q)), c.spans[0], c.spans[1], c.spans[2], c.spans[3],
+                      span(cu_rows, (batch + 1) * 4), span(kv_len, batch * 4),
+                      span(block_table, batch * max_pages * 4), span(k_global_scale, 4), span(v_global_scale, 4),
+                      tree_mask ? span(tree_mask, rows * 8) : Span{0, 0}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& in : ins)
+      if (overlap(outs[i], in)) return invalid(fn, "an output or the workspace overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return invalid(fn, "outputs and workspace overlap each other");
+  }
+  const h3q::PagedRows at{cu_rows, kv_len, block_table, max_pages, static_cast<int>(batch)};
+  cudaError_t err = h3q::launch_cache_attention(
+      paged_cache(c), at, static_cast<const uint16_t*>(q), ld_q, rows, static_cast<int>(heads),
+      static_cast<int>(max_rows), tree_mask, k_global_scale, v_global_scale, scale, static_cast<uint16_t*>(o), lse,
+      static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 

@@ -114,6 +114,19 @@ cudaError_t launch_cache_write(const PagedCache& cache, const PagedRows& at, con
 cudaError_t launch_cache_read(const PagedCache& cache, const PagedRows& at, uint16_t* const out[2],
                               const float* const gsf[2], int64_t rows, cudaStream_t stream);
 
+// Attention of up to 64 new tokens a sequence over the paged cache that holds them at
+// its end; `mask` (bit j of a token's mask: it sees new token j) or nullptr for a
+// chain; the workspace as h3q_attention_cache_workspace_bytes (include/h3q.h): per CTA
+// a record, then maxima and sums, then outputs of the parts that two CTAs share.
+constexpr int kCacheAttentionMaxCtas = 608;
+constexpr int kCacheAttentionCutBytes = 64;
+cudaError_t launch_cache_attention(const PagedCache& cache, const PagedRows& at, const uint16_t* q, int64_t ld_q,
+                                   int64_t rows, int heads, int max_rows, const int64_t* mask, const float* k_gsf,
+                                   const float* v_gsf, float scale, uint16_t* o, float* lse, uint8_t* workspace,
+                                   cudaStream_t stream);
+// As gemm_error_flag, for the kernel of launch_cache_attention.
+cudaError_t cache_attention_error_flag(int* flag);
+
 // RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
 // copies pipelined with the producer over chunk_rows-row chunks; `workspace`
 // holds h3q_host_workspace_bytes(chunk_rows, cols, rows, row_frame == nullptr)

@@ -78,3 +78,54 @@ def values32(codes, scales, gsf):
     s = scales.astype(np.int32) & 127
     f = np.where(s >> 3 == 0, (s & 7) * 2.0 ** -9, (1 + (s & 7) / 8) * 2.0 ** ((s >> 3) - 7.0)).astype(np.float32)
     return (v * np.repeat(f, 16, -1)) / np.float32(gsf)
+
+
+def cache_values64(cache, gs, table_row, length, page):
+    """k and v [length, heads, dim] in 64 bits of one sequence's positions (on the cache's device)."""
+    at = np.arange(length)
+    pages = torch.as_tensor(np.asarray(table_row.cpu())[at // page].astype(np.int64), device=cache[0].device)
+    row = torch.as_tensor(at % page, device=cache[0].device)
+    lut = torch.tensor(np.concatenate([E2M1, -E2M1]).astype(np.float64), device=cache[0].device)
+    out = []
+    for t in (0, 1):
+        codes, scales = cache[2 * t][pages, :, row], cache[2 * t + 1][pages, :, row].long() & 127
+        c = lut[torch.stack((codes & 15, codes >> 4), -1).flatten(-2).long()]
+        e, m = scales >> 3, (scales & 7).double()
+        f = torch.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * torch.pow(2.0, (e - 7).double()))
+        out.append(c * f.repeat_interleave(16, -1) / gs[t])
+    return out
+
+
+def attention64(q, k, v, seen, scale):
+    """Attention of q [n, H, D] over k, v [keys, KH, D] in 64 bits where seen [n, keys]: o [n, H, D], lse [H, n],
+    and what the tolerances need: w|v| [n, H, D] and the largest sum of |products| in units of log2."""
+    n, heads, dim = q.shape
+    group = heads // k.shape[1]
+    q, k, v = q.double(), k.double().repeat_interleave(group, 1), v.double().repeat_interleave(group, 1)
+    x = torch.einsum("nhd,khd->hnk", q, k) * scale
+    if k.shape[0] == 0:
+        zero = torch.zeros((n, heads, dim), dtype=torch.float64, device=q.device)
+        return zero, torch.full((heads, n), -np.inf, dtype=torch.float64, device=q.device), zero, 0.0
+    size = float((torch.einsum("nhd,khd->hnk", q.abs(), k.abs())).max()) * scale * 1.4427
+    x = x.masked_fill(~seen[None], -np.inf)
+    lse = torch.logsumexp(x, -1)
+    w = torch.where(seen[None], torch.exp(x - lse[..., None].clamp(min=-1e300)), torch.zeros_like(x))
+    return torch.einsum("hnk,khd->nhd", w, v), lse, torch.einsum("hnk,khd->nhd", w, v.abs()), size
+
+
+def check_attention(o, lse, ref, keys, weight_step, what=""):
+    """o and lse against attention64's answer.  The output is rounded once to bf16 (2^-8 of it).  Each weight
+    has a relative error of its own rounding (weight_step, 0 where it is not rounded), and of its exponent:
+    fp32 sums of at most 256 products err by 2^-19 of the sum of magnitudes at most (16 steps of four
+    roundings of 2^-23 or better), the power of two by 2^-22, and the running sums over `keys` / 16 steps by 2^-22
+    each.  An error e of all weights moves the output by at most 2 e sum(w |v|): numerator and denominator."""
+    want, want_lse, spread, size = ref
+    e = weight_step + 2.0 ** -19 * (size + 8) + 2.0 ** -22 * (keys / 16 + 8)
+    tol = want.abs() * 2.0 ** -8 + 2 * e * spread * (1 + 2.0 ** -8) + 1e-38
+    err = (o.double() - want).abs()
+    assert bool((err <= tol).all()), f"{what}: o off by {float((err / tol).max()):.3g} of what is allowed"
+    empty = torch.isinf(want_lse)
+    assert bool((lse[empty] == -np.inf).all()), f"{what}: lse of rows that see nothing"
+    err = (lse.double() - want_lse)[~empty].abs()
+    allowed = 2 * (e - weight_step) + want_lse[~empty].abs() * 2.0 ** -22
+    assert bool((err <= allowed).all()), f"{what}: lse off by {float((err / allowed).max()):.3g} of what is allowed"

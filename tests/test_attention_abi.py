@@ -93,3 +93,45 @@ def test_python_binding_refuses_host_tensors():
         h3q.h3q_kv_cache_write_nvfp4(x, x, cache, *lists, g, g)
     with pytest.raises(ValueError, match="CUDA tensor"):
         h3q.h3q_kv_cache_read_nvfp4(cache, *lists, g, g, rows=1)
+
+
+CACHED = ["q", "ld_q", "rows", "heads", "max_rows", "cu", "len", "table", "batch", "max_pages", "mask", "kc", "ks", "vc",
+          "vs", "pages", "page", "kv_heads", "dim", "kg", "vg", "scale", "o", "lse", "ws", "wsb", "stream"]
+CACHED_GOOD = [0x1000000, 1024, 10, 8, 4, 0x1200000, 0x1201000, 0x1202000, 3, 4, None, 0x2000000, 0x2100000, 0x2200000,
+               0x2300000, 16, 16, 2, 128, 0x1203000, 0x1203004, 0.1, 0x3000000, None, 0x10000000,
+               h3q.attention_cache_workspace_bytes(4, 8, 2, 128), None]
+
+
+def test_cache_attention_refusals(lib):
+    call = caller(lib.h3q_attention_cache_nvfp4, CACHED, CACHED_GOOD)
+    assert call() in (0, 2)
+    for kw, what in (({"dim": 96}, "head_dim"), ({"heads": 7}, "multiple of kv_heads"), ({"heads": 0}, "multiple"),
+                     ({"heads": 1 << 18}, "2^24"), ({"max_rows": 0}, "max_rows"), ({"max_rows": 65}, "max_rows"),
+                     ({"scale": 0.0}, "scale"), ({"scale": -1.0}, "scale"), ({"scale": float("nan")}, "scale"),
+                     ({"scale": float("inf")}, "scale"), ({"rows": -1}, "rows"), ({"batch": -1}, "batch"),
+                     ({"q": None}, "q is NULL"), ({"q": 0x1000010}, "32-byte"), ({"ld_q": 1000}, "ld of q"),
+                     ({"ld_q": 512}, "ld of q"), ({"mask": 0x1300004}, "8-byte"), ({"o": 0x3000008}, "16-byte"),
+                     ({"o": None}, "16-byte"), ({"lse": 0x3100002}, "4-byte"), ({"ws": None}, "256-byte"),
+                     ({"ws": 0x10000080}, "256-byte"), ({"wsb": CACHED_GOOD[-2] - 1}, "workspace_bytes"),
+                     ({"o": 0x1000000 + 2048}, "overlaps"), ({"lse": 0x3000000}, "overlap"),
+                     ({"ws": 0x2fff000 // 256 * 256}, "overlap"), ({"page": 40}, "page_size"),
+                     ({"table": None}, "block_table"), ({"kg": None}, "global_scale")):
+        assert call(**kw) == h3q.H3Q_ERR_INVALID_ARGUMENT, kw
+        assert what in h3q.h3q_last_error(), (kw, h3q.h3q_last_error())
+    assert call(rows=0, q=None, o=None) == h3q.H3Q_OK
+    assert call(batch=0, cu=None, len=None, table=None) == h3q.H3Q_OK
+
+
+def test_workspace_bytes_of_header_and_binding_agree(tmp_path):
+    src = tmp_path / "ws.c"
+    src.write_text('#include <stdio.h>\n#include "h3q.h"\nint main(void){\n'
+                   'int64_t a[][4]={{1,8,8,64},{1,32,8,128},{4,8,2,128},{9,8,2,128},{16,32,8,256},{64,64,1,64}};\n'
+                   'for(int i=0;i<6;++i)printf("%lld\\n",(long long)h3q_attention_cache_workspace_bytes('
+                   'a[i][0],a[i][1],a[i][2],a[i][3]));return 0;}\n')
+    exe = str(tmp_path / "ws")
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(os.path.dirname(HERE), "include"), str(src), "-o", exe],
+                   check=True)
+    got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()]
+    want = [h3q.attention_cache_workspace_bytes(*a) for a in ((1, 8, 8, 64), (1, 32, 8, 128), (4, 8, 2, 128),
+                                                             (9, 8, 2, 128), (16, 32, 8, 256), (64, 64, 1, 64))]
+    assert got == want
