@@ -532,6 +532,37 @@ int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, con
                             int64_t max_pages, void *k_out, void *v_out, void *stream);
 
 /*
+ * Softmax attention over whole packed sequences: prompts, chunks of prompts over their
+ * prefixes (h3q_kv_cache_read_nvfp4), the tokens of video frames.  For query token i of
+ * sequence b and head h, with key head h / (heads / kv_heads),
+ *   x_j = scale * (q . k_j),  o = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  m = max x_j,
+ * over the sequence's keys j, with `causal` those with j <= i + (keys - queries): the
+ * last query sees the last key.  lse = m + log(sum_j e^(x_j - m)), natural.  A query that
+ * sees no key gets o = 0 and lse = -inf.  Products are of bf16 values with fp32 sums, the
+ * weights are rounded to bf16, everything else is fp32.  A key or value that is no
+ * number reaches only the rows that see it (an infinite value as if its weight were
+ * positive).
+ *
+ *   q           bf16 [rows_q, heads * head_dim], row stride ld_q; k, v bf16 [rows_k,
+ *               kv_heads * head_dim], row strides ld_k, ld_v.  32-byte aligned.
+ *   cu_q, cu_k  int32 [batch + 1] on the device, not decreasing: sequence b has queries
+ *               cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1.  Not checked on the
+ *               host; no contents make the kernel touch memory outside the buffers.
+ *   rows_q, rows_k  0 .. 2^31 - 512.   heads  a multiple of kv_heads; heads * head_dim <= 2^24.
+ *   head_dim    64, 128 or 256.        scale  finite, > 0 (e.g. head_dim^-0.5).
+ *   causal      0 or 1.
+ *   o           out, bf16 [rows_q, heads, head_dim] contiguous, 16-byte aligned.
+ *   lse         out, fp32 [heads, rows_q], 4-byte aligned, or NULL.
+ *               Rows of no sequence are left as they were in both.
+ * The kernel's waits are bounded (2 s): if one runs out it stops early, the outputs are
+ * unspecified, and h3q_kernel_error_flag reports it.
+ */
+int h3q_attention_varlen(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                         const int32_t *cu_q, const int32_t *cu_k, int64_t batch, int64_t rows_q,
+                         int64_t rows_k, int64_t heads, int64_t kv_heads, int64_t head_dim, int causal,
+                         float scale, void *o, float *lse, void *stream);
+
+/*
  * Attention of one or a few new tokens a sequence over the paged cache that holds the
  * sequence's context and, at its last positions, the new tokens themselves (written
  * before by h3q_kv_cache_write_nvfp4 with the same lists): decoding (one token), several

@@ -28,7 +28,7 @@ __all__ = [
     "h3q_qkv_epilogue", "h3q_rmsnorm_adaln_nvfp4_host", "host_workspace_bytes",
     "h3q_gemm_swiglu_nvfp4", "h3q_kernel_error_flag",
     "kv_cache_nvfp4", "h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4",
-    "h3q_attention_cache_nvfp4", "attention_cache_workspace_bytes",
+    "h3q_attention_cache_nvfp4", "attention_cache_workspace_bytes", "h3q_attention_varlen",
 ]
 
 H3Q_OK = 0
@@ -62,6 +62,8 @@ _SIGNATURES = {
                                  _I64, _I64, _I64, _P],
     "h3q_kv_cache_read_nvfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _P,
                                 _P, _P],
+    "h3q_attention_varlen": [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_int,
+                             ctypes.c_float, _P, _P, _P],
     "h3q_attention_cache_nvfp4": [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64,
                                   _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64, _P],
 }
@@ -823,4 +825,39 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
             float(dim ** -0.5 if scale is None else scale), out.data_ptr(), lse_ptr, workspace.data_ptr(),
             workspace.numel(), _stream(stream, dev))
     _check("h3q_attention_cache_nvfp4", rc)
+    return out
+
+
+def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=None, lse=None, stream=None):
+    """Softmax attention over packed sequences: q bf16 [rows_q, heads, head_dim], k and v bf16
+    [rows_k, kv_heads, head_dim] (contiguous rows of any stride; heads a multiple of kv_heads).
+    Sequence b has queries cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1 (int32 CUDA tensors);
+    with ``causal`` its last query sees its last key and every query one fewer than the next.
+    ``scale`` defaults to head_dim ** -0.5.  ``lse`` (fp32 [heads, rows_q], optional) receives the log
+    of the sums of exponentials.  Returns out, bf16 [rows_q, heads, head_dim]; rows of no sequence are
+    left as they were."""
+    import torch
+
+    q, rows_q, heads, dim, ld_q = _head_rows("q", q)
+    dev = q.device
+    k, rows_k, kv_heads, dim_k, ld_k = _head_rows("k", k, dev)
+    v, rows_v, heads_v, dim_v, ld_v = _head_rows("v", v, dev)
+    if dim_k != dim or (rows_v, heads_v, dim_v) != (rows_k, kv_heads, dim):
+        raise ValueError("k and v must have the same shape, and q's head_dim")
+    _cuda_tensor("cu_q", cu_q, torch.int32, dev)
+    if cu_q.dim() != 1 or cu_q.shape[0] < 1 or not cu_q.is_contiguous():
+        raise ValueError("cu_q must be contiguous [batch + 1]")
+    _contiguous("cu_k", cu_k, torch.int32, cu_q.shape, dev)
+    if out is None:
+        out = torch.empty((rows_q, heads, dim), dtype=torch.bfloat16, device=dev)
+    _contiguous("out", out, torch.bfloat16, (rows_q, heads, dim), dev)
+    lse_ptr = None
+    if lse is not None:
+        lse_ptr = _contiguous("lse", lse, torch.float32, (heads, rows_q), dev).data_ptr()
+    with torch.cuda.device(dev):
+        rc = library().h3q_attention_varlen(
+            q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, cu_q.data_ptr(), cu_k.data_ptr(),
+            cu_q.shape[0] - 1, rows_q, rows_k, heads, kv_heads, dim, int(bool(causal)),
+            float(dim ** -0.5 if scale is None else scale), out.data_ptr(), lse_ptr, _stream(stream, dev))
+    _check("h3q_attention_varlen", rc)
     return out

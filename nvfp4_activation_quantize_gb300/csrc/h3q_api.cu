@@ -536,10 +536,11 @@ int h3q_kernel_error_flag(int* flag) {
   static const char* fn = "h3q_kernel_error_flag";
   g_last_error.clear();
   if (flag == nullptr) return invalid(fn, "flag must not be NULL");
-  int gemm = 0, cache = 0;
+  int gemm = 0, cache = 0, attention = 0;
   cudaError_t err = h3q::gemm_error_flag(&gemm);
   if (err == cudaSuccess) err = h3q::cache_attention_error_flag(&cache);
-  *flag = gemm | cache;
+  if (err == cudaSuccess) err = h3q::attention_error_flag(&attention);
+  *flag = gemm | cache | attention;
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 
@@ -840,6 +841,49 @@ int h3q_kv_cache_read_nvfp4(const uint8_t* k_codes, const uint8_t* k_scales, con
   const float* gsf[2] = {k_global_scale, v_global_scale};
   const h3q::PagedRows at{cu_rows, kv_len, block_table, max_pages, static_cast<int>(batch)};
   cudaError_t err = h3q::launch_cache_read(paged_cache(c), at, out, gsf, rows, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+int h3q_attention_varlen(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                         const int32_t* cu_q, const int32_t* cu_k, int64_t batch, int64_t rows_q, int64_t rows_k,
+                         int64_t heads, int64_t kv_heads, int64_t head_dim, int causal, float scale, void* o,
+                         float* lse, void* stream) {
+  static const char* fn = "h3q_attention_varlen";
+  g_last_error.clear();
+  constexpr int64_t kMaxPacked = (int64_t(1) << 31) - 512;   // tensor-copy coordinates are 32-bit
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return invalid(fn, "head_dim must be 64, 128 or 256");
+  if (kv_heads < 1) return invalid(fn, "kv_heads must be >= 1");
+  if (heads < 1 || heads % kv_heads != 0) return invalid(fn, "heads must be a positive multiple of kv_heads");
+  if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
+  if (rows_q < 0 || rows_q > kMaxPacked) return invalid(fn, "rows_q must be in [0, 2^31 - 512]");
+  if (rows_k < 0 || rows_k > kMaxPacked) return invalid(fn, "rows_k must be in [0, 2^31 - 512]");
+  if (batch < 0 || batch >= (int64_t(1) << 31)) return invalid(fn, "batch must be in [0, 2^31)");
+  if (causal != 0 && causal != 1) return invalid(fn, "causal must be 0 or 1");
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
+  if (rows_q == 0 || batch == 0) return H3Q_OK;
+  const int64_t dq = heads * head_dim, dk = kv_heads * head_dim;
+  if (int e = check_input(fn, "q", q, ld_q, rows_q, dq)) return e;
+  if (rows_k > 0) {
+    if (int e = check_input(fn, "k", k, ld_k, rows_k, dk)) return e;
+    if (int e = check_input(fn, "v", v, ld_v, rows_k, dk)) return e;
+  }
+  if (cu_q == nullptr || cu_k == nullptr || !aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return invalid(fn, "cu_q and cu_k must be 4-byte aligned and not NULL");
+  if (o == nullptr || !aligned(o, 16)) return invalid(fn, "o must be 16-byte aligned and not NULL");
+  if (lse != nullptr && !aligned(lse, 4)) return invalid(fn, "lse must be 4-byte aligned");
+  const Span outs[2] = {span(o, rows_q * dq * 2), lse ? span(lse, heads * rows_q * 4) : Span{0, 0}};
+  const Span ins[] = {span(q, view_bytes(rows_q, dq, ld_q)),
+                      rows_k > 0 ? span(k, view_bytes(rows_k, dk, ld_k)) : Span{0, 0},
+                      rows_k > 0 ? span(v, view_bytes(rows_k, dk, ld_v)) : Span{0, 0},
+                      span(cu_q, (batch + 1) * 4), span(cu_k, (batch + 1) * 4)};
+  for (const Span& out : outs)
+    for (const Span& in : ins)
+      if (overlap(out, in)) return invalid(fn, "an output overlaps an input");
+  if (overlap(outs[0], outs[1])) return invalid(fn, "o and lse overlap");
+  cudaError_t err = h3q::launch_attention(
+      static_cast<const uint16_t*>(q), ld_q, static_cast<const uint16_t*>(k), ld_k, static_cast<const uint16_t*>(v),
+      ld_v, cu_q, cu_k, static_cast<int>(batch), rows_q, rows_k, static_cast<int>(heads), static_cast<int>(kv_heads),
+      static_cast<int>(head_dim), causal, scale, static_cast<uint16_t*>(o), lse, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 

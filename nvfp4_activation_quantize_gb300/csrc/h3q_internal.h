@@ -127,6 +127,14 @@ cudaError_t launch_cache_attention(const PagedCache& cache, const PagedRows& at,
 // As gemm_error_flag, for the kernel of launch_cache_attention.
 cudaError_t cache_attention_error_flag(int* flag);
 
+// Softmax attention over packed sequences (rows cu_q[b] .. of q, cu_k[b] .. of k and v);
+// lse fp32 [heads, rows_q] or nullptr.
+cudaError_t launch_attention(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k, const uint16_t* v,
+                             int64_t ld_v, const int32_t* cu_q, const int32_t* cu_k, int batch, int64_t rows_q,
+                             int64_t rows_k, int heads, int kv_heads, int head_dim, int causal, float scale,
+                             uint16_t* o, float* lse, cudaStream_t stream);
+cudaError_t attention_error_flag(int* flag);
+
 // RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
 // copies pipelined with the producer over chunk_rows-row chunks; `workspace`
 // holds h3q_host_workspace_bytes(chunk_rows, cols, rows, row_frame == nullptr)

@@ -135,3 +135,27 @@ def test_workspace_bytes_of_header_and_binding_agree(tmp_path):
     want = [h3q.attention_cache_workspace_bytes(*a) for a in ((1, 8, 8, 64), (1, 32, 8, 128), (4, 8, 2, 128),
                                                              (9, 8, 2, 128), (16, 32, 8, 256), (64, 64, 1, 64))]
     assert got == want
+
+
+VARLEN = ["q", "ld_q", "k", "ld_k", "v", "ld_v", "cu_q", "cu_k", "batch", "rows_q", "rows_k", "heads", "kv_heads", "dim",
+          "causal", "scale", "o", "lse", "stream"]
+VARLEN_GOOD = [0x1000000, 1024, 0x1100000, 256, 0x1200000, 256, 0x1300000, 0x1301000, 3, 10, 12, 8, 2, 128, 1, 0.1,
+               0x2000000, None, None]
+
+
+def test_varlen_refusals(lib):
+    call = caller(lib.h3q_attention_varlen, VARLEN, VARLEN_GOOD)
+    assert call() in (0, 2)
+    for kw, what in (({"dim": 80}, "head_dim"), ({"heads": 3}, "multiple of kv_heads"), ({"kv_heads": 0}, "kv_heads"),
+                     ({"heads": 1 << 18}, "2^24"), ({"rows_q": -1}, "rows_q"), ({"rows_k": 1 << 31}, "rows_k"),
+                     ({"batch": -2}, "batch"), ({"causal": 2}, "causal"), ({"scale": 0.0}, "scale"),
+                     ({"scale": float("inf")}, "scale"), ({"q": None}, "q is NULL"), ({"k": 0x1100010}, "32-byte"),
+                     ({"v": None}, "v is NULL"), ({"ld_q": 1000}, "ld of q"), ({"ld_k": 264}, "ld of k"),
+                     ({"cu_q": None}, "cu_q"), ({"cu_k": 0x1301002}, "4-byte"), ({"o": None}, "16-byte"),
+                     ({"o": 0x2000008}, "16-byte"), ({"lse": 0x2100001}, "4-byte"), ({"o": 0x1000000}, "overlaps"),
+                     ({"lse": 0x2000000 + 16}, "overlap"), ({"lse": 0x1300000}, "overlaps")):
+        assert call(**kw) == h3q.H3Q_ERR_INVALID_ARGUMENT, kw
+        assert what in h3q.h3q_last_error(), (kw, h3q.h3q_last_error())
+    assert call(rows_q=0, q=None) == h3q.H3Q_OK
+    assert call(batch=0, cu_q=None) == h3q.H3Q_OK
+    assert call(rows_k=0, k=None, v=None) in (0, 2)
