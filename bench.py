@@ -117,7 +117,7 @@ KERNEL_SOURCES = {
     "adaln_block_kernel": ("adaln.cu", "h3q_device.cuh"),
     "swiglu_kernel": ("swiglu.cu", "h3q_device.cuh", "h3q_silu.cuh"),
     "swiglu_ring_kernel": ("swiglu.cu", "h3q_device.cuh", "h3q_silu.cuh"),
-    "gemm_swiglu_kernel": ("gemm_swiglu.cu", "h3q_device.cuh", "h3q_silu.cuh", "h3q_async.cuh"),
+    "gemm_swiglu_kernel": ("gemm_swiglu.cu", "h3q_device.cuh", "h3q_silu.cuh", "h3q_async.cuh", "h3q_tcgen05.cuh"),
     "quantize_kernel": ("quantize.cu", "h3q_device.cuh"),
 }
 

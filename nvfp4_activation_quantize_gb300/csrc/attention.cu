@@ -19,15 +19,16 @@
 // While the softmax of one tile runs, the tensor cores work on the other.
 //
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns one row of S in TMEM.  It
-//                     reads the row, moves the reference maximum only when the row's
-//                     maximum has grown by more than 2^8 (weights then stay below 2^8 and
-//                     the output is rescaled rarely), writes the weights as bf16
-//                     over S, and sums them in fp32 unrounded.  A weight's rounding to
+//                     reads the row, takes the weights against a reference that follows the
+//                     row's maximum only when that has grown by more than 2^8 (the
+//                     output is rescaled rarely, and the powers do not wait for the
+//                     maximum), writes them as bf16 over S in two halves, and sums
+//                     them in fp32 unrounded.  A weight's rounding to
 //                     bf16 (at most 2^-8 of it, the type of V that it is multiplied with) is
 //                     the format's; maxima, sums and outputs are fp32.  At the end
 //                     it scales its row of O and stores it.
 //   warp 8, one lane  TMA: Q once, then K and V tiles in a ring
-//   warp 9, one lane  the products: S = Q K^T (operands in shared memory), O += P V (P in
+//   warp 9            the products: S = Q K^T (operands in shared memory), O += P V (P in
 //                     TMEM, V as it lies in memory: its rows are the reduction)
 //   warps 10, 11      V tiles that some row does not see whole: rows past the sequence's end
 //                     become zero, and so do values that are no numbers (0 * NaN
@@ -54,7 +55,8 @@ constexpr int kCheckThreads = 64;
 constexpr int kTileRows = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;  // how far (log2) a row's maximum may pass its reference
+constexpr float kSlack = 8.0f;  // a row's reference moves when its maximum has passed it by 2^8,
+constexpr float kJump = 64.0f;  // at once when a tile passes it by 2^64 (sums then stay far below 2^127)
 
 __device__ int g_attention_fault;
 
@@ -84,7 +86,7 @@ struct Shape {
   static constexpr int kStages = 4;                     // K and V tiles in the ring (even: V tiles take every other)
   static constexpr int kOffKv = kTiles * kQBytes;
   static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
-  static constexpr int kBars = 4 * kStages + 2 + 2 + 2 + 2 + 1;  // full, empty, v_raw, v_ok, q, s, p, o, drain
+  static constexpr int kBars = 4 * kStages + 2 + 2 + 4 + 2 + 2;  // full, empty, v_raw, v_ok, q, s, p, o, drain
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
   static constexpr int kSmem = kOffMisc + 64 + 1024;
   // TMEM: two S buffers (P over them), then O
@@ -121,26 +123,59 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The product warp runs converged, so that addresses and descriptors stay in uniform
+// registers; one elected lane issues.  (Issued from a branch of one lane, each product
+// took about 100 clocks to issue, its operands being moved one by one: more than the 64
+// that it runs for.)  A descriptor's upper word is a constant of its operand, the lower
+// one the address and the leading offset.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1,024 bytes apart, 128-byte swizzle
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3fffu) | (lbo >> 4) << 16; }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
       : "memory");
 }
+
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A value that is the same in all lanes, as one that the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Words of packed weights -> as many TMEM columns.
+template <int N>
+__device__ __forceinline__ void store_weights(uint32_t taddr, uint32_t (&w)[N]) {
+  if constexpr (N == 32) {
+    tc_store32(taddr, w);
+  } else {
+    tc_store16(taddr, w);
+  }
 }
 
 // The CTA's work: one sequence's pair of row tiles of one group of heads.
@@ -151,6 +186,7 @@ struct Unit {
   int tok[2];            // first token of each row tile
   int tiles[2];          // key tiles that each reads (0: none, or no rows)
   int partial[2];        // first of them that some row does not see whole
+  int least[2];          // keys that every row sees
 };
 
 __device__ __forceinline__ int clamp_keys(int64_t x, int len) {
@@ -186,9 +222,9 @@ __device__ __forceinline__ Unit unit_of_block(const Args& a, int b, int64_t rank
     const bool any = x < S::kTiles && u.tok[x] < u.n;
     const int last = u.tok[x] + a.tokens < u.n ? u.tok[x] + a.tokens - 1 : u.n - 1;
     const int most = !any ? 0 : a.causal ? clamp_keys(last + shift, u.len) : u.len;
-    const int least = a.causal ? clamp_keys(u.tok[x] + shift, u.len) : u.len;
+    u.least[x] = a.causal ? clamp_keys(u.tok[x] + shift, u.len) : u.len;
     u.tiles[x] = (most + S::kKeys - 1) / S::kKeys;
-    u.partial[x] = least / S::kKeys;
+    u.partial[x] = u.least[x] / S::kKeys;
   }
   return u;
 }
@@ -201,47 +237,23 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int b, int span) {
   return (n + span - 1) / span * a.tile_groups;
 }
 
-// One key tile of one row: S in, weights out, over S.  `seen`: how many of the tile's keys the row sees
-// (MASK).  Returns through m_ref and l; `alpha` is what the row of O has to be scaled with.
-template <int KEYS, bool MASK>
-__device__ __forceinline__ float softmax_tile(uint32_t taddr, int seen, float c, float& m_ref, float& l) {
-  uint32_t s[KEYS / 32][32];
+// max(a, b, c) in one instruction (a NaN loses against a number).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 16 scores -> weights 2^(s * c + base), packed to bf16, and their sum added.
+__device__ __forceinline__ void weights16(const uint32_t* s, float2 c2, float2 b2, float2& sum, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < KEYS / 32; ++i) tc_load32(taddr + 32 * i, s[i]);
-  tc_wait_load();
-  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int i = 0; i < KEYS / 32; ++i)
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      if (MASK && 32 * i + j >= seen) s[i][j] = 0xff800000u;
-      m[j & 3] = fmaxf(m[j & 3], __uint_as_float(s[i][j]));
-    }
-  const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-  float alpha = 1.0f;
-  if (__fmul_rn(__fadd_rn(top, -m_ref), c) > kSlack) {   // (false where both are -inf)
-    alpha = ex2(__fmul_rn(__fadd_rn(m_ref, -top), c));
-    m_ref = top;
-    l = __fmul_rn(l, alpha);
+  for (int j = 0; j < 8; ++j) {
+    float2 p = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
+    p.x = ex2(p.x);
+    p.y = ex2(p.y);
+    sum = add2(sum, p);
+    w[j] = float2_to_bf16x2(p);
   }
-  const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
-  const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
-  float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int i = 0; i < KEYS / 32; ++i) {
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      float2 p = fma2(make_float2(__uint_as_float(s[i][2 * j]), __uint_as_float(s[i][2 * j + 1])), c2, b2);
-      p.x = ex2(p.x);
-      p.y = ex2(p.y);
-      sum = add2(sum, p);
-      w[j] = float2_to_bf16x2(p);
-    }
-    tc_store16(taddr + 16 * i, w);
-  }
-  l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
-  return alpha;
 }
 
 template <int HD>
@@ -259,7 +271,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const uint32_t bar_q = bar_vok + 8 * S::kStages;         // + 8 * row tile
   const uint32_t bar_s = bar_q + 16;                       // + 8 * S buffer
   const uint32_t bar_p = bar_s + 16;
-  const uint32_t bar_o = bar_p + 16;                       // + 8 * row tile
+  const uint32_t bar_p2 = bar_p + 16;                      // the weights of the second half of a tile's keys
+  const uint32_t bar_o = bar_p2 + 16;                      // + 8 * row tile
   const uint32_t bar_drain = bar_o + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
@@ -303,6 +316,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       mbar_init(bar_q + 8 * i, 1);
       mbar_init(bar_s + 8 * i, 1);
       mbar_init(bar_p + 8 * i, kTileRows);
+      mbar_init(bar_p2 + 8 * i, kTileRows);
       mbar_init(bar_o + 8 * i, 1);
     }
     mbar_init(bar_drain, 1);
@@ -315,6 +329,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const Unit u = unit_of_block<HD>(a, *found_b, *found_rank);
   const int tiles = u.tiles[0] > u.tiles[1] ? u.tiles[0] : u.tiles[1];
   const int partial = u.tiles[0] == 0 ? u.partial[1] : u.partial[0];   // a causal tile 0 sees less
+  const int from = u.tiles[0] == 0 ? u.least[1] : u.least[0];          // keys below are seen by every row
   const int kv_head = u.head0 / a.group;
   // V tiles take every other stage of the ring; those from `partial` on are the last, and
   // arrive on barriers of their own, whose phases count them alone.
@@ -328,198 +343,35 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // All 512 columns are this CTA's, so they begin at 0 (lane 0, column 0).
+  constexpr uint32_t tmem = 0;
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      bool ok = true;
-      const int rows = a.tokens * a.heads_per_tile;
-      auto load_q = [&](int x) {
-        if (u.tiles[x] == 0) return;
-        mbar_expect_tx(bar_q + 8 * x, rows * HD * 2);
-        for (int h = 0; h < S::kHalves; ++h)
-          tma_load_3d(base + x * S::kQBytes + h * (kTileRows * 128), &map_q, 64 * h, u.head0,
-                      static_cast<int>(u.q0 + u.tok[x]), bar_q + 8 * x);
-      };
-      load_q(0);
-      int pos = 0;
-      for (; pos < 2 * tiles; ++pos) {   // K0 V0 K1 V1 ...
-        const int stage = pos % S::kStages;
-        if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
-        const uint32_t bar = ((pos & 1) && (pos >> 1) >= partial ? bar_vraw : bar_full) + 8 * stage;
-        mbar_expect_tx(bar, S::kKvBytes);
-        for (int h = 0; h < S::kHalves; ++h)
-          tma_load_3d(base + S::kOffKv + stage * S::kKvBytes + h * (S::kKeys * 128), pos & 1 ? &map_v : &map_k, 64 * h,
-                      kv_head, static_cast<int>(u.k0) + (pos >> 1) * S::kKeys, bar);
-        if (pos == 0 && S::kTiles == 2) load_q(1);
-      }
-      // Before the CTA goes: every stage's last use is released (the products' commits
-      // arrive here), and after an abort every copy issued has landed.
-      for (int i = pos - S::kStages < 0 ? 0 : pos - S::kStages; i < pos; ++i) {
-        const int stage = i % S::kStages;
-        if (ok) {
-          (void)wait_or_abort(bar_empty + 8 * stage, (i / S::kStages) & 1, abort);
-        } else if ((i & 1) && (i >> 1) >= partial) {
-          (void)wait_bounded(bar_vraw + 8 * stage, checked_parity(i >> 1));
-        } else {
-          (void)wait_bounded(bar_full + 8 * stage, (i / S::kStages) & 1);
-        }
-      }
-      if (!ok)
-        for (int x = 0; x < S::kTiles; ++x)
-          if (u.tiles[x] != 0 && (x == 0 || pos > 0)) (void)wait_bounded(bar_q + 8 * x, 0);
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    if (lane == 0 && tiles > 0) {
-      bool ok = true;
-      auto kv = [&](int pos) { return base + S::kOffKv + (pos % S::kStages) * S::kKvBytes; };
-      auto wait_kv = [&](int pos) {
-        return wait_or_abort(bar_full + 8 * (pos % S::kStages), (pos / S::kStages) & 1, abort);
-      };
-      auto wait_v = [&](int j) {
-        const int pos = 2 * j + 1;
-        if (j < partial) return wait_kv(pos);
-        return wait_or_abort(bar_vok + 8 * (pos % S::kStages), checked_parity(j), abort);
-      };
-      auto s_product = [&](int x, int buf, int j) {   // S[buf] = Q[x] K[j]^T
-        const uint32_t q = base + x * S::kQBytes, k = kv(2 * j);
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i)
-          mma_ss(tmem + buf * S::kS, operand_desc(q + (i / 4) * (kTileRows * 128) + (i % 4) * 32),
-                 operand_desc(k + (i / 4) * (S::kKeys * 128) + (i % 4) * 32), S::kIdescS, i > 0);
-        tc_commit(bar_s + 8 * buf);
-      };
-      auto o_product = [&](int x, int buf, int j) {   // O[x] += P[buf] V[j]
-        const uint32_t v = kv(2 * j + 1);
-#pragma unroll
-        for (int i = 0; i < S::kKeys / 16; ++i)       // rows of V 16 i ..: two 8-row groups of 1,024 bytes
-          mma_ts(tmem + S::kO + x * HD, tmem + buf * S::kS + 8 * i, smem_desc(v + i * 2048, S::kKeys * 128, 1024, 2),
-                 S::kIdescO, j > 0 || i > 0);
-      };
-      auto release = [&](int pos) { tc_commit(bar_empty + 8 * (pos % S::kStages)); };
-      if constexpr (S::kTiles == 2) {
-        const int n0 = u.tiles[0], n1 = u.tiles[1];
-        ok = wait_kv(0);
-        if (ok && n0 > 0 && (ok = wait_or_abort(bar_q, 0, abort))) {
-          tc_fence_after();
-          s_product(0, 0, 0);
-        }
-        if (ok && n1 > 0 && (ok = wait_or_abort(bar_q + 8, 0, abort))) {
-          tc_fence_after();
-          s_product(1, 1, 0);
-        }
-        if (ok) release(0);
-        for (int j = 0; j < tiles && ok; ++j) {
-          for (int x = 0; x < 2 && ok; ++x) {
-            const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
-            if (j >= n) continue;
-            const bool first = x == 0 || j >= n0;             // the first of the tiles that use V[j]
-            const bool last = x == 1 || j >= other;
-            if (first && !(ok = wait_v(j))) break;
-            if (!(ok = wait_or_abort(bar_p + 8 * x, j & 1, abort))) break;
-            tc_fence_after();
-            o_product(x, x, j);
-            if (last) release(2 * j + 1);
-            if (j + 1 < n) {
-              if (!(ok = wait_kv(2 * j + 2))) break;          // (a phase already seen to be complete stays so)
-              tc_fence_after();
-              s_product(x, x, j + 1);
-              if (x == 1 || j + 1 >= other) release(2 * j + 2);
-            } else {
-              tc_commit(bar_o + 8 * x);
-            }
-          }
-        }
-      } else {
-        ok = wait_kv(0) && wait_or_abort(bar_q, 0, abort);
-        if (ok) {
-          tc_fence_after();
-          s_product(0, 0, 0);
-          release(0);
-        }
-        for (int j = 0; j < tiles && ok; ++j) {
-          if (j + 1 < tiles) {   // the next S goes into the other buffer while this one's softmax runs
-            if (!(ok = wait_kv(2 * j + 2))) break;
-            tc_fence_after();
-            s_product(0, (j + 1) & 1, j + 1);
-            release(2 * j + 2);
-          }
-          if (!(ok = wait_v(j))) break;
-          if (!(ok = wait_or_abort(bar_p + 8 * (j & 1), (j >> 1) & 1, abort))) break;
-          tc_fence_after();
-          o_product(0, j & 1, j);
-          release(2 * j + 1);
-          tc_commit(bar_o);
-        }
-      }
-      if (!ok) {   // let what is issued finish before the TMEM is freed
-        tc_commit(bar_drain);
-        (void)wait_bounded(bar_drain, 0);
-      }
-    }
-    __syncwarp();
-  } else if (warp >= kCheckWarp0) {
-    const int tid = threadIdx.x - kCheckWarp0 * 32;
-    for (int j = partial; j < tiles; ++j) {
-      const int pos = 2 * j + 1, stage = pos % S::kStages;
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, checked_parity(j), abort))) break;
-      uint8_t* v = smem + S::kOffKv + stage * S::kKvBytes;
-      const int live = u.len - j * S::kKeys;       // rows of the sequence in this tile
-      bool bad = false;
-      for (int i = tid; i < S::kKvBytes / 16; i += kCheckThreads) {
-        uint4* p = reinterpret_cast<uint4*>(v) + i;
-        const int row = (i >> 3) % S::kKeys;       // 128 bytes of a row are 8 pieces, whatever their order
-        if (row >= live) {
-          *p = make_uint4(0, 0, 0, 0);
-        } else if (a.causal) {
-          uint4 w = *p;
-          // a half whose exponent is all ones carries into its top bit
-          auto odd = [](uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-          if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
-            auto clean = [&](uint32_t x) {
-              const uint32_t o = odd(x);
-              return x & ~((o & 0x8000u ? 0xffffu : 0u) | (o & 0x80000000u ? 0xffff0000u : 0u));
-            };
-            *p = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
-            bad = true;
-          }
-        }
-      }
-      if (bad) atomicOr(bad_v, 1 << (j - partial));
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was written here
-      mbar_arrive(bar_vok + 8 * stage);
-    }
-  } else if (warp < 4 * S::kTiles) {
+  // (384 threads have 168 registers each.  A split by setmaxnreg, 208 for the softmax warps and
+  // 88 for the others, was no faster: 1.32 ms both ways at 8,160 x 56 heads.)
+  if (warp < kTmaWarp) {
+    if (warp < 4 * S::kTiles) {
     // ---- softmax and epilogue of one row tile
-    const int x = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const int tok = u.tok[x] + row / a.heads_per_tile;
-    const int head = u.head0 + row % a.heads_per_tile;
-    const bool valid = row < a.tokens * a.heads_per_tile && tok < u.n;
-    const int sees = !valid ? 0 : a.causal ? clamp_keys(static_cast<int64_t>(tok) + u.len - u.n + 1, u.len) : u.len;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t taddr_o = lane_base + S::kO + x * HD;
-    const float c = fmaxf(__fmul_rn(a.scale, kLog2e), 0x1p-126f);   // never 0: a hidden key's -inf stays one
-    const int n = u.tiles[x];
-    float m_ref = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int buf = S::kTiles == 2 ? x : j & 1;
-      const uint32_t parity = S::kTiles == 2 ? j & 1 : (j >> 1) & 1;
-      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_s + 8 * buf, parity, abort)))) break;
-      tc_fence_after();
-      const uint32_t taddr = lane_base + buf * S::kS;
-      const float alpha = j >= u.partial[x] ? softmax_tile<S::kKeys, true>(taddr, sees - j * S::kKeys, c, m_ref, l)
-                                            : softmax_tile<S::kKeys, false>(taddr, 0, c, m_ref, l);
-      // O is at rest: with two tiles S[j] was issued after P[j-1] V[j-1]; with one it was
-      // issued before, so that product is waited for (each in turn: a phase that is two
-      // behind looks like one to come).
-      if constexpr (S::kTiles == 1) {
-        if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o, (j - 1) & 1, abort)))) break;
-        tc_fence_after();
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+      const int x = warp >> 2;
+      const int row = (warp & 3) * 32 + lane;
+      const int tok = u.tok[x] + row / a.heads_per_tile;
+      const int head = u.head0 + row % a.heads_per_tile;
+      const bool valid = row < a.tokens * a.heads_per_tile && tok < u.n;
+      const int sees = !valid ? 0 : a.causal ? clamp_keys(static_cast<int64_t>(tok) + u.len - u.n + 1, u.len) : u.len;
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const uint32_t taddr_o = lane_base + S::kO + x * HD;
+      const float c = fmaxf(__fmul_rn(a.scale, kLog2e), 0x1p-126f);   // never 0: a hidden key's -inf stays one
+      const int n = u.tiles[x];
+      float m_ref = -INFINITY, m_seen = -INFINITY, l = 0.0f;
+      bool ok = true;
+      // Move the reference to the maximum seen, where that has grown: scale the sum and O.
+      auto rescale = [&](bool any_o) {
+        float alpha = 1.0f;
+        if (__fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack) {
+          alpha = ex2(__fmul_rn(__fadd_rn(m_ref, -m_seen), c));
+          m_ref = m_seen;
+          l = __fmul_rn(l, alpha);
+        }
+        if (!any_o) return;
 #pragma unroll 1
         for (int i = 0; i < HD; i += 32) {
           uint32_t o[32];
@@ -529,64 +381,298 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__fmul_rn(__uint_as_float(o[k]), alpha));
           tc_store32(taddr_o + i, o);
         }
-      }
-      tc_wait_store();
-      tc_fence_before();
-      mbar_arrive(bar_p + 8 * buf);
-    }
-    if (n > 0 && ok) {
-      const uint32_t parity = S::kTiles == 2 ? 0 : (n - 1) & 1;
-      ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + 8 * x, parity, abort));
-      tc_fence_after();
-    }
-    if (ok) {
-      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-      const int64_t out_row = u.q0 + tok;
-      const int bad = *static_cast<volatile int*>(bad_v);
-      uint16_t* dst = a.o + (out_row * a.heads + head) * HD;
-#pragma unroll 1
-      for (int i = 0; i < HD; i += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          __syncwarp();
-          tc_load32(taddr_o + i, o);
+        tc_wait_store();
+      };
+      for (int j = 0; j < n; ++j) {
+        const int buf = S::kTiles == 2 ? x : j & 1;
+        const uint32_t parity = S::kTiles == 2 ? j & 1 : (j >> 1) & 1;
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_s + 8 * buf, parity, abort)))) break;
+        // O is at rest: with two tiles S[j] was issued after P[j-1] V[j-1]; with one it was
+        // issued before, so that product is waited for (each in turn: a phase that is two
+        // behind looks like one to come).
+        if constexpr (S::kTiles == 1)
+          if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o, (j - 1) & 1, abort)))) break;
+        tc_fence_after();
+        const uint32_t taddr = lane_base + buf * S::kS;
+        if (j > 0 && __any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack)) rescale(true);
+        constexpr int kHalf = S::kKeys / 2;
+        const int seen = sees - j * S::kKeys;
+        const bool masked = j >= u.partial[x];
+        const float2 c2 = make_float2(c, c);
+        uint32_t s[S::kKeys];
+        uint32_t w[kHalf / 2];
+        float2 sum;
+        // The weights of this tile are taken against the reference as it is, while the tile's
+        // maximum is still being formed; only where a row passes it by 2^kJump (every first
+        // tile) is the reference moved at once and the tile read again.
+        for (;;) {
+#pragma unroll
+          for (int i = 0; i < S::kKeys / 32; ++i) tc_load32(taddr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
           tc_wait_load();
-        } else {
+          if (masked) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0;
+            for (int i = 0; i < S::kKeys; ++i)
+              if (i >= seen) s[i] = 0xff800000u;
+          }
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < S::kKeys; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              m[k] = max3(m[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
+          const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
+          const float2 b2 = make_float2(base, base);
+          sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 16) weights16(s + i, c2, b2, sum, w + i / 2);
+          m_seen = fmaxf(max3(m_seen, m[0], m[1]), fmaxf(m[2], m[3]));
+          // (a difference of two -inf is no number, and not above)
+          if (!__any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kJump)) break;
+          rescale(j > 0);
         }
-        if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
-          for (int j = partial; j < n; ++j) {
-            if (!(bad >> (j - partial) & 1)) continue;
-            const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
-            for (int key = j * S::kKeys; key < end; ++key) {
-              const uint16_t* src = a.v + (u.k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i;
+        const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
+        const float2 b2 = make_float2(base, base);
+        store_weights<kHalf / 2>(taddr, w);
+        tc_wait_store();
+        tc_fence_before();
+        mbar_arrive(bar_p + 8 * buf);            // the products of the first half of the keys may start
 #pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const uint32_t w = src[k];
-                if ((w & 0x7f80u) == 0x7f80u)
-                  o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
+        for (int i = 0; i < kHalf; i += 16) weights16(s + kHalf + i, c2, b2, sum, w + i / 2);
+        store_weights<kHalf / 2>(taddr + kHalf / 2, w);
+        l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
+        tc_wait_store();
+        tc_fence_before();
+        mbar_arrive(bar_p2 + 8 * buf);
+      }
+      if (n > 0 && ok) {
+        const uint32_t parity = S::kTiles == 2 ? 0 : (n - 1) & 1;
+        ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + 8 * x, parity, abort));
+        tc_fence_after();
+      }
+      if (ok) {
+        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+        const int64_t out_row = u.q0 + tok;
+        const int bad = *static_cast<volatile int*>(bad_v);
+        uint16_t* dst = a.o + (out_row * a.heads + head) * HD;
+#pragma unroll 1
+        for (int i = 0; i < HD; i += 32) {
+          uint32_t o[32];
+          if (n > 0) {
+            __syncwarp();
+            tc_load32(taddr_o + i, o);
+            tc_wait_load();
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0;
+          }
+          if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
+            for (int j = partial; j < n; ++j) {
+              if (!(bad >> (j - partial) & 1)) continue;
+              const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
+              for (int key = j * S::kKeys > from ? j * S::kKeys : from; key < end; ++key) {
+                const uint16_t* src = a.v + (u.k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i;
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const uint32_t w = src[k];
+                  if ((w & 0x7f80u) == 0x7f80u)
+                    o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
+                }
               }
             }
           }
-        }
-        if (valid) {
+          if (valid) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[8];
+            for (int half = 0; half < 2; ++half) {
+              uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float lo = __uint_as_float(o[16 * half + 2 * k]), hi = __uint_as_float(o[16 * half + 2 * k + 1]);
-              w[k] = l == 0.0f ? 0u : float2_to_bf16x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)));
+              for (int k = 0; k < 8; ++k) {
+                const float lo = __uint_as_float(o[16 * half + 2 * k]), hi = __uint_as_float(o[16 * half + 2 * k + 1]);
+                w[k] = l == 0.0f ? 0u : float2_to_bf16x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)));
+              }
+              store16(dst + i + 16 * half, make_uint4(w[0], w[1], w[2], w[3]));
+              store16(dst + i + 16 * half + 8, make_uint4(w[4], w[5], w[6], w[7]));
             }
-            store16(dst + i + 16 * half, make_uint4(w[0], w[1], w[2], w[3]));
-            store16(dst + i + 16 * half + 8, make_uint4(w[4], w[5], w[6], w[7]));
           }
         }
+        if (valid && a.lse != nullptr)
+          a.lse[head * a.rows_q + out_row] =
+              l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m_ref, c), log2f(l)), kLn2);
       }
-      if (valid && a.lse != nullptr)
-        a.lse[head * a.rows_q + out_row] =
-            l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m_ref, c), log2f(l)), kLn2);
+    }
+  } else {
+    if (warp == kTmaWarp) {
+      if (lane == 0) {
+        bool ok = true;
+        const int rows = a.tokens * a.heads_per_tile;
+        auto load_q = [&](int x) {
+          if (u.tiles[x] == 0) return;
+          mbar_expect_tx(bar_q + 8 * x, rows * HD * 2);
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(base + x * S::kQBytes + h * (kTileRows * 128), &map_q, 64 * h, u.head0,
+                        static_cast<int>(u.q0 + u.tok[x]), bar_q + 8 * x);
+        };
+        load_q(0);
+        int pos = 0;
+        for (; pos < 2 * tiles; ++pos) {   // K0 V0 K1 V1 ...
+          const int stage = pos % S::kStages;
+          if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
+          const uint32_t bar = ((pos & 1) && (pos >> 1) >= partial ? bar_vraw : bar_full) + 8 * stage;
+          mbar_expect_tx(bar, S::kKvBytes);
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(base + S::kOffKv + stage * S::kKvBytes + h * (S::kKeys * 128), pos & 1 ? &map_v : &map_k, 64 * h,
+                        kv_head, static_cast<int>(u.k0) + (pos >> 1) * S::kKeys, bar);
+          if (pos == 0 && S::kTiles == 2) load_q(1);
+        }
+        // Before the CTA goes: every stage's last use is released (the products' commits
+        // arrive here), and after an abort every copy issued has landed.
+        for (int i = pos - S::kStages < 0 ? 0 : pos - S::kStages; i < pos; ++i) {
+          const int stage = i % S::kStages;
+          if (ok) {
+            (void)wait_or_abort(bar_empty + 8 * stage, (i / S::kStages) & 1, abort);
+          } else if ((i & 1) && (i >> 1) >= partial) {
+            (void)wait_bounded(bar_vraw + 8 * stage, checked_parity(i >> 1));
+          } else {
+            (void)wait_bounded(bar_full + 8 * stage, (i / S::kStages) & 1);
+          }
+        }
+        if (!ok)
+          for (int x = 0; x < S::kTiles; ++x)
+            if (u.tiles[x] != 0 && (x == 0 || pos > 0)) (void)wait_bounded(bar_q + 8 * x, 0);
+      }
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // One warp issues both tiles' products, a tile's O and next S after the other's: that
+      // order keeps the tiles half a step apart, one in its softmax while the other has the
+      // tensor cores.  (A warp for each tile lets them fall into step: both in their softmax,
+      // then both waiting for the tensor cores; 8,160 x 56 heads took 1.676 ms against 1.392.)
+      const int tiles_u = uniform(tiles), partial_u = uniform(partial);
+      const int n0 = uniform(u.tiles[0]), n1 = uniform(u.tiles[1]);
+      if (tiles_u > 0) {
+        bool ok = true;
+        // (the whole warp: one decision)
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)));
+        };
+        auto stage_of = [&](int pos) { return static_cast<uint32_t>(pos % S::kStages); };
+        auto wait_kv = [&](int pos) { return wait(bar_full + 8 * stage_of(pos), (pos / S::kStages) & 1); };
+        auto wait_v = [&](int j) {
+          const int pos = 2 * j + 1;
+          if (j < partial_u) return wait_kv(pos);
+          return wait(bar_vok + 8 * stage_of(pos), static_cast<uint32_t>((j - partial_u) / (S::kStages / 2)) & 1u);
+        };
+        const uint32_t q_low = desc_low(base, 16);
+        const uint32_t k_low = desc_low(base + S::kOffKv, 16);
+        const uint32_t v_low = desc_low(base + S::kOffKv, S::kKeys * 128);   // 64 columns of V, then the next 64
+        auto s_product = [&](int x, int buf, int j) {   // S[buf] = Q[x] K[j]^T
+          const uint32_t q = q_low + x * (S::kQBytes >> 4), k = k_low + stage_of(2 * j) * (S::kKvBytes >> 4);
+#pragma unroll
+          for (int i = 0; i < HD / 16; ++i)
+            mma_ss(buf * S::kS, q + (((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4),
+                   k + (((i / 4) * (S::kKeys * 128) + (i % 4) * 32) >> 4), S::kIdescS, i > 0);
+          commit_elected(bar_s + 8 * buf);
+        };
+        // O[x] += P[buf] V[j], each half of the keys as its weights are there
+        auto o_product = [&](int x, int buf, int j, uint32_t parity) {
+          const uint32_t v = v_low + stage_of(2 * j + 1) * (S::kKvBytes >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait((half == 0 ? bar_p : bar_p2) + 8 * buf, parity)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int i = half * S::kKeys / 32; i < (half + 1) * S::kKeys / 32; ++i)
+              // rows of V 16 i ..: two 8-row groups of 1,024 bytes
+              mma_ts(S::kO + x * HD, buf * S::kS + 8 * i, v + (i * 2048 >> 4), S::kIdescO, j > 0 || i > 0);
+          }
+          return true;
+        };
+        auto release = [&](int pos) { commit_elected(bar_empty + 8 * stage_of(pos)); };
+        if constexpr (S::kTiles == 2) {
+          ok = wait_kv(0);
+          if (ok && n0 > 0 && (ok = wait(bar_q, 0))) {
+            tc_fence_after();
+            s_product(0, 0, 0);
+          }
+          if (ok && n1 > 0 && (ok = wait(bar_q + 8, 0))) {
+            tc_fence_after();
+            s_product(1, 1, 0);
+          }
+          if (ok) release(0);
+          for (int j = 0; j < tiles_u && ok; ++j) {
+            // (what the loop needs of K and V is looked for once, before the tiles' weights)
+            if (!(ok = wait_v(j) && (j + 1 >= tiles_u || wait_kv(2 * j + 2)))) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
+              if (!ok || j >= n) continue;
+              if (!(ok = o_product(x, x, j, j & 1))) continue;
+              if (x == 1 || j >= other) release(2 * j + 1);     // the last of the tiles that use V[j]
+              if (j + 1 < n) {
+                s_product(x, x, j + 1);
+                if (x == 1 || j + 1 >= other) release(2 * j + 2);
+              } else {
+                commit_elected(bar_o + 8 * x);
+              }
+            }
+          }
+        } else {
+          ok = wait_kv(0) && wait(bar_q, 0);
+          if (ok) {
+            tc_fence_after();
+            s_product(0, 0, 0);
+            release(0);
+          }
+          for (int j = 0; j < tiles_u && ok; ++j) {
+            if (j + 1 < tiles_u) {   // the next S goes into the other buffer while this one's softmax runs
+              if (!(ok = wait_kv(2 * j + 2))) break;
+              tc_fence_after();
+              s_product(0, (j + 1) & 1, j + 1);
+              release(2 * j + 2);
+            }
+            if (!(ok = wait_v(j) && o_product(0, j & 1, j, (j >> 1) & 1))) break;
+            release(2 * j + 1);
+            commit_elected(bar_o);
+          }
+        }
+        if (!ok) {   // let what is issued finish before the TMEM is freed
+          commit_elected(bar_drain);
+          (void)wait_bounded(bar_drain, 0);
+        }
+      }
+      __syncwarp();
+    } else if (warp >= kCheckWarp0) {
+      const int tid = threadIdx.x - kCheckWarp0 * 32;
+      // Only rows that some row of the tiles does not see matter.
+      for (int j = partial; j < tiles; ++j) {
+        const int pos = 2 * j + 1, stage = pos % S::kStages;
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, checked_parity(j), abort))) break;
+        uint8_t* v = smem + S::kOffKv + stage * S::kKvBytes;
+        const int live = u.len - j * S::kKeys;       // rows of the sequence in this tile
+        const int row0 = from - j * S::kKeys > 0 ? from - j * S::kKeys : 0;
+        bool bad = false;
+#pragma unroll 1
+        for (int h = 0; h < S::kHalves; ++h) {
+          uint4* col = reinterpret_cast<uint4*>(v + h * (S::kKeys * 128));
+#pragma unroll 4
+          for (int i = row0 * 8 + tid; i < S::kKeys * 8; i += kCheckThreads) {   // 128 bytes of a row: 8 pieces in some order
+            uint4 w = col[i];
+            // a half whose exponent is all ones carries into its top bit
+            auto odd = [](uint32_t y) { return ((y & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+            if ((i >> 3) >= live) {
+              col[i] = make_uint4(0, 0, 0, 0);
+            } else if (odd(w.x) | odd(w.y) | odd(w.z) | odd(w.w)) {
+              auto clean = [&](uint32_t y) {
+                const uint32_t z = odd(y);
+                return y & ~((z & 0x8000u ? 0xffffu : 0u) | (z & 0x80000000u ? 0xffff0000u : 0u));
+              };
+              col[i] = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+              bad = true;
+            }
+          }
+        }
+        if (bad) atomicOr(bad_v, 1 << (j - partial));
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was written here
+        mbar_arrive(bar_vok + 8 * stage);
+      }
     }
   }
 
@@ -594,7 +680,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(512)
+                 : "memory");
   }
 }
 
