@@ -548,7 +548,8 @@ int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, con
  *   cu_q, cu_k  int32 [batch + 1] on the device, not decreasing: sequence b has queries
  *               cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1.  Not checked on the
  *               host; no contents make the kernel touch memory outside the buffers.
- *   rows_q, rows_k  0 .. 2^31 - 512.   heads  a multiple of kv_heads; heads * head_dim <= 2^24.
+ *   rows_q      0 .. 2^31 - 512.   rows_k  0 .. 2^25.
+ *   heads       a multiple of kv_heads; heads * head_dim <= 2^24.
  *   head_dim    64, 128 or 256.        scale  finite, > 0 (e.g. head_dim^-0.5).
  *   causal      0 or 1.
  *   o           out, bf16 [rows_q, heads, head_dim] contiguous, 16-byte aligned.

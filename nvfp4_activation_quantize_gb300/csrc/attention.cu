@@ -30,10 +30,12 @@
 //   warp 8, one lane  TMA: Q once, then K and V tiles in a ring
 //   warp 9            the products: S = Q K^T (operands in shared memory), O += P V (P in
 //                     TMEM, V as it lies in memory: its rows are the reduction)
-//   warps 10, 11      V tiles that some row does not see whole: rows past the sequence's end
+//   warp 10           V tiles that some row does not see whole: rows past the sequence's end
 //                     become zero, and so do values that are no numbers (0 * NaN
 //                     would reach rows that do not see them); the epilogue adds these back
 //                     for the rows that do
+//   warp 11           the plan: which unit is next.  The CTA's own block first, then those of
+//                     blocks that have not started, which it takes over from the launch
 //
 // Every wait is bounded: one that runs out sets a device flag and tells the other roles
 // to stop; the CTA drains what it has in flight, frees its TMEM and returns.
@@ -50,8 +52,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kCheckWarp0 = 10;
-constexpr int kCheckThreads = 64;
+constexpr int kCheckWarp = 10;
+constexpr int kPlanWarp = 11;
+constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -85,10 +88,13 @@ struct Shape {
   static constexpr int kKvBytes = kKeys * HD * 2;
   static constexpr int kStages = 4;                     // K and V tiles in the ring (even: V tiles take every other)
   static constexpr int kOffKv = kTiles * kQBytes;
-  static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
-  static constexpr int kBars = 4 * kStages + 2 + 2 + 4 + 2 + 2;  // full, empty, v_raw, v_ok, q, s, p, o, drain
-  static constexpr int kOffMisc = kOffBar + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 64 + 1024;
+  static constexpr int kOffOut = kOffKv + kStages * kKvBytes;   // 32 rows x 64 columns of output per softmax warp
+  static constexpr int kOffBar = kOffOut + kTiles * 4 * 4096;
+  static constexpr int kBars = 4 * kStages + 12 + 2 * kSlots + 2;   // named in the kernel
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;    // TMEM address, abort; a taken block's id (16-byte aligned)
+  static constexpr int kOffSlots = kOffMisc + 32;
+  static constexpr int kSmem = kOffSlots + kSlots * 96 + 1024;
+  static_assert(kOffMisc % 16 == 0, "alignment");
   // TMEM: two S buffers (P over them), then O
   static constexpr uint32_t kS = kKeys;                 // columns of an S buffer
   static constexpr uint32_t kO = 256;
@@ -178,25 +184,31 @@ __device__ __forceinline__ void store_weights(uint32_t taddr, uint32_t (&w)[N]) 
   }
 }
 
-// The CTA's work: one sequence's pair of row tiles of one group of heads.
+// A unit of work: one sequence's pair of row tiles of one group of heads, as the planning
+// warp hands it to the others.
 struct Unit {
   int64_t q0, k0;        // first packed rows of the sequence
-  int n, len;            // its queries and keys
+  int n, len;            // its queries and keys; n < 0: no more units
   int head0;             // first head of the tile
   int tok[2];            // first token of each row tile
   int tiles[2];          // key tiles that each reads (0: none, or no rows)
-  int partial[2];        // first of them that some row does not see whole
-  int least[2];          // keys that every row sees
+  int partial[2];        // first of them that some row of the tile does not see whole
+  int least;             // keys that every row of the unit sees
+  int bad;               // which V tiles (from the unit's first partial one) held values that are no numbers
 };
+
+// Key tiles of the unit, and the first that some row does not see whole (a causal tile 0
+// sees less than tile 1).
+__device__ __forceinline__ int tiles_of(const Unit& u) { return u.tiles[0] > u.tiles[1] ? u.tiles[0] : u.tiles[1]; }
+__device__ __forceinline__ int partial_of(const Unit& u) { return u.tiles[0] == 0 ? u.partial[1] : u.partial[0]; }
 
 __device__ __forceinline__ int clamp_keys(int64_t x, int len) {
   return x < 0 ? 0 : x > len ? len : static_cast<int>(x);
 }
 
 template <int HD>
-__device__ __forceinline__ Unit unit_of_block(const Args& a, int b, int64_t rank) {
+__device__ __forceinline__ void write_unit(const Args& a, int b, int64_t rank, Unit& u) {
   using S = Shape<HD>;
-  Unit u;
   const int64_t q0 = a.cu_q[b], k0 = a.cu_k[b];
   int64_t n = static_cast<int64_t>(a.cu_q[b + 1]) - q0, len = static_cast<int64_t>(a.cu_k[b + 1]) - k0;
   // (n is in range where it is counted; lists of keys that point past the rows hold none)
@@ -218,15 +230,17 @@ __device__ __forceinline__ Unit unit_of_block(const Args& a, int b, int64_t rank
   const int64_t shift = static_cast<int64_t>(u.len) - u.n + 1;  // token t sees keys below t + shift
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    u.tok[x] = qt * span + x * a.tokens;
-    const bool any = x < S::kTiles && u.tok[x] < u.n;
-    const int last = u.tok[x] + a.tokens < u.n ? u.tok[x] + a.tokens - 1 : u.n - 1;
+    const int tok = qt * span + x * a.tokens;
+    const bool any = x < S::kTiles && tok < u.n;
+    const int last = tok + a.tokens < u.n ? tok + a.tokens - 1 : u.n - 1;
     const int most = !any ? 0 : a.causal ? clamp_keys(last + shift, u.len) : u.len;
-    u.least[x] = a.causal ? clamp_keys(u.tok[x] + shift, u.len) : u.len;
+    const int least = a.causal ? clamp_keys(tok + shift, u.len) : u.len;
+    u.tok[x] = tok;
     u.tiles[x] = (most + S::kKeys - 1) / S::kKeys;
-    u.partial[x] = u.least[x] / S::kKeys;
+    u.partial[x] = least / S::kKeys;
+    if (x == 0 || u.tiles[0] == 0) u.least = least;
   }
-  return u;
+  u.bad = 0;
 }
 
 __device__ __forceinline__ int64_t units_of(const Args& a, int b, int span) {
@@ -266,394 +280,460 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const uint32_t base = smem_u32(smem);
   const uint32_t bar_full = base + S::kOffBar;             // + 8 * stage
   const uint32_t bar_empty = bar_full + 8 * S::kStages;
-  const uint32_t bar_vraw = bar_empty + 8 * S::kStages;    // a V tile that the checkers look at first ...
-  const uint32_t bar_vok = bar_vraw + 8 * S::kStages;      // ... and have passed on
-  const uint32_t bar_q = bar_vok + 8 * S::kStages;         // + 8 * row tile
-  const uint32_t bar_s = bar_q + 16;                       // + 8 * S buffer
+  const uint32_t bar_vraw = bar_empty + 8 * S::kStages;    // a V tile that the check warp looks at first ...
+  const uint32_t bar_vok = bar_vraw + 8 * S::kStages;      // ... and has passed on
+  const uint32_t bar_q = bar_vok + 8 * S::kStages;         // + 8 * row tile: Q has landed,
+  const uint32_t bar_qfree = bar_q + 16;                   // is no longer read
+  const uint32_t bar_s = bar_qfree + 16;                   // + 8 * S buffer
   const uint32_t bar_p = bar_s + 16;
   const uint32_t bar_p2 = bar_p + 16;                      // the weights of the second half of a tile's keys
   const uint32_t bar_o = bar_p2 + 16;                      // + 8 * row tile
-  const uint32_t bar_drain = bar_o + 16;
+  const uint32_t bar_unit = bar_o + 16;                    // + 8 * slot: a unit is there,
+  const uint32_t bar_slot = bar_unit + 8 * kSlots;         // all have read it
+  const uint32_t bar_next = bar_slot + 8 * kSlots;         // a waiting block was taken over, or none was left
+  const uint32_t bar_drain = bar_next + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
-  int* bad_v = reinterpret_cast<int*>(smem + S::kOffMisc + 8);
-  int* found_b = reinterpret_cast<int*>(smem + S::kOffMisc + 12);
-  int64_t* found_rank = reinterpret_cast<int64_t*>(smem + S::kOffMisc + 16);
+  const uint32_t next_block = base + S::kOffMisc + 16;
+  Unit* units = reinterpret_cast<Unit*>(smem + S::kOffSlots);
+  static_assert(sizeof(Unit) <= 96, "slots");
+  constexpr int kReaders = 4 * S::kTiles + 3;   // warps that read a slot: softmax, TMA, products, check
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- which unit: warp 0 counts the sequences' units, 32 at a time
-  if (warp == 0) {
-    const int span = a.tokens * S::kTiles;
-    int64_t before = 0;
-    int found = -1;
-    for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
-      const int b = b0 + lane;
-      const int64_t mine = b < a.batch ? units_of(a, b, span) : 0;
-      int64_t upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      const int64_t u = static_cast<int64_t>(blockIdx.x) - before;
-      const uint32_t hit = __ballot_sync(0xffffffffu, u >= upto - mine && u < upto);
-      if (hit) {
-        found = b0 + __ffs(hit) - 1;
-        if (lane == __ffs(hit) - 1) *found_rank = u - (upto - mine);
-      }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (lane == 0) *found_b = found;
-  }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(bar_full + 8 * i, 1);
       mbar_init(bar_empty + 8 * i, 1);
       mbar_init(bar_vraw + 8 * i, 1);
-      mbar_init(bar_vok + 8 * i, kCheckThreads);
+      mbar_init(bar_vok + 8 * i, 32);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_q + 8 * i, 1);
+      mbar_init(bar_qfree + 8 * i, 1);
       mbar_init(bar_s + 8 * i, 1);
       mbar_init(bar_p + 8 * i, kTileRows);
       mbar_init(bar_p2 + 8 * i, kTileRows);
       mbar_init(bar_o + 8 * i, 1);
     }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar_unit + 8 * i, 1);
+      mbar_init(bar_slot + 8 * i, kReaders);
+    }
+    mbar_init(bar_next, 1);
     mbar_init(bar_drain, 1);
     *abort = 0;
-    *bad_v = 0;
     mbar_init_fence();
   }
   __syncthreads();
-  if (*found_b < 0) return;   // more CTAs than units
-  const Unit u = unit_of_block<HD>(a, *found_b, *found_rank);
-  const int tiles = u.tiles[0] > u.tiles[1] ? u.tiles[0] : u.tiles[1];
-  const int partial = u.tiles[0] == 0 ? u.partial[1] : u.partial[0];   // a causal tile 0 sees less
-  const int from = u.tiles[0] == 0 ? u.least[1] : u.least[0];          // keys below are seen by every row
-  const int kv_head = u.head0 / a.group;
-  // V tiles take every other stage of the ring; those from `partial` on are the last, and
-  // arrive on barriers of their own, whose phases count them alone.
-  auto checked_parity = [&](int j) { return static_cast<uint32_t>((j - partial) / (S::kStages / 2)) & 1u; };
-  if (warp == kMmaWarp) {   // the whole warp allocates the CTA's TMEM (one CTA per SM)
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  // All 512 columns are this CTA's, so they begin at 0 (lane 0, column 0).
-  constexpr uint32_t tmem = 0;
+
+  // The unit number `it` of this CTA, or nullptr after the last (or an abort).  Whole warp.
+  auto unit_at = [&](int it) -> Unit* {
+    const int slot = it % kSlots;
+    if (!__all_sync(0xffffffffu, wait_or_abort(bar_unit + 8 * slot, (it / kSlots) & 1, abort))) return nullptr;
+    return units[slot].n < 0 ? nullptr : units + slot;
+  };
+  auto leave_unit = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_slot + 8 * (it % kSlots));
+  };
 
   // (384 threads have 168 registers each.  A split by setmaxnreg, 208 for the softmax warps and
   // 88 for the others, was no faster: 1.32 ms both ways at 8,160 x 56 heads.)
   if (warp < kTmaWarp) {
     if (warp < 4 * S::kTiles) {
-    // ---- softmax and epilogue of one row tile
+      // ---- softmax and epilogue of one row tile
       const int x = warp >> 2;
       const int row = (warp & 3) * 32 + lane;
-      const int tok = u.tok[x] + row / a.heads_per_tile;
-      const int head = u.head0 + row % a.heads_per_tile;
-      const bool valid = row < a.tokens * a.heads_per_tile && tok < u.n;
-      const int sees = !valid ? 0 : a.causal ? clamp_keys(static_cast<int64_t>(tok) + u.len - u.n + 1, u.len) : u.len;
-      const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      const int row_tok = row / a.heads_per_tile, row_head = row % a.heads_per_tile;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;   // the TMEM of all 512 columns begins at 0
       const uint32_t taddr_o = lane_base + S::kO + x * HD;
       const float c = fmaxf(__fmul_rn(a.scale, kLog2e), 0x1p-126f);   // never 0: a hidden key's -inf stays one
-      const int n = u.tiles[x];
-      float m_ref = -INFINITY, m_seen = -INFINITY, l = 0.0f;
+      uint8_t* staged = smem + S::kOffOut + warp * 4096;
+      uint32_t s_count = 0, o_count = 0;   // S tiles and outputs waited for
       bool ok = true;
-      // Move the reference to the maximum seen, where that has grown: scale the sum and O.
-      auto rescale = [&](bool any_o) {
-        float alpha = 1.0f;
-        if (__fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack) {
-          alpha = ex2(__fmul_rn(__fadd_rn(m_ref, -m_seen), c));
-          m_ref = m_seen;
-          l = __fmul_rn(l, alpha);
-        }
-        if (!any_o) return;
-#pragma unroll 1
-        for (int i = 0; i < HD; i += 32) {
-          uint32_t o[32];
-          tc_load32(taddr_o + i, o);
-          tc_wait_load();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__fmul_rn(__uint_as_float(o[k]), alpha));
-          tc_store32(taddr_o + i, o);
-        }
-        tc_wait_store();
-      };
-      for (int j = 0; j < n; ++j) {
-        const int buf = S::kTiles == 2 ? x : j & 1;
-        const uint32_t parity = S::kTiles == 2 ? j & 1 : (j >> 1) & 1;
-        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_s + 8 * buf, parity, abort)))) break;
-        // O is at rest: with two tiles S[j] was issued after P[j-1] V[j-1]; with one it was
-        // issued before, so that product is waited for (each in turn: a phase that is two
-        // behind looks like one to come).
-        if constexpr (S::kTiles == 1)
-          if (j > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o, (j - 1) & 1, abort)))) break;
-        tc_fence_after();
-        const uint32_t taddr = lane_base + buf * S::kS;
-        if (j > 0 && __any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack)) rescale(true);
-        constexpr int kHalf = S::kKeys / 2;
-        const int seen = sees - j * S::kKeys;
-        const bool masked = j >= u.partial[x];
-        const float2 c2 = make_float2(c, c);
-        uint32_t s[S::kKeys];
-        uint32_t w[kHalf / 2];
-        float2 sum;
-        // The weights of this tile are taken against the reference as it is, while the tile's
-        // maximum is still being formed; only where a row passes it by 2^kJump (every first
-        // tile) is the reference moved at once and the tile read again.
-        for (;;) {
-#pragma unroll
-          for (int i = 0; i < S::kKeys / 32; ++i) tc_load32(taddr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-          tc_wait_load();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < S::kKeys; ++i)
-              if (i >= seen) s[i] = 0xff800000u;
+      Unit* u;
+      for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
+        const int tok = u->tok[x] + row_tok;
+        const bool valid = row < a.tokens * a.heads_per_tile && tok < u->n;
+        const int len = u->len;
+        const int sees = !valid ? 0 : a.causal ? clamp_keys(static_cast<int64_t>(tok) + len - u->n + 1, len) : len;
+        const int n = u->tiles[x], partial = u->partial[x];
+        float m_ref = -INFINITY, m_seen = -INFINITY, l = 0.0f;
+        // Move the reference to the maximum seen, where that has grown: scale the sum and O.
+        auto rescale = [&](bool any_o) {
+          float alpha = 1.0f;
+          if (__fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack) {
+            alpha = ex2(__fmul_rn(__fadd_rn(m_ref, -m_seen), c));
+            m_ref = m_seen;
+            l = __fmul_rn(l, alpha);
           }
-          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < S::kKeys; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              m[k] = max3(m[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
-          const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
-          const float2 b2 = make_float2(base, base);
-          sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < kHalf; i += 16) weights16(s + i, c2, b2, sum, w + i / 2);
-          m_seen = fmaxf(max3(m_seen, m[0], m[1]), fmaxf(m[2], m[3]));
-          // (a difference of two -inf is no number, and not above)
-          if (!__any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kJump)) break;
-          rescale(j > 0);
-        }
-        const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
-        const float2 b2 = make_float2(base, base);
-        store_weights<kHalf / 2>(taddr, w);
-        tc_wait_store();
-        tc_fence_before();
-        mbar_arrive(bar_p + 8 * buf);            // the products of the first half of the keys may start
-#pragma unroll
-        for (int i = 0; i < kHalf; i += 16) weights16(s + kHalf + i, c2, b2, sum, w + i / 2);
-        store_weights<kHalf / 2>(taddr + kHalf / 2, w);
-        l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
-        tc_wait_store();
-        tc_fence_before();
-        mbar_arrive(bar_p2 + 8 * buf);
-      }
-      if (n > 0 && ok) {
-        const uint32_t parity = S::kTiles == 2 ? 0 : (n - 1) & 1;
-        ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + 8 * x, parity, abort));
-        tc_fence_after();
-      }
-      if (ok) {
-        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        const int64_t out_row = u.q0 + tok;
-        const int bad = *static_cast<volatile int*>(bad_v);
-        uint16_t* dst = a.o + (out_row * a.heads + head) * HD;
+          if (!any_o) return;
 #pragma unroll 1
-        for (int i = 0; i < HD; i += 32) {
-          uint32_t o[32];
-          if (n > 0) {
-            __syncwarp();
+          for (int i = 0; i < HD; i += 32) {
+            uint32_t o[32];
             tc_load32(taddr_o + i, o);
             tc_wait_load();
-          } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0;
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__fmul_rn(__uint_as_float(o[k]), alpha));
+            tc_store32(taddr_o + i, o);
           }
-          if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
-            for (int j = partial; j < n; ++j) {
-              if (!(bad >> (j - partial) & 1)) continue;
-              const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
-              for (int key = j * S::kKeys > from ? j * S::kKeys : from; key < end; ++key) {
-                const uint16_t* src = a.v + (u.k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i;
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const uint32_t w = src[k];
-                  if ((w & 0x7f80u) == 0x7f80u)
-                    o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
-                }
-              }
+          tc_wait_store();
+        };
+        for (int j = 0; j < n; ++j) {
+          const int buf = S::kTiles == 2 ? x : s_count & 1;
+          const uint32_t parity = S::kTiles == 2 ? s_count & 1 : (s_count >> 1) & 1;
+          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_s + 8 * buf, parity, abort)))) break;
+          ++s_count;
+          // O is at rest: with two tiles S[j] was issued after P[j-1] V[j-1]; with one it was
+          // issued before, so that product is waited for (each in turn: a phase that is two
+          // behind looks like one to come).
+          if constexpr (S::kTiles == 1) {
+            if (j > 0) {
+              if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_o, o_count & 1, abort)))) break;
+              ++o_count;
             }
           }
-          if (valid) {
+          tc_fence_after();
+          const uint32_t taddr = lane_base + buf * S::kS;
+          if (j > 0 && __any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack)) rescale(true);
+          constexpr int kHalf = S::kKeys / 2;
+          const int seen = sees - j * S::kKeys;
+          const bool masked = j >= partial;
+          const float2 c2 = make_float2(c, c);
+          uint32_t s[S::kKeys];
+          uint32_t w[kHalf / 2];
+          float2 sum;
+          // The weights of this tile are taken against the reference as it is, while the tile's
+          // maximum is still being formed; only where a row passes it by 2^kJump is the reference
+          // moved at once and the tile read again.
+          bool fresh = j == 0;   // no reference yet: only the maximum is formed
+          for (;;) {
+#pragma unroll
+            for (int i = 0; i < S::kKeys / 32; ++i)
+              tc_load32(taddr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+            tc_wait_load();
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < S::kKeys; ++i)
+                if (i >= seen) s[i] = 0xff800000u;
+            }
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < S::kKeys; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                m[k] = max3(m[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
+            if (fresh) {
+              fresh = false;
+              m_seen = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+              rescale(false);
+              continue;
+            }
+            const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
+            const float2 b2 = make_float2(base, base);
+            sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kHalf; i += 16) weights16(s + i, c2, b2, sum, w + i / 2);
+            m_seen = fmaxf(max3(m_seen, m[0], m[1]), fmaxf(m[2], m[3]));
+            // (a difference of two -inf is no number, and not above)
+            if (!__any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kJump)) break;
+            rescale(j > 0);
+          }
+          const float base = m_ref == -INFINITY ? 0.0f : -__fmul_rn(m_ref, c);
+          const float2 b2 = make_float2(base, base);
+          store_weights<kHalf / 2>(taddr, w);
+          tc_wait_store();
+          tc_fence_before();
+          mbar_arrive(bar_p + 8 * buf);            // the products of the first half of the keys may start
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 16) weights16(s + kHalf + i, c2, b2, sum, w + i / 2);
+          store_weights<kHalf / 2>(taddr + kHalf / 2, w);
+          l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
+          tc_wait_store();
+          tc_fence_before();
+          mbar_arrive(bar_p2 + 8 * buf);
+        }
+        if (n > 0 && ok) {
+          ok = __all_sync(0xffffffffu, wait_or_abort(bar_o + 8 * x, o_count & 1, abort));
+          ++o_count;
+          tc_fence_after();
+        }
+        if (ok) {
+          // The row of O, scaled, through shared memory (the 16-byte pieces of a row in the order of
+          // their number's exclusive or with the row's, so that no two rows' meet in a bank), 128
+          // bytes of a row at a time, and out eight lanes a row.  (A thread that stores its own row
+          // takes a transaction per 16 bytes: 2.8 us a unit, against 0.7.)
+          const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+          const int64_t out_row = u->q0 + tok;
+          const int head = u->head0 + row_head;
+          const int bad = *static_cast<volatile int*>(&u->bad);
+          const unsigned long long dst =
+              valid ? reinterpret_cast<unsigned long long>(a.o + (out_row * a.heads + head) * HD) : 0ull;
+#pragma unroll 1
+          for (int i = 0; i < HD; i += 64) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              uint32_t w[8];
+              uint32_t o[32];
+              if (n > 0) {
+                __syncwarp();
+                tc_load32(taddr_o + i + 32 * half, o);
+                tc_wait_load();
+              } else {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float lo = __uint_as_float(o[16 * half + 2 * k]), hi = __uint_as_float(o[16 * half + 2 * k + 1]);
-                w[k] = l == 0.0f ? 0u : float2_to_bf16x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)));
+                for (int k = 0; k < 32; ++k) o[k] = 0;
               }
-              store16(dst + i + 16 * half, make_uint4(w[0], w[1], w[2], w[3]));
-              store16(dst + i + 16 * half + 8, make_uint4(w[4], w[5], w[6], w[7]));
+              if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
+                const int first = partial_of(*u), from = u->least, kv_head = u->head0 / a.group;
+                for (int j = first; j < n; ++j) {
+                  if (!(bad >> (j - first) & 1)) continue;
+                  const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
+                  for (int key = j * S::kKeys > from ? j * S::kKeys : from; key < end; ++key) {
+                    const uint16_t* src =
+                        a.v + (u->k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i + 32 * half;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                      const uint32_t w = src[k];
+                      if ((w & 0x7f80u) == 0x7f80u)
+                        o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
+                    }
+                  }
+                }
+              }
+#pragma unroll
+              for (int piece = 0; piece < 4; ++piece) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float lo = __uint_as_float(o[8 * piece + 2 * k]), hi = __uint_as_float(o[8 * piece + 2 * k + 1]);
+                  w[k] = l == 0.0f ? 0u : float2_to_bf16x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)));
+                }
+                *reinterpret_cast<uint4*>(staged + lane * 128 + (((4 * half + piece) ^ (lane & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = 4 * k + (lane >> 3), piece = lane & 7;
+              const unsigned long long to = __shfl_sync(0xffffffffu, dst, r);
+              const uint4 v = *reinterpret_cast<const uint4*>(staged + r * 128 + ((piece ^ (r & 7)) << 4));
+              if (to != 0) store16(reinterpret_cast<uint16_t*>(to) + i + 8 * piece, v);
+            }
+            __syncwarp();
           }
+          if (valid && a.lse != nullptr)
+            a.lse[head * a.rows_q + out_row] =
+                l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m_ref, c), log2f(l)), kLn2);
+          tc_fence_before();   // O has been read before the next unit's first weights are announced
         }
-        if (valid && a.lse != nullptr)
-          a.lse[head * a.rows_q + out_row] =
-              l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m_ref, c), log2f(l)), kLn2);
+        leave_unit(it);
       }
     }
-  } else {
-    if (warp == kTmaWarp) {
+  } else if (warp == kTmaWarp) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    const int rows = a.tokens * a.heads_per_tile;
+    bool ok = true;
+    uint32_t pos = 0;                            // tiles issued: K0 V0 K1 V1 ..., unit after unit
+    uint32_t q_count[2] = {0, 0};                // Q tiles issued
+    uint32_t full_phase = 0, raw_phase = 0;      // per stage: the phases of its full and v_raw barriers
+    uint32_t last_raw = 0;                       // per stage: its last tile went to the check warp
+    Unit* u;
+    for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
+      const int tiles = tiles_of(*u), partial = partial_of(*u), kv_head = u->head0 / a.group;
+      const int row_q0 = static_cast<int>(u->q0), row_k0 = static_cast<int>(u->k0), head0 = u->head0;
+      const int tok[2] = {u->tok[0], u->tok[1]};
+      const bool any[2] = {u->tiles[0] > 0, u->tiles[1] > 0};
+      leave_unit(it);
       if (lane == 0) {
-        bool ok = true;
-        const int rows = a.tokens * a.heads_per_tile;
         auto load_q = [&](int x) {
-          if (u.tiles[x] == 0) return;
+          if (!any[x]) return true;
+          if (!wait_or_abort(bar_qfree + 8 * x, (q_count[x] & 1) ^ 1u, abort)) return false;
+          ++q_count[x];
           mbar_expect_tx(bar_q + 8 * x, rows * HD * 2);
           for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(base + x * S::kQBytes + h * (kTileRows * 128), &map_q, 64 * h, u.head0,
-                        static_cast<int>(u.q0 + u.tok[x]), bar_q + 8 * x);
-        };
-        load_q(0);
-        int pos = 0;
-        for (; pos < 2 * tiles; ++pos) {   // K0 V0 K1 V1 ...
-          const int stage = pos % S::kStages;
-          if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
-          const uint32_t bar = ((pos & 1) && (pos >> 1) >= partial ? bar_vraw : bar_full) + 8 * stage;
-          mbar_expect_tx(bar, S::kKvBytes);
-          for (int h = 0; h < S::kHalves; ++h)
-            tma_load_3d(base + S::kOffKv + stage * S::kKvBytes + h * (S::kKeys * 128), pos & 1 ? &map_v : &map_k, 64 * h,
-                        kv_head, static_cast<int>(u.k0) + (pos >> 1) * S::kKeys, bar);
-          if (pos == 0 && S::kTiles == 2) load_q(1);
-        }
-        // Before the CTA goes: every stage's last use is released (the products' commits
-        // arrive here), and after an abort every copy issued has landed.
-        for (int i = pos - S::kStages < 0 ? 0 : pos - S::kStages; i < pos; ++i) {
-          const int stage = i % S::kStages;
-          if (ok) {
-            (void)wait_or_abort(bar_empty + 8 * stage, (i / S::kStages) & 1, abort);
-          } else if ((i & 1) && (i >> 1) >= partial) {
-            (void)wait_bounded(bar_vraw + 8 * stage, checked_parity(i >> 1));
-          } else {
-            (void)wait_bounded(bar_full + 8 * stage, (i / S::kStages) & 1);
-          }
-        }
-        if (!ok)
-          for (int x = 0; x < S::kTiles; ++x)
-            if (u.tiles[x] != 0 && (x == 0 || pos > 0)) (void)wait_bounded(bar_q + 8 * x, 0);
-      }
-      __syncwarp();
-    } else if (warp == kMmaWarp) {
-      // One warp issues both tiles' products, a tile's O and next S after the other's: that
-      // order keeps the tiles half a step apart, one in its softmax while the other has the
-      // tensor cores.  (A warp for each tile lets them fall into step: both in their softmax,
-      // then both waiting for the tensor cores; 8,160 x 56 heads took 1.676 ms against 1.392.)
-      const int tiles_u = uniform(tiles), partial_u = uniform(partial);
-      const int n0 = uniform(u.tiles[0]), n1 = uniform(u.tiles[1]);
-      if (tiles_u > 0) {
-        bool ok = true;
-        // (the whole warp: one decision)
-        auto wait = [&](uint32_t bar, uint32_t parity) {
-          return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)));
-        };
-        auto stage_of = [&](int pos) { return static_cast<uint32_t>(pos % S::kStages); };
-        auto wait_kv = [&](int pos) { return wait(bar_full + 8 * stage_of(pos), (pos / S::kStages) & 1); };
-        auto wait_v = [&](int j) {
-          const int pos = 2 * j + 1;
-          if (j < partial_u) return wait_kv(pos);
-          return wait(bar_vok + 8 * stage_of(pos), static_cast<uint32_t>((j - partial_u) / (S::kStages / 2)) & 1u);
-        };
-        const uint32_t q_low = desc_low(base, 16);
-        const uint32_t k_low = desc_low(base + S::kOffKv, 16);
-        const uint32_t v_low = desc_low(base + S::kOffKv, S::kKeys * 128);   // 64 columns of V, then the next 64
-        auto s_product = [&](int x, int buf, int j) {   // S[buf] = Q[x] K[j]^T
-          const uint32_t q = q_low + x * (S::kQBytes >> 4), k = k_low + stage_of(2 * j) * (S::kKvBytes >> 4);
-#pragma unroll
-          for (int i = 0; i < HD / 16; ++i)
-            mma_ss(buf * S::kS, q + (((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4),
-                   k + (((i / 4) * (S::kKeys * 128) + (i % 4) * 32) >> 4), S::kIdescS, i > 0);
-          commit_elected(bar_s + 8 * buf);
-        };
-        // O[x] += P[buf] V[j], each half of the keys as its weights are there
-        auto o_product = [&](int x, int buf, int j, uint32_t parity) {
-          const uint32_t v = v_low + stage_of(2 * j + 1) * (S::kKvBytes >> 4);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (!wait((half == 0 ? bar_p : bar_p2) + 8 * buf, parity)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int i = half * S::kKeys / 32; i < (half + 1) * S::kKeys / 32; ++i)
-              // rows of V 16 i ..: two 8-row groups of 1,024 bytes
-              mma_ts(S::kO + x * HD, buf * S::kS + 8 * i, v + (i * 2048 >> 4), S::kIdescO, j > 0 || i > 0);
-          }
+            tma_load_3d(base + x * S::kQBytes + h * (kTileRows * 128), &map_q, 64 * h, head0, row_q0 + tok[x],
+                        bar_q + 8 * x);
           return true;
         };
-        auto release = [&](int pos) { commit_elected(bar_empty + 8 * stage_of(pos)); };
-        if constexpr (S::kTiles == 2) {
-          ok = wait_kv(0);
-          if (ok && n0 > 0 && (ok = wait(bar_q, 0))) {
-            tc_fence_after();
-            s_product(0, 0, 0);
-          }
-          if (ok && n1 > 0 && (ok = wait(bar_q + 8, 0))) {
-            tc_fence_after();
-            s_product(1, 1, 0);
-          }
-          if (ok) release(0);
-          for (int j = 0; j < tiles_u && ok; ++j) {
-            // (what the loop needs of K and V is looked for once, before the tiles' weights)
-            if (!(ok = wait_v(j) && (j + 1 >= tiles_u || wait_kv(2 * j + 2)))) break;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
-              if (!ok || j >= n) continue;
-              if (!(ok = o_product(x, x, j, j & 1))) continue;
-              if (x == 1 || j >= other) release(2 * j + 1);     // the last of the tiles that use V[j]
-              if (j + 1 < n) {
-                s_product(x, x, j + 1);
-                if (x == 1 || j + 1 >= other) release(2 * j + 2);
-              } else {
-                commit_elected(bar_o + 8 * x);
-              }
-            }
-          }
-        } else {
-          ok = wait_kv(0) && wait(bar_q, 0);
-          if (ok) {
-            tc_fence_after();
-            s_product(0, 0, 0);
-            release(0);
-          }
-          for (int j = 0; j < tiles_u && ok; ++j) {
-            if (j + 1 < tiles_u) {   // the next S goes into the other buffer while this one's softmax runs
-              if (!(ok = wait_kv(2 * j + 2))) break;
-              tc_fence_after();
-              s_product(0, (j + 1) & 1, j + 1);
-              release(2 * j + 2);
-            }
-            if (!(ok = wait_v(j) && o_product(0, j & 1, j, (j >> 1) & 1))) break;
-            release(2 * j + 1);
-            commit_elected(bar_o);
-          }
-        }
-        if (!ok) {   // let what is issued finish before the TMEM is freed
-          commit_elected(bar_drain);
-          (void)wait_bounded(bar_drain, 0);
+        ok = load_q(0);
+        for (int i = 0; i < 2 * tiles && ok; ++i) {
+          const uint32_t stage = pos % S::kStages;
+          if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
+          const bool raw = (i & 1) && (i >> 1) >= partial;
+          const uint32_t bar = (raw ? bar_vraw : bar_full) + 8 * stage;
+          last_raw = (last_raw & ~(1u << stage)) | static_cast<uint32_t>(raw) << stage;
+          (raw ? raw_phase : full_phase) ^= 1u << stage;
+          mbar_expect_tx(bar, S::kKvBytes);
+          for (int h = 0; h < S::kHalves; ++h)
+            tma_load_3d(base + S::kOffKv + stage * S::kKvBytes + h * (S::kKeys * 128), i & 1 ? &map_v : &map_k, 64 * h,
+                        kv_head, row_k0 + (i >> 1) * S::kKeys, bar);
+          ++pos;
+          if (i == 0 && S::kTiles == 2) ok = load_q(1);
         }
       }
+      ok = __shfl_sync(0xffffffffu, static_cast<int>(ok), 0);
+    }
+    // Before the CTA goes: every stage's last tile is released (the products' commits arrive
+    // here); after an abort, every copy issued has landed.
+    if (lane == 0) {
+      const uint32_t first = pos < S::kStages ? 0 : pos - S::kStages;
+      for (uint32_t i = first; i < pos && !*abort; ++i)
+        (void)wait_or_abort(bar_empty + 8 * (i % S::kStages), (i / S::kStages) & 1, abort);
+      if (*abort) {
+        for (uint32_t i = first; i < pos; ++i) {
+          const uint32_t stage = i % S::kStages;
+          const bool raw = last_raw >> stage & 1;
+          (void)wait_bounded((raw ? bar_vraw : bar_full) + 8 * stage, ((raw ? raw_phase : full_phase) >> stage & 1) ^ 1u);
+        }
+        for (int x = 0; x < S::kTiles; ++x)
+          if (q_count[x] > 0) (void)wait_bounded(bar_q + 8 * x, (q_count[x] - 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // The whole warp allocates the CTA's TMEM (one CTA per SM): all 512 columns, so they begin at 0.
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    // One warp issues both tiles' products, a tile's O and next S after the other's: that
+    // order keeps the tiles half a step apart, one in its softmax while the other has the
+    // tensor cores.  (A warp for each tile lets them fall into step: both in their softmax,
+    // then both waiting for the tensor cores; 8,160 x 56 heads took 1.676 ms against 1.392.)
+    const uint32_t q_low = desc_low(base, 16);
+    const uint32_t k_low = desc_low(base + S::kOffKv, 16);
+    const uint32_t v_low = desc_low(base + S::kOffKv, S::kKeys * 128);   // 64 columns of V, then the next 64
+    uint32_t pos0 = 0;                      // ring position of the unit's first K tile
+    uint32_t full_phase = 0, ok_phase = 0;  // per stage: phases of the full and v_ok barriers
+    uint32_t p_count[2] = {0, 0}, q_count[2] = {0, 0};
+    bool ok = true;
+    // (the whole warp: one decision)
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)));
+    };
+    auto stage_of = [&](int i) { return (pos0 + i) % S::kStages; };
+    auto wait_tile = [&](int i, bool checked) {   // each tile once
+      const uint32_t stage = stage_of(i);
+      const uint32_t parity = (checked ? ok_phase : full_phase) >> stage & 1;
+      (checked ? ok_phase : full_phase) ^= 1u << stage;
+      return wait((checked ? bar_vok : bar_full) + 8 * stage, parity);
+    };
+    auto s_product = [&](int x, int buf, int j) {   // S[buf] = Q[x] K[j]^T
+      const uint32_t q = q_low + x * (S::kQBytes >> 4), k = k_low + stage_of(2 * j) * (S::kKvBytes >> 4);
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i)
+        mma_ss(buf * S::kS, q + (((i / 4) * (kTileRows * 128) + (i % 4) * 32) >> 4),
+               k + (((i / 4) * (S::kKeys * 128) + (i % 4) * 32) >> 4), S::kIdescS, i > 0);
+      commit_elected(bar_s + 8 * buf);
+    };
+    // O[x] += P[buf] V[j], each half of the keys as its weights are there
+    auto o_product = [&](int x, int buf, int j) {
+      const uint32_t v = v_low + stage_of(2 * j + 1) * (S::kKvBytes >> 4);
+      const uint32_t parity = p_count[buf] & 1;
+      ++p_count[buf];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!wait((half == 0 ? bar_p : bar_p2) + 8 * buf, parity)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int i = half * S::kKeys / 32; i < (half + 1) * S::kKeys / 32; ++i)
+          // rows of V 16 i ..: two 8-row groups of 1,024 bytes
+          mma_ts(S::kO + x * HD, buf * S::kS + 8 * i, v + (i * 2048 >> 4), S::kIdescO, j > 0 || i > 0);
+      }
+      return true;
+    };
+    auto release = [&](int i) { commit_elected(bar_empty + 8 * stage_of(i)); };
+    auto wait_q = [&](int x) { return wait(bar_q + 8 * x, q_count[x]++ & 1); };
+    uint32_t s_next = 0;   // (one tile: S buffers in turn)
+    Unit* u;
+    for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
+      const int tiles = uniform(tiles_of(*u)), partial = uniform(partial_of(*u));
+      const int n0 = uniform(u->tiles[0]), n1 = uniform(u->tiles[1]);
+      leave_unit(it);
+      if (tiles == 0) continue;
+      if constexpr (S::kTiles == 2) {
+        ok = wait_tile(0, false);
+        if (ok && n0 > 0 && (ok = wait_q(0))) {
+          tc_fence_after();
+          s_product(0, 0, 0);
+          if (n0 == 1) commit_elected(bar_qfree);
+        }
+        if (ok && n1 > 0 && (ok = wait_q(1))) {
+          tc_fence_after();
+          s_product(1, 1, 0);
+          if (n1 == 1) commit_elected(bar_qfree + 8);
+        }
+        if (ok) release(0);
+        for (int j = 0; j < tiles && ok; ++j) {
+          // (what the loop needs of K and V is looked for once, before the tiles' weights)
+          if (!(ok = wait_tile(2 * j + 1, j >= partial) && (j + 1 >= tiles || wait_tile(2 * j + 2, false)))) break;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
+            if (!ok || j >= n) continue;
+            if (!(ok = o_product(x, x, j))) continue;
+            if (x == 1 || j >= other) release(2 * j + 1);     // the last of the tiles that use V[j]
+            if (j + 1 < n) {
+              s_product(x, x, j + 1);
+              if (x == 1 || j + 1 >= other) release(2 * j + 2);
+              if (j + 2 == n) commit_elected(bar_qfree + 8 * x);
+            } else {
+              commit_elected(bar_o + 8 * x);
+            }
+          }
+        }
+      } else {
+        ok = wait_tile(0, false) && wait_q(0);
+        if (ok) {
+          tc_fence_after();
+          s_product(0, s_next & 1, 0);
+          if (tiles == 1) commit_elected(bar_qfree);
+          release(0);
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+          if (j + 1 < tiles) {   // the next S goes into the other buffer while this one's softmax runs
+            if (!(ok = wait_tile(2 * j + 2, false))) break;
+            tc_fence_after();
+            s_product(0, (s_next + 1) & 1, j + 1);
+            if (j + 2 == tiles) commit_elected(bar_qfree);
+            release(2 * j + 2);
+          }
+          if (!(ok = wait_tile(2 * j + 1, j >= partial) && (s_next & 1 ? o_product(0, 1, j) : o_product(0, 0, j)))) break;
+          ++s_next;
+          release(2 * j + 1);
+          commit_elected(bar_o);
+        }
+      }
+      pos0 += 2 * tiles;
+    }
+    if (*abort) {   // let what is issued finish before the TMEM is freed
       __syncwarp();
-    } else if (warp >= kCheckWarp0) {
-      const int tid = threadIdx.x - kCheckWarp0 * 32;
-      // Only rows that some row of the tiles does not see matter.
+      commit_elected(bar_drain);
+      (void)wait_bounded(bar_drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == kCheckWarp) {
+    uint32_t pos0 = 0, raw_phase = 0;
+    bool ok = true;
+    Unit* u;
+    for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
+      const int tiles = tiles_of(*u), partial = partial_of(*u);
+      const int from = a.causal ? u->least : u->len;   // only rows that some row of the unit does not see matter
       for (int j = partial; j < tiles; ++j) {
-        const int pos = 2 * j + 1, stage = pos % S::kStages;
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, checked_parity(j), abort))) break;
+        const uint32_t stage = (pos0 + 2 * j + 1) % S::kStages;
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, raw_phase >> stage & 1, abort)))) break;
+        raw_phase ^= 1u << stage;
         uint8_t* v = smem + S::kOffKv + stage * S::kKvBytes;
-        const int live = u.len - j * S::kKeys;       // rows of the sequence in this tile
+        const int live = u->len - j * S::kKeys;       // rows of the sequence in this tile
         const int row0 = from - j * S::kKeys > 0 ? from - j * S::kKeys : 0;
         bool bad = false;
 #pragma unroll 1
         for (int h = 0; h < S::kHalves; ++h) {
           uint4* col = reinterpret_cast<uint4*>(v + h * (S::kKeys * 128));
 #pragma unroll 4
-          for (int i = row0 * 8 + tid; i < S::kKeys * 8; i += kCheckThreads) {   // 128 bytes of a row: 8 pieces in some order
+          for (int i = row0 * 8 + lane; i < S::kKeys * 8; i += 32) {   // 128 bytes of a row: 8 pieces in some order
             uint4 w = col[i];
             // a half whose exponent is all ones carries into its top bit
             auto odd = [](uint32_t y) { return ((y & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
@@ -669,10 +749,80 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
           }
         }
-        if (bad) atomicOr(bad_v, 1 << (j - partial));
+        if (bad) atomicOr(&u->bad, 1 << (j - partial));
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read what was written here
         mbar_arrive(bar_vok + 8 * stage);
       }
+      pos0 += 2 * tiles;
+      leave_unit(it);
+    }
+  } else {
+    // ---- the plan: this block's unit, then those of blocks that have not started, which the CTA
+    // takes over one after the other: no launch, allocation or empty pipeline between units, and
+    // whichever CTA is free takes the next
+    int64_t block = blockIdx.x;
+    for (int it = 0;; ++it) {
+      const int slot = it % kSlots;
+      if (!__all_sync(0xffffffffu, wait_or_abort(bar_slot + 8 * slot, ((it / kSlots) & 1) ^ 1u, abort))) break;
+      int found = -1;
+      int64_t rank = 0;
+      if (block >= 0) {
+        if (lane == 0) {   // ask for the next while this one is looked up
+          mbar_expect_tx(bar_next, 16);
+          asm volatile(
+              "fence.proxy.async.shared::cta;\n\t"
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                  next_block),
+              "r"(bar_next)
+              : "memory");
+        }
+        // the sequences' units are counted 32 at a time
+        const int span = a.tokens * S::kTiles;
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
+          const int b = b0 + lane;
+          const int64_t mine = b < a.batch ? units_of(a, b, span) : 0;
+          int64_t upto = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+          }
+          const int64_t r = block - before;
+          const uint32_t hit = __ballot_sync(0xffffffffu, r >= upto - mine && r < upto);
+          if (hit) {
+            found = b0 + __ffs(hit) - 1;
+            rank = __shfl_sync(0xffffffffu, r - (upto - mine), __ffs(hit) - 1);
+          }
+          before += __shfl_sync(0xffffffffu, upto, 31);
+        }
+      }
+      if (lane == 0) {
+        if (found >= 0)
+          write_unit<HD>(a, found, rank, units[slot]);
+        else
+          units[slot].n = -1;
+        mbar_arrive(bar_unit + 8 * slot);
+      }
+      if (block >= 0) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar_next, it & 1, abort))) {
+          (void)wait_bounded(bar_next, it & 1);
+          break;
+        }
+        uint32_t taken, x;
+        asm volatile(
+            "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+            "ld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+            : "=r"(taken), "=r"(x)
+            : "r"(next_block)
+            : "memory");
+        block = taken ? static_cast<int64_t>(x) : -1;
+      }
+      if (found < 0) break;
+      __syncwarp();
     }
   }
 
@@ -680,8 +830,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(512)
-                 : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(512) : "memory");
   }
 }
 

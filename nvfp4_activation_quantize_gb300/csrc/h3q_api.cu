@@ -851,12 +851,13 @@ int h3q_attention_varlen(const void* q, int64_t ld_q, const void* k, int64_t ld_
   static const char* fn = "h3q_attention_varlen";
   g_last_error.clear();
   constexpr int64_t kMaxPacked = (int64_t(1) << 31) - 512;   // tensor-copy coordinates are 32-bit
+  constexpr int64_t kMaxKeys = int64_t(1) << 25;   // a unit of work stays far inside the kernel's bounded waits
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return invalid(fn, "head_dim must be 64, 128 or 256");
   if (kv_heads < 1) return invalid(fn, "kv_heads must be >= 1");
   if (heads < 1 || heads % kv_heads != 0) return invalid(fn, "heads must be a positive multiple of kv_heads");
   if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
   if (rows_q < 0 || rows_q > kMaxPacked) return invalid(fn, "rows_q must be in [0, 2^31 - 512]");
-  if (rows_k < 0 || rows_k > kMaxPacked) return invalid(fn, "rows_k must be in [0, 2^31 - 512]");
+  if (rows_k < 0 || rows_k > kMaxKeys) return invalid(fn, "rows_k must be in [0, 2^25]");
   if (batch < 0 || batch >= (int64_t(1) << 31)) return invalid(fn, "batch must be in [0, 2^31)");
   if (causal != 0 && causal != 1) return invalid(fn, "causal must be 0 or 1");
   if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
