@@ -30,10 +30,12 @@
 //   warp 8, one lane  TMA: Q once, then K and V tiles in a ring
 //   warp 9            the products: S = Q K^T (operands in shared memory), O += P V (P in
 //                     TMEM, V as it lies in memory: its rows are the reduction)
-//   warp 10           V tiles that some row does not see whole: rows past the sequence's end
-//                     become zero, and so do values that are no numbers (0 * NaN
-//                     would reach rows that do not see them); the epilogue adds these back
-//                     for the rows that do
+//   warp 10           only where an output came out as no number: 0 * NaN in the tiles of V that
+//                     some row does not see whole (keys to come, rows of the next sequence) can
+//                     have done that, so the unit is taken again with those tiles cleaned first.
+//                     Rows past the sequence's end become zero, and so do values that are no
+//                     numbers; the epilogue adds these back for the rows that see them.
+//                     (Every such tile looked at, the products waited 1 to 3 us a unit.)
 //   warp 11           the plan: which unit is next.  The CTA's own block first, then those of
 //                     blocks that have not started, which it takes over from the launch
 //
@@ -194,6 +196,8 @@ struct Unit {
   int tiles[2];          // key tiles that each reads (0: none, or no rows)
   int partial[2];        // first of them that some row of the tile does not see whole
   int least;             // keys that every row of the unit sees
+  int checked;           // the second time round: partial V tiles go through the check warp
+  int redo;              // an output was no number
   int bad;               // which V tiles (from the unit's first partial one) held values that are no numbers
 };
 
@@ -240,7 +244,7 @@ __device__ __forceinline__ void write_unit(const Args& a, int b, int64_t rank, U
     u.partial[x] = least / S::kKeys;
     if (x == 0 || u.tiles[0] == 0) u.least = least;
   }
-  u.bad = 0;
+  u.checked = u.redo = u.bad = 0;
 }
 
 __device__ __forceinline__ int64_t units_of(const Args& a, int b, int span) {
@@ -469,58 +473,64 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           const int bad = *static_cast<volatile int*>(&u->bad);
           const unsigned long long dst =
               valid ? reinterpret_cast<unsigned long long>(a.o + (out_row * a.heads + head) * HD) : 0ull;
+          float2 odd = make_float2(0.0f, 0.0f);   // no number if an output is none
 #pragma unroll 1
           for (int i = 0; i < HD; i += 64) {
+            uint32_t o[64];
+            if (n > 0) {
+              __syncwarp();
+              tc_load32(taddr_o + i, *reinterpret_cast<uint32_t(*)[32]>(o));
+              tc_load32(taddr_o + i + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+              tc_wait_load();
+            } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t o[32];
-              if (n > 0) {
-                __syncwarp();
-                tc_load32(taddr_o + i + 32 * half, o);
-                tc_wait_load();
-              } else {
+              for (int k = 0; k < 64; ++k) o[k] = 0;
+            }
+            if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
+              const int first = partial_of(*u), from = u->least, kv_head = u->head0 / a.group;
+              for (int j = first; j < n; ++j) {
+                if (!(bad >> (j - first) & 1)) continue;
+                const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
+                for (int key = j * S::kKeys > from ? j * S::kKeys : from; key < end; ++key) {
+                  const uint16_t* src = a.v + (u->k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i;
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = 0;
-              }
-              if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
-                const int first = partial_of(*u), from = u->least, kv_head = u->head0 / a.group;
-                for (int j = first; j < n; ++j) {
-                  if (!(bad >> (j - first) & 1)) continue;
-                  const int end = sees < (j + 1) * S::kKeys ? sees : (j + 1) * S::kKeys;
-                  for (int key = j * S::kKeys > from ? j * S::kKeys : from; key < end; ++key) {
-                    const uint16_t* src =
-                        a.v + (u->k0 + key) * a.ld_v + static_cast<int64_t>(kv_head) * HD + i + 32 * half;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                      const uint32_t w = src[k];
-                      if ((w & 0x7f80u) == 0x7f80u)
-                        o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
-                    }
+                  for (int k = 0; k < 64; ++k) {
+                    const uint32_t w = src[k];
+                    if ((w & 0x7f80u) == 0x7f80u)
+                      o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
                   }
                 }
               }
+            }
 #pragma unroll
-              for (int piece = 0; piece < 4; ++piece) {
-                uint32_t w[4];
+            for (int piece = 0; piece < 8; ++piece) {
+              uint32_t w[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float lo = __uint_as_float(o[8 * piece + 2 * k]), hi = __uint_as_float(o[8 * piece + 2 * k + 1]);
-                  w[k] = l == 0.0f ? 0u : float2_to_bf16x2(make_float2(__fmul_rn(lo, inv), __fmul_rn(hi, inv)));
-                }
-                *reinterpret_cast<uint4*>(staged + lane * 128 + (((4 * half + piece) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+              for (int k = 0; k < 4; ++k) {
+                const float2 y = make_float2(__uint_as_float(o[8 * piece + 2 * k]), __uint_as_float(o[8 * piece + 2 * k + 1]));
+                odd = fma2(y, make_float2(0.0f, 0.0f), odd);
+                w[k] = l == 0.0f ? 0u : float2_to_bf16x2(mul2(y, make_float2(inv, inv)));
               }
+              *reinterpret_cast<uint4*>(staged + lane * 128 + ((piece ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
             __syncwarp();
+            uint4 v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int r = 4 * k + (lane >> 3), piece = lane & 7;
-              const unsigned long long to = __shfl_sync(0xffffffffu, dst, r);
-              const uint4 v = *reinterpret_cast<const uint4*>(staged + r * 128 + ((piece ^ (r & 7)) << 4));
-              if (to != 0) store16(reinterpret_cast<uint16_t*>(to) + i + 8 * piece, v);
+              v[k] = *reinterpret_cast<const uint4*>(staged + r * 128 + ((piece ^ (r & 7)) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const unsigned long long to = __shfl_sync(0xffffffffu, dst, 4 * k + (lane >> 3));
+              if (to != 0) store16(reinterpret_cast<uint16_t*>(to) + i + 8 * (lane & 7), v[k]);
             }
             __syncwarp();
           }
+          const float odd_sum = __fadd_rn(odd.x, odd.y);
+          if (valid && odd_sum != odd_sum && u->checked == 0 && partial_of(*u) < tiles_of(*u))
+            *static_cast<volatile int*>(&u->redo) = 1;
           if (valid && a.lse != nullptr)
             a.lse[head * a.rows_q + out_row] =
                 l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(__fmul_rn(m_ref, c), log2f(l)), kLn2);
@@ -544,7 +554,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       const int tiles = tiles_of(*u), partial = partial_of(*u), kv_head = u->head0 / a.group;
       const int row_q0 = static_cast<int>(u->q0), row_k0 = static_cast<int>(u->k0), head0 = u->head0;
       const int tok[2] = {u->tok[0], u->tok[1]};
-      const bool any[2] = {u->tiles[0] > 0, u->tiles[1] > 0};
+      const bool any[2] = {u->tiles[0] > 0, u->tiles[1] > 0}, checked = u->checked != 0;
       leave_unit(it);
       if (lane == 0) {
         auto load_q = [&](int x) {
@@ -561,7 +571,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         for (int i = 0; i < 2 * tiles && ok; ++i) {
           const uint32_t stage = pos % S::kStages;
           if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
-          const bool raw = (i & 1) && (i >> 1) >= partial;
+          const bool raw = checked && (i & 1) && (i >> 1) >= partial;
           const uint32_t bar = (raw ? bar_vraw : bar_full) + 8 * stage;
           last_raw = (last_raw & ~(1u << stage)) | static_cast<uint32_t>(raw) << stage;
           (raw ? raw_phase : full_phase) ^= 1u << stage;
@@ -649,7 +659,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     uint32_t s_next = 0;   // (one tile: S buffers in turn)
     Unit* u;
     for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
-      const int tiles = uniform(tiles_of(*u)), partial = uniform(partial_of(*u));
+      const int tiles = uniform(tiles_of(*u));
+      const int partial = uniform(u->checked ? partial_of(*u) : tiles);   // V tiles from here on are checked
       const int n0 = uniform(u->tiles[0]), n1 = uniform(u->tiles[1]);
       leave_unit(it);
       if (tiles == 0) continue;
@@ -719,7 +730,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     bool ok = true;
     Unit* u;
     for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
-      const int tiles = tiles_of(*u), partial = partial_of(*u);
+      const int tiles = tiles_of(*u), partial = u->checked ? partial_of(*u) : tiles;
       const int from = a.causal ? u->least : u->len;   // only rows that some row of the unit does not see matter
       for (int j = partial; j < tiles; ++j) {
         const uint32_t stage = (pos0 + 2 * j + 1) % S::kStages;
@@ -761,12 +772,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // takes over one after the other: no launch, allocation or empty pipeline between units, and
     // whichever CTA is free takes the next
     int64_t block = blockIdx.x;
+    uint32_t asked = 0;   // blocks asked for
+    auto done = [&](int it) {   // unit `it` has been left by all
+      return static_cast<bool>(
+          __all_sync(0xffffffffu, wait_or_abort(bar_slot + 8 * (it % kSlots), (it / kSlots) & 1, abort)));
+    };
     for (int it = 0;; ++it) {
-      const int slot = it % kSlots;
-      if (!__all_sync(0xffffffffu, wait_or_abort(bar_slot + 8 * slot, ((it / kSlots) & 1) ^ 1u, abort))) break;
+      if (it >= kSlots && !done(it - kSlots)) break;
+      Unit& slot = units[it % kSlots];
+      int from = -1;   // a finished unit's slot that has to be taken again
+      if (it >= kSlots && slot.redo != 0) from = it % kSlots;
       int found = -1;
       int64_t rank = 0;
-      if (block >= 0) {
+      if (from < 0 && block >= 0) {
+        __syncwarp();
         if (lane == 0) {   // ask for the next while this one is looked up
           mbar_expect_tx(bar_next, 16);
           asm volatile(
@@ -796,19 +815,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           }
           before += __shfl_sync(0xffffffffu, upto, 31);
         }
-      }
-      if (lane == 0) {
-        if (found >= 0)
-          write_unit<HD>(a, found, rank, units[slot]);
-        else
-          units[slot].n = -1;
-        mbar_arrive(bar_unit + 8 * slot);
-      }
-      if (block >= 0) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar_next, it & 1, abort))) {
-          (void)wait_bounded(bar_next, it & 1);
+        if (found >= 0 && lane == 0) {
+          write_unit<HD>(a, found, rank, slot);
+          mbar_arrive(bar_unit + 8 * (it % kSlots));
+        }
+        if (!__all_sync(0xffffffffu, wait_or_abort(bar_next, asked & 1, abort))) {
+          (void)wait_bounded(bar_next, asked & 1);
           break;
         }
+        ++asked;
         uint32_t taken, x;
         asm volatile(
             "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
@@ -819,10 +834,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             : "=r"(taken), "=r"(x)
             : "r"(next_block)
             : "memory");
-        block = taken ? static_cast<int64_t>(x) : -1;
+        block = taken && found >= 0 ? static_cast<int64_t>(x) : -1;   // (blocks past the last unit have none)
+        if (found >= 0) continue;
       }
-      if (found < 0) break;
+      // No block left: the units under way may still have to be taken again.
+      bool ok = true;
+      for (int k = it - 1; from < 0 && ok && k >= 0 && k > it - kSlots; --k) {
+        ok = done(k);
+        if (ok && units[k % kSlots].redo != 0) from = k % kSlots;
+      }
+      if (!ok) break;
       __syncwarp();
+      if (lane == 0) {
+        if (from >= 0) {
+          if (from != it % kSlots) slot = units[from];
+          units[from].redo = 0;
+          slot.checked = 1;
+          slot.redo = slot.bad = 0;
+        } else {
+          slot.n = -1;
+        }
+        mbar_arrive(bar_unit + 8 * (it % kSlots));
+      }
+      __syncwarp();
+      if (from < 0) break;
     }
   }
 
