@@ -92,7 +92,7 @@ struct Shape {
   static constexpr int kOffKv = kTiles * kQBytes;
   static constexpr int kOffOut = kOffKv + kStages * kKvBytes;   // 32 rows x 64 columns of output per softmax warp
   static constexpr int kOffBar = kOffOut + kTiles * 4 * 4096;
-  static constexpr int kBars = 4 * kStages + 12 + 2 * kSlots + 2;   // named in the kernel
+  static constexpr int kBars = 4 * kStages + 12 + 2 * kSlots + 4;   // named in the kernel
   static constexpr int kOffMisc = kOffBar + 8 * kBars;    // TMEM address, abort; a taken block's id (16-byte aligned)
   static constexpr int kOffSlots = kOffMisc + 32;
   static constexpr int kSmem = kOffSlots + kSlots * 96 + 1024;
@@ -295,7 +295,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const uint32_t bar_unit = bar_o + 16;                    // + 8 * slot: a unit is there,
   const uint32_t bar_slot = bar_unit + 8 * kSlots;         // all have read it
   const uint32_t bar_next = bar_slot + 8 * kSlots;         // a waiting block was taken over, or none was left
-  const uint32_t bar_drain = bar_next + 8;
+  const uint32_t bar_want = bar_next + 8;                  // the loads of a unit are about to end
+  const uint32_t bar_drain = bar_want + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
   const uint32_t next_block = base + S::kOffMisc + 16;
@@ -324,6 +325,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       mbar_init(bar_slot + 8 * i, kReaders);
     }
     mbar_init(bar_next, 1);
+    mbar_init(bar_want, 1);
     mbar_init(bar_drain, 1);
     *abort = 0;
     mbar_init_fence();
@@ -567,8 +569,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         bar_q + 8 * x);
           return true;
         };
+        if (tiles == 0) mbar_arrive(bar_want);
         ok = load_q(0);
         for (int i = 0; i < 2 * tiles && ok; ++i) {
+          if (i == 2 * tiles - 2) mbar_arrive(bar_want);
           const uint32_t stage = pos % S::kStages;
           if (!(ok = wait_or_abort(bar_empty + 8 * stage, ((pos / S::kStages) & 1) ^ 1u, abort))) break;
           const bool raw = checked && (i & 1) && (i >> 1) >= partial;
@@ -778,6 +782,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           __all_sync(0xffffffffu, wait_or_abort(bar_slot + 8 * (it % kSlots), (it / kSlots) & 1, abort)));
     };
     for (int it = 0;; ++it) {
+      // The next unit is looked for when the loads of the one before are at its last tile: two
+      // or three tiles before its end, which is when it is needed.  (Taken as early as there was a
+      // slot, a CTA held two units while others had none: the last of 16 packed prompts' CTAs
+      // ended 49 us after the first.)
+      if (it > 0 && !__all_sync(0xffffffffu, wait_or_abort(bar_want, (it - 1) & 1, abort))) break;
       if (it >= kSlots && !done(it - kSlots)) break;
       Unit& slot = units[it % kSlots];
       int from = -1;   // a finished unit's slot that has to be taken again
