@@ -378,7 +378,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           for (int i = 0; i < HD; i += 32) {
             uint32_t o[32];
             tc_load32(taddr_o + i, o);
-            tc_wait_load();
+            tc_wait_load(o);
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__fmul_rn(__uint_as_float(o[k]), alpha));
             tc_store32(taddr_o + i, o);
@@ -406,7 +406,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           const int seen = sees - j * S::kKeys;
           const bool masked = j >= partial;
           const float2 c2 = make_float2(c, c);
-          uint32_t s[S::kKeys];
+          uint32_t s[S::kKeys / 32][32];
           uint32_t w[kHalf / 2];
           float2 sum;
           // The weights of this tile are taken against the reference as it is, while the tile's
@@ -415,20 +415,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           bool fresh = j == 0;   // no reference yet: only the maximum is formed
           for (;;) {
 #pragma unroll
-            for (int i = 0; i < S::kKeys / 32; ++i)
-              tc_load32(taddr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
-            tc_wait_load();
+            for (int i = 0; i < S::kKeys / 32; ++i) tc_load32(taddr + 32 * i, s[i]);
+            tc_wait_load(s[0]);
+#pragma unroll
+            for (int i = 1; i < S::kKeys / 32; ++i) tc_loaded(s[i]);
             if (masked) {
 #pragma unroll
               for (int i = 0; i < S::kKeys; ++i)
-                if (i >= seen) s[i] = 0xff800000u;
+                if (i >= seen) s[i / 32][i % 32] = 0xff800000u;
             }
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < S::kKeys; i += 8)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                m[k] = max3(m[k], __uint_as_float(s[i + 2 * k]), __uint_as_float(s[i + 2 * k + 1]));
+                m[k] = max3(m[k], __uint_as_float(s[i / 32][i % 32 + 2 * k]), __uint_as_float(s[i / 32][i % 32 + 2 * k + 1]));
             if (fresh) {
               fresh = false;
               m_seen = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
@@ -439,7 +440,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const float2 b2 = make_float2(base, base);
             sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < kHalf; i += 16) weights16(s + i, c2, b2, sum, w + i / 2);
+            for (int i = 0; i < kHalf; i += 16) weights16(s[i / 32] + i % 32, c2, b2, sum, w + i / 2);
             m_seen = fmaxf(max3(m_seen, m[0], m[1]), fmaxf(m[2], m[3]));
             // (a difference of two -inf is no number, and not above)
             if (!__any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kJump)) break;
@@ -452,7 +453,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           tc_fence_before();
           mbar_arrive(bar_p + 8 * buf);            // the products of the first half of the keys may start
 #pragma unroll
-          for (int i = 0; i < kHalf; i += 16) weights16(s + kHalf + i, c2, b2, sum, w + i / 2);
+          for (int i = 0; i < kHalf; i += 16)
+            weights16(s[(kHalf + i) / 32] + i % 32, c2, b2, sum, w + i / 2);
           store_weights<kHalf / 2>(taddr + kHalf / 2, w);
           l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
           tc_wait_store();
@@ -478,15 +480,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           float2 odd = make_float2(0.0f, 0.0f);   // no number if an output is none
 #pragma unroll 1
           for (int i = 0; i < HD; i += 64) {
-            uint32_t o[64];
+            uint32_t o[2][32];
             if (n > 0) {
               __syncwarp();
-              tc_load32(taddr_o + i, *reinterpret_cast<uint32_t(*)[32]>(o));
-              tc_load32(taddr_o + i + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
-              tc_wait_load();
+              tc_load32(taddr_o + i, o[0]);
+              tc_load32(taddr_o + i + 32, o[1]);
+              tc_wait_load(o[0]);
+              tc_loaded(o[1]);
             } else {
 #pragma unroll
-              for (int k = 0; k < 64; ++k) o[k] = 0;
+              for (int k = 0; k < 64; ++k) o[k / 32][k % 32] = 0;
             }
             if (bad != 0 && valid) {   // values that are no numbers, of keys that this row sees
               const int first = partial_of(*u), from = u->least, kv_head = u->head0 / a.group;
@@ -499,7 +502,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                   for (int k = 0; k < 64; ++k) {
                     const uint32_t w = src[k];
                     if ((w & 0x7f80u) == 0x7f80u)
-                      o[k] = __float_as_uint(__fadd_rn(__uint_as_float(o[k]), __uint_as_float(w << 16)));
+                      o[k / 32][k % 32] =
+                          __float_as_uint(__fadd_rn(__uint_as_float(o[k / 32][k % 32]), __uint_as_float(w << 16)));
                   }
                 }
               }
@@ -509,7 +513,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
-                const float2 y = make_float2(__uint_as_float(o[8 * piece + 2 * k]), __uint_as_float(o[8 * piece + 2 * k + 1]));
+                const uint32_t* pair = o[piece / 4] + piece % 4 * 8 + 2 * k;
+                const float2 y = make_float2(__uint_as_float(pair[0]), __uint_as_float(pair[1]));
                 odd = fma2(y, make_float2(0.0f, 0.0f), odd);
                 w[k] = l == 0.0f ? 0u : float2_to_bf16x2(mul2(y, make_float2(inv, inv)));
               }
@@ -623,16 +628,38 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     uint32_t full_phase = 0, ok_phase = 0;  // per stage: phases of the full and v_ok barriers
     uint32_t p_count[2] = {0, 0}, q_count[2] = {0, 0};
     bool ok = true;
-    // (the whole warp: one decision)
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)));
+    // Each lane waits for a barrier of its own (0: none), the warp for all of them: a wait that
+    // is met at once still takes a hundred clocks or more, so what a turn needs is one wait.
+    auto wait_lanes = [&](uint32_t bar, uint32_t parity) {
+      bool done = bar == 0 || mbar_try_wait(bar, parity);
+      if (__all_sync(0xffffffffu, done)) return true;
+      const uint64_t start = now_ns();
+      for (uint32_t i = 1;; ++i) {
+        if (!done) done = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if ((i & 255u) == 0) {
+          const bool late = now_ns() - start > kWaitNs;
+          if (late && lane == 0) {
+            *abort = 1;
+            atomicExch(&g_attention_fault, 1);
+          }
+          if (__any_sync(0xffffffffu, late || *abort)) return false;
+        }
+      }
     };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_lanes(lane == 0 ? bar : 0u, parity); };
     auto stage_of = [&](int i) { return (pos0 + i) % S::kStages; };
-    auto wait_tile = [&](int i, bool checked) {   // each tile once
+    // The barrier of ring tile i and its parity, each tile once.
+    auto tile_bar = [&](int i, bool checked, uint32_t& parity) {
       const uint32_t stage = stage_of(i);
-      const uint32_t parity = (checked ? ok_phase : full_phase) >> stage & 1;
+      parity = (checked ? ok_phase : full_phase) >> stage & 1;
       (checked ? ok_phase : full_phase) ^= 1u << stage;
-      return wait((checked ? bar_vok : bar_full) + 8 * stage, parity);
+      return (checked ? bar_vok : bar_full) + 8 * stage;
+    };
+    auto wait_tile = [&](int i, bool checked) {
+      uint32_t parity;
+      const uint32_t bar = tile_bar(i, checked, parity);
+      return wait(bar, parity);
     };
     auto s_product = [&](int x, int buf, int j) {   // S[buf] = Q[x] K[j]^T
       const uint32_t q = q_low + x * (S::kQBytes >> 4), k = k_low + stage_of(2 * j) * (S::kKvBytes >> 4);
@@ -642,20 +669,22 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                k + (((i / 4) * (S::kKeys * 128) + (i % 4) * 32) >> 4), S::kIdescS, i > 0);
       commit_elected(bar_s + 8 * buf);
     };
-    // O[x] += P[buf] V[j], each half of the keys as its weights are there
-    auto o_product = [&](int x, int buf, int j) {
+    // half of O[x] += P[buf] V[j]
+    auto o_half = [&](int x, int buf, int j, int half) {
       const uint32_t v = v_low + stage_of(2 * j + 1) * (S::kKvBytes >> 4);
-      const uint32_t parity = p_count[buf] & 1;
-      ++p_count[buf];
+      tc_fence_after();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (!wait((half == 0 ? bar_p : bar_p2) + 8 * buf, parity)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int i = half * S::kKeys / 32; i < (half + 1) * S::kKeys / 32; ++i)
-          // rows of V 16 i ..: two 8-row groups of 1,024 bytes
-          mma_ts(S::kO + x * HD, buf * S::kS + 8 * i, v + (i * 2048 >> 4), S::kIdescO, j > 0 || i > 0);
-      }
+      for (int i = half * S::kKeys / 32; i < (half + 1) * S::kKeys / 32; ++i)
+        // rows of V 16 i ..: two 8-row groups of 1,024 bytes
+        mma_ts(S::kO + x * HD, buf * S::kS + 8 * i, v + (i * 2048 >> 4), S::kIdescO, j > 0 || i > 0);
+    };
+    // each half of the keys as its weights are there
+    auto o_product = [&](int x, int buf, int j) {
+      const uint32_t parity = p_count[buf]++ & 1;
+      if (!wait(bar_p + 8 * buf, parity)) return false;
+      o_half(x, buf, j, 0);
+      if (!wait(bar_p2 + 8 * buf, parity)) return false;
+      o_half(x, buf, j, 1);
       return true;
     };
     auto release = [&](int i) { commit_elected(bar_empty + 8 * stage_of(i)); };
@@ -681,24 +710,41 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           if (n1 == 1) commit_elected(bar_qfree + 8);
         }
         if (ok) release(0);
+        int held = -1;   // a K tile and the V tile before it whose release waits for the next turn
+        auto release_held = [&]() {
+          if (held < 0) return;
+          release(held - 1);
+          if (held < 2 * tiles) release(held);
+          held = -1;
+        };
         for (int j = 0; j < tiles && ok; ++j) {
-          // (what the loop needs of K and V is looked for once, before the tiles' weights)
-          if (!(ok = wait_tile(2 * j + 1, j >= partial) && (j + 1 >= tiles || wait_tile(2 * j + 2, false)))) break;
+          uint32_t v_parity, k_parity = 0;
+          const uint32_t v_bar = tile_bar(2 * j + 1, j >= partial, v_parity);
+          const uint32_t k_bar = j + 1 < tiles ? tile_bar(2 * j + 2, false, k_parity) : 0u;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
             if (!ok || j >= n) continue;
-            if (!(ok = o_product(x, x, j))) continue;
-            if (x == 1 || j >= other) release(2 * j + 1);     // the last of the tiles that use V[j]
+            // V[j], K[j + 1] and the first half of the weights, all at once
+            const uint32_t parity = p_count[x]++ & 1;
+            const uint32_t bar = lane == 0 ? bar_p + 8 * x : lane == 1 ? v_bar : lane == 2 ? k_bar : 0u;
+            if (!(ok = wait_lanes(bar, lane == 0 ? parity : lane == 1 ? v_parity : k_parity))) continue;
+            // Commits go in where the queue of products is short (behind a full one they would
+            // keep the warp until it has run), so the turn before left its stages to this one.
+            release_held();
+            o_half(x, x, j, 0);
+            if (!(ok = wait(bar_p2 + 8 * x, parity))) continue;
+            o_half(x, x, j, 1);
             if (j + 1 < n) {
               s_product(x, x, j + 1);
-              if (x == 1 || j + 1 >= other) release(2 * j + 2);
               if (j + 2 == n) commit_elected(bar_qfree + 8 * x);
             } else {
               commit_elected(bar_o + 8 * x);
             }
+            if (x == 1 || j >= other) held = 2 * j + 2;   // the last of the tiles that read V[j]
           }
         }
+        if (ok) release_held();
       } else {
         ok = wait_tile(0, false) && wait_q(0);
         if (ok) {
