@@ -191,6 +191,10 @@ def _stream(stream, device) -> int:
     import torch
 
     if stream is None:
+        # (the handle alone: the stream object takes twenty times as long)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device.index is not None:
+            return raw(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -665,46 +669,101 @@ def kv_cache_nvfp4(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
                  for per in (2, 16, 2, 16))
 
 
-def _cache(cache, device=None):
-    """Checks the four cache tensors; returns (pages, kv_heads, page_size, head_dim, device)."""
+# The calls of a decoding step run for a few microseconds on the GPU, so what they check of
+# their arguments is checked once each: a tensor that passes the one test below is what the
+# call needs, and only one that does not goes through the helpers that say what is wrong.
+
+_torch = None
+
+
+def _load_torch():
+    global _torch
     import torch
 
+    _torch = torch
+    return torch
+
+
+def _is(t, dtype, shape, device) -> bool:
+    return (isinstance(t, _torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.is_contiguous())
+
+
+def _dense(name, t, dtype, shape, device) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape."""
+    if not _is(t, dtype, shape, device):
+        _contiguous(name, t, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _scale_ptr(t, device) -> int:
+    if not (isinstance(t, _torch.Tensor) and t.dtype is _torch.float32 and t.device == device and t.numel() == 1):
+        _gsf(t, device)
+    return t.data_ptr()
+
+
+def _invoke(fn, device, stream, args):
+    """fn(*args, stream) of the library on the device, which is the current one or becomes it for the call."""
+    torch = _torch
+    call = getattr(_lib or library(), fn)
+    if torch.cuda.current_device() == device.index:
+        rc = call(*args, _stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            rc = call(*args, _stream(stream, device))
+    if rc != H3Q_OK:
+        raise H3QError(fn, rc, h3q_last_error())
+
+
+def _cache(cache):
+    """Checks the four cache tensors; returns (their addresses, (pages, page_size, kv_heads, head_dim),
+    device)."""
+    torch = _torch
     if len(cache) != 4:
         raise ValueError("cache must be (k_codes, k_scales, v_codes, v_scales)")
-    _cuda_tensor("k_codes", cache[0], torch.uint8, device)
-    if cache[0].dim() != 4:
+    kc, ks, vc, vs = cache
+    _cuda_tensor("k_codes", kc, torch.uint8)
+    if kc.dim() != 4:
         raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
-    pages, heads, page, half = cache[0].shape
-    for name, t, per in zip(("k_codes", "k_scales", "v_codes", "v_scales"), cache, (2, 16, 2, 16)):
-        _contiguous(name, t, torch.uint8, (pages, heads, page, 2 * half // per), cache[0].device)
-    return pages, heads, page, 2 * half, cache[0].device
+    codes = kc.shape
+    pages, heads, page, half = codes
+    scales = (pages, heads, page, half // 8)
+    dev = kc.device
+    return ((_dense("k_codes", kc, torch.uint8, codes, dev), _dense("k_scales", ks, torch.uint8, scales, dev),
+             _dense("v_codes", vc, torch.uint8, codes, dev), _dense("v_scales", vs, torch.uint8, scales, dev)),
+            (pages, page, heads, 2 * half), dev)
 
 
 def _head_rows(name, t, device=None):
     """bf16 [rows, heads, dim] whose rows are contiguous (any row stride); returns
-    (tensor, rows, heads, dim, ld)."""
-    import torch
-
-    _cuda_tensor(name, t, torch.bfloat16, device)
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    (address, shape, row stride)."""
+    torch = _torch
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda
+            and (device is None or t.device == device)):
+        _cuda_tensor(name, t, torch.bfloat16, device)
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous rows")
-    rows, heads, dim = t.shape
-    return t, rows, heads, dim, t.stride(0) if rows > 1 else heads * dim
+    rows, heads, dim = shape
+    ld, sh, sd = t.stride()
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim):
+        raise ValueError(f"{name} must be [rows, heads, head_dim] with contiguous rows")
+    return t.data_ptr(), shape, ld if rows > 1 else heads * dim
 
 
 def _row_lists(cu_rows, kv_len, block_table, device):
-    """Checks the lists of packed rows; returns (batch, max_pages)."""
-    import torch
-
-    _cuda_tensor("kv_len", kv_len, torch.int32, device)
-    if kv_len.dim() != 1 or not kv_len.is_contiguous():
+    """Checks the lists of packed rows; returns (cu_rows, kv_len, block_table addresses, batch, max_pages)."""
+    i32 = _torch.int32
+    if not (isinstance(kv_len, _torch.Tensor) and kv_len.dim() == 1):
+        _cuda_tensor("kv_len", kv_len, i32, device)
         raise ValueError("kv_len must be contiguous [batch]")
     batch = kv_len.shape[0]
-    _contiguous("cu_rows", cu_rows, torch.int32, (batch + 1,), device)
-    _cuda_tensor("block_table", block_table, torch.int32, device)
-    if block_table.dim() != 2 or block_table.shape[0] != batch or not block_table.is_contiguous():
+    if not (isinstance(block_table, _torch.Tensor) and block_table.dim() == 2 and block_table.shape[0] == batch):
+        _cuda_tensor("block_table", block_table, i32, device)
         raise ValueError("block_table must be contiguous [batch, max_pages]")
-    return batch, block_table.shape[1]
+    max_pages = block_table.shape[1]
+    return (_dense("cu_rows", cu_rows, i32, (batch + 1,), device), _dense("kv_len", kv_len, i32, (batch,), device),
+            _dense("block_table", block_table, i32, (batch, max_pages), device), batch, max_pages)
 
 
 def h3q_kv_cache_write_nvfp4(k, v, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale,
@@ -714,22 +773,17 @@ def h3q_kv_cache_write_nvfp4(k, v, cache, cu_rows, kv_len, block_table, k_global
     are the last positions of sequence b, which has kv_len[b] positions with them; position p is row
     p % page_size of page block_table[b, p // page_size].  All lists are int32 CUDA tensors.  Returns
     the cache."""
-    import torch
-
-    pages, heads, page, dim, dev = _cache(cache)
-    k, rows, heads_k, dim_k, ld_k = _head_rows("k", k, dev)
-    v, rows_v, heads_v, dim_v, ld_v = _head_rows("v", v, dev)
-    if (heads_k, dim_k) != (heads, dim) or (rows_v, heads_v, dim_v) != (rows, heads, dim):
+    if _torch is None:
+        _load_torch()
+    ptrs, shape, dev = _cache(cache)
+    kp, k_shape, ld_k = _head_rows("k", k, dev)
+    vp, v_shape, ld_v = _head_rows("v", v, dev)
+    if k_shape[1:] != shape[2:] or v_shape != k_shape:
         raise ValueError("k and v must be [rows, kv_heads, head_dim] of the cache's heads")
-    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
-    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
-    with torch.cuda.device(dev):
-        rc = library().h3q_kv_cache_write_nvfp4(
-            k.data_ptr(), ld_k, v.data_ptr(), ld_v, rows, cu_rows.data_ptr(), kv_len.data_ptr(),
-            block_table.data_ptr(), batch, max_pages, kg.data_ptr(), vg.data_ptr(), cache[0].data_ptr(),
-            cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), pages, page, heads, dim,
-            _stream(stream, dev))
-    _check("h3q_kv_cache_write_nvfp4", rc)
+    cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    _invoke("h3q_kv_cache_write_nvfp4", dev, stream,
+            (kp, ld_k, vp, ld_v, k_shape[0], cu, lens, table, batch, max_pages, _scale_ptr(k_global_scale, dev),
+             _scale_ptr(v_global_scale, dev), *ptrs, *shape))
     return cache
 
 
@@ -739,24 +793,21 @@ def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale,
     h3q_kv_cache_write_nvfp4; a whole prefix where cu_rows[b+1] - cu_rows[b] = kv_len[b]).  Give
     ``rows`` (the packed rows) or ``outs`` = (k_out, v_out), bf16 [rows, kv_heads, head_dim].
     Returns (k_out, v_out)."""
-    import torch
-
-    pages, heads, page, dim, dev = _cache(cache)
-    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    torch = _torch or _load_torch()
+    ptrs, shape, dev = _cache(cache)
+    cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
     if outs is None:
         if rows is None:
             raise ValueError("give rows or outs")
-        outs = [torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev) for _ in range(2)]
-    rows = outs[0].shape[0]
-    outs = [_contiguous(n, t, torch.bfloat16, (rows, heads, dim), dev) for n, t in zip(("k_out", "v_out"), outs)]
-    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
-    with torch.cuda.device(dev):
-        rc = library().h3q_kv_cache_read_nvfp4(
-            cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), pages, page, heads,
-            dim, kg.data_ptr(), vg.data_ptr(), rows, cu_rows.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
-            batch, max_pages, outs[0].data_ptr(), outs[1].data_ptr(), _stream(stream, dev))
-    _check("h3q_kv_cache_read_nvfp4", rc)
-    return outs[0], outs[1]
+        outs = [torch.empty((rows, *shape[2:]), dtype=torch.bfloat16, device=dev) for _ in range(2)]
+    k_out, v_out = outs
+    rows = k_out.shape[0]
+    out_shape = (rows, *shape[2:])
+    _invoke("h3q_kv_cache_read_nvfp4", dev, stream,
+            (*ptrs, *shape, _scale_ptr(k_global_scale, dev), _scale_ptr(v_global_scale, dev), rows, cu, lens, table,
+             batch, max_pages, _dense("k_out", k_out, torch.bfloat16, out_shape, dev),
+             _dense("v_out", v_out, torch.bfloat16, out_shape, dev)))
+    return k_out, v_out
 
 
 def attention_cache_workspace_bytes(max_rows: int, heads: int, kv_heads: int, head_dim: int) -> int:
@@ -769,8 +820,7 @@ def attention_cache_workspace_bytes(max_rows: int, heads: int, kv_heads: int, he
 
 def _workspace(workspace, nbytes, stream, device):
     """The caller's workspace, or one of torch's allocator that outlives the work on the stream."""
-    import torch
-
+    torch = _torch or _load_torch()
     if workspace is not None:
         _cuda_tensor("workspace", workspace, torch.uint8, device)
         if not workspace.is_contiguous() or workspace.numel() < nbytes:
@@ -799,32 +849,27 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
     receives the log of the sums of exponentials.  ``workspace`` (uint8, at least
     attention_cache_workspace_bytes) is allocated when not given.  Returns out, bf16 [rows, heads,
     head_dim]; rows of no sequence are left as they were."""
-    import torch
-
-    pages, kv_heads, page, dim, dev = _cache(cache)
-    q, rows, heads, dim_q, ld = _head_rows("q", q, dev)
+    torch = _torch or _load_torch()
+    ptrs, shape, dev = _cache(cache)
+    kv_heads, dim = shape[2:]
+    qp, q_shape, ld = _head_rows("q", q, dev)
+    rows, heads, dim_q = q_shape
     if dim_q != dim:
         raise ValueError(f"q has head_dim {dim_q}, the cache {dim}")
-    batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
-    kg, vg = _gsf(k_global_scale, dev), _gsf(v_global_scale, dev)
-    mask_ptr = lse_ptr = None
-    if tree_mask is not None:
-        mask_ptr = _contiguous("tree_mask", tree_mask, torch.int64, (rows,), dev).data_ptr()
-    if lse is not None:
-        lse_ptr = _contiguous("lse", lse, torch.float32, (heads, rows), dev).data_ptr()
+    cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
+    mask_ptr = _dense("tree_mask", tree_mask, torch.int64, (rows,), dev) if tree_mask is not None else None
+    lse_ptr = _dense("lse", lse, torch.float32, (heads, rows), dev) if lse is not None else None
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
-    _contiguous("out", out, torch.bfloat16, (rows, heads, dim), dev)
-    with torch.cuda.device(dev):
-        nbytes = attention_cache_workspace_bytes(int(max_rows), heads, kv_heads, dim)
-        workspace = _workspace(workspace, nbytes, stream, dev)
-        rc = library().h3q_attention_cache_nvfp4(
-            q.data_ptr(), ld, rows, heads, int(max_rows), cu_rows.data_ptr(), kv_len.data_ptr(),
-            block_table.data_ptr(), batch, max_pages, mask_ptr, cache[0].data_ptr(), cache[1].data_ptr(),
-            cache[2].data_ptr(), cache[3].data_ptr(), pages, page, kv_heads, dim, kg.data_ptr(), vg.data_ptr(),
-            float(dim ** -0.5 if scale is None else scale), out.data_ptr(), lse_ptr, workspace.data_ptr(),
-            workspace.numel(), _stream(stream, dev))
-    _check("h3q_attention_cache_nvfp4", rc)
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+    out_ptr = _dense("out", out, torch.bfloat16, q_shape, dev)
+    max_rows = int(max_rows)
+    nbytes = attention_cache_workspace_bytes(max_rows, heads, kv_heads, dim)
+    workspace = _workspace(workspace, nbytes, stream, dev)
+    _invoke("h3q_attention_cache_nvfp4", dev, stream,
+            (qp, ld, rows, heads, max_rows, cu, lens, table, batch, max_pages, mask_ptr, *ptrs, *shape,
+             _scale_ptr(k_global_scale, dev), _scale_ptr(v_global_scale, dev),
+             float(dim ** -0.5 if scale is None else scale), out_ptr, lse_ptr, workspace.data_ptr(),
+             workspace.numel()))
     return out
 
 
@@ -836,28 +881,26 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     ``scale`` defaults to head_dim ** -0.5.  ``lse`` (fp32 [heads, rows_q], optional) receives the log
     of the sums of exponentials.  Returns out, bf16 [rows_q, heads, head_dim]; rows of no sequence are
     left as they were."""
-    import torch
-
-    q, rows_q, heads, dim, ld_q = _head_rows("q", q)
+    torch = _torch or _load_torch()
+    qp, q_shape, ld_q = _head_rows("q", q)
     dev = q.device
-    k, rows_k, kv_heads, dim_k, ld_k = _head_rows("k", k, dev)
-    v, rows_v, heads_v, dim_v, ld_v = _head_rows("v", v, dev)
-    if dim_k != dim or (rows_v, heads_v, dim_v) != (rows_k, kv_heads, dim):
+    kp, k_shape, ld_k = _head_rows("k", k, dev)
+    vp, v_shape, ld_v = _head_rows("v", v, dev)
+    rows_q, heads, dim = q_shape
+    rows_k, kv_heads, dim_k = k_shape
+    if dim_k != dim or v_shape != k_shape:
         raise ValueError("k and v must have the same shape, and q's head_dim")
-    _cuda_tensor("cu_q", cu_q, torch.int32, dev)
-    if cu_q.dim() != 1 or cu_q.shape[0] < 1 or not cu_q.is_contiguous():
+    if not (isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.shape[0] >= 1):
+        _cuda_tensor("cu_q", cu_q, torch.int32, dev)
         raise ValueError("cu_q must be contiguous [batch + 1]")
-    _contiguous("cu_k", cu_k, torch.int32, cu_q.shape, dev)
+    lists = cu_q.shape
+    cu_q_ptr = _dense("cu_q", cu_q, torch.int32, lists, dev)
+    cu_k_ptr = _dense("cu_k", cu_k, torch.int32, lists, dev)
     if out is None:
-        out = torch.empty((rows_q, heads, dim), dtype=torch.bfloat16, device=dev)
-    _contiguous("out", out, torch.bfloat16, (rows_q, heads, dim), dev)
-    lse_ptr = None
-    if lse is not None:
-        lse_ptr = _contiguous("lse", lse, torch.float32, (heads, rows_q), dev).data_ptr()
-    with torch.cuda.device(dev):
-        rc = library().h3q_attention_varlen(
-            q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, cu_q.data_ptr(), cu_k.data_ptr(),
-            cu_q.shape[0] - 1, rows_q, rows_k, heads, kv_heads, dim, int(bool(causal)),
-            float(dim ** -0.5 if scale is None else scale), out.data_ptr(), lse_ptr, _stream(stream, dev))
-    _check("h3q_attention_varlen", rc)
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+    out_ptr = _dense("out", out, torch.bfloat16, q_shape, dev)
+    lse_ptr = _dense("lse", lse, torch.float32, (heads, rows_q), dev) if lse is not None else None
+    _invoke("h3q_attention_varlen", dev, stream,
+            (qp, ld_q, kp, ld_k, vp, ld_v, cu_q_ptr, cu_k_ptr, lists[0] - 1, rows_q, rows_k, heads, kv_heads, dim,
+             1 if causal else 0, float(dim ** -0.5 if scale is None else scale), out_ptr, lse_ptr))
     return out
