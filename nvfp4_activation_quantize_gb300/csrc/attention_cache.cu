@@ -27,13 +27,16 @@
 // runs at 77 elements a clock and SM (the copy rate needs 42), bit-field arithmetic
 // instead at 44; mma.sync at 1,024 products a clock and SM, a third of it used at NT 1.
 //
-// Work: tiles of 32 keys of one (sequence, key head, row tile), in that order, dealt
-// out in equal contiguous ranges to the CTAs of one wave, whatever the lengths; the four
-// warps of a CTA take its tiles in turn, each with its own ring of bulk copies
-// and its own running maximum, sum and output, joined through shared memory at the end
-// of a (sequence, head).  One that a range's end cuts leaves its parts in the
-// workspace, which the second kernel joins in order of the ranges: no atomics, the same
-// result every time.
+// Work: tiles of 256 keys (128 at head_dim 256) of one (sequence, key head, row tile), in that
+// order, dealt out in equal contiguous ranges to the CTAs of one wave, whatever the lengths.
+// In a CTA one warp copies: the tile's keys, then its values, into a ring of such slots, a
+// copy a lane (a page's codes, its scales), the page numbers looked up a tile ahead.
+// Four warps take 64 keys of each tile, each with its own running maximum, sum and output,
+// and are joined through shared memory at the end of a (sequence, head).  One that a
+// range's end cuts leaves its parts in the workspace, which the second kernel joins in order of
+// the ranges: no atomics, the same result every time.  (With a ring of 32-key tiles to each
+// warp, four copies of 256 bytes and 2 KB a tile: 103 us for 64 tokens over 4,346 positions
+// each, 68 of them in the copies alone.)
 #include <cmath>
 
 #include "h3q_async.cuh"
@@ -44,10 +47,8 @@
 namespace h3q {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 32;     // keys per tile
-constexpr int kStages = 3;    // tiles in flight per warp
+constexpr int kWarps = 4;                        // that compute; one more copies
+constexpr int kMaxWarps = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.0f;  // weights are held as 2^14 * e^(x - m)
@@ -94,7 +95,7 @@ struct Seq {
   int row_tiles;
 };
 
-__device__ __forceinline__ Seq sequence(const Args& a, int b, int tile_rows) {
+__device__ __forceinline__ Seq sequence(const Args& a, int b, int tile_rows, int tile_keys) {
   Seq s;
   const int64_t c0 = a.at.cu[b], c1 = a.at.cu[b + 1];
   int64_t n = c1 - c0;
@@ -108,7 +109,7 @@ __device__ __forceinline__ Seq sequence(const Args& a, int b, int tile_rows) {
   s.row0 = c0;
   s.n = static_cast<int>(n);
   s.len = static_cast<int>(len);
-  s.tiles = s.len > kKeys ? static_cast<int>((static_cast<int64_t>(s.len) + kKeys - 1) / kKeys) : 1;
+  s.tiles = s.len > tile_keys ? static_cast<int>((static_cast<int64_t>(s.len) + tile_keys - 1) / tile_keys) : 1;
   s.row_tiles = (s.n * a.group + tile_rows - 1) / tile_rows;
   s.groups = s.row_tiles * a.cache.kv_heads;
   return s;
@@ -177,6 +178,7 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
 }
 
 // A sum over the CTA of one value a thread, and the exclusive prefix of this thread.
+template <int WARPS>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* prefix) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t x = v;
@@ -189,7 +191,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
   __syncthreads();
   int64_t before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
@@ -201,53 +203,60 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
 template <int HD, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;                 // rows per tile
-  static constexpr int kCodeBytes = kKeys * HD / 2;    // a tile's codes, its scales
-  static constexpr int kScaleBytes = kKeys * HD / 16;
-  static constexpr int kStageBytes = 2 * (kCodeBytes + kScaleBytes);
+  static constexpr int kWarpKeys = HD == 256 || NT == 4 ? 32 : 64;   // keys of a tile per warp
+  static constexpr int kKeys = kWarps * kWarpKeys;     // keys per tile
+  static constexpr int kMt = NT == 1 ? kWarpKeys / 16 : 2;   // 16-key products whose scores are held at once
+  static constexpr int kCodeBytes = kKeys * HD / 2;    // a slot: a tile's codes of keys or values, then their scales
+  static constexpr int kSlotBytes = kCodeBytes + kKeys * HD / 16;
+  static constexpr int kSlots = HD == 64 || kKeys == 128 ? 4 : 3;
+  // Many rows need more registers than an even split leaves: there the copying warp has three
+  // idle ones beside it, and the four hand theirs over (256 x 128 = 128 x 200 + 128 x 56).
+  static constexpr bool kSplit = NT > 1 || HD == 256;
+  static constexpr int kThreads = (kWarps + (kSplit ? 4 : 1)) * 32;
+  static constexpr int kCtas = kSplit ? 2 : 3;         // per SM
   static constexpr int kSteps = HD / 16;               // products of 16 along the head
   static constexpr bool kQShared = NT > 2;             // query fragments in shared memory
   static constexpr int kPitch = HD + 4;                // floats per row of the joining buffer
-  static constexpr int kOffRing = 0;
-  static constexpr int kOffJoin = kOffRing + kWarps * kStages * kStageBytes;
+  static constexpr int kOffJoin = kSlots * kSlotBytes;
   static constexpr int kOffMl = kOffJoin + kWarps * 8 * kPitch * 4;
-  static constexpr int kOffQ = kOffMl + kWarps * kRows * 8;
+  static constexpr int kOffQ = kOffMl + kWarps * 8 * 8;
   static constexpr int kOffMask = kOffQ + (kQShared ? NT * kSteps * 32 * 8 : 0);
   static constexpr int kOffFactor = kOffMask + kRows * 8;
   static constexpr int kOffBar = kOffFactor + kRows * 4;
-  static constexpr int kSmem = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffBar + 2 * kSlots * 8 + 8;
 };
 
+// The computing warps' barrier (the copying warp runs ahead).
+__device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) cache_attention_kernel(const Args a) {
+__global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas) cache_attention_kernel(const Args a) {
   using S = Shape<HD, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scratch[kWarps];
+  __shared__ int64_t scratch[kMaxWarps];
   __shared__ int64_t found_base;
   __shared__ int found_b;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + S::kOffRing + warp * kStages * S::kStageBytes;
-  const uint32_t ring_u = smem_u32(ring);
-  float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
-  float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl);
-  uint2* q_shared = reinterpret_cast<uint2*>(smem + S::kOffQ);
-  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + S::kOffMask);
-  float* row_factor = reinterpret_cast<float*>(smem + S::kOffFactor);
-  const uint32_t bars = smem_u32(smem + S::kOffBar) + warp * kStages * 8;
+  const uint32_t bar_full = smem_u32(smem + S::kOffBar);   // + 8 * slot
+  const uint32_t bar_empty = bar_full + 8 * S::kSlots;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffBar + 16 * S::kSlots);
 
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(bars + 8 * s, 1);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, kWarps);
+    }
+    *abort = 0;
     mbar_init_fence();
   }
   // ---- the plan: all tiles counted, this CTA's range found
   int64_t total = 0;
-  for (int b0 = 0; b0 < a.at.batch; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.at.batch; b0 += S::kThreads) {
     const int b = b0 + threadIdx.x;
     int64_t prefix;
-    total += block_scan(b < a.at.batch ? tiles_of(sequence(a, b, S::kRows)) : 0, scratch, &prefix);
+    total += block_scan<S::kThreads / 32>(b < a.at.batch ? tiles_of(sequence(a, b, S::kRows, S::kKeys)) : 0, scratch, &prefix);
   }
-  const int64_t want = (total + kWarps - 1) / kWarps;
-  const int ctas = static_cast<int>(want < gridDim.x ? want : gridDim.x);
+  const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) {
     if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
     return;
@@ -255,11 +264,11 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
   const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
   {
     int64_t base = 0;
-    for (int b0 = 0; b0 < a.at.batch && base <= t0; b0 += kThreads) {
+    for (int b0 = 0; b0 < a.at.batch && base <= t0; b0 += S::kThreads) {
       const int b = b0 + threadIdx.x;
-      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, S::kRows)) : 0;
+      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, S::kRows, S::kKeys)) : 0;
       int64_t prefix;
-      const int64_t sum = block_scan(mine, scratch, &prefix);
+      const int64_t sum = block_scan<S::kThreads / 32>(mine, scratch, &prefix);
       if (base + prefix <= t0 && t0 < base + prefix + mine) {
         found_b = b;
         found_base = base + prefix;
@@ -268,90 +277,88 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
     }
     __syncthreads();
   }
+  int b = found_b;
+  Seq s = sequence(a, b, S::kRows, S::kKeys);
+  int group = static_cast<int>((t0 - found_base) / s.tiles);   // (key head, row tile) of the sequence
+  int64_t begin = found_base + static_cast<int64_t>(group) * s.tiles;   // its first tile
 
+  if (warp >= kWarps) {
+    if constexpr (S::kSplit) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp > kWarps) return;
+    }
+    // ---- copies.  A lane has one page of the tile (`per` lanes more than one page's codes and
+    // scales at the smaller pages): lane 2 i its codes, lane 2 i + 1 its scales.
+    const int page_shift = a.cache.page_shift;
+    const int page_keys = 1 << page_shift;
+    const int piece_keys = page_keys < S::kKeys ? page_keys : S::kKeys;
+    const int pieces = S::kKeys / piece_keys;
+    const int piece = lane >> 1, what = lane & 1;
+    const int per = what ? HD / 16 : HD / 2;   // bytes a key
+    const uint32_t dst_off = (what ? S::kCodeBytes : 0) + piece * piece_keys * per;
+    const uint32_t slots = smem_u32(smem);
+    int tile = static_cast<int>(t0 - begin);
+    auto page_number = [&]() -> int {   // of this lane's piece of the tile, -1 for none
+      const int64_t pos = static_cast<int64_t>(tile) * S::kKeys + piece * piece_keys;
+      if (piece >= pieces || pos >= s.len) return -1;
+      const int64_t p = a.at.table[b * a.at.max_pages + (pos >> page_shift)];
+      return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
+    };
+    int kv_head = group / s.row_tiles;
+    int page = page_number();
+    uint32_t n = 0;   // slots filled
+    bool ok = true;
+    for (int64_t t = t0; t < t1 && ok; ++t) {
+      const int64_t in_page = (static_cast<int64_t>(tile) * S::kKeys + piece * piece_keys) & (page_keys - 1);
+      const int64_t row = ((static_cast<int64_t>(page) * a.cache.kv_heads + kv_head) << page_shift) + in_page;
+      const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
+      const bool mine = page >= 0;
+      // the next tile's pages, before this one's slots are waited for
+      if (t + 1 < t1) {
+        if (++tile == s.tiles) {
+          tile = 0;
+          if (++group == s.groups) {
+            group = 0;
+            do {
+              s = sequence(a, ++b, S::kRows, S::kKeys);
+            } while (s.groups == 0);
+          }
+          kv_head = group / s.row_tiles;
+        }
+        page = page_number();
+      }
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const uint32_t slot = n % S::kSlots, bar = bar_full + 8 * slot;
+        if (!__all_sync(0xffffffffu, wait_bounded(bar_empty + 8 * slot, ((n / S::kSlots) & 1) ^ 1u))) {
+          ok = false;   // a computing warp never came: nothing more is copied (it gives up by itself)
+          if (lane == 0) {
+            *abort = 1;
+            atomicExch(&g_cache_attention_fault, 1);
+          }
+          break;
+        }
+        if (lane == 0) mbar_expect_tx(bar, __popc(live) / 2 * piece_keys * (HD / 2 + HD / 16));
+        __syncwarp();
+        if (mine)
+          bulk_load(slots + slot * S::kSlotBytes + dst_off, (what ? a.cache.scales[v] : a.cache.codes[v]) + row * per,
+                    piece_keys * per, bar);
+        ++n;
+      }
+    }
+    return;
+  }
+
+  // ---- the computing warps
+  if constexpr (S::kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+  const int g = lane >> 2, t = lane & 3;
+  float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
+  float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl);
+  uint2* q_shared = reinterpret_cast<uint2*>(smem + S::kOffQ);
+  uint64_t* row_mask = reinterpret_cast<uint64_t*>(smem + S::kOffMask);
+  float* row_factor = reinterpret_cast<float*>(smem + S::kOffFactor);
   const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
   const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
-  const int page_shift = a.cache.page_shift;
-  const int piece_keys = page_shift == 4 ? 16 : kKeys;
-  const int pieces = page_shift == 4 ? 8 : 4;
-
-  // ---- loading: this warp's tiles t0 + warp, + kWarps, ... in order, kStages ahead
-  Seq ls = sequence(a, found_b, S::kRows);   // the sequence that the loads are in
-  int lb = found_b, l_group, l_tile;         // (key head, row tile) and key tile in it
-  int64_t l_next = t0 + warp;                // the next tile to load
-  {
-    const int64_t rel = t0 - found_base;
-    l_group = static_cast<int>(rel / ls.tiles);
-    l_tile = static_cast<int>(rel - static_cast<int64_t>(l_group) * ls.tiles) + warp;
-  }
-  auto settle = [&]() {  // carry l_tile past the ends of groups and sequences
-    while (l_tile >= ls.tiles || l_group >= ls.groups) {
-      if (l_group < ls.groups) {
-        l_tile -= ls.tiles;
-        ++l_group;
-      }
-      if (l_group >= ls.groups) {
-        ++lb;
-        ls = sequence(a, lb, S::kRows);
-        l_group = 0;  // (a sequence of no rows has no groups: the loop goes on)
-      }
-    }
-  };
-  const int piece_at = (lane >> 2) * 16;     // lanes 0..7: a copy each (two pages of 16 keys to a tile)
-  auto page_number = [&]() -> int {          // this lane's page of the tile to load, -1 for none
-    const int64_t pos = static_cast<int64_t>(l_tile) * kKeys + piece_at;
-    if (lane >= pieces || pos >= ls.len) return -1;
-    const int64_t p = a.at.table[lb * a.at.max_pages + (pos >> page_shift)];
-    return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
-  };
-  int l_page = -1;
-  if (l_next < t1) {
-    settle();
-    l_page = page_number();
-  }
-  int l_stage = 0;
-  auto issue = [&]() {
-    if (l_next >= t1) return;
-    const int what = lane & 3;
-    const int per = what & 1 ? HD / 16 : HD / 2;   // bytes a key
-    const uint32_t bytes = piece_keys * per;
-    const uint32_t live = __ballot_sync(0xffffffffu, l_page >= 0);
-    const uint32_t bar = bars + 8 * l_stage;
-    if (lane == 0) mbar_expect_tx(bar, (__popc(live) / 4) * piece_keys * 2 * (HD / 2 + HD / 16));
-    __syncwarp();
-    if (l_page >= 0) {
-      const int64_t pos = static_cast<int64_t>(l_tile) * kKeys + piece_at;
-      const int kv_head = l_group / ls.row_tiles;
-      const int64_t row = ((static_cast<int64_t>(l_page) * a.cache.kv_heads + kv_head) << page_shift) +
-                          (pos & ((1 << page_shift) - 1));
-      const uint8_t* src = (what == 0   ? a.cache.codes[0]
-                            : what == 1 ? a.cache.scales[0]
-                            : what == 2 ? a.cache.codes[1]
-                                        : a.cache.scales[1]) +
-                           row * per;
-      const uint32_t off = (what >= 2 ? S::kCodeBytes + S::kScaleBytes : 0) + (what & 1 ? S::kCodeBytes : 0) +
-                           piece_at * per;
-      bulk_load(ring_u + l_stage * S::kStageBytes + off, src, bytes, bar);
-    }
-    if (++l_stage == kStages) l_stage = 0;
-    l_next += kWarps;
-    if (l_next < t1) {
-      l_tile += kWarps;
-      settle();
-      l_page = page_number();  // used by the next issue: the load has a tile's time to arrive
-    }
-  };
-  for (int s = 0; s < kStages; ++s) issue();
-
-  // ---- the segments of the range: the part of each group that lies in it
-  int stage = 0;
-  uint32_t phase = 0;
-  bool alive = true;                 // false: a wait ran out; the rest is computed from whatever is there
-  int64_t mine = t0 + warp;          // this warp's next tile
-  int b = found_b;
-  Seq s = sequence(a, b, S::kRows);
-  int group = static_cast<int>((t0 - found_base) / s.tiles);
-  int64_t begin = found_base + static_cast<int64_t>(group) * s.tiles;   // the group's first tile
   if (threadIdx.x == 0) {
     Cut c;
     c.begin = begin;
@@ -365,8 +372,29 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
     c.pad = 0;
     a.cut[blockIdx.x] = c;
   }
+  uint32_t n = 0;        // slots taken
+  bool alive = true;     // false: a wait ran out; the rest is computed from whatever is there
+  auto take = [&]() {    // the next slot, once it is full
+    const uint32_t slot = n % S::kSlots;
+    if (alive && !__all_sync(0xffffffffu, *abort == 0 && wait_bounded(bar_full + 8 * slot, (n / S::kSlots) & 1))) {
+      alive = false;
+      if (lane == 0) {
+        *abort = 1;
+        atomicExch(&g_cache_attention_fault, 1);
+      }
+    }
+    return smem + slot * S::kSlotBytes;
+  };
+  auto give = [&]() {    // every lane has read it
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_empty + 8 * (n % S::kSlots));
+    ++n;
+  };
+
+  // the segments of the range: the part of each group that lies in it
   bool first_segment = true;
-  while (begin < t1) {
+  int64_t tile0 = t0;
+  while (true) {
     const int64_t seg_end = begin + s.tiles < t1 ? begin + s.tiles : t1;
     const bool whole = begin >= t0 && begin + s.tiles <= t1;
     const int kv_head = group / s.row_tiles;
@@ -376,58 +404,54 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
 
     // query fragments: lane (g, t) holds elements t * HD/4 .. of row g of each 8-row tile
     uint32_t qf[S::kQShared ? 1 : NT][S::kQShared ? 1 : S::kSteps][2];
-    const bool work = mine < seg_end;
-    if (S::kQShared || work) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (S::kQShared && nt != warp) continue;  // the warps share the work (NT == kWarps)
-        const int rho = nt * 8 + g;
-        uint32_t w[HD / 8];
-        if (rho < live_rows) {
-          const int tok = (tile_row0 + rho) / a.group;
-          const int head = kv_head * a.group + (tile_row0 + rho) - tok * a.group;
-          const uint16_t* src = a.q + (s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD + t * (HD / 4);
+    for (int nt = 0; nt < NT; ++nt) {
+      if (S::kQShared && nt != warp) continue;  // the warps share the work (NT == kWarps)
+      const int rho = nt * 8 + g;
+      const int tok = (tile_row0 + rho) / a.group;
+      uint32_t w[HD / 8];
+      if (rho < live_rows) {
+        const int head = kv_head * a.group + (tile_row0 + rho) - tok * a.group;
+        const uint16_t* src = a.q + (s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD + t * (HD / 4);
 #pragma unroll
-          for (int i = 0; i < HD / 32; ++i) {
-            const uint4 v = load16_reused(src + 8 * i);
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-          }
+        for (int i = 0; i < HD / 32; ++i) {
+          const uint4 v = load16_reused(src + 8 * i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) w[i] = 0;
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) m = absmax_bf16x2(m, w[i]) & 0x7fff7fffu;
+      m = max(m & 0xffffu, m >> 16);   // magnitudes order as their bits
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i)  // (the paired maximum skips a NaN: look for exponents of all ones)
+        if ((w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u) m = 0x7f80u;
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const int e = m >> 7;            // biased exponent of the row's largest magnitude
+      const int fe = e == 255 || m == 0 ? 127 : 268 - e > 254 ? 254 : 268 - e;
+      const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) {
+        const float2 v = bf16x2_to_float2(w[i]);
+        const uint32_t h = half2_of(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+        if constexpr (S::kQShared) {
+          reinterpret_cast<uint32_t*>(q_shared)[((nt * S::kSteps + i / 2) * 32 + lane) * 2 + (i & 1)] = h;
         } else {
-#pragma unroll
-          for (int i = 0; i < HD / 8; ++i) w[i] = 0;
-        }
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i) m = absmax_bf16x2(m, w[i]) & 0x7fff7fffu;
-        m = max(m & 0xffffu, m >> 16);   // magnitudes order as their bits; NaN is the largest
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i)  // (the paired maximum skips a NaN: look for exponents of all ones)
-          if ((w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u) m = 0x7f80u;
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const int e = m >> 7;            // biased exponent of the row's largest magnitude
-        const int fe = e == 255 || m == 0 ? 127 : 268 - e > 254 ? 254 : 268 - e;
-        const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
-#pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          const float2 v = bf16x2_to_float2(w[i]);
-          const uint32_t h = half2_of(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
-          if constexpr (S::kQShared) {
-            reinterpret_cast<uint32_t*>(q_shared)[((nt * S::kSteps + i / 2) * 32 + lane) * 2 + (i & 1)] = h;
-          } else {
-            qf[nt][i / 2][i & 1] = h;
-          }
-        }
-        if (t == 0) {   // (several warps may write the same values)
-          const int tok = (tile_row0 + rho) / a.group;
-          row_factor[rho] = __fdiv_rn(1.0f, f);
-          row_mask[rho] = rho >= live_rows    ? 0
-                          : a.mask != nullptr ? static_cast<uint64_t>(a.mask[s.row0 + tok])
-                                              : ~uint64_t{0} >> (63 - tok);
+          qf[nt][i / 2][i & 1] = h;
         }
       }
+      if (t == 0) {   // (several warps may write the same values)
+        row_factor[rho] = __fdiv_rn(1.0f, f);
+        row_mask[rho] = rho >= live_rows    ? 0
+                        : a.mask != nullptr ? static_cast<uint64_t>(a.mask[s.row0 + tok])
+                                            : ~uint64_t{0} >> (63 - tok);
+      }
     }
-    if constexpr (S::kQShared) __syncthreads(); else __syncwarp();
+    if constexpr (S::kQShared) sync_compute(); else __syncwarp();
 
     float cf[NT][2];    // x = cf * S of the lane's columns (rows 2t, 2t + 1 of each tile), in units of
                         // log2; never 0, so that a hidden key's -inf stays one
@@ -437,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        cf[nt][i] = work ? fmaxf(__fmul_rn(k_factor, row_factor[nt * 8 + 2 * t + i]), 0x1p-126f) : 0.0f;
+        cf[nt][i] = fmaxf(__fmul_rn(k_factor, row_factor[nt * 8 + 2 * t + i]), 0x1p-126f);
         m_run[nt][i] = -INFINITY;
         l_run[nt][i] = 0.0f;
       }
@@ -445,176 +469,193 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
       for (int i = 0; i < S::kSteps; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.0f;
     }
 
-    for (; mine < seg_end; mine += kWarps) {
-      if (alive && !__all_sync(0xffffffffu, wait_bounded(bars + 8 * stage, phase))) {
-        alive = false;
-        if (lane == 0) atomicExch(&g_cache_attention_fault, 1);
-      }
-      const uint8_t* kc = ring + stage * S::kStageBytes;
-      const uint8_t* ks = kc + S::kCodeBytes;
-      const uint8_t* vc = ks + S::kScaleBytes;
-      const uint8_t* vs = vc + S::kCodeBytes;
-      const int64_t key0 = (mine - begin) * kKeys;
-
-      // S^T: rows of the left operand are keys 4 (g / 2) + g % 2 and that + 2, so that the
-      // values' operand below finds its four keys 4t .. 4t + 3 side by side
-      float sc[2][NT][4];
+    for (; tile0 < seg_end; ++tile0) {
+      // this warp's keys of the tile; -1: none of them is in the sequence
+      const int64_t first_key = (tile0 - begin) * S::kKeys + warp * S::kWarpKeys;
+      const bool work = first_key < s.len;
+      // Scores and weights of all the warp's keys (kept as the right operand of the second
+      // product), 16 * kMt keys at a time.
+      uint32_t pf[S::kWarpKeys / 16][NT][2];
+      const uint8_t* kc = take();
+      if (work) {
+        const uint8_t* ks = kc + S::kCodeBytes + warp * S::kWarpKeys * (HD / 16);
+        kc += warp * S::kWarpKeys * (HD / 2);
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+        for (int sub = 0; sub < S::kWarpKeys / 16; sub += S::kMt) {
+          const int64_t key0 = first_key + 16 * sub;
+          // S^T: rows of the left operand are keys 4 (g / 2) + g % 2 and that + 2, so that the
+          // values' operand below finds its four keys 4t .. 4t + 3 side by side
+          float sc[S::kMt][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
+          for (int mt = 0; mt < S::kMt; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        const int r0 = mt * 16 + 4 * (g >> 1) + (g & 1);
-        uint32_t w0[HD / 32], w1[HD / 32];
-        lds<HD / 8>(kc + r0 * (HD / 2) + t * (HD / 8), w0);
-        lds<HD / 8>(kc + (r0 + 2) * (HD / 2) + t * (HD / 8), w1);
-        uint32_t b0, b1;    // the lane's HD / 64 scale bytes of both keys
-        if constexpr (HD == 64) {
-          b0 = ks[r0 * 4 + t];
-          b1 = ks[(r0 + 2) * 4 + t];
-        } else if constexpr (HD == 128) {
-          b0 = *reinterpret_cast<const uint16_t*>(ks + r0 * 8 + t * 2);
-          b1 = *reinterpret_cast<const uint16_t*>(ks + (r0 + 2) * 8 + t * 2);
-        } else {
-          b0 = *reinterpret_cast<const uint32_t*>(ks + r0 * 16 + t * 4);
-          b1 = *reinterpret_cast<const uint32_t*>(ks + (r0 + 2) * 16 + t * 4);
-        }
+            for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < HD / 32; ++w) {   // a word: 8 codes, two steps of 4; 16 codes share a scale
-          const uint32_t f0 = scale_half(b0 >> (8 * (w >> 1))) * 0x10001u;
-          const uint32_t f1 = scale_half(b1 >> (8 * (w >> 1))) * 0x10001u;
-          uint32_t h0[4], h1[4];
-          codes_to_half(w0[w], h0);
-          codes_to_half(w1[w], h1);
+          for (int mt = 0; mt < S::kMt; ++mt) {
+            const int r0 = (sub + mt) * 16 + 4 * (g >> 1) + (g & 1);
+            uint32_t w0[HD / 32], w1[HD / 32];
+            lds<HD / 8>(kc + r0 * (HD / 2) + t * (HD / 8), w0);
+            lds<HD / 8>(kc + (r0 + 2) * (HD / 2) + t * (HD / 8), w1);
+            uint32_t b0, b1;    // the lane's HD / 64 scale bytes of both keys
+            if constexpr (HD == 64) {
+              b0 = ks[r0 * 4 + t];
+              b1 = ks[(r0 + 2) * 4 + t];
+            } else if constexpr (HD == 128) {
+              b0 = *reinterpret_cast<const uint16_t*>(ks + r0 * 8 + t * 2);
+              b1 = *reinterpret_cast<const uint16_t*>(ks + (r0 + 2) * 8 + t * 2);
+            } else {
+              b0 = *reinterpret_cast<const uint32_t*>(ks + r0 * 16 + t * 4);
+              b1 = *reinterpret_cast<const uint32_t*>(ks + (r0 + 2) * 16 + t * 4);
+            }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h0[i] = hmul2(h0[i], f0);
-            h1[i] = hmul2(h1[i], f1);
-          }
+            for (int w = 0; w < HD / 32; ++w) {   // a word: 8 codes, two steps of 4; 16 codes share a scale
+              const uint32_t f0 = scale_half(b0 >> (8 * (w >> 1))) * 0x10001u;
+              const uint32_t f1 = scale_half(b1 >> (8 * (w >> 1))) * 0x10001u;
+              uint32_t h0[4], h1[4];
+              codes_to_half(w0[w], h0);
+              codes_to_half(w1[w], h1);
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              uint32_t qb0, qb1;
-              if constexpr (S::kQShared) {
-                const uint2 v = q_shared[(nt * S::kSteps + 2 * w + half) * 32 + lane];
-                qb0 = v.x, qb1 = v.y;
-              } else {
-                qb0 = qf[nt][2 * w + half][0], qb1 = qf[nt][2 * w + half][1];
+              for (int i = 0; i < 4; ++i) {
+                h0[i] = hmul2(h0[i], f0);
+                h1[i] = hmul2(h1[i], f1);
               }
-              mma(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], qb0, qb1);
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint32_t qb0, qb1;
+                  if constexpr (S::kQShared) {
+                    const uint2 v = q_shared[(nt * S::kSteps + 2 * w + half) * 32 + lane];
+                    qb0 = v.x, qb1 = v.y;
+                  } else {
+                    qb0 = qf[nt][2 * w + half][0], qb1 = qf[nt][2 * w + half][1];
+                  }
+                  mma(sc[mt][nt], h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], qb0, qb1);
+                }
             }
-        }
-      }
+          }
 
-      // keys that a row does not see
-      if (key0 + kKeys > s.ctx || key0 + kKeys > s.len) {
+          // keys that a row does not see
+          if (key0 + 16 * S::kMt > s.ctx || key0 + 16 * S::kMt > s.len) {
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < S::kMt; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+              for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int64_t key = key0 + mt * 16 + 4 * (g >> 1) + (g & 1) + (i & 2);
-              const int64_t draft = key - s.ctx;
-              const uint64_t bits = row_mask[nt * 8 + 2 * t + (i & 1)];
-              const bool seen = key < s.len && (draft < 0 || (draft < 64 && ((bits >> draft) & 1)));
-              if (!seen) sc[mt][nt][i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) {
+                  const int64_t key = key0 + mt * 16 + 4 * (g >> 1) + (g & 1) + (i & 2);
+                  const int64_t draft = key - s.ctx;
+                  const uint64_t bits = row_mask[nt * 8 + 2 * t + (i & 1)];
+                  const bool seen = key < s.len && (draft < 0 || (draft < 64 && ((bits >> draft) & 1)));
+                  if (!seen) sc[mt][nt][i] = -INFINITY;
+                }
+          }
+
+          // running maximum and sum, and the weights
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float alpha[2], base[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float m = fmaxf(sc[0][nt][i], sc[0][nt][i + 2]);
+#pragma unroll
+              for (int mt = 1; mt < S::kMt; ++mt) m = fmaxf(m, fmaxf(sc[mt][nt][i], sc[mt][nt][i + 2]));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              m = fmaxf(m_run[nt][i], m == -INFINITY ? -INFINITY : __fmul_rn(m, cf[nt][i]));
+              const float use = m == -INFINITY ? 0.0f : m;
+              alpha[i] = ex2(__fadd_rn(m_run[nt][i], -use));
+              base[i] = __fadd_rn(kPShift, -use);
+              m_run[nt][i] = m;
             }
-      }
-
-      // running maximum and sum; the weights as the right operand of the second product
-      uint32_t pf[2][NT][2];
+            float add[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2], base[2];
+            for (int mt = 0; mt < S::kMt; ++mt) {
+              float p[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float m = fmaxf(fmaxf(sc[0][nt][i], sc[0][nt][i + 2]), fmaxf(sc[1][nt][i], sc[1][nt][i + 2]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          m = fmaxf(m_run[nt][i], m == -INFINITY ? -INFINITY : __fmul_rn(m, cf[nt][i]));
-          const float use = m == -INFINITY ? 0.0f : m;
-          alpha[i] = ex2(__fadd_rn(m_run[nt][i], -use));
-          base[i] = __fadd_rn(kPShift, -use);
-          m_run[nt][i] = m;
-        }
-        float add[2] = {0.0f, 0.0f};
+              for (int i = 0; i < 4; ++i) {
+                p[i] = ex2(__fmaf_rn(sc[mt][nt][i], cf[nt][i & 1], base[i & 1]));
+                add[i & 1] = __fadd_rn(add[i & 1], p[i]);
+              }
+              pf[sub + mt][nt][0] = transpose8x8(half2_of(p[0], p[1]));
+              pf[sub + mt][nt][1] = transpose8x8(half2_of(p[2], p[3]));
+            }
+            l_run[nt][0] = __fmaf_rn(l_run[nt][0], alpha[0], add[0]);
+            l_run[nt][1] = __fmaf_rn(l_run[nt][1], alpha[1], add[1]);
+            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+              if constexpr (S::kMt * 16 < S::kWarpKeys) {   // weights of this tile that were formed before
+                const uint32_t other = half2_of(__shfl_sync(0xffffffffu, alpha[0], g >> 1),
+                                                __shfl_sync(0xffffffffu, alpha[1], g >> 1));
+                const uint32_t al = __byte_perm(other, other, g & 1 ? 0x3232 : 0x1010);   // row g's factor, twice
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          float p[4];
+                for (int mt = 0; mt < sub; ++mt) {
+                  pf[mt][nt][0] = hmul2(pf[mt][nt][0], al);
+                  pf[mt][nt][1] = hmul2(pf[mt][nt][1], al);
+                }
+              }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = ex2(__fmaf_rn(sc[mt][nt][i], cf[nt][i & 1], base[i & 1]));
-            add[i & 1] = __fadd_rn(add[i & 1], p[i]);
-          }
-          pf[mt][nt][0] = transpose8x8(half2_of(p[0], p[1]));
-          pf[mt][nt][1] = transpose8x8(half2_of(p[2], p[3]));
-        }
-        l_run[nt][0] = __fmaf_rn(l_run[nt][0], alpha[0], add[0]);
-        l_run[nt][1] = __fmaf_rn(l_run[nt][1], alpha[1], add[1]);
-        if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-          for (int i = 0; i < S::kSteps; ++i) {
-            acc[nt][i][0] = __fmul_rn(acc[nt][i][0], alpha[0]);
-            acc[nt][i][1] = __fmul_rn(acc[nt][i][1], alpha[1]);
-            acc[nt][i][2] = __fmul_rn(acc[nt][i][2], alpha[0]);
-            acc[nt][i][3] = __fmul_rn(acc[nt][i][3], alpha[1]);
+              for (int i = 0; i < S::kSteps; ++i) {
+                acc[nt][i][0] = __fmul_rn(acc[nt][i][0], alpha[0]);
+                acc[nt][i][1] = __fmul_rn(acc[nt][i][1], alpha[1]);
+                acc[nt][i][2] = __fmul_rn(acc[nt][i][2], alpha[0]);
+                acc[nt][i][3] = __fmul_rn(acc[nt][i][3], alpha[1]);
+              }
+            }
           }
         }
       }
+      give();
 
       // O^T: lane (g, t) holds columns g * HD/8 .. of keys 4t .. 4t + 3
+      const uint8_t* vc = take();
+      if (work) {
+        const uint8_t* vs = vc + S::kCodeBytes + warp * S::kWarpKeys * (HD / 16);
+        vc += warp * S::kWarpKeys * (HD / 2);
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t w[4][HD / 64 > 0 ? HD / 64 : 1];
-        uint32_t f[4];
+        for (int mt = 0; mt < S::kWarpKeys / 16; ++mt) {
+          uint32_t w[4][HD / 64];
+          uint32_t f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = mt * 16 + 4 * t + k;
-          lds<HD / 16>(vc + key * (HD / 2) + g * (HD / 16), w[k]);
-          if constexpr (HD == 64)
-            f[k] = vs[key * 4 + (g >> 1)];
-          else if constexpr (HD == 128)
-            f[k] = vs[key * 8 + g];
-          else
-            f[k] = *reinterpret_cast<const uint16_t*>(vs + key * 16 + g * 2);
-        }
+          for (int k = 0; k < 4; ++k) {
+            const int key = mt * 16 + 4 * t + k;
+            lds<HD / 16>(vc + key * (HD / 2) + g * (HD / 16), w[k]);
+            if constexpr (HD == 64)
+              f[k] = vs[key * 4 + (g >> 1)];
+            else if constexpr (HD == 128)
+              f[k] = vs[key * 8 + g];
+            else
+              f[k] = *reinterpret_cast<const uint16_t*>(vs + key * 16 + g * 2);
+          }
 #pragma unroll
-        for (int j = 0; j < HD / 64; ++j) {   // a word: 8 columns of each key
-          const int sh = HD == 256 ? 8 * (j >> 1) : 0;
-          const uint32_t f01 = scale_half(f[0] >> sh) | scale_half(f[1] >> sh) << 16;
-          const uint32_t f23 = scale_half(f[2] >> sh) | scale_half(f[3] >> sh) << 16;
-          // bytes of (first key's, second key's) codes of the even and of the odd columns
-          const uint32_t e01 = (w[0][j] & 0x0f0f0f0fu) | ((w[1][j] << 4) & 0xf0f0f0f0u);
-          const uint32_t o01 = ((w[0][j] >> 4) & 0x0f0f0f0fu) | (w[1][j] & 0xf0f0f0f0u);
-          const uint32_t e23 = (w[2][j] & 0x0f0f0f0fu) | ((w[3][j] << 4) & 0xf0f0f0f0u);
-          const uint32_t o23 = ((w[2][j] >> 4) & 0x0f0f0f0fu) | (w[3][j] & 0xf0f0f0f0u);
-          uint32_t a0[4], a1[4], a2[4], a3[4];
-          codes_to_half(e01, a0);
-          codes_to_half(o01, a1);
-          codes_to_half(e23, a2);
-          codes_to_half(o23, a3);
+          for (int j = 0; j < HD / 64; ++j) {   // a word: 8 columns of each key
+            const int sh = HD == 256 ? 8 * (j >> 1) : 0;
+            const uint32_t f01 = scale_half(f[0] >> sh) | scale_half(f[1] >> sh) << 16;
+            const uint32_t f23 = scale_half(f[2] >> sh) | scale_half(f[3] >> sh) << 16;
+            // bytes of (first key's, second key's) codes of the even and of the odd columns
+            const uint32_t e01 = (w[0][j] & 0x0f0f0f0fu) | ((w[1][j] << 4) & 0xf0f0f0f0u);
+            const uint32_t o01 = ((w[0][j] >> 4) & 0x0f0f0f0fu) | (w[1][j] & 0xf0f0f0f0u);
+            const uint32_t e23 = (w[2][j] & 0x0f0f0f0fu) | ((w[3][j] << 4) & 0xf0f0f0f0u);
+            const uint32_t o23 = ((w[2][j] >> 4) & 0x0f0f0f0fu) | (w[3][j] & 0xf0f0f0f0u);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            codes_to_half(e01, a0);
+            codes_to_half(o01, a1);
+            codes_to_half(e23, a2);
+            codes_to_half(o23, a3);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a0[i] = hmul2(a0[i], f01);
-            a1[i] = hmul2(a1[i], f01);
-            a2[i] = hmul2(a2[i], f23);
-            a3[i] = hmul2(a3[i], f23);
+            for (int i = 0; i < 4; ++i) {
+              a0[i] = hmul2(a0[i], f01);
+              a1[i] = hmul2(a1[i], f01);
+              a2[i] = hmul2(a2[i], f23);
+              a3[i] = hmul2(a3[i], f23);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma(acc[nt][4 * j + i], a0[i], a1[i], a2[i], a3[i], pf[mt][nt][0], pf[mt][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma(acc[nt][4 * j + i], a0[i], a1[i], a2[i], a3[i], pf[mt][nt][0], pf[mt][nt][1]);
+            }
           }
         }
       }
-      __syncwarp();   // every lane has read the stage before it is filled again
-      issue();
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      give();
     }
 
     // ---- join the warps, eight rows at a time; write the outputs or leave the part
@@ -628,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
         l = __fadd_rn(l, __shfl_xor_sync(0xffffffffu, l, 16));
         if (g == 0) join_ml[warp * 8 + 2 * t + i] = make_float2(m_run[nt][i], l);
       }
-      if (work) {
+      {
         float* dst = join + warp * 8 * S::kPitch + g * (HD / 8);
 #pragma unroll
         for (int i = 0; i < S::kSteps; ++i) {
@@ -637,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
               make_float2(acc[nt][i][1], acc[nt][i][3]);
         }
       }
-      __syncthreads();
+      sync_compute();
       {
         constexpr int kPer = HD / 16;        // columns per thread, 16 threads a row
         const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
@@ -653,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float2 ml = join_ml[w * 8 + row];
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;   // no key of this warp's: its rows may hold anything
             const float f = ex2(__fadd_rn(ml.x, -use));
             l = __fmaf_rn(ml.y, f, l);
 #pragma unroll
@@ -695,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
           }
         }
       }
-      __syncthreads();
+      sync_compute();
     }
     // ---- the next group
     first_segment = false;
@@ -704,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, (NT == 4 || HD * NT > 256) ? 2 : 3) 
     if (++group >= s.groups) {
       group = 0;
       do {
-        s = sequence(a, ++b, S::kRows);
+        s = sequence(a, ++b, S::kRows, S::kKeys);
       } while (s.groups == 0);
     }
   }
@@ -722,7 +762,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args
   if (!cut.valid) return;
   const int lane = threadIdx.x & 31;
   const int rho = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const Seq s = sequence(a, cut.b, S::kRows);
+  const Seq s = sequence(a, cut.b, S::kRows, S::kKeys);
   const int tile_row0 = cut.row_tile * S::kRows;
   if (tile_row0 + rho >= s.n * a.group) return;
   // the first range's part is its last segment: slot 0 if the range began in this group too
@@ -773,14 +813,14 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   static_assert(S::kSmem <= 227 * 1024, "shared memory");
   static_assert(!S::kQShared || NT == kWarps, "a warp loads one 8-row tile of queries");
   int blocks = 0;
-  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_kernel<HD, NT>), kThreads,
+  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_kernel<HD, NT>), S::kThreads,
                                       S::kSmem, kCacheAttentionMaxCtas, &blocks);
   if (err != cudaSuccess) return err;
   a.cut = reinterpret_cast<Cut*>(workspace);
   static_assert(sizeof(Cut) <= kCacheAttentionCutBytes, "workspace");
   a.part_ml = reinterpret_cast<float*>(workspace + kCacheAttentionCutBytes * kCacheAttentionMaxCtas);
   a.part = a.part_ml + int64_t{kCacheAttentionMaxCtas} * 2 * S::kRows * 2;
-  cache_attention_kernel<HD, NT><<<blocks, kThreads, S::kSmem, stream>>>(a);
+  cache_attention_kernel<HD, NT><<<blocks, S::kThreads, S::kSmem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), S::kRows / kMergeWarps, 1);

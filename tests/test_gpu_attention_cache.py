@@ -244,10 +244,11 @@ def test_two_streams(dev):
 
 def test_more_new_tokens_than_max_rows_are_left(dev):
     c = _case(dev, [(5, 100), (2, 50)], 4, 2, 64, 16, seed=12)
-    want, _ = _run(c)
+    whole, whole_lse = _run(c)
     out, lse = _run(c, max_rows=3)
-    assert torch.equal(out[:3], want[:3]) and torch.equal(out[5:], want[5:])
     assert bool((out[3:5] == 5.0).all()) and bool((lse[:, 3:5] == 6.0).all())
+    out[3:5], lse[:, 3:5] = whole[3:5], whole_lse[:, 3:5]
+    _check(c, out, lse)   # (other rows a tile: other roundings, the same formula)
 
 
 def test_given_workspace_of_any_contents(dev):
