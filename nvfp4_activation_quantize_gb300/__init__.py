@@ -669,19 +669,43 @@ def kv_cache_nvfp4(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
                  for per in (2, 16, 2, 16))
 
 
-# The calls of a decoding step run for a few microseconds on the GPU, so what they check of
-# their arguments is checked once each: a tensor that passes the one test below is what the
-# call needs, and only one that does not goes through the helpers that say what is wrong.
+# The calls of a decoding step run for a few microseconds on the GPU, so they go a short way
+# through a C module (csrc/binding.c): it checks the tensors and calls the library, or, where
+# anything is not as the call needs it, returns None and leaves it to the code below, whose
+# checks say what is wrong.
 
 _torch = None
+_native = None
 
 
 def _load_torch():
-    global _torch
+    global _torch, _native
+    import importlib.util
+
     import torch
 
+    lib = library()
+    path = _build.BINDING_PATH
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with nvfp4_activation_quantize_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("h3q_binding", path)
+    native = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(native)
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    native.setup(torch.Tensor, torch.bfloat16, torch.uint8, torch.int32, torch.int64, torch.float32,
+                 getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+                 raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream),
+                 *(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in
+                   ("h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4", "h3q_attention_cache_nvfp4",
+                    "h3q_attention_varlen")))
+    _native = native
     _torch = torch
     return torch
+
+
+def _handle(stream):
+    """The stream argument as the C module takes it: None for the current one, or its handle."""
+    return None if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _is(t, dtype, shape, device) -> bool:
@@ -775,6 +799,12 @@ def h3q_kv_cache_write_nvfp4(k, v, cache, cu_rows, kv_len, block_table, k_global
     the cache."""
     if _torch is None:
         _load_torch()
+    rc = _native.write(k, v, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale,
+                       getattr(k, "device", None), _handle(stream))
+    if rc is not None:
+        if rc != H3Q_OK:
+            raise H3QError("h3q_kv_cache_write_nvfp4", rc, h3q_last_error())
+        return cache
     ptrs, shape, dev = _cache(cache)
     kp, k_shape, ld_k = _head_rows("k", k, dev)
     vp, v_shape, ld_v = _head_rows("v", v, dev)
@@ -794,13 +824,20 @@ def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale,
     ``rows`` (the packed rows) or ``outs`` = (k_out, v_out), bf16 [rows, kv_heads, head_dim].
     Returns (k_out, v_out)."""
     torch = _torch or _load_torch()
-    ptrs, shape, dev = _cache(cache)
-    cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
     if outs is None:
+        _, shape, dev = _cache(cache)
         if rows is None:
             raise ValueError("give rows or outs")
         outs = [torch.empty((rows, *shape[2:]), dtype=torch.bfloat16, device=dev) for _ in range(2)]
     k_out, v_out = outs
+    rc = _native.read(cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, k_out, v_out,
+                      getattr(k_out, "device", None), _handle(stream))
+    if rc is not None:
+        if rc != H3Q_OK:
+            raise H3QError("h3q_kv_cache_read_nvfp4", rc, h3q_last_error())
+        return k_out, v_out
+    ptrs, shape, dev = _cache(cache)
+    cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
     rows = k_out.shape[0]
     out_shape = (rows, *shape[2:])
     _invoke("h3q_kv_cache_read_nvfp4", dev, stream,
@@ -850,26 +887,37 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
     attention_cache_workspace_bytes) is allocated when not given.  Returns out, bf16 [rows, heads,
     head_dim]; rows of no sequence are left as they were."""
     torch = _torch or _load_torch()
+    _, q_shape, _ = _head_rows("q", q)
+    rows, heads, dim = q_shape
+    dev = q.device
+    max_rows = int(max_rows)
+    scale = float(dim ** -0.5 if scale is None else scale)
+    if out is None:
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+    if len(cache) != 4 or len(getattr(cache[0], "shape", ())) != 4:
+        _cache(cache)
+    kv_heads = cache[0].shape[1]
+    # (a number of heads that the call refuses needs no workspace to be refused)
+    nbytes = attention_cache_workspace_bytes(max_rows, heads, kv_heads, dim) if kv_heads and heads >= kv_heads else 256
+    workspace = _workspace(workspace, nbytes, stream, dev)
+    rc = _native.cached(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, max_rows, tree_mask,
+                        scale, out, lse, workspace, dev, _handle(stream))
+    if rc is not None:
+        if rc != H3Q_OK:
+            raise H3QError("h3q_attention_cache_nvfp4", rc, h3q_last_error())
+        return out
     ptrs, shape, dev = _cache(cache)
-    kv_heads, dim = shape[2:]
     qp, q_shape, ld = _head_rows("q", q, dev)
-    rows, heads, dim_q = q_shape
-    if dim_q != dim:
-        raise ValueError(f"q has head_dim {dim_q}, the cache {dim}")
+    if dim != shape[3]:
+        raise ValueError(f"q has head_dim {dim}, the cache {shape[3]}")
     cu, lens, table, batch, max_pages = _row_lists(cu_rows, kv_len, block_table, dev)
     mask_ptr = _dense("tree_mask", tree_mask, torch.int64, (rows,), dev) if tree_mask is not None else None
     lse_ptr = _dense("lse", lse, torch.float32, (heads, rows), dev) if lse is not None else None
-    if out is None:
-        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
     out_ptr = _dense("out", out, torch.bfloat16, q_shape, dev)
-    max_rows = int(max_rows)
-    nbytes = attention_cache_workspace_bytes(max_rows, heads, kv_heads, dim)
-    workspace = _workspace(workspace, nbytes, stream, dev)
     _invoke("h3q_attention_cache_nvfp4", dev, stream,
             (qp, ld, rows, heads, max_rows, cu, lens, table, batch, max_pages, mask_ptr, *ptrs, *shape,
-             _scale_ptr(k_global_scale, dev), _scale_ptr(v_global_scale, dev),
-             float(dim ** -0.5 if scale is None else scale), out_ptr, lse_ptr, workspace.data_ptr(),
-             workspace.numel()))
+             _scale_ptr(k_global_scale, dev), _scale_ptr(v_global_scale, dev), scale, out_ptr, lse_ptr,
+             workspace.data_ptr(), workspace.numel()))
     return out
 
 
@@ -884,6 +932,15 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     torch = _torch or _load_torch()
     qp, q_shape, ld_q = _head_rows("q", q)
     dev = q.device
+    scale = float(q_shape[2] ** -0.5 if scale is None else scale)
+    if out is None:
+        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+    causal = bool(causal)
+    rc = _native.varlen(q, k, v, cu_q, cu_k, causal, scale, out, lse, dev, _handle(stream))
+    if rc is not None:
+        if rc != H3Q_OK:
+            raise H3QError("h3q_attention_varlen", rc, h3q_last_error())
+        return out
     kp, k_shape, ld_k = _head_rows("k", k, dev)
     vp, v_shape, ld_v = _head_rows("v", v, dev)
     rows_q, heads, dim = q_shape
@@ -896,11 +953,9 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     lists = cu_q.shape
     cu_q_ptr = _dense("cu_q", cu_q, torch.int32, lists, dev)
     cu_k_ptr = _dense("cu_k", cu_k, torch.int32, lists, dev)
-    if out is None:
-        out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
     out_ptr = _dense("out", out, torch.bfloat16, q_shape, dev)
     lse_ptr = _dense("lse", lse, torch.float32, (heads, rows_q), dev) if lse is not None else None
     _invoke("h3q_attention_varlen", dev, stream,
             (qp, ld_q, kp, ld_k, vp, ld_v, cu_q_ptr, cu_k_ptr, lists[0] - 1, rows_q, rows_k, heads, kv_heads, dim,
-             1 if causal else 0, float(dim ** -0.5 if scale is None else scale), out_ptr, lse_ptr))
+             int(causal), scale, out_ptr, lse_ptr))
     return out

@@ -3,7 +3,8 @@
 Each translation unit under ``csrc/`` is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into
 ``_build/libh3q.so`` (CUDA runtime linked statically, so the library loads
-without a GPU).  ``-fmad=false`` and the absence of fast-math keep every
+without a GPU); the Python binding's C part (``binding.c``, gcc) becomes
+``_build/h3q_binding.so``.  ``-fmad=false`` and the absence of fast-math keep every
 binary32 operation a separately rounded IEEE operation, which the kernels'
 bit-exactness relies on.  ptxas resource usage is kept in
 ``_build/ptxas.log``.
@@ -14,12 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libh3q.so")
+BINDING_PATH = os.path.join(BUILD_DIR, "h3q_binding.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "h3q.h")
 
 SOURCES = ["h3q_api.cu", "quantize.cu", "adaln.cu", "swiglu.cu", "dequantize.cu", "amax.cu",
@@ -42,9 +45,9 @@ def _inputs():
 
 
 def is_fresh() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -63,8 +66,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as pool:
+    def compile_binding():
+        tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+               os.path.join(CSRC, "binding.c"), "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"gcc failed on binding.c:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, BINDING_PATH)
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+        binding = pool.submit(compile_binding)
         results = list(pool.map(compile_one, SOURCES))
+        binding.result()
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as log:
         for (_, err), src in zip(results, SOURCES):
             log.write(f"== {src}\n{err}\n")
