@@ -825,11 +825,16 @@ def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale,
     Returns (k_out, v_out)."""
     torch = _torch or _load_torch()
     if outs is None:
-        _, shape, dev = _cache(cache)
         if rows is None:
             raise ValueError("give rows or outs")
-        outs = [torch.empty((rows, *shape[2:]), dtype=torch.bfloat16, device=dev) for _ in range(2)]
-    k_out, v_out = outs
+        if len(cache) != 4 or len(getattr(cache[0], "shape", ())) != 4:
+            _cache(cache)
+        codes = cache[0].shape
+        shape, dev = (rows, codes[1], 2 * codes[3]), cache[0].device
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        k_out, v_out = outs
     rc = _native.read(cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, k_out, v_out,
                       getattr(k_out, "device", None), _handle(stream))
     if rc is not None:
@@ -887,7 +892,9 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
     attention_cache_workspace_bytes) is allocated when not given.  Returns out, bf16 [rows, heads,
     head_dim]; rows of no sequence are left as they were."""
     torch = _torch or _load_torch()
-    _, q_shape, _ = _head_rows("q", q)
+    if len(getattr(q, "shape", ())) != 3:
+        _head_rows("q", q)
+    q_shape = q.shape
     rows, heads, dim = q_shape
     dev = q.device
     max_rows = int(max_rows)
@@ -930,8 +937,9 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     of the sums of exponentials.  Returns out, bf16 [rows_q, heads, head_dim]; rows of no sequence are
     left as they were."""
     torch = _torch or _load_torch()
-    qp, q_shape, ld_q = _head_rows("q", q)
-    dev = q.device
+    if len(getattr(q, "shape", ())) != 3:
+        _head_rows("q", q)
+    q_shape, dev = q.shape, q.device
     scale = float(q_shape[2] ** -0.5 if scale is None else scale)
     if out is None:
         out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
@@ -941,6 +949,7 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
         if rc != H3Q_OK:
             raise H3QError("h3q_attention_varlen", rc, h3q_last_error())
         return out
+    qp, q_shape, ld_q = _head_rows("q", q)
     kp, k_shape, ld_k = _head_rows("k", k, dev)
     vp, v_shape, ld_v = _head_rows("v", v, dev)
     rows_q, heads, dim = q_shape
