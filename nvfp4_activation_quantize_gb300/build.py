@@ -26,7 +26,8 @@ BINDING_PATH = os.path.join(BUILD_DIR, "h3q_binding.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "h3q.h")
 
 SOURCES = ["h3q_api.cu", "quantize.cu", "adaln.cu", "swiglu.cu", "dequantize.cu", "amax.cu",
-           "residual.cu", "qkv.cu", "host_pipeline.cu", "gemm_swiglu.cu", "kv_cache.cu", "attention_cache.cu", "attention.cu"]
+           "residual.cu", "qkv.cu", "host_pipeline.cu", "gemm_swiglu.cu", "kv_cache.cu", "attention_cache.cu",
+           "attention_cache_wide.cu", "attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-fmad=false", "-Xcompiler", "-fPIC",
                      "-Xptxas", "-v"]

@@ -46,6 +46,7 @@
 #include "h3q_async.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
+#include "h3q_softmax.cuh"
 #include "h3q_tcgen05.cuh"
 
 namespace h3q {
@@ -58,8 +59,6 @@ constexpr int kCheckWarp = 10;
 constexpr int kPlanWarp = 11;
 constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;  // a row's reference moves when its maximum has passed it by 2^8,
 constexpr float kJump = 64.0f;  // at once when a tile passes it by 2^64 (sums then stay far below 2^127)
 
@@ -109,18 +108,7 @@ struct Shape {
 };
 
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t start = now_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
-      if (*abort) return false;
-      if (now_ns() - start > kWaitNs) break;
-    }
-  }
-  *abort = 1;
-  atomicExch(&g_attention_fault, 1);
-  return false;
+  return h3q::wait_or_abort(bar, parity, abort, &g_attention_fault);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -129,61 +117,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-
-// The product warp runs converged, so that addresses and descriptors stay in uniform
-// registers; one elected lane issues.  (Issued from a branch of one lane, each product
-// took about 100 clocks to issue, its operands being moved one by one: more than the 64
-// that it runs for.)  A descriptor's upper word is a constant of its operand, the lower
-// one the address and the leading offset.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1,024 bytes apart, 128-byte swizzle
-
-__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return ((addr >> 4) & 0x3fffu) | (lbo >> 4) << 16; }
-
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
-      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
-      "mov.b64 y, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(kDescHigh)
-      : "memory");
-}
-
-__device__ __forceinline__ void commit_elected(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-// A value that is the same in all lanes, as one that the compiler knows to be.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Words of packed weights -> as many TMEM columns.
-template <int N>
-__device__ __forceinline__ void store_weights(uint32_t taddr, uint32_t (&w)[N]) {
-  if constexpr (N == 32) {
-    tc_store32(taddr, w);
-  } else {
-    tc_store16(taddr, w);
-  }
 }
 
 // A unit of work: one sequence's pair of row tiles of one group of heads, as the planning
@@ -253,13 +186,6 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int b, int span) {
   if (n > a.rows_q - q0) n = a.rows_q - q0;
   if (q0 < 0 || n < 0) n = 0;
   return (n + span - 1) / span * a.tile_groups;
-}
-
-// max(a, b, c) in one instruction (a NaN loses against a number).
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 
 // 16 scores -> weights 2^(s * c + base), packed to bf16, and their sum added.

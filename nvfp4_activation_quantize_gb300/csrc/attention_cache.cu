@@ -39,114 +39,17 @@
 // each, 68 of them in the copies alone.)
 #include <cmath>
 
-#include "h3q_async.cuh"
-#include "h3q_cache.cuh"
-#include "h3q_device.cuh"
-#include "h3q_internal.h"
+#include "attention_cache.cuh"
 
 namespace h3q {
 namespace {
 
+using namespace cached;
+
 constexpr int kWarps = 4;                        // that compute; one more copies
 constexpr int kMaxWarps = 8;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kPShift = 14.0f;  // weights are held as 2^14 * e^(x - m)
-constexpr int kMergeWarps = 4;    // rows per CTA of the joining kernel
 
 __device__ int g_cache_attention_fault;
-
-struct Args {
-  PagedCache cache;
-  PagedRows at;
-  const uint16_t* q;
-  int64_t ld_q;
-  int64_t rows;
-  int heads, group;        // query heads, and per key head
-  int max_rows;
-  const int64_t* mask;     // or nullptr
-  const float* k_gsf;
-  const float* v_gsf;
-  float scale;
-  uint16_t* o;
-  float* lse;              // or nullptr
-  float* part;             // workspace: [ctas][2][tile rows][head_dim] unnormalised outputs
-  float* part_ml;          // [ctas][2][tile rows][2] maxima and sums
-  struct Cut* cut;         // [ctas]
-};
-
-// What the joining kernel needs to know of the group that the start of a CTA's range cuts:
-// written by that CTA; valid for the first range's start inside the group.
-struct Cut {
-  int64_t begin, end;      // the group's tiles
-  int64_t total;           // all tiles
-  int valid, ctas;
-  int b, kv_head, row_tile, pad;
-};
-
-// One sequence as the work is counted.
-struct Seq {
-  int64_t row0;            // its first packed row
-  int n;                   // rows that are computed
-  int ctx;                 // keys before its new tokens; negative where it has more rows than keys, and
-                           // -64 or less hides every key (a mask has 64 bits)
-  int len;                 // keys in the cache
-  int tiles, groups;       // key tiles; (key head, row tile) pairs
-  int row_tiles;
-};
-
-__device__ __forceinline__ Seq sequence(const Args& a, int b, int tile_rows, int tile_keys) {
-  Seq s;
-  const int64_t c0 = a.at.cu[b], c1 = a.at.cu[b + 1];
-  int64_t n = c1 - c0;
-  const int64_t cap = a.at.max_pages << a.cache.page_shift;
-  int64_t len = a.at.kv_len[b];
-  s.ctx = len - n < -64 ? -64 : static_cast<int>(len - n > 0x7fffffff ? 0x7fffffff : len - n);
-  if (n > a.max_rows) n = a.max_rows;
-  if (c0 + n > a.rows) n = a.rows - c0;
-  if (c0 < 0 || n < 0) n = 0;
-  len = len < 0 ? 0 : len > cap ? cap : len;
-  s.row0 = c0;
-  s.n = static_cast<int>(n);
-  s.len = static_cast<int>(len);
-  s.tiles = s.len > tile_keys ? static_cast<int>((static_cast<int64_t>(s.len) + tile_keys - 1) / tile_keys) : 1;
-  s.row_tiles = (s.n * a.group + tile_rows - 1) / tile_rows;
-  s.groups = s.row_tiles * a.cache.kv_heads;
-  return s;
-}
-
-__device__ __forceinline__ int64_t tiles_of(const Seq& s) { return static_cast<int64_t>(s.tiles) * s.groups; }
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Four bytes of two E2M1 codes -> four pairs of fp16 (exact).
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
-}
-
-// The low seven bits of an E4M3 byte as fp16: its exponent and mantissa in place, which
-// is its value times 2^-8, subnormals included (and finite for all bits set).
-__device__ __forceinline__ uint32_t scale_half(uint32_t byte) { return (byte & 0x7fu) << 7; }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -175,29 +78,6 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
       w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
     }
   }
-}
-
-// A sum over the CTA of one value a thread, and the exclusive prefix of this thread.
-template <int WARPS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* prefix) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) scratch[warp] = x;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
-  }
-  __syncthreads();
-  *prefix = before + x - v;
-  return total;
 }
 
 template <int HD, int NT>
@@ -422,18 +302,10 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i) w[i] = 0;
       }
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i) m = absmax_bf16x2(m, w[i]) & 0x7fff7fffu;
-      m = max(m & 0xffffu, m >> 16);   // magnitudes order as their bits
-#pragma unroll
-      for (int i = 0; i < HD / 8; ++i)  // (the paired maximum skips a NaN: look for exponents of all ones)
-        if ((w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u) m = 0x7f80u;
+      uint32_t m = magnitude_bits(w);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-      const int e = m >> 7;            // biased exponent of the row's largest magnitude
-      const int fe = e == 255 || m == 0 ? 127 : 268 - e > 254 ? 254 : 268 - e;
-      const float f = __uint_as_float(static_cast<uint32_t>(fe) << 23);
+      const float f = query_factor(m);
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         const float2 v = bf16x2_to_float2(w[i]);
@@ -750,63 +622,6 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
   }
 }
 
-// Joins the parts of the groups that the ranges' starts cut: CTA (c, r) takes the group
-// that the start of range c is the first to cut, a warp each of its rows.
-template <int HD, int NT>
-__global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args a) {
-  using S = Shape<HD, NT>;
-  constexpr int kPer = HD / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are written
-  const int c = blockIdx.x + 1;
-  const Cut cut = a.cut[c];
-  if (!cut.valid) return;
-  const int lane = threadIdx.x & 31;
-  const int rho = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  const Seq s = sequence(a, cut.b, S::kRows, S::kKeys);
-  const int tile_row0 = cut.row_tile * S::kRows;
-  if (tile_row0 + rho >= s.n * a.group) return;
-  // the first range's part is its last segment: slot 0 if the range began in this group too
-  const int64_t prev0 = cut.total * (c - 1) / cut.ctas;
-  const int64_t first = static_cast<int64_t>(c - 1) * 2 + (prev0 >= cut.begin ? 0 : 1);
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  int last = c;   // one past the last range that starts inside the group
-  while (last < cut.ctas && cut.total * last / cut.ctas < cut.end) ++last;
-  auto slot = [&](int k) { return (k == c - 1 ? first : static_cast<int64_t>(k) * 2) * S::kRows + rho; };
-  float m = -INFINITY;
-  for (int k = c - 1 + lane; k < last; k += 32) m = fmaxf(m, ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float use = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, v[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
-#pragma unroll 4
-  for (int k = c - 1; k < last; ++k) {
-    const float2 x = ml[slot(k)];
-    const float f = x.x == -INFINITY ? 0.0f : ex2(__fadd_rn(x.x, -use));
-    l = __fmaf_rn(x.y, f, l);
-    const float* src = a.part + slot(k) * HD + lane * kPer;
-#pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + i);
-      v[i] = __fmaf_rn(y.x, f, v[i]);
-      v[i + 1] = __fmaf_rn(y.y, f, v[i + 1]);
-    }
-  }
-  const int tok = (tile_row0 + rho) / a.group;
-  const int head = cut.kv_head * a.group + (tile_row0 + rho) - tok * a.group;
-  const int64_t out_row = s.row0 + tok;
-  const float f = l == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(256.0f, *a.v_gsf), l);
-  uint16_t* dst = a.o + (out_row * a.heads + head) * HD + lane * kPer;
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2)
-    *reinterpret_cast<uint32_t*>(dst + i) =
-        float2_to_bf16x2(make_float2(__fmul_rn(v[i], f), __fmul_rn(v[i + 1], f)));
-  if (a.lse != nullptr && lane == 0)
-    a.lse[head * a.rows + out_row] =
-        l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, __fadd_rn(log2f(l), -kPShift)), kLn2);
-}
-
 template <int HD, int NT>
 cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   using S = Shape<HD, NT>;
@@ -816,33 +631,25 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_kernel<HD, NT>), S::kThreads,
                                       S::kSmem, kCacheAttentionMaxCtas, &blocks);
   if (err != cudaSuccess) return err;
-  a.cut = reinterpret_cast<Cut*>(workspace);
-  static_assert(sizeof(Cut) <= kCacheAttentionCutBytes, "workspace");
-  a.part_ml = reinterpret_cast<float*>(workspace + kCacheAttentionCutBytes * kCacheAttentionMaxCtas);
-  a.part = a.part_ml + int64_t{kCacheAttentionMaxCtas} * 2 * S::kRows * 2;
+  place_workspace(a, workspace, kCacheAttentionMaxCtas, S::kRows);
   cache_attention_kernel<HD, NT><<<blocks, S::kThreads, S::kSmem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), S::kRows / kMergeWarps, 1);
-  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD, NT>, a);
+  return launch_join<HD, S::kRows, S::kKeys>(a, blocks, stream);
 }
 
 // Rows that share a key head are taken 8, 16 or 32 at a time: the fewest that hold them
 // all, so the cache is read once for up to 32 rows (16 at head_dim 256, where the
-// outputs of 32 would not fit the registers).
+// outputs of 32 would not fit the registers).  More than kWideRows go to the tcgen05 kernel.
+constexpr int kWideRows = 32;
 template <int HD>
 cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group;
   if (rows <= 8) return launch<HD, 1>(a, workspace, stream);
   if constexpr (HD == 256) return launch<HD, 2>(a, workspace, stream);
-  else return rows <= 16 ? launch<HD, 2>(a, workspace, stream) : launch<HD, 4>(a, workspace, stream);
+  else
+    return rows <= 16          ? launch<HD, 2>(a, workspace, stream)
+           : rows <= kWideRows ? launch<HD, 4>(a, workspace, stream)
+                               : launch_cache_attention_wide(a, workspace, stream);
 }
 
 }  // namespace
@@ -874,9 +681,11 @@ cudaError_t launch_cache_attention(const PagedCache& cache, const PagedRows& at,
 }
 
 cudaError_t cache_attention_error_flag(int* flag) {
-  int zero = 0;
+  int zero = 0, wide = 0;
   cudaError_t err = cudaMemcpyFromSymbol(flag, g_cache_attention_fault, sizeof(int));
   if (err == cudaSuccess) err = cudaMemcpyToSymbol(g_cache_attention_fault, &zero, sizeof(int));
+  if (err == cudaSuccess) err = cache_attention_wide_error_flag(&wide);
+  *flag |= wide;
   return err;
 }
 

@@ -1,0 +1,652 @@
+// attention_cache_wide.cu -- attention over the paged NVFP4 cache where many rows share a
+// key head: trees of drafted tokens, or large groups of query heads.
+//
+// The mathematics is attention_cache.cu's; there the products are mma.sync's, 1,024 a clock and
+// SM, which 32 rows use up at the rate the cache arrives.  Here up to 128 rows are one tile of
+// the fifth-generation tensor cores (4,096 a clock), and the values of the cache are
+// laid out for them: exact fp16 in shared memory.
+//
+// Bound: the cache's bytes (18.4 KB a tile of 128 keys at head_dim 128: 787 clocks of an SM's
+// share of the copy rate), closely followed by the way from codes to fp16 (32,768 elements a
+// tile: about 750 clocks of four warps) and by the powers (128 rows: 512).  The products are
+// 1,024 clocks of M = 128 whether or not its rows are used; they run beside everything else.
+//
+//   warps 0..3, 4..7  softmax of the even and of the odd tiles: a thread owns one row of S in
+//                     TMEM and writes its weights, 2^6 e^(x - reference) in fp16, over it in two
+//                     halves; the reference follows the row's maximum when that has grown by
+//                     more than 2^8 (weights stay below 2^14).  Two streams with outputs of their
+//                     own, so that the tensor cores work on one while the other has its
+//                     softmax; joined at the end of a (sequence, head).
+//   warps 8..11       codes and scales -> fp16 tiles, 128-byte swizzle, keys and values alike (a
+//                     value tile's rows are the reduction of its product)
+//   warp 12           copies pages of codes and scales into a raw ring, a lane each
+//   warp 13           the products
+// Work is dealt out and joined as in attention_cache.cu, in tiles of 128 keys, one CTA per SM.
+// Every wait is bounded: one that runs out sets a device flag and tells the other roles to stop.
+#include "attention_cache.cuh"
+#include "h3q_tcgen05.cuh"
+
+namespace h3q {
+namespace {
+
+using namespace cached;
+
+constexpr int kThreads = 512;
+constexpr int kConvertWarp0 = 8;
+constexpr int kCopyWarp = 12;
+constexpr int kMmaWarp = 13;
+constexpr int kRows = 128;             // rows per tile
+constexpr int kKeys = 128;             // keys per tile
+constexpr int kMaxCtas = 152;          // the workspace holds the parts of so many (608 of 32 rows)
+constexpr float kInShift = 6.0f;       // weights are held as 2^6 e^(x - reference)
+constexpr float kSlack = 8.0f;         // how far (log2) a row's maximum may pass its reference
+
+__device__ int g_wide_fault;
+
+template <int HD>
+struct Shape {
+  static constexpr int kTileBytes = kKeys * HD * 2;           // a tile of keys or values in fp16
+  static constexpr int kCodeBytes = kKeys * HD / 2;
+  static constexpr int kRawBytes = kCodeBytes + kKeys * HD / 16;
+  static constexpr int kSlots = 4;                            // fp16 tiles: K0 V0 K1 V1 ...
+  static constexpr int kRaw = 4;                              // raw tiles, in the same order
+  static constexpr int kOffTiles = kRows * HD * 2;            // after Q
+  static constexpr int kOffRaw = kOffTiles + kSlots * kTileBytes;
+  static constexpr int kOffJoin = kOffRaw + kRaw * kRawBytes; // 32 columns of 128 rows, fp32
+  static constexpr int kOffMl = kOffJoin + 32 * kRows * 4;
+  static constexpr int kOffFactor = kOffMl + kRows * 8;
+  static constexpr int kOffBar = kOffFactor + kRows * 4;
+  static constexpr int kBars = 2 * kSlots + 2 * kRaw + 1 + 8 + 1;
+  static constexpr int kOffMisc = kOffBar + 8 * kBars;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;
+  // TMEM: two S buffers (weights over them), then two outputs
+  static constexpr uint32_t kO = 256;
+  // Instruction descriptors (kind::f16): fp32 result (bit 4), fp16 operands (0), N >> 3 at bits
+  // 17-22, M >> 4 at 24-28; V is transposed (bit 16).
+  static constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kKeys >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (uint32_t(HD >> 3) << 17) | (8u << 24);
+};
+
+// The groups of a CTA's range one after the other, as every role walks them.
+struct Walk {
+  Seq s;
+  int b, group;
+  int64_t begin;           // the group's first tile
+  __device__ __forceinline__ void next(const Args& a) {
+    begin += s.tiles;
+    if (++group >= s.groups) {
+      group = 0;
+      do {
+        s = sequence(a, ++b, kRows, kKeys);
+      } while (s.groups == 0);
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t ones(int64_t n) {
+  return n <= 0 ? 0 : n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
+}
+
+// 16 scores -> weights 2^(s * c + base), packed to fp16, and their sum added.
+__device__ __forceinline__ void weights16(const uint32_t* s, float2 c2, float2 b2, float2& sum, uint32_t* w) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float2 p = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
+    p.x = ex2(p.x);
+    p.y = ex2(p.y);
+    sum = add2(sum, p);
+    w[j] = half2_of(p.x, p.y);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const Args a) {
+  using S = Shape<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
+  __shared__ int64_t scratch[kThreads / 32];
+  __shared__ int64_t found_base;
+  __shared__ int found_b;
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bar_full = base + S::kOffBar;              // + 8 * slot
+  const uint32_t bar_empty = bar_full + 8 * S::kSlots;
+  const uint32_t bar_raw = bar_empty + 8 * S::kSlots;       // + 8 * raw slot
+  const uint32_t bar_used = bar_raw + 8 * S::kRaw;
+  const uint32_t bar_q = bar_used + 8 * S::kRaw;
+  const uint32_t bar_s = bar_q + 8;                         // + 8 * stream
+  const uint32_t bar_p = bar_s + 16;
+  const uint32_t bar_p2 = bar_p + 16;
+  const uint32_t bar_o = bar_p2 + 16;
+  const uint32_t bar_drain = bar_o + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(bar_full + 8 * i, 128);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < S::kRaw; ++i) {
+      mbar_init(bar_raw + 8 * i, 1);
+      mbar_init(bar_used + 8 * i, 4);
+    }
+    mbar_init(bar_q, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + 8 * i, 1);
+      mbar_init(bar_p + 8 * i, 128);
+      mbar_init(bar_p2 + 8 * i, 128);
+      mbar_init(bar_o + 8 * i, 1);
+    }
+    mbar_init(bar_drain, 1);
+    *abort = 0;
+    mbar_init_fence();
+  }
+  // ---- the plan: all tiles counted, this CTA's range found
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.at.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int64_t prefix;
+    total += block_scan<kThreads / 32>(b < a.at.batch ? tiles_of(sequence(a, b, kRows, kKeys)) : 0, scratch, &prefix);
+  }
+  const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
+    return;
+  }
+  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
+  {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.at.batch && before <= t0; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, kRows, kKeys)) : 0;
+      int64_t prefix;
+      const int64_t sum = block_scan<kThreads / 32>(mine, scratch, &prefix);
+      if (before + prefix <= t0 && t0 < before + prefix + mine) {
+        found_b = b;
+        found_base = before + prefix;
+      }
+      before += sum;
+    }
+    __syncthreads();
+  }
+  Walk w;
+  w.b = found_b;
+  w.s = sequence(a, w.b, kRows, kKeys);
+  w.group = static_cast<int>((t0 - found_base) / w.s.tiles);
+  w.begin = found_base + static_cast<int64_t>(w.group) * w.s.tiles;
+
+  auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp: one decision
+    return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_wide_fault)));
+  };
+
+  // Registers: 8 softmax warps 168, 4 converting warps 96, the other four 80 (512 x 128 in all).
+  if (warp < kConvertWarp0) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ---- softmax of one stream
+    const int x = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;   // the TMEM of all 512 columns begins at 0
+    const uint32_t taddr = lane_base + x * kKeys, taddr_o = lane_base + S::kO + x * HD;
+    float* join = reinterpret_cast<float*>(smem + S::kOffJoin) + row;          // [column][row]
+    float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl) + row;
+    float* factor = reinterpret_cast<float*>(smem + S::kOffFactor) + row;
+    const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
+    const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
+    auto sync_both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    if (threadIdx.x == 0) {
+      Cut cut;
+      cut.begin = w.begin;
+      cut.end = w.begin + w.s.tiles;
+      cut.total = total;
+      cut.ctas = ctas;
+      cut.b = w.b;
+      cut.kv_head = w.group / w.s.row_tiles;
+      cut.row_tile = w.group % w.s.row_tiles;
+      cut.valid = t0 > w.begin && total * (blockIdx.x - 1) / ctas <= w.begin;   // blockIdx.x > 0 where t0 > begin
+      cut.pad = 0;
+      a.cut[blockIdx.x] = cut;
+    }
+    bool first_segment = true, ok = true;
+    uint32_t s_count = 0, o_count = 0;
+    for (int64_t seg = t0; seg < t1;) {
+      const int64_t seg_end = w.begin + w.s.tiles < t1 ? w.begin + w.s.tiles : t1;
+      const bool whole = seg == w.begin && seg_end == w.begin + w.s.tiles;
+      const int count = static_cast<int>(seg_end - seg);
+      const int kv_head = w.group / w.s.row_tiles, row_tile = w.group - kv_head * w.s.row_tiles;
+      const int rho = row_tile * kRows + row;
+      const bool valid = rho < w.s.n * a.group;
+      const int tok = rho / a.group, head = kv_head * a.group + rho - tok * a.group;
+      const uint64_t mask = !valid ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[w.s.row0 + tok])
+                                                           : ~uint64_t{0} >> (63 - tok);
+      if (x == 0) {
+        // the row's query, scaled, in fp16: rows of 128 bytes, their 16-byte pieces swizzled
+        const uint16_t* src = a.q + (w.s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD;
+        uint32_t m = 0;
+        uint32_t q[HD / 2];
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) v = load16_reused(src + 8 * i);
+          q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
+        }
+        m = magnitude_bits(q);
+        const float f = query_factor(m);
+        *factor = __fdiv_rn(1.0f, f);
+#pragma unroll
+        for (int i = 0; i < HD / 8; ++i) {
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = bf16x2_to_float2(q[4 * i + k]);
+            h[k] = half2_of(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+          }
+          *reinterpret_cast<uint4*>(smem + (i / 8) * (kRows * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4)) =
+              make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it
+        mbar_arrive(bar_q);
+      }
+      sync_both();
+      const float c = fmaxf(__fmul_rn(k_factor, *factor), 0x1p-126f);   // never 0: a hidden key's -inf stays one
+      float m_ref = -INFINITY, m_seen = -INFINITY, l = 0.0f;
+      // Move the reference to the maximum seen, where that has grown: scale the sum and O.
+      auto rescale = [&](bool any_o) {
+        float alpha = 1.0f;
+        if (__fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack) {
+          alpha = ex2(__fmul_rn(__fadd_rn(m_ref, -m_seen), c));
+          m_ref = m_seen;
+          l = __fmul_rn(l, alpha);
+        }
+        if (!any_o) return;
+#pragma unroll 1
+        for (int i = 0; i < HD; i += 32) {
+          uint32_t o[32];
+          tc_load32(taddr_o + i, o);
+          tc_wait_load(o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__fmul_rn(__uint_as_float(o[k]), alpha));
+          tc_store32(taddr_o + i, o);
+        }
+        tc_wait_store();
+      };
+      for (int i = x; i < count && ok; i += 2) {
+        if (!(ok = wait(bar_s + 8 * x, s_count & 1))) break;
+        ++s_count;
+        tc_fence_after();   // S was issued after the product before it of this stream: O is at rest
+        const int64_t key0 = (seg + i - w.begin) * kKeys;
+        const bool masked = w.s.ctx - key0 < kKeys || w.s.len - key0 < kKeys;
+        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+        if (masked) {   // which of the tile's keys the row sees
+          const int64_t d = w.s.ctx - key0;
+          uint64_t lo = ones(d), hi = ones(d - 64);
+          if (d >= 64 && d < 128) {
+            hi |= mask << (d - 64);
+          } else if (d > 0 && d < 64) {
+            lo |= mask << d;
+            hi |= mask >> (64 - d);
+          } else if (d <= 0 && d > -64) {
+            lo |= mask >> -d;
+          }
+          lo &= ones(w.s.len - key0);
+          hi &= ones(w.s.len - key0 - 64);
+          see[0] = static_cast<uint32_t>(lo), see[1] = static_cast<uint32_t>(lo >> 32);
+          see[2] = static_cast<uint32_t>(hi), see[3] = static_cast<uint32_t>(hi >> 32);
+        }
+        const float2 c2 = make_float2(c, c);
+        uint32_t s[4][32];
+        uint32_t wt[32];
+        float2 sum;
+        bool fresh = i < 2;   // no reference yet: only the maximum is formed
+        for (;;) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tc_load32(taddr + 32 * k, s[k]);
+          tc_wait_load(s[0]);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) tc_loaded(s[k]);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 128; ++k)
+              if (!(see[k / 32] >> (k % 32) & 1)) s[k / 32][k % 32] = 0xff800000u;
+          }
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 128; k += 8)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              m[h] = max3(m[h], __uint_as_float(s[k / 32][k % 32 + 2 * h]), __uint_as_float(s[k / 32][k % 32 + 2 * h + 1]));
+          if (fresh) {
+            fresh = false;
+            m_seen = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            rescale(false);
+            continue;
+          }
+          const float shift = m_ref == -INFINITY ? kInShift : __fadd_rn(kInShift, -__fmul_rn(m_ref, c));
+          const float2 b2 = make_float2(shift, shift);
+          sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int k = 0; k < 64; k += 16) weights16(s[k / 32] + k % 32, c2, b2, sum, wt + k / 2);
+          m_seen = fmaxf(max3(m_seen, m[0], m[1]), fmaxf(m[2], m[3]));
+          // (a difference of two -inf is no number, and not above)
+          if (!__any_sync(0xffffffffu, __fmul_rn(__fadd_rn(m_seen, -m_ref), c) > kSlack)) break;
+          rescale(i >= 2);
+        }
+        const float shift = m_ref == -INFINITY ? kInShift : __fadd_rn(kInShift, -__fmul_rn(m_ref, c));
+        const float2 b2 = make_float2(shift, shift);
+        store_weights<32>(taddr, wt);
+        tc_wait_store();
+        tc_fence_before();
+        mbar_arrive(bar_p + 8 * x);
+#pragma unroll
+        for (int k = 0; k < 64; k += 16) weights16(s[2 + k / 32] + k % 32, c2, b2, sum, wt + k / 2);
+        store_weights<32>(taddr + 32, wt);
+        l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
+        tc_wait_store();
+        tc_fence_before();
+        mbar_arrive(bar_p2 + 8 * x);
+      }
+      if (ok && x < count) {
+        ok = wait(bar_o + 8 * x, o_count & 1);
+        ++o_count;
+        tc_fence_after();
+      }
+      if (*abort) ok = false;
+      // ---- join the streams, 32 columns at a time; write the outputs or leave the part
+      const float m_mine = m_ref == -INFINITY ? -INFINITY : __fmul_rn(m_ref, c);
+      if (x == 1) *join_ml = make_float2(m_mine, l);
+      sync_both();
+      const bool two = count > 1;
+      float f0 = 0.0f, f1 = 0.0f, m = m_mine;
+      if (x == 0) {
+        const float2 other = *join_ml;
+        if (two) m = fmaxf(m, other.x);
+        const float use = m == -INFINITY ? 0.0f : m;
+        f0 = ex2(__fadd_rn(m_mine, -use));
+        f1 = two ? ex2(__fadd_rn(other.x, -use)) : 0.0f;
+        l = __fmul_rn(l, f0);
+        if (two) l = __fmaf_rn(other.y, f1, l);
+      }
+      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
+      const int64_t out_row = w.s.row0 + tok;
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * kRows + row;
+#pragma unroll 1
+      for (int i = 0; i < HD; i += 32) {
+        uint32_t o[32];
+        __syncwarp();
+        if (x == 0 || two) {
+          tc_load32(taddr_o + i, o);
+          tc_wait_load(o);
+        }
+        if (x == 1 && two) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) join[k * kRows] = __uint_as_float(o[k]);
+        }
+        if (two) sync_both();
+        if (x == 0 && valid && ok) {
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            v[k] = __fmul_rn(__uint_as_float(o[k]), f0);
+            if (two) v[k] = __fmaf_rn(join[k * kRows], f1, v[k]);
+          }
+          if (whole) {
+            uint16_t* dst = a.o + (out_row * a.heads + head) * HD + i;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              uint32_t p[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                p[h] = l == 0.0f ? 0u
+                                 : float2_to_bf16x2(make_float2(__fmul_rn(v[k + 2 * h], inv), __fmul_rn(v[k + 2 * h + 1], inv)));
+              store16(dst + k, make_uint4(p[0], p[1], p[2], p[3]));
+            }
+          } else {
+            constexpr float kUp = 256.0f;   // parts hold 2^14 e^(x - m): 2^(kPShift - kInShift) times more
+            float* dst = a.part + part * HD + i;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(dst + k) = make_float4(__fmul_rn(v[k], kUp), __fmul_rn(v[k + 1], kUp),
+                                                                __fmul_rn(v[k + 2], kUp), __fmul_rn(v[k + 3], kUp));
+          }
+        }
+        if (two) sync_both();
+      }
+      if (x == 0 && valid && ok) {
+        if (!whole)
+          reinterpret_cast<float2*>(a.part_ml)[part] = make_float2(m, __fmul_rn(l, 256.0f));
+        else if (a.lse != nullptr)
+          a.lse[head * a.rows + out_row] =
+              l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, __fadd_rn(log2f(l), -kInShift)), kLn2);
+      }
+      tc_fence_before();   // O has been read before the next segment's first weights are announced
+      first_segment = false;
+      seg = seg_end;
+      if (seg < t1) w.next(a);
+    }
+  } else if (warp < kCopyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    // ---- codes and scales -> fp16.  A lane takes 32 codes of a row (16 bytes), a row's lanes
+    // side by side; it writes four 16-byte pieces.  Lanes of the upper 64 columns take theirs in
+    // another order, so that eight lanes' pieces fall into eight banks.
+    constexpr int kRowLanes = HD / 32;
+    constexpr int kStepRows = 32 / kRowLanes;
+    const int part = lane % kRowLanes, row_in = lane / kRowLanes;
+    const int half = part >> 1;
+    for (int64_t t = t0, n = 0; t < t1; ++t) {
+      bool ok = true;
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v, ++n) {
+        const uint32_t slot = n % S::kSlots, raw = n % S::kRaw;
+        if (!(ok = wait(bar_raw + 8 * raw, (n / S::kRaw) & 1) && wait(bar_empty + 8 * slot, ((n / S::kSlots) & 1) ^ 1u)))
+          break;
+        const uint8_t* codes = smem + S::kOffRaw + raw * S::kRawBytes;
+        const uint8_t* scales = codes + S::kCodeBytes;
+        uint8_t* tile = smem + S::kOffTiles + slot * S::kTileBytes + half * (kKeys * 128);
+#pragma unroll
+        for (int i = 0; i < kRowLanes; ++i) {
+          const int row = (warp - kConvertWarp0) * 32 + i * kStepRows + row_in;
+          const uint4 c4 = *reinterpret_cast<const uint4*>(codes + row * (HD / 2) + part * 16);
+          const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + row * (HD / 16) + part * 2);
+          uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+          uint32_t f[2] = {scale_half(sc) * 0x10001u, scale_half(sc >> 8) * 0x10001u};
+          const int flip = half * 2;
+          if (half) {
+            cw[0] = c4.z, cw[1] = c4.w, cw[2] = c4.x, cw[3] = c4.y;
+            const uint32_t f0 = f[0];
+            f[0] = f[1], f[1] = f0;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+            codes_to_half(cw[k], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], f[k >> 1]);
+            const int piece = (part & 1) * 4 + (k ^ flip);
+            *reinterpret_cast<uint4*>(tile + row * 128 + ((piece ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it
+        mbar_arrive(bar_full + 8 * slot);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_used + 8 * raw);
+      }
+      if (!ok) break;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kCopyWarp) {
+      // ---- copies: lane 2 i has the codes of page i of the tile, lane 2 i + 1 its scales
+      const int page_shift = a.cache.page_shift;
+      const int piece_keys = 1 << page_shift;   // at most a tile's 128
+      const int pieces = kKeys >> page_shift;
+      const int piece = lane >> 1, what = lane & 1;
+      const int per = what ? HD / 16 : HD / 2;   // bytes a key
+      const uint32_t dst = base + S::kOffRaw + (what ? S::kCodeBytes : 0) + piece * piece_keys * per;
+      int tile = static_cast<int>(t0 - w.begin);
+      auto page_number = [&]() -> int {   // of this lane's piece of the tile, -1 for none
+        const int64_t pos = static_cast<int64_t>(tile) * kKeys + piece * piece_keys;
+        if (piece >= pieces || pos >= w.s.len) return -1;
+        const int64_t p = a.at.table[w.b * a.at.max_pages + (pos >> page_shift)];
+        return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
+      };
+      int page = page_number();
+      uint32_t n = 0;
+      bool ok = true;
+      for (int64_t t = t0; t < t1 && ok; ++t) {
+        const int kv_head = w.group / w.s.row_tiles;
+        const int64_t row = (static_cast<int64_t>(page) * a.cache.kv_heads + kv_head) << page_shift;
+        const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
+        const bool mine = page >= 0;
+        if (t + 1 < t1) {   // the next tile's pages, before this one's slots are waited for
+          if (++tile == w.s.tiles) {
+            tile = 0;
+            w.next(a);
+          }
+          page = page_number();
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t raw = n % S::kRaw, bar = bar_raw + 8 * raw;
+          if (!(ok = wait(bar_used + 8 * raw, ((n / S::kRaw) & 1) ^ 1u))) break;
+          if (lane == 0) mbar_expect_tx(bar, __popc(live) / 2 * piece_keys * (HD / 2 + HD / 16));
+          __syncwarp();
+          if (mine)
+            bulk_load(dst + raw * S::kRawBytes, (what ? a.cache.scales[v] : a.cache.codes[v]) + row * per,
+                      piece_keys * per, bar);
+          ++n;
+        }
+      }
+      if (!ok)   // every copy issued has landed before the CTA goes
+        for (uint32_t k = n < S::kRaw ? 0 : n - S::kRaw; k < n; ++k)
+          (void)wait_bounded(bar_raw + 8 * (k % S::kRaw), (k / S::kRaw) & 1);
+    } else if (warp == kMmaWarp) {
+      // ---- products.  The whole warp allocates the CTA's TMEM: all 512 columns, so they begin at 0.
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+      const uint32_t q_low = desc_low(base, 16);
+      const uint32_t k_low = desc_low(base + S::kOffTiles, 16);
+      const uint32_t v_low = desc_low(base + S::kOffTiles, kKeys * 128);   // 64 columns of V, then the next 64
+      uint32_t n0 = 0;                   // slot number of the segment's first K tile
+      uint32_t p_count[2] = {0, 0}, segments = 0;
+      bool ok = true;
+      // Each lane waits for a barrier of its own (0: none), the warp for all of them.
+      auto wait_lanes = [&](uint32_t bar, uint32_t parity) {
+        bool done = bar == 0 || mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        const uint64_t start = now_ns();
+        for (uint32_t i = 1;; ++i) {
+          if (!done) done = mbar_try_wait(bar, parity);
+          if (__all_sync(0xffffffffu, done)) return true;
+          if ((i & 255u) == 0) {
+            const bool late = now_ns() - start > kWaitNs;
+            if (late && lane == 0) {
+              *abort = 1;
+              atomicExch(&g_wide_fault, 1);
+            }
+            if (__any_sync(0xffffffffu, late || *abort)) return false;
+          }
+        }
+      };
+      auto slot_of = [&](int i) { return (n0 + i) % S::kSlots; };
+      auto full = [&](int i) { return bar_full + 8 * slot_of(i); };
+      auto full_parity = [&](int i) { return ((n0 + i) / S::kSlots) & 1u; };
+      auto release = [&](int i) { commit_elected(bar_empty + 8 * slot_of(i)); };
+      auto s_product = [&](int x, int i) {   // S[x] = Q K[i]^T
+        const uint32_t k = k_low + slot_of(2 * i) * (S::kTileBytes >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int d = 0; d < HD / 16; ++d)
+          mma_ss(x * kKeys, q_low + (((d / 4) * (kRows * 128) + (d % 4) * 32) >> 4),
+                 k + (((d / 4) * (kKeys * 128) + (d % 4) * 32) >> 4), S::kIdescS, d > 0);
+        commit_elected(bar_s + 8 * x);
+        release(2 * i);
+      };
+      auto o_half = [&](int x, int i, int half) {   // half of O[x] += P[x] V[i]
+        const uint32_t v = v_low + slot_of(2 * i + 1) * (S::kTileBytes >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int d = half * 4; d < half * 4 + 4; ++d)
+          mma_ts(S::kO + x * HD, x * kKeys + 8 * d, v + (d * 2048 >> 4), S::kIdescO, i > 1 || d > 0);
+      };
+      for (int64_t seg = t0; seg < t1 && ok;) {
+        const int64_t seg_end = w.begin + w.s.tiles < t1 ? w.begin + w.s.tiles : t1;
+        const int count = uniform(static_cast<int>(seg_end - seg));
+        ok = wait_lanes(lane == 0 ? bar_q : lane == 1 ? full(0) : lane == 2 && count > 1 ? full(2) : 0u,
+                        lane == 0 ? segments & 1 : lane == 1 ? full_parity(0) : full_parity(2));
+        ++segments;
+        if (ok) {
+          s_product(0, 0);
+          if (count > 1) s_product(1, 1);
+        }
+        for (int i0 = 0; i0 < count && ok; i0 += 2) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int i = i0 + x;
+            if (!ok || i >= count) continue;
+            const bool more = i + 2 < count;
+            const uint32_t parity = p_count[x]++ & 1;
+            const uint32_t bar = lane == 0 ? bar_p + 8 * x : lane == 1 ? full(2 * i + 1) : lane == 2 && more ? full(2 * i + 4) : 0u;
+            if (!(ok = wait_lanes(bar, lane == 0 ? parity : lane == 1 ? full_parity(2 * i + 1) : full_parity(2 * i + 4)))) continue;
+            o_half(x, i, 0);
+            if (!(ok = wait_lanes(lane == 0 ? bar_p2 + 8 * x : 0u, parity))) continue;
+            o_half(x, i, 1);
+            if (more)
+              s_product(x, i + 2);
+            else
+              commit_elected(bar_o + 8 * x);
+            release(2 * i + 1);
+          }
+        }
+        n0 += 2 * count;
+        seg = seg_end;
+        if (seg < t1) w.next(a);
+      }
+      if (*abort) {   // let what is issued finish before the TMEM is freed
+        __syncwarp();
+        commit_elected(bar_drain);
+        (void)wait_bounded(bar_drain, 0);
+      }
+      // the commits to the empty barriers arrive before the CTA goes
+      for (uint32_t k = n0 < S::kSlots ? 0 : n0 - S::kSlots; ok && k < n0; ++k)
+        ok = wait(bar_empty + 8 * (k % S::kSlots), (k / S::kSlots) & 1);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(512) : "memory");
+  }
+}
+
+template <int HD>
+cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
+  using S = Shape<HD>;
+  static_assert(S::kSmem <= 227 * 1024, "shared memory");
+  int blocks = 0;
+  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_wide_kernel<HD>), kThreads, S::kSmem,
+                                      kMaxCtas, &blocks);
+  if (err != cudaSuccess) return err;
+  place_workspace(a, workspace, kMaxCtas, kRows);
+  cache_attention_wide_kernel<HD><<<blocks, kThreads, S::kSmem, stream>>>(a);
+  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
+  return launch_join<HD, kRows, kKeys>(a, blocks, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_attention_wide(const cached::Args& a, uint8_t* workspace, cudaStream_t stream) {
+  return a.cache.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
+}
+
+cudaError_t cache_attention_wide_error_flag(int* flag) {
+  int zero = 0;
+  cudaError_t err = cudaMemcpyFromSymbol(flag, g_wide_fault, sizeof(int));
+  if (err == cudaSuccess) err = cudaMemcpyToSymbol(g_wide_fault, &zero, sizeof(int));
+  return err;
+}
+
+}  // namespace h3q

@@ -67,6 +67,23 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// The same for a role among others of a CTA: gives up too when another has raised *abort; one
+// that runs out of time raises it, and *fault.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort, int* fault) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t start = now_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0) {
+      if (*abort) return false;
+      if (now_ns() - start > kWaitNs) break;
+    }
+  }
+  *abort = 1;
+  atomicExch(fault, 1);
+  return false;
+}
+
 // 1-D bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
 // from global to shared memory, completing on the barrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {

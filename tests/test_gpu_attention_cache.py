@@ -106,6 +106,11 @@ CASES = [  # sequences, query heads, key heads, dim, page
     ([(7, 200), (16, 16)], 6, 2, 256, 32),
     ([(1, 70000)], 8, 1, 128, 64),
     ([(1, 40000), (1, 1), (3, 30000)], 32, 8, 64, 128),
+    ([(9, 9), (16, 800), (12, 129), (1, 5000)], 32, 8, 128, 64),      # 36 to 64 rows a key head
+    ([(33, 300), (64, 4000), (2, 2)], 10, 2, 128, 16),                # 320 rows: three row tiles
+    ([(40, 20000)], 2, 1, 64, 32),
+    ([(1, 700), (1, 128), (1, 129), (1, 255), (1, 257)], 128, 2, 128, 128),   # 64 query heads a key head
+    ([(3, 10), (5, 140), (0, 9), (64, 64)], 24, 2, 64, 16),
 ]
 
 
