@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       mbar_init(bar_raw + 8 * i, 1);
       mbar_init(bar_used + 8 * i, 4);
     }
-    mbar_init(bar_q, 128);
+    mbar_init(bar_q, 256);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar_s + 8 * i, 1);
       mbar_init(bar_p + 8 * i, 128);
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     const uint32_t taddr = lane_base + x * kKeys, taddr_o = lane_base + S::kO + x * HD;
     float* join = reinterpret_cast<float*>(smem + S::kOffJoin) + row;          // [column][row]
     float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl) + row;
-    float* factor = reinterpret_cast<float*>(smem + S::kOffFactor) + row;
+    float* factors = reinterpret_cast<float*>(smem + S::kOffFactor);
     const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
     const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
     auto sync_both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
@@ -216,39 +216,48 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       const int kv_head = w.group / w.s.row_tiles, row_tile = w.group - kv_head * w.s.row_tiles;
       const int rho = row_tile * kRows + row;
       const bool valid = rho < w.s.n * a.group;
+      const bool rows = rho - lane < w.s.n * a.group;   // any of the warp's
       const int tok = rho / a.group, head = kv_head * a.group + rho - tok * a.group;
       const uint64_t mask = !valid ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[w.s.row0 + tok])
                                                            : ~uint64_t{0} >> (63 - tok);
-      if (x == 0) {
-        // the row's query, scaled, in fp16: rows of 128 bytes, their 16-byte pieces swizzled
-        const uint16_t* src = a.q + (w.s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD;
-        uint32_t m = 0;
-        uint32_t q[HD / 2];
+      {
+        // the rows' queries, scaled, in fp16: rows of 128 bytes, their 16-byte pieces swizzled; a
+        // row's lanes are side by side
+        constexpr int kLanes = HD / 8, kStep = 32 / kLanes;   // lanes a row, rows a step of a warp
+        const int col = lane % kLanes;
+        uint4 q[16 / kStep];
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) v = load16_reused(src + 8 * i);
-          q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
+        for (int i = 0; i < 16 / kStep; ++i) {
+          const int r = row_tile * kRows + warp * 16 + i * kStep + lane / kLanes;
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (r < w.s.n * a.group) {
+            const int t = r / a.group, hd = kv_head * a.group + r - t * a.group;
+            q[i] = load16_reused(a.q + (w.s.row0 + t) * a.ld_q + static_cast<int64_t>(hd) * HD + col * 8);
+          }
         }
-        m = magnitude_bits(q);
-        const float f = query_factor(m);
-        *factor = __fdiv_rn(1.0f, f);
 #pragma unroll
-        for (int i = 0; i < HD / 8; ++i) {
+        for (int i = 0; i < 16 / kStep; ++i) {
+          const int r = warp * 16 + i * kStep + lane / kLanes;
+          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          uint32_t m = magnitude_bits(words);
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const float f = query_factor(m);
+          if (col == 0) factors[r] = __fdiv_rn(1.0f, f);
           uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 v = bf16x2_to_float2(q[4 * i + k]);
+            const float2 v = bf16x2_to_float2(words[k]);
             h[k] = half2_of(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
           }
-          *reinterpret_cast<uint4*>(smem + (i / 8) * (kRows * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(smem + (col / 8) * (kRows * 128) + r * 128 + (((col % 8) ^ (r & 7)) << 4)) =
               make_uint4(h[0], h[1], h[2], h[3]);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read them
         mbar_arrive(bar_q);
       }
       sync_both();
-      const float c = fmaxf(__fmul_rn(k_factor, *factor), 0x1p-126f);   // never 0: a hidden key's -inf stays one
+      const float c = fmaxf(__fmul_rn(k_factor, factors[row]), 0x1p-126f);   // never 0: a hidden key's -inf stays one
       float m_ref = -INFINITY, m_seen = -INFINITY, l = 0.0f;
       // Move the reference to the maximum seen, where that has grown: scale the sum and O.
       auto rescale = [&](bool any_o) {
@@ -273,6 +282,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       for (int i = x; i < count && ok; i += 2) {
         if (!(ok = wait(bar_s + 8 * x, s_count & 1))) break;
         ++s_count;
+        if (!rows) {   // no row of this warp exists: its weights are nobody's
+          mbar_arrive(bar_p + 8 * x);
+          mbar_arrive(bar_p2 + 8 * x);
+          continue;
+        }
         tc_fence_after();   // S was issued after the product before it of this stream: O is at rest
         const int64_t key0 = (seg + i - w.begin) * kKeys;
         const bool masked = w.s.ctx - key0 < kKeys || w.s.len - key0 < kKeys;
@@ -373,11 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       for (int i = 0; i < HD; i += 32) {
         uint32_t o[32];
         __syncwarp();
-        if (x == 0 || two) {
+        if (rows && (x == 0 || two)) {
           tc_load32(taddr_o + i, o);
           tc_wait_load(o);
         }
-        if (x == 1 && two) {
+        if (rows && x == 1 && two) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) join[k * kRows] = __uint_as_float(o[k]);
         }
@@ -442,19 +456,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         const uint8_t* codes = smem + S::kOffRaw + raw * S::kRawBytes;
         const uint8_t* scales = codes + S::kCodeBytes;
         uint8_t* tile = smem + S::kOffTiles + slot * S::kTileBytes + half * (kKeys * 128);
+        const int row0 = (warp - kConvertWarp0) * 32 + row_in;
+        uint4 c4[kRowLanes];
+        uint32_t sc[kRowLanes];
+#pragma unroll
+        for (int i = 0; i < kRowLanes; ++i) {   // all loads before the first store
+          const int row = row0 + i * kStepRows;
+          c4[i] = *reinterpret_cast<const uint4*>(codes + row * (HD / 2) + part * 16);
+          sc[i] = *reinterpret_cast<const uint16_t*>(scales + row * (HD / 16) + part * 2);
+        }
 #pragma unroll
         for (int i = 0; i < kRowLanes; ++i) {
-          const int row = (warp - kConvertWarp0) * 32 + i * kStepRows + row_in;
-          const uint4 c4 = *reinterpret_cast<const uint4*>(codes + row * (HD / 2) + part * 16);
-          const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + row * (HD / 16) + part * 2);
-          uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
-          uint32_t f[2] = {scale_half(sc) * 0x10001u, scale_half(sc >> 8) * 0x10001u};
+          const int row = row0 + i * kStepRows;
+          uint32_t cw[4] = {c4[i].x, c4[i].y, c4[i].z, c4[i].w};
+          uint32_t f[2] = {scale_half(sc[i]) * 0x10001u, scale_half(sc[i] >> 8) * 0x10001u};
           const int flip = half * 2;
           if (half) {
-            cw[0] = c4.z, cw[1] = c4.w, cw[2] = c4.x, cw[3] = c4.y;
+            cw[0] = c4[i].z, cw[1] = c4[i].w, cw[2] = c4[i].x, cw[3] = c4[i].y;
             const uint32_t f0 = f[0];
             f[0] = f[1], f[1] = f0;
           }
+          uint8_t* dst = tile + row * 128;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t h[4];
@@ -462,13 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = hmul2(h[e], f[k >> 1]);
             const int piece = (part & 1) * 4 + (k ^ flip);
-            *reinterpret_cast<uint4*>(tile + row * 128 + ((piece ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + ((piece ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it
-        mbar_arrive(bar_full + 8 * slot);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_used + 8 * raw);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the products read it
+        mbar_arrive(bar_full + 8 * slot);
       }
       if (!ok) break;
     }
@@ -587,16 +609,19 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
             if (!ok || i >= count) continue;
             const bool more = i + 2 < count;
             const uint32_t parity = p_count[x]++ & 1;
-            const uint32_t bar = lane == 0 ? bar_p + 8 * x : lane == 1 ? full(2 * i + 1) : lane == 2 && more ? full(2 * i + 4) : 0u;
-            if (!(ok = wait_lanes(bar, lane == 0 ? parity : lane == 1 ? full_parity(2 * i + 1) : full_parity(2 * i + 4)))) continue;
+            if (!(ok = wait_lanes(lane == 0 ? bar_p + 8 * x : lane == 1 ? full(2 * i + 1) : 0u,
+                                  lane == 0 ? parity : full_parity(2 * i + 1))))
+              continue;
             o_half(x, i, 0);
             if (!(ok = wait_lanes(lane == 0 ? bar_p2 + 8 * x : 0u, parity))) continue;
             o_half(x, i, 1);
-            if (more)
+            release(2 * i + 1);   // (its successor is converted before K[i + 2]'s)
+            if (more) {
+              if (!(ok = wait_lanes(lane == 0 ? full(2 * i + 4) : 0u, full_parity(2 * i + 4)))) continue;
               s_product(x, i + 2);
-            else
+            } else {
               commit_elected(bar_o + 8 * x);
-            release(2 * i + 1);
+            }
           }
         }
         n0 += 2 * count;
