@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         }
       }
       if (t == 0) {   // (several warps may write the same values)
-        row_factor[rho] = __fdiv_rn(1.0f, f);
+        row_factor[rho] = inverse_power(f);
         row_mask[rho] = rho >= live_rows    ? 0
                         : a.mask != nullptr ? static_cast<uint64_t>(a.mask[s.row0 + tok])
                                             : ~uint64_t{0} >> (63 - tok);

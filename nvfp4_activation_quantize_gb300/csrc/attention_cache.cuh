@@ -110,6 +110,12 @@ __device__ __forceinline__ float query_factor(uint32_t m) {
   return __uint_as_float(static_cast<uint32_t>(fe) << 23);
 }
 
+// 1 / f of a power of two f in [2^-126, 2^127].
+__device__ __forceinline__ float inverse_power(float f) {
+  const uint32_t e = __float_as_uint(f) >> 23;
+  return __uint_as_float(e == 254 ? 0x00400000u : (254u - e) << 23);
+}
+
 // Largest magnitude (bits) of two bf16 pairs' worth of words, folded into m; all ones in an exponent win.
 template <int N>
 __device__ __forceinline__ uint32_t magnitude_bits(const uint32_t (&w)[N]) {

@@ -224,26 +224,36 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         // the rows' queries, scaled, in fp16: rows of 128 bytes, their 16-byte pieces swizzled; a
         // row's lanes are side by side
         constexpr int kLanes = HD / 8, kStep = 32 / kLanes;   // lanes a row, rows a step of a warp
-        const int col = lane % kLanes;
-        uint4 q[16 / kStep];
+        constexpr int kSteps = 16 / kStep;
+        const int col = lane % kLanes, r0 = warp * 16 + lane / kLanes;
+        uint4 q[kSteps];
+        uint32_t m[kSteps];
+        {
+          int t = (row_tile * kRows + r0) / a.group;
+          int h = row_tile * kRows + r0 - t * a.group;
 #pragma unroll
-        for (int i = 0; i < 16 / kStep; ++i) {
-          const int r = row_tile * kRows + warp * 16 + i * kStep + lane / kLanes;
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (r < w.s.n * a.group) {
-            const int t = r / a.group, hd = kv_head * a.group + r - t * a.group;
-            q[i] = load16_reused(a.q + (w.s.row0 + t) * a.ld_q + static_cast<int64_t>(hd) * HD + col * 8);
+          for (int i = 0; i < kSteps; ++i) {
+            q[i] = make_uint4(0, 0, 0, 0);
+            if (t < w.s.n)
+              q[i] = load16_reused(a.q + (w.s.row0 + t) * a.ld_q + static_cast<int64_t>(kv_head * a.group + h) * HD + col * 8);
+            for (h += kStep; h >= a.group; h -= a.group) ++t;
           }
         }
 #pragma unroll
-        for (int i = 0; i < 16 / kStep; ++i) {
-          const int r = warp * 16 + i * kStep + lane / kLanes;
+        for (int i = 0; i < kSteps; ++i) {
           const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-          uint32_t m = magnitude_bits(words);
+          m[i] = magnitude_bits(words);
+        }
 #pragma unroll
-          for (int o = kLanes / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const float f = query_factor(m);
-          if (col == 0) factors[r] = __fdiv_rn(1.0f, f);
+        for (int o = kLanes / 2; o >= 1; o >>= 1)
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          const uint32_t words[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+          const int r = r0 + i * kStep;
+          const float f = query_factor(m[i]);
+          if (col == 0) factors[r] = inverse_power(f);
           uint32_t h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
