@@ -47,7 +47,9 @@ namespace {
 using namespace cached;
 
 constexpr int kWarps = 4;                        // that compute; one more copies
-constexpr int kMaxWarps = 8;
+constexpr int kGroupCost = 1;                    // the time of a group's start and end, in tiles
+constexpr float kInShift = 6.0f;                 // weights are held as 2^6 e^(x - reference)
+constexpr float kSlack = 8.0f;                   // how far (log2) a maximum may pass its reference
 
 __device__ int g_cache_attention_fault;
 
@@ -113,9 +115,7 @@ template <int HD, int NT>
 __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas) cache_attention_kernel(const Args a) {
   using S = Shape<HD, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t scratch[kMaxWarps];
-  __shared__ int64_t found_base;
-  __shared__ int found_b;
+  __shared__ PlanScratch<S::kThreads / 32> scratch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bar_full = smem_u32(smem + S::kOffBar);   // + 8 * slot
   const uint32_t bar_empty = bar_full + 8 * S::kSlots;
@@ -129,38 +129,8 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     *abort = 0;
     mbar_init_fence();
   }
-  // ---- the plan: all tiles counted, this CTA's range found
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.at.batch; b0 += S::kThreads) {
-    const int b = b0 + threadIdx.x;
-    int64_t prefix;
-    total += block_scan<S::kThreads / 32>(b < a.at.batch ? tiles_of(sequence(a, b, S::kRows, S::kKeys)) : 0, scratch, &prefix);
-  }
-  const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ctas) {
-    if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
-    return;
-  }
-  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
-  {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.at.batch && base <= t0; b0 += S::kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, S::kRows, S::kKeys)) : 0;
-      int64_t prefix;
-      const int64_t sum = block_scan<S::kThreads / 32>(mine, scratch, &prefix);
-      if (base + prefix <= t0 && t0 < base + prefix + mine) {
-        found_b = b;
-        found_base = base + prefix;
-      }
-      base += sum;
-    }
-    __syncthreads();
-  }
-  int b = found_b;
-  Seq s = sequence(a, b, S::kRows, S::kKeys);
-  int group = static_cast<int>((t0 - found_base) / s.tiles);   // (key head, row tile) of the sequence
-  int64_t begin = found_base + static_cast<int64_t>(group) * s.tiles;   // its first tile
+  Range r;
+  if (!plan<S::kThreads / 32, kGroupCost>(a, S::kRows, S::kKeys, scratch, r)) return;
 
   if (warp >= kWarps) {
     if constexpr (S::kSplit) {
@@ -177,36 +147,23 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     const int per = what ? HD / 16 : HD / 2;   // bytes a key
     const uint32_t dst_off = (what ? S::kCodeBytes : 0) + piece * piece_keys * per;
     const uint32_t slots = smem_u32(smem);
-    int tile = static_cast<int>(t0 - begin);
     auto page_number = [&]() -> int {   // of this lane's piece of the tile, -1 for none
-      const int64_t pos = static_cast<int64_t>(tile) * S::kKeys + piece * piece_keys;
-      if (piece >= pieces || pos >= s.len) return -1;
-      const int64_t p = a.at.table[b * a.at.max_pages + (pos >> page_shift)];
+      const int64_t pos = static_cast<int64_t>(r.tile) * S::kKeys + piece * piece_keys;
+      if (piece >= pieces || pos >= r.s.len) return -1;
+      const int64_t p = a.at.table[r.b * a.at.max_pages + (pos >> page_shift)];
       return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
     };
-    int kv_head = group / s.row_tiles;
     int page = page_number();
     uint32_t n = 0;   // slots filled
     bool ok = true;
-    for (int64_t t = t0; t < t1 && ok; ++t) {
-      const int64_t in_page = (static_cast<int64_t>(tile) * S::kKeys + piece * piece_keys) & (page_keys - 1);
-      const int64_t row = ((static_cast<int64_t>(page) * a.cache.kv_heads + kv_head) << page_shift) + in_page;
+    while (r.count > 0 && ok) {
+      const int64_t in_page = (static_cast<int64_t>(r.tile) * S::kKeys + piece * piece_keys) & (page_keys - 1);
+      const int64_t row = ((static_cast<int64_t>(page) * a.cache.kv_heads + r.kv_head()) << page_shift) + in_page;
       const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
       const bool mine = page >= 0;
       // the next tile's pages, before this one's slots are waited for
-      if (t + 1 < t1) {
-        if (++tile == s.tiles) {
-          tile = 0;
-          if (++group == s.groups) {
-            group = 0;
-            do {
-              s = sequence(a, ++b, S::kRows, S::kKeys);
-            } while (s.groups == 0);
-          }
-          kv_head = group / s.row_tiles;
-        }
-        page = page_number();
-      }
+      r.advance(a, 1, S::kRows, S::kKeys);
+      if (r.count > 0) page = page_number();
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         const uint32_t slot = n % S::kSlots, bar = bar_full + 8 * slot;
@@ -239,46 +196,28 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
   float* row_factor = reinterpret_cast<float*>(smem + S::kOffFactor);
   const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
   const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
-  if (threadIdx.x == 0) {
-    Cut c;
-    c.begin = begin;
-    c.end = begin + s.tiles;
-    c.total = total;
-    c.ctas = ctas;
-    c.b = b;
-    c.kv_head = group / s.row_tiles;
-    c.row_tile = group % s.row_tiles;
-    c.valid = t0 > begin && total * (blockIdx.x - 1) / ctas <= begin;   // blockIdx.x > 0 where t0 > begin
-    c.pad = 0;
-    a.cut[blockIdx.x] = c;
-  }
-  uint32_t n = 0;        // slots taken
+  uint32_t slot = 0, parity = 0;   // of the slot that is taken next
   bool alive = true;     // false: a wait ran out; the rest is computed from whatever is there
-  auto take = [&]() {    // the next slot, once it is full
-    const uint32_t slot = n % S::kSlots;
-    if (alive && !__all_sync(0xffffffffu, *abort == 0 && wait_bounded(bar_full + 8 * slot, (n / S::kSlots) & 1))) {
-      alive = false;
-      if (lane == 0) {
-        *abort = 1;
-        atomicExch(&g_cache_attention_fault, 1);
-      }
-    }
+  auto take = [&]() {    // the slot, once it is full
+    const uint32_t bar = bar_full + 8 * slot;
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) && alive)
+      alive = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_cache_attention_fault));
     return smem + slot * S::kSlotBytes;
   };
   auto give = [&]() {    // every lane has read it
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * (n % S::kSlots));
-    ++n;
+    if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
+    if (++slot == S::kSlots) slot = 0, parity ^= 1u;
   };
 
   // the segments of the range: the part of each group that lies in it
   bool first_segment = true;
-  int64_t tile0 = t0;
-  while (true) {
-    const int64_t seg_end = begin + s.tiles < t1 ? begin + s.tiles : t1;
-    const bool whole = begin >= t0 && begin + s.tiles <= t1;
-    const int kv_head = group / s.row_tiles;
-    const int row_tile = group - kv_head * s.row_tiles;
+  while (r.count > 0) {
+    const Seq& s = r.s;
+    const int count = r.here(), seg_end = r.tile + count;
+    const bool whole = r.tile == 0 && count == s.tiles;
+    const int kv_head = r.kv_head();
+    const int row_tile = r.group - kv_head * s.row_tiles;
     const int tile_row0 = row_tile * S::kRows;
     const int live_rows = s.n * a.group - tile_row0;   // rows of the tile that exist (may be more than it holds)
 
@@ -341,10 +280,11 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
       for (int i = 0; i < S::kSteps; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.0f;
     }
 
-    for (; tile0 < seg_end; ++tile0) {
+    const uint32_t seen_by_all = s.ctx < 0 ? 0 : min(s.ctx, s.len);
+    for (int tile = r.tile; tile < seg_end; ++tile) {
       // this warp's keys of the tile; -1: none of them is in the sequence
-      const int64_t first_key = (tile0 - begin) * S::kKeys + warp * S::kWarpKeys;
-      const bool work = first_key < s.len;
+      const uint32_t first_key = static_cast<uint32_t>(tile) * S::kKeys + warp * S::kWarpKeys;
+      const bool work = first_key < static_cast<uint32_t>(s.len);
       // Scores and weights of all the warp's keys (kept as the right operand of the second
       // product), 16 * kMt keys at a time.
       uint32_t pf[S::kWarpKeys / 16][NT][2];
@@ -354,7 +294,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         kc += warp * S::kWarpKeys * (HD / 2);
 #pragma unroll
         for (int sub = 0; sub < S::kWarpKeys / 16; sub += S::kMt) {
-          const int64_t key0 = first_key + 16 * sub;
+          const uint32_t key0 = first_key + 16 * sub;
           // S^T: rows of the left operand are keys 4 (g / 2) + g % 2 and that + 2, so that the
           // values' operand below finds its four keys 4t .. 4t + 3 side by side
           float sc[S::kMt][NT][4];
@@ -408,14 +348,14 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
           }
 
           // keys that a row does not see
-          if (key0 + 16 * S::kMt > s.ctx || key0 + 16 * S::kMt > s.len) {
+          if (key0 + 16 * S::kMt > seen_by_all) {
 #pragma unroll
             for (int mt = 0; mt < S::kMt; ++mt)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const int64_t key = key0 + mt * 16 + 4 * (g >> 1) + (g & 1) + (i & 2);
+                  const int64_t key = static_cast<int64_t>(key0) + mt * 16 + 4 * (g >> 1) + (g & 1) + (i & 2);
                   const int64_t draft = key - s.ctx;
                   const uint64_t bits = row_mask[nt * 8 + 2 * t + (i & 1)];
                   const bool seen = key < s.len && (draft < 0 || (draft < 64 && ((bits >> draft) & 1)));
@@ -426,36 +366,27 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
           // running maximum and sum, and the weights
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float alpha[2], base[2];
+            float top[2];   // of the lane's keys, in units of log2
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               float m = fmaxf(sc[0][nt][i], sc[0][nt][i + 2]);
 #pragma unroll
-              for (int mt = 1; mt < S::kMt; ++mt) m = fmaxf(m, fmaxf(sc[mt][nt][i], sc[mt][nt][i + 2]));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              m = fmaxf(m_run[nt][i], m == -INFINITY ? -INFINITY : __fmul_rn(m, cf[nt][i]));
-              const float use = m == -INFINITY ? 0.0f : m;
-              alpha[i] = ex2(__fadd_rn(m_run[nt][i], -use));
-              base[i] = __fadd_rn(kPShift, -use);
-              m_run[nt][i] = m;
+              for (int mt = 1; mt < S::kMt; ++mt) m = max3(m, sc[mt][nt][i], sc[mt][nt][i + 2]);
+              top[i] = __fmul_rn(m, cf[nt][i]);
             }
-            float add[2] = {0.0f, 0.0f};
+            if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] + kSlack || top[1] > m_run[nt][1] + kSlack)) {
+              float alpha[2];
 #pragma unroll
-            for (int mt = 0; mt < S::kMt; ++mt) {
-              float p[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                p[i] = ex2(__fmaf_rn(sc[mt][nt][i], cf[nt][i & 1], base[i & 1]));
-                add[i & 1] = __fadd_rn(add[i & 1], p[i]);
+              for (int i = 0; i < 2; ++i) {
+                float m = top[i];
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                m = fmaxf(m_run[nt][i], m);
+                alpha[i] = ex2(__fadd_rn(m_run[nt][i], m == -INFINITY ? 0.0f : -m));
+                l_run[nt][i] = __fmul_rn(l_run[nt][i], alpha[i]);
+                m_run[nt][i] = m;
               }
-              pf[sub + mt][nt][0] = transpose8x8(half2_of(p[0], p[1]));
-              pf[sub + mt][nt][1] = transpose8x8(half2_of(p[2], p[3]));
-            }
-            l_run[nt][0] = __fmaf_rn(l_run[nt][0], alpha[0], add[0]);
-            l_run[nt][1] = __fmaf_rn(l_run[nt][1], alpha[1], add[1]);
-            if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
               if constexpr (S::kMt * 16 < S::kWarpKeys) {   // weights of this tile that were formed before
                 const uint32_t other = half2_of(__shfl_sync(0xffffffffu, alpha[0], g >> 1),
                                                 __shfl_sync(0xffffffffu, alpha[1], g >> 1));
@@ -474,6 +405,23 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
                 acc[nt][i][3] = __fmul_rn(acc[nt][i][3], alpha[1]);
               }
             }
+            const float2 c2 = make_float2(cf[nt][0], cf[nt][1]);
+            const float2 b2 = make_float2(__fadd_rn(kInShift, m_run[nt][0] == -INFINITY ? 0.0f : -m_run[nt][0]),
+                                          __fadd_rn(kInShift, m_run[nt][1] == -INFINITY ? 0.0f : -m_run[nt][1]));
+            float2 add = make_float2(l_run[nt][0], l_run[nt][1]);
+#pragma unroll
+            for (int mt = 0; mt < S::kMt; ++mt) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float2 p = fma2(make_float2(sc[mt][nt][2 * i], sc[mt][nt][2 * i + 1]), c2, b2);
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                add = add2(add, p);
+                pf[sub + mt][nt][i] = transpose8x8(half2_of(p.x, p.y));
+              }
+            }
+            l_run[nt][0] = add.x;
+            l_run[nt][1] = add.y;
           }
         }
       }
@@ -566,7 +514,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             const float2 ml = join_ml[w * 8 + row];
-            const float f = ex2(__fadd_rn(ml.x, -use));
+            const float f = ex2(__fadd_rn(__fadd_rn(ml.x, -use), kPShift - kInShift));
             l = __fmaf_rn(ml.y, f, l);
 #pragma unroll
             for (int i = 0; i < kPer; i += 4) {
@@ -609,16 +557,8 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
       }
       sync_compute();
     }
-    // ---- the next group
     first_segment = false;
-    begin += s.tiles;
-    if (begin >= t1) break;
-    if (++group >= s.groups) {
-      group = 0;
-      do {
-        s = sequence(a, ++b, S::kRows, S::kKeys);
-      } while (s.groups == 0);
-    }
+    r.advance(a, count, S::kRows, S::kKeys);
   }
 }
 

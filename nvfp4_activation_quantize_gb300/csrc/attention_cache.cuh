@@ -21,7 +21,8 @@ namespace h3q {
 namespace cached {
 
 constexpr float kPShift = 14.0f;  // parts and sums hold 2^14 * e^(x - m)
-constexpr int kMergeWarps = 4;    // rows per CTA of the joining kernel
+constexpr int kMergeWarps = 4;    // of a CTA of the joining kernel
+constexpr int kMergeRows = 4;     // that it joins, a warp each in the end
 
 struct Args {
   PagedCache cache;
@@ -45,8 +46,8 @@ struct Args {
 // What the joining kernel needs to know of the group that the start of a CTA's range cuts:
 // written by that CTA; valid for the first range's start inside the group.
 struct Cut {
-  int64_t begin, end;      // the group's tiles
-  int64_t total;           // all tiles
+  int64_t begin, end;      // the group, in units of work
+  int64_t total;           // of all groups
   int valid, ctas;
   int b, kv_head, row_tile, pad;
 };
@@ -152,68 +153,209 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
   return total;
 }
 
-// Joins the parts of the groups that the ranges' starts cut: CTA (c, r) takes the group
-// that the start of range c is the first to cut, a warp each of its rows.
+// The tiles of sequence s that lie before its unit x of work (a group is `cost` units, then its tiles).
+__device__ __forceinline__ int64_t tiles_before(const Seq& s, int cost, int64_t x) {
+  const int64_t unit = s.tiles + cost;
+  if (x <= 0) return 0;
+  if (x >= unit * s.groups) return tiles_of(s);
+  const int64_t q = x / unit, r = x - q * unit - cost;
+  return q * s.tiles + (r > 0 ? r : 0);
+}
+
+// A CTA's part of the work: `count` tiles, from tile `tile` of a group of sequence b on.
+struct Range {
+  Seq s;
+  int b, group, tile;
+  int count;               // (2^31 tiles would be minutes)
+  __device__ __forceinline__ int kv_head() const { return group / s.row_tiles; }
+  // tiles of the group that are in the range
+  __device__ __forceinline__ int here() const {
+    return min(count, s.tiles - tile);
+  }
+  // On by n tiles, at most to the end of the group.
+  __device__ __forceinline__ void advance(const Args& a, int n, int tile_rows, int tile_keys) {
+    count -= n;
+    tile += n;
+    if (tile < s.tiles || count == 0) return;
+    tile = 0;
+    if (++group < s.groups) return;
+    group = 0;
+    do {
+      s = sequence(a, ++b, tile_rows, tile_keys);
+    } while (s.groups == 0);
+  }
+};
+
+template <int WARPS>
+struct PlanScratch {
+  int64_t scan[WARPS];
+  int64_t base;
+  int b;
+};
+
+// The range of this CTA, and its entry of a.cut; false for one that has nothing to do.  The work is
+// counted in tiles, and COST more for each group (its queries, its join, its output): equal counts
+// are equal times whether a range is one long group or many short ones.  Where there are no more
+// tiles than CTAs each takes one.  The whole CTA calls it.
+template <int WARPS, int COST>
+__device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys, PlanScratch<WARPS>& sh, Range& r) {
+  int64_t tiles = 0, groups = 0, prefix;
+  for (int b0 = 0; b0 < a.at.batch; b0 += WARPS * 32) {
+    const int b = b0 + threadIdx.x;
+    int64_t t = 0, g = 0;
+    if (b < a.at.batch) {
+      const Seq s = sequence(a, b, tile_rows, tile_keys);
+      t = tiles_of(s);
+      g = s.groups;
+    }
+    tiles += block_scan<WARPS>(t, sh.scan, &prefix);
+    groups += block_scan<WARPS>(g, sh.scan, &prefix);
+  }
+  const int cost = tiles <= gridDim.x ? 0 : COST;
+  const int64_t total = tiles + cost * groups;
+  const int64_t most = total / (cost + 1);   // (a range has a tile: it is longer than cost)
+  const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
+    return false;
+  }
+  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
+  int64_t base = 0;
+  int64_t count = 0;
+  for (int b0 = 0; b0 < a.at.batch && base < t1; b0 += WARPS * 32) {
+    const int b = b0 + threadIdx.x;
+    int64_t mine = 0;
+    Seq s;
+    if (b < a.at.batch) {
+      s = sequence(a, b, tile_rows, tile_keys);
+      mine = tiles_of(s) + static_cast<int64_t>(cost) * s.groups;
+    }
+    const int64_t sum = block_scan<WARPS>(mine, sh.scan, &prefix);
+    const int64_t at = base + prefix;
+    if (at <= t0 && t0 < at + mine) {
+      sh.b = b;
+      sh.base = at;
+    }
+    const int64_t part = mine == 0 ? 0 : tiles_before(s, cost, t1 - at) - tiles_before(s, cost, t0 - at);
+    count += block_scan<WARPS>(part, sh.scan, &prefix);   // (its barriers publish sh.b and sh.base too)
+    base += sum;
+  }
+  r.count = static_cast<int>(count);
+  r.b = sh.b;
+  r.s = sequence(a, r.b, tile_rows, tile_keys);
+  const int64_t unit = r.s.tiles + cost;
+  r.group = static_cast<int>((t0 - sh.base) / unit);
+  const int64_t begin = sh.base + r.group * unit;
+  r.tile = t0 - begin > cost ? static_cast<int>(t0 - begin) - cost : 0;
+  if (threadIdx.x == 0) {
+    Cut c;
+    c.begin = begin;
+    c.end = begin + unit;
+    c.total = total;
+    c.ctas = ctas;
+    c.b = r.b;
+    c.kv_head = r.kv_head();
+    c.row_tile = r.group % r.s.row_tiles;
+    c.valid = r.tile > 0 && total * (blockIdx.x - 1) / ctas <= begin + cost;   // blockIdx.x > 0 where tile > 0
+    c.pad = 0;
+    a.cut[blockIdx.x] = c;
+  }
+  return true;
+}
+
+// Joins the parts of the groups that the ranges' starts cut: CTA (c, r) takes kMergeRows rows of
+// the group that the start of range c is the first to cut.  Its warps take the parts in turn
+// (a group of 120,000 keys has 57), and are added up in their order.
 template <int HD, int ROWS, int KEYS>
 __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args a) {
   constexpr int kPer = HD / 32;
+  __shared__ float sum[kMergeWarps][kMergeRows][HD];
+  __shared__ float sum_l[kMergeWarps][kMergeRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are written
   const int c = blockIdx.x + 1;
   const Cut cut = a.cut[c];
   if (!cut.valid) return;
-  const int lane = threadIdx.x & 31;
-  const int rho = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rho0 = blockIdx.y * kMergeRows;
   const Seq s = sequence(a, cut.b, ROWS, KEYS);
-  const int tile_row0 = cut.row_tile * ROWS;
-  if (tile_row0 + rho >= s.n * a.group) return;
+  const int row0 = cut.row_tile * ROWS + rho0;
+  if (row0 >= s.n * a.group) return;
   // the first range's part is its last segment: slot 0 if the range began in this group too
   const int64_t prev0 = cut.total * (c - 1) / cut.ctas;
   const int64_t first = static_cast<int64_t>(c - 1) * 2 + (prev0 >= cut.begin ? 0 : 1);
+  // one past the last range that starts inside the group: total * last / ctas < end
+  const int64_t past = (cut.end * cut.ctas + cut.total - 1) / cut.total;
+  const int last = static_cast<int>(past < cut.ctas ? past : cut.ctas);
+  auto slot = [&](int k) { return (k == c - 1 ? first : static_cast<int64_t>(k) * 2) * ROWS + rho0; };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
-  int last = c;   // one past the last range that starts inside the group
-  while (last < cut.ctas && cut.total * last / cut.ctas < cut.end) ++last;
-  auto slot = [&](int k) { return (k == c - 1 ? first : static_cast<int64_t>(k) * 2) * ROWS + rho; };
-  float m = -INFINITY;
-  for (int k = c - 1 + lane; k < last; k += 32) m = fmaxf(m, ml[slot(k)].x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float use = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, v[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+  float top = -INFINITY;   // of row lane / 8
 #pragma unroll 4
-  for (int k = c - 1; k < last; ++k) {
-    const float2 x = ml[slot(k)];
-    const float f = x.x == -INFINITY ? 0.0f : ex2(__fadd_rn(x.x, -use));
-    l = __fmaf_rn(x.y, f, l);
-    const float* src = a.part + slot(k) * HD + lane * kPer;
+  for (int k = c - 1 + (lane & 7); k < last; k += 8) top = fmaxf(top, ml[slot(k) + (lane >> 3)].x);
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + i);
-      v[i] = __fmaf_rn(y.x, f, v[i]);
-      v[i + 1] = __fmaf_rn(y.y, f, v[i + 1]);
+  for (int o = 1; o <= 4; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float m[kMergeRows], l[kMergeRows], v[kMergeRows][kPer];
+#pragma unroll
+  for (int r = 0; r < kMergeRows; ++r) {
+    m[r] = __shfl_sync(0xffffffffu, top, 8 * r);
+    l[r] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[r][i] = 0.0f;
+  }
+#pragma unroll 2
+  for (int k = c - 1 + warp; k < last; k += kMergeWarps) {
+    const int64_t at = slot(k);
+#pragma unroll
+    for (int r = 0; r < kMergeRows; ++r) {
+      const float2 x = ml[at + r];
+      const float f = x.x == -INFINITY ? 0.0f : ex2(__fadd_rn(x.x, -m[r]));
+      l[r] = __fmaf_rn(x.y, f, l[r]);
+      const float* src = a.part + (at + r) * HD + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + i);
+        v[r][i] = __fmaf_rn(y.x, f, v[r][i]);
+        v[r][i + 1] = __fmaf_rn(y.y, f, v[r][i + 1]);
+      }
     }
   }
-  const int tok = (tile_row0 + rho) / a.group;
-  const int head = cut.kv_head * a.group + (tile_row0 + rho) - tok * a.group;
+#pragma unroll
+  for (int r = 0; r < kMergeRows; ++r) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum[warp][r][lane * kPer + i] = v[r][i];
+    if (lane == 0) sum_l[warp][r] = l[r];
+  }
+  __syncthreads();
+  // a warp a row
+  if (row0 + warp >= s.n * a.group) return;
+  const float mw = __shfl_sync(0xffffffffu, top, 8 * warp);
+  float lw = 0.0f, o[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    lw = __fadd_rn(lw, sum_l[w][warp]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) o[i] = __fadd_rn(o[i], sum[w][warp][lane * kPer + i]);
+  }
+  const int tok = (row0 + warp) / a.group;
+  const int head = cut.kv_head * a.group + (row0 + warp) - tok * a.group;
   const int64_t out_row = s.row0 + tok;
-  const float f = l == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(256.0f, *a.v_gsf), l);
+  const float f = lw == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(256.0f, *a.v_gsf), lw);
   uint16_t* dst = a.o + (out_row * a.heads + head) * HD + lane * kPer;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
     *reinterpret_cast<uint32_t*>(dst + i) =
-        float2_to_bf16x2(make_float2(__fmul_rn(v[i], f), __fmul_rn(v[i + 1], f)));
+        float2_to_bf16x2(make_float2(__fmul_rn(o[i], f), __fmul_rn(o[i + 1], f)));
   if (a.lse != nullptr && lane == 0)
     a.lse[head * a.rows + out_row] =
-        l == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, __fadd_rn(log2f(l), -kPShift)), kLn2);
+        lw == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(mw, __fadd_rn(log2f(lw), -kPShift)), kLn2);
 }
-
 
 // The kernel that joins the parts, after the one before it on the stream.
 template <int HD, int ROWS, int KEYS>
 cudaError_t launch_join(const Args& a, int blocks, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), ROWS / kMergeWarps, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), ROWS / kMergeRows, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -38,6 +38,7 @@ constexpr int kMmaWarp = 13;
 constexpr int kRows = 128;             // rows per tile
 constexpr int kKeys = 128;             // keys per tile
 constexpr int kMaxCtas = 152;          // the workspace holds the parts of so many (608 of 32 rows)
+constexpr int kGroupCost = 6;          // the time of a group's start and end, in tiles
 constexpr float kInShift = 6.0f;       // weights are held as 2^6 e^(x - reference)
 constexpr float kSlack = 8.0f;         // how far (log2) a row's maximum may pass its reference
 
@@ -67,22 +68,6 @@ struct Shape {
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (uint32_t(HD >> 3) << 17) | (8u << 24);
 };
 
-// The groups of a CTA's range one after the other, as every role walks them.
-struct Walk {
-  Seq s;
-  int b, group;
-  int64_t begin;           // the group's first tile
-  __device__ __forceinline__ void next(const Args& a) {
-    begin += s.tiles;
-    if (++group >= s.groups) {
-      group = 0;
-      do {
-        s = sequence(a, ++b, kRows, kKeys);
-      } while (s.groups == 0);
-    }
-  }
-};
-
 __device__ __forceinline__ uint64_t ones(int64_t n) {
   return n <= 0 ? 0 : n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1;
 }
@@ -104,9 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
   using S = Shape<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
-  __shared__ int64_t scratch[kThreads / 32];
-  __shared__ int64_t found_base;
-  __shared__ int found_b;
+  __shared__ PlanScratch<kThreads / 32> scratch;
   const uint32_t base = smem_u32(smem);
   const uint32_t bar_full = base + S::kOffBar;              // + 8 * slot
   const uint32_t bar_empty = bar_full + 8 * S::kSlots;
@@ -142,39 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     *abort = 0;
     mbar_init_fence();
   }
-  // ---- the plan: all tiles counted, this CTA's range found
-  int64_t total = 0;
-  for (int b0 = 0; b0 < a.at.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int64_t prefix;
-    total += block_scan<kThreads / 32>(b < a.at.batch ? tiles_of(sequence(a, b, kRows, kKeys)) : 0, scratch, &prefix);
-  }
-  const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
-  if (static_cast<int>(blockIdx.x) >= ctas) {
-    if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
-    return;
-  }
-  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
-  {
-    int64_t before = 0;
-    for (int b0 = 0; b0 < a.at.batch && before <= t0; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int64_t mine = b < a.at.batch ? tiles_of(sequence(a, b, kRows, kKeys)) : 0;
-      int64_t prefix;
-      const int64_t sum = block_scan<kThreads / 32>(mine, scratch, &prefix);
-      if (before + prefix <= t0 && t0 < before + prefix + mine) {
-        found_b = b;
-        found_base = before + prefix;
-      }
-      before += sum;
-    }
-    __syncthreads();
-  }
-  Walk w;
-  w.b = found_b;
-  w.s = sequence(a, w.b, kRows, kKeys);
-  w.group = static_cast<int>((t0 - found_base) / w.s.tiles);
-  w.begin = found_base + static_cast<int64_t>(w.group) * w.s.tiles;
+  Range w;
+  if (!plan<kThreads / 32, kGroupCost>(a, kRows, kKeys, scratch, w)) return;
 
   auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp: one decision
     return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_wide_fault)));
@@ -194,26 +146,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
     const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
     auto sync_both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    if (threadIdx.x == 0) {
-      Cut cut;
-      cut.begin = w.begin;
-      cut.end = w.begin + w.s.tiles;
-      cut.total = total;
-      cut.ctas = ctas;
-      cut.b = w.b;
-      cut.kv_head = w.group / w.s.row_tiles;
-      cut.row_tile = w.group % w.s.row_tiles;
-      cut.valid = t0 > w.begin && total * (blockIdx.x - 1) / ctas <= w.begin;   // blockIdx.x > 0 where t0 > begin
-      cut.pad = 0;
-      a.cut[blockIdx.x] = cut;
-    }
     bool first_segment = true, ok = true;
     uint32_t s_count = 0, o_count = 0;
-    for (int64_t seg = t0; seg < t1;) {
-      const int64_t seg_end = w.begin + w.s.tiles < t1 ? w.begin + w.s.tiles : t1;
-      const bool whole = seg == w.begin && seg_end == w.begin + w.s.tiles;
-      const int count = static_cast<int>(seg_end - seg);
-      const int kv_head = w.group / w.s.row_tiles, row_tile = w.group - kv_head * w.s.row_tiles;
+    while (w.count > 0) {
+      const int count = w.here();
+      const bool whole = w.tile == 0 && count == w.s.tiles;
+      const int kv_head = w.kv_head(), row_tile = w.group - kv_head * w.s.row_tiles;
       const int rho = row_tile * kRows + row;
       const bool valid = rho < w.s.n * a.group;
       const bool rows = rho - lane < w.s.n * a.group;   // any of the warp's
@@ -289,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         }
         tc_wait_store();
       };
+      const uint32_t seen_by_all = w.s.ctx < 0 ? 0 : min(w.s.ctx, w.s.len);
       for (int i = x; i < count && ok; i += 2) {
         if (!(ok = wait(bar_s + 8 * x, s_count & 1))) break;
         ++s_count;
@@ -298,11 +237,11 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           continue;
         }
         tc_fence_after();   // S was issued after the product before it of this stream: O is at rest
-        const int64_t key0 = (seg + i - w.begin) * kKeys;
-        const bool masked = w.s.ctx - key0 < kKeys || w.s.len - key0 < kKeys;
+        const uint32_t key0 = static_cast<uint32_t>(w.tile + i) * kKeys;
+        const bool masked = key0 + kKeys > seen_by_all;
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked) {   // which of the tile's keys the row sees
-          const int64_t d = w.s.ctx - key0;
+          const int64_t d = w.s.ctx - static_cast<int64_t>(key0);
           uint64_t lo = ones(d), hi = ones(d - 64);
           if (d >= 64 && d < 128) {
             hi |= mask << (d - 64);
@@ -312,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           } else if (d <= 0 && d > -64) {
             lo |= mask >> -d;
           }
-          lo &= ones(w.s.len - key0);
-          hi &= ones(w.s.len - key0 - 64);
+          lo &= ones(w.s.len - static_cast<int64_t>(key0));
+          hi &= ones(w.s.len - static_cast<int64_t>(key0) - 64);
           see[0] = static_cast<uint32_t>(lo), see[1] = static_cast<uint32_t>(lo >> 32);
           see[2] = static_cast<uint32_t>(hi), see[3] = static_cast<uint32_t>(hi >> 32);
         }
@@ -444,8 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       }
       tc_fence_before();   // O has been read before the next segment's first weights are announced
       first_segment = false;
-      seg = seg_end;
-      if (seg < t1) w.next(a);
+      w.advance(a, count, kRows, kKeys);
     }
   } else if (warp < kCopyWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
@@ -456,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     constexpr int kStepRows = 32 / kRowLanes;
     const int part = lane % kRowLanes, row_in = lane / kRowLanes;
     const int half = part >> 1;
-    for (int64_t t = t0, n = 0; t < t1; ++t) {
+    uint32_t n = 0;
+    for (int left = w.count; left > 0; --left) {
       bool ok = true;
 #pragma unroll 1
       for (int v = 0; v < 2; ++v, ++n) {
@@ -514,9 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       const int piece = lane >> 1, what = lane & 1;
       const int per = what ? HD / 16 : HD / 2;   // bytes a key
       const uint32_t dst = base + S::kOffRaw + (what ? S::kCodeBytes : 0) + piece * piece_keys * per;
-      int tile = static_cast<int>(t0 - w.begin);
       auto page_number = [&]() -> int {   // of this lane's piece of the tile, -1 for none
-        const int64_t pos = static_cast<int64_t>(tile) * kKeys + piece * piece_keys;
+        const int64_t pos = static_cast<int64_t>(w.tile) * kKeys + piece * piece_keys;
         if (piece >= pieces || pos >= w.s.len) return -1;
         const int64_t p = a.at.table[w.b * a.at.max_pages + (pos >> page_shift)];
         return p < 0 || p >= a.cache.num_pages ? 0 : static_cast<int>(p);  // any page, so that the read is of the cache
@@ -524,18 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       int page = page_number();
       uint32_t n = 0;
       bool ok = true;
-      for (int64_t t = t0; t < t1 && ok; ++t) {
-        const int kv_head = w.group / w.s.row_tiles;
-        const int64_t row = (static_cast<int64_t>(page) * a.cache.kv_heads + kv_head) << page_shift;
+      while (w.count > 0 && ok) {
+        const int64_t row = (static_cast<int64_t>(page) * a.cache.kv_heads + w.kv_head()) << page_shift;
         const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
         const bool mine = page >= 0;
-        if (t + 1 < t1) {   // the next tile's pages, before this one's slots are waited for
-          if (++tile == w.s.tiles) {
-            tile = 0;
-            w.next(a);
-          }
-          page = page_number();
-        }
+        w.advance(a, 1, kRows, kKeys);   // the next tile's pages, before this one's slots are waited for
+        if (w.count > 0) page = page_number();
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const uint32_t raw = n % S::kRaw, bar = bar_raw + 8 * raw;
@@ -602,9 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         for (int d = half * 4; d < half * 4 + 4; ++d)
           mma_ts(S::kO + x * HD, x * kKeys + 8 * d, v + (d * 2048 >> 4), S::kIdescO, i > 1 || d > 0);
       };
-      for (int64_t seg = t0; seg < t1 && ok;) {
-        const int64_t seg_end = w.begin + w.s.tiles < t1 ? w.begin + w.s.tiles : t1;
-        const int count = uniform(static_cast<int>(seg_end - seg));
+      while (w.count > 0 && ok) {
+        const int count = uniform(w.here());
         ok = wait_lanes(lane == 0 ? bar_q : lane == 1 ? full(0) : lane == 2 && count > 1 ? full(2) : 0u,
                         lane == 0 ? segments & 1 : lane == 1 ? full_parity(0) : full_parity(2));
         ++segments;
@@ -635,8 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           }
         }
         n0 += 2 * count;
-        seg = seg_end;
-        if (seg < t1) w.next(a);
+        w.advance(a, count, kRows, kKeys);
       }
       if (*abort) {   // let what is issued finish before the TMEM is freed
         __syncwarp();
