@@ -264,3 +264,33 @@ def test_given_workspace_of_any_contents(dev):
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     with pytest.raises(ValueError, match="workspace"):
         _run(c, workspace=ws[:-1])
+
+
+@pytest.mark.parametrize("heads, kv_heads, dim, page, new", [(8, 2, 128, 64, 1), (12, 2, 64, 16, 2), (4, 2, 256, 32, 3), (64, 8, 128, 16, 1),
+                                                             (24, 2, 128, 64, 4)])
+def test_more_groups_than_ctas(dev, heads, kv_heads, dim, page, new):
+    """Many short sequences beside a few long ones: ranges of many groups, of one, and ends of ranges in all places."""
+    rng = np.random.default_rng(17)
+    length = [int(n) for n in rng.integers(new, 400, 230)]
+    for b, n in ((3, 17000), (120, 9000), (229, 4000)):
+        length[b] = n
+    c = _case(dev, [(new if b % 7 else 0, n) for b, n in enumerate(length)], heads, kv_heads, dim, page, seed=18)
+    out, lse = _run(c)
+    _check(c, out, lse)
+    again = _run(c)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert h3q.h3q_kernel_error_flag() == 0
+
+
+@pytest.mark.parametrize("gain", [0.01, 4.0, 40.0])
+@pytest.mark.parametrize("heads, kv_heads, dim", [(8, 2, 128), (16, 1, 128), (32, 1, 64), (8, 1, 256), (40, 1, 128)])
+def test_scores_that_grow_along_the_cache(dev, gain, heads, kv_heads, dim):
+    """The running maximum moves a little in each tile, or far: keys whose scales grow with their position."""
+    c = _case(dev, [(1, 2500), (1, 700)], heads, kv_heads, dim, 16, seed=19, gain=gain)
+    scales = c["cache"][1]
+    for b in range(2):
+        n = c["len"][b].item()
+        for i, page in enumerate(c["table"][b, :(n + 15) // 16].tolist()):
+            scales[page] = 8 + min(100, 100 * 16 * i // n)
+    out, lse = _run(c)
+    _check(c, out, lse)
