@@ -28,7 +28,8 @@
 // instead at 44; mma.sync at 1,024 products a clock and SM, a third of it used at NT 1.
 //
 // Work: tiles of 256 keys (128 at head_dim 256) of one (sequence, key head, row tile), in that
-// order, dealt out in equal contiguous ranges to the CTAs of one wave, whatever the lengths.
+// order, dealt out in contiguous ranges to the CTAs of one wave, equal in tiles and one more for
+// each group (without it the CTAs of short sequences came last: 78 us for 64 tokens, not 72).
 // In a CTA one warp copies: the tile's keys, then its values, into a ring of such slots, a
 // copy a lane (a page's codes, its scales), the page numbers looked up a tile ahead.
 // Four warps take 64 keys of each tile, each with its own running maximum, sum and output,
@@ -37,6 +38,13 @@
 // the ranges: no atomics, the same result every time.  (With a ring of 32-key tiles to each
 // warp, four copies of 256 bytes and 2 KB a tile: 103 us for 64 tokens over 4,503 positions
 // each, 68 of them in the copies alone.)
+//
+// A row's weights are taken against a reference that follows its maximum only where that has
+// grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
+//
+// Measured, 32 query heads over 8 key heads of 128: 64 tokens over 500 to 8,191 positions each in
+// 70 us (49 is the bytes' time at the copy rate; 62 with the copies alone, 62 with the
+// arithmetic alone), two tokens over 120,000 to 131,071 in 64 us (44).
 #include <cmath>
 
 #include "attention_cache.cuh"

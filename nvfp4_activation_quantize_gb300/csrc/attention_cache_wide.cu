@@ -22,6 +22,9 @@
 //   warp 12           copies pages of codes and scales into a raw ring, a lane each
 //   warp 13           the products
 // Work is dealt out and joined as in attention_cache.cu, in tiles of 128 keys, one CTA per SM.
+// Measured, 32 query heads over 8 key heads of 128: 16 trees of 9 to 16 tokens (36 to 64 rows a
+// key head) over 1,000 to 8,000 positions in 72 us, where the bytes take 13: a tile of 128 keys
+// takes about 2,400 clocks, the conversion of its keys and values alone 2,000 with its waits.
 // Every wait is bounded: one that runs out sets a device flag and tells the other roles to stop.
 #include "attention_cache.cuh"
 #include "h3q_tcgen05.cuh"
@@ -132,9 +135,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_wide_fault)));
   };
 
-  // Registers: 8 softmax warps 168, 4 converting warps 96, the other four 80 (512 x 128 in all).
+  // Registers: 8 softmax warps 200, 4 converting warps 72, the other four 40 (512 x 128 in all); with 168,
+  // 96 and 80 the scores did not fit, 80 us for 16 trees.
   if (warp < kConvertWarp0) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ---- softmax of one stream
     const int x = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
@@ -155,9 +159,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       const int rho = row_tile * kRows + row;
       const bool valid = rho < w.s.n * a.group;
       const bool rows = rho - lane < w.s.n * a.group;   // any of the warp's
-      const int tok = rho / a.group, head = kv_head * a.group + rho - tok * a.group;
-      const uint64_t mask = !valid ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[w.s.row0 + tok])
-                                                           : ~uint64_t{0} >> (63 - tok);
       {
         // the rows' queries, scaled, in fp16: rows of 128 bytes, their 16-byte pieces swizzled; a
         // row's lanes are side by side
@@ -242,6 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
         if (masked) {   // which of the tile's keys the row sees
           const int64_t d = w.s.ctx - static_cast<int64_t>(key0);
+          const int tok = rho / a.group;
+          const uint64_t mask = !valid ? 0 : a.mask != nullptr ? static_cast<uint64_t>(a.mask[w.s.row0 + tok])
+                                                               : ~uint64_t{0} >> (63 - tok);
           uint64_t lo = ones(d), hi = ones(d - 64);
           if (d >= 64 && d < 128) {
             hi |= mask << (d - 64);
@@ -330,6 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         if (two) l = __fmaf_rn(other.y, f1, l);
       }
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
+      int rho_out = rho;
+      asm volatile("" : "+r"(rho_out));   // (where it goes is formed here, not kept over the tiles)
+      const int tok = rho_out / a.group, head = kv_head * a.group + rho_out - tok * a.group;
       const int64_t out_row = w.s.row0 + tok;
       const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * kRows + row;
 #pragma unroll 1
@@ -386,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       w.advance(a, count, kRows, kKeys);
     }
   } else if (warp < kCopyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---- codes and scales -> fp16.  A lane takes 32 codes of a row (16 bytes), a row's lanes
     // side by side; it writes four 16-byte pieces.  Lanes of the upper 64 columns take theirs in
     // another order, so that eight lanes' pieces fall into eight banks.
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       if (!ok) break;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == kCopyWarp) {
       // ---- copies: lane 2 i has the codes of page i of the tile, lane 2 i + 1 its scales
       const int page_shift = a.cache.page_shift;
