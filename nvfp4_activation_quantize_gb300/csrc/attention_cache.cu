@@ -43,7 +43,7 @@
 // grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
 //
 // Measured, 32 query heads over 8 key heads of 128: 64 tokens over 500 to 8,191 positions each in
-// 70 us (49 is the bytes' time at the copy rate; 62 with the copies alone, 62 with the
+// 70 us (49 is the bytes' time at the copy rate; 63 with the copies alone, 64 with the
 // arithmetic alone), two tokens over 120,000 to 131,071 in 64 us (44).
 #include <cmath>
 
