@@ -6,8 +6,11 @@
  * and the standalone (attention-output) quantize; the residual fold before the
  * norm and the SwiGLU of a packed projection with its bias; abs-max passes for
  * dynamic and calibrated global scales.  Beside them, the QKV epilogue (bias,
- * per-head RMSNorm and rotate-half RoPE, bf16 outputs) and a dequantize used
- * for checking.  Every NVFP4 producer writes:
+ * per-head RMSNorm and rotate-half RoPE, bf16 outputs), a dequantize used
+ * for checking, and what takes the epilogue's outputs on to the next projection:
+ * a paged key/value cache that holds its rows in NVFP4 (write, read), attention of
+ * packed sequences over bf16 keys and values, and attention of a few new tokens a
+ * sequence over that cache.  Every NVFP4 producer writes:
  *
  *   codes   uint8 [rows, cols/2]: E2M1 codes, two per byte, the even column in
  *           the low nibble (FastVideo compare "fasth3-spark-exact-perf",
@@ -424,9 +427,10 @@ int h3q_gemm_swiglu_nvfp4(const uint8_t *a_codes, const uint8_t *a_scales, int64
 
 /*
  * *flag = 1 if a kernel launched since the last call had one of its bounded
- * waits run out, else 0; the flag is cleared.  The kernel that waits on
- * mbarriers (the GEMM of h3q_gemm_swiglu_nvfp4) bounds every wait (2 s) and then
- * stops early, leaving that call's outputs unspecified.  Synchronous: it waits
+ * waits run out, else 0; the flag is cleared.  The kernels that wait on
+ * mbarriers between their warps (the GEMM of h3q_gemm_swiglu_nvfp4, and those of
+ * h3q_attention_varlen and h3q_attention_cache_nvfp4) bound every wait (2 s) and
+ * then stop early, leaving that call's outputs unspecified.  Synchronous: it waits
  * for the device.  Not on any page; a diagnostic of this library.
  */
 int h3q_kernel_error_flag(int *flag);

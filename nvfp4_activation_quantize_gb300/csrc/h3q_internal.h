@@ -104,7 +104,7 @@ cudaError_t launch_gemm_swiglu(const uint8_t* a, const uint8_t* sfa, int64_t m, 
                                const uint8_t* sfb, int64_t n, const float* alpha, const float* gsf,
                                uint8_t* codes, uint8_t* scales, uint16_t* y, float* acc, cudaStream_t stream);
 // Reads and clears the flag a kernel sets when one of its bounded waits ran out
-// (synchronous); the GEMM is the library's kernel with such waits.
+// (synchronous); the GEMM and the attention kernels have such waits.
 cudaError_t gemm_error_flag(int* flag);
 
 // New key (index 0) and value (1) rows into the paged NVFP4 cache, and rows of the
