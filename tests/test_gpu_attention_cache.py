@@ -294,3 +294,51 @@ def test_scores_that_grow_along_the_cache(dev, gain, heads, kv_heads, dim):
             scales[page] = 8 + min(100, 100 * 16 * i // n)
     out, lse = _run(c)
     _check(c, out, lse)
+
+
+def test_sequences_that_share_pages(dev):
+    """A prefix that several sequences have: their tables name the same pages."""
+    c = _case(dev, [(1, 200), (1, 200), (2, 130)], 8, 2, 128, 16, seed=21)
+    c["table"][1, :12] = c["table"][0, :12]
+    c["table"][2, :8] = c["table"][0, :8]
+    out, lse = _run(c)
+    _check(c, out, lse)
+
+
+@pytest.mark.parametrize("new, keys", [(1, 9000), (12, 3000)])
+def test_graphs_that_share_a_workspace(dev, new, keys):
+    """Two captured calls with one workspace, replayed one after the other in any order, and an eager one between."""
+    cases = [_case(dev, [(new, keys), (1, keys // 3 + s)], 16, 4, 128, 64, seed=22 + s) for s in range(2)]
+    want = [_run(c) for c in cases]
+    ws = torch.empty(h3q.attention_cache_workspace_bytes(new, 16, 4, 128), dtype=torch.uint8, device=dev)
+    graphs, got = [], []
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(_run(c, workspace=ws))
+    for order in ((0, 1), (1, 0), (0, 0, 1)):
+        for i in order:
+            for t in got[i]:
+                t.fill_(7.0)
+            graphs[i].replay()
+        _run(cases[0], workspace=ws)
+        for a, b in zip(want, got):
+            n = cases[0]["cu"][-1]
+            assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:, :n], b[1][:, :n])
+
+
+@pytest.mark.parametrize("new, heads", [(1, 8), (3, 32), (8, 64)])
+def test_pages_past_2_32_bytes(dev, new, heads):
+    """The same pages at the end of a cache of 4.6 GB of codes give the same bits."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    c = _case(dev, [(new, 900), (new, 333)], heads, 8, 128, 128, seed=25)
+    want = _run(c)
+    pages = 70000
+    far = [torch.zeros((pages, *t.shape[1:]), dtype=torch.uint8, device=dev) for t in c["cache"]]
+    shift = pages - c["cache"][0].shape[0]
+    for t, f in zip(c["cache"], far):
+        f[shift:] = t
+    assert far[0].numel() > 2 ** 32
+    got = _run({**c, "cache": tuple(far), "table": c["table"] + shift})
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
