@@ -595,8 +595,8 @@ int h3q_attention_varlen(const void *q, int64_t ld_q, const void *k, int64_t ld_
  * The cache and the lists as above.  A page that is not in [0, num_pages) is read as
  * page 0, and the outputs of its sequence are unspecified; kv_len counts at most
  * max_pages * page_size positions.  A scale byte of all ones (which a NaN leaves in the
- * cache) counts as 480.  Launches two kernels.  The result does not depend on what
- * else runs.
+ * cache) counts as 480.  Launches one or two kernels.  The result does not depend
+ * on what else runs.
  */
 static inline int64_t h3q_attention_cache_workspace_bytes(int64_t max_rows, int64_t heads, int64_t kv_heads,
                                                           int64_t head_dim)

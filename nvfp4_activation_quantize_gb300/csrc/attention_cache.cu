@@ -580,8 +580,9 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
                                       S::kSmem, kCacheAttentionMaxCtas, &blocks);
   if (err != cudaSuccess) return err;
   place_workspace(a, workspace, kCacheAttentionMaxCtas, S::kRows);
+  a.whole = whole_groups(a, blocks, S::kRows, S::kKeys);
   cache_attention_kernel<HD, NT><<<blocks, S::kThreads, S::kSmem, stream>>>(a);
-  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
+  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2 || a.whole) return err;
   return launch_join<HD, S::kRows, S::kKeys>(a, blocks, stream);
 }
 

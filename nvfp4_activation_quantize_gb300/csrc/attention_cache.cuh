@@ -22,6 +22,7 @@ namespace cached {
 
 constexpr float kPShift = 14.0f;  // parts and sums hold 2^14 * e^(x - m)
 constexpr int kMergeWarps = 4;    // of a CTA of the joining kernel
+constexpr int kWholeTiles = 2;    // tiles that one CTA takes rather than leave parts of
 constexpr int kMergeRows = 4;     // that it joins, a warp each in the end
 
 struct Args {
@@ -41,6 +42,7 @@ struct Args {
   float* part;             // workspace: [ctas][2][tile rows][head_dim] unnormalised outputs
   float* part_ml;          // [ctas][2][tile rows][2] maxima and sums
   struct Cut* cut;         // [ctas]
+  int whole;               // no range cuts a group
 };
 
 // What the joining kernel needs to know of the group that the start of a CTA's range cuts:
@@ -153,9 +155,9 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
   return total;
 }
 
-// The tiles of sequence s that lie before its unit x of work (a group is `cost` units, then its tiles).
-__device__ __forceinline__ int64_t tiles_before(const Seq& s, int cost, int64_t x) {
-  const int64_t unit = s.tiles + cost;
+// The tiles of sequence s that lie before its x-th unit of work, where a group is `unit` of them: `cost`,
+// then its tiles (or one for all of it).
+__device__ __forceinline__ int64_t tiles_before(const Seq& s, int64_t unit, int cost, int64_t x) {
   if (x <= 0) return 0;
   if (x >= unit * s.groups) return tiles_of(s);
   const int64_t q = x / unit, r = x - q * unit - cost;
@@ -196,7 +198,7 @@ struct PlanScratch {
 // The range of this CTA, and its entry of a.cut; false for one that has nothing to do.  The work is
 // counted in tiles, and COST more for each group (its queries, its join, its output): equal counts
 // are equal times whether a range is one long group or many short ones.  Where there are no more
-// tiles than CTAs each takes one.  The whole CTA calls it.
+// tiles than CTAs each takes one.  With a.whole groups are counted instead.  The whole CTA calls it.
 template <int WARPS, int COST>
 __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys, PlanScratch<WARPS>& sh, Range& r) {
   int64_t tiles = 0, groups = 0, prefix;
@@ -211,8 +213,9 @@ __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys
     tiles += block_scan<WARPS>(t, sh.scan, &prefix);
     groups += block_scan<WARPS>(g, sh.scan, &prefix);
   }
-  const int cost = tiles <= gridDim.x ? 0 : COST;
-  const int64_t total = tiles + cost * groups;
+  const int cost = a.whole || tiles <= gridDim.x ? 0 : COST;
+  const int64_t total = a.whole ? groups : tiles + cost * groups;
+  auto unit_of = [&](const Seq& s) { return a.whole ? int64_t{1} : static_cast<int64_t>(s.tiles) + cost; };
   const int64_t most = total / (cost + 1);   // (a range has a tile: it is longer than cost)
   const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) {
@@ -228,7 +231,7 @@ __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys
     Seq s;
     if (b < a.at.batch) {
       s = sequence(a, b, tile_rows, tile_keys);
-      mine = tiles_of(s) + static_cast<int64_t>(cost) * s.groups;
+      mine = unit_of(s) * s.groups;
     }
     const int64_t sum = block_scan<WARPS>(mine, sh.scan, &prefix);
     const int64_t at = base + prefix;
@@ -236,14 +239,14 @@ __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys
       sh.b = b;
       sh.base = at;
     }
-    const int64_t part = mine == 0 ? 0 : tiles_before(s, cost, t1 - at) - tiles_before(s, cost, t0 - at);
+    const int64_t part = mine == 0 ? 0 : tiles_before(s, unit_of(s), cost, t1 - at) - tiles_before(s, unit_of(s), cost, t0 - at);
     count += block_scan<WARPS>(part, sh.scan, &prefix);   // (its barriers publish sh.b and sh.base too)
     base += sum;
   }
   r.count = static_cast<int>(count);
   r.b = sh.b;
   r.s = sequence(a, r.b, tile_rows, tile_keys);
-  const int64_t unit = r.s.tiles + cost;
+  const int64_t unit = unit_of(r.s);
   r.group = static_cast<int>((t0 - sh.base) / unit);
   const int64_t begin = sh.base + r.group * unit;
   r.tile = t0 - begin > cost ? static_cast<int>(t0 - begin) - cost : 0;
@@ -349,6 +352,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args
   if (a.lse != nullptr && lane == 0)
     a.lse[head * a.rows + out_row] =
         lw == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(mw, __fadd_rn(log2f(lw), -kPShift)), kLn2);
+}
+
+// Whether ranges are of whole groups, so that nothing has to be joined: the tables hold one tile a
+// sequence; or two, and there is a CTA for every group.  (One token, 2 key heads of 64, GPU time: 101
+// positions 7.2 us with the joining kernel, 6.2 without; 301 positions, two tiles, 8.9 and 8.7; 777, four,
+// 9.1 and 13.7.  On the host the second launch is 2.4 us.)
+inline bool whole_groups(const Args& a, int blocks, int tile_rows, int tile_keys) {
+  const int64_t cap = a.at.max_pages << a.cache.page_shift;
+  const int64_t row_tiles = (static_cast<int64_t>(a.max_rows) * a.group + tile_rows - 1) / tile_rows;
+  return cap <= tile_keys || (cap <= kWholeTiles * tile_keys && row_tiles * a.cache.kv_heads <= blocks / a.at.batch);
 }
 
 // The kernel that joins the parts, after the one before it on the stream.

@@ -606,8 +606,9 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
                                       kMaxCtas, &blocks);
   if (err != cudaSuccess) return err;
   place_workspace(a, workspace, kMaxCtas, kRows);
+  a.whole = whole_groups(a, blocks, kRows, kKeys);
   cache_attention_wide_kernel<HD><<<blocks, kThreads, S::kSmem, stream>>>(a);
-  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2) return err;
+  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2 || a.whole) return err;
   return launch_join<HD, kRows, kKeys>(a, blocks, stream);
 }
 
