@@ -93,19 +93,21 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[BYTES / 4]) 
 template <int HD, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;                 // rows per tile
-  static constexpr int kWarpKeys = HD == 256 || NT == 4 ? 32 : 64;   // keys of a tile per warp
+  static constexpr int kWarpKeys = HD == 256 || NT == 3 || (NT == 4 && HD == 128) ? 32 : 64;   // keys of a tile per warp
   static constexpr int kKeys = kWarps * kWarpKeys;     // keys per tile
   static constexpr int kMt = NT == 1 ? kWarpKeys / 16 : 2;   // 16-key products whose scores are held at once
   static constexpr int kCodeBytes = kKeys * HD / 2;    // a slot: a tile's codes of keys or values, then their scales
   static constexpr int kSlotBytes = kCodeBytes + kKeys * HD / 16;
   static constexpr int kSlots = HD == 64 || kKeys == 128 ? 4 : 3;
   // Many rows need more registers than an even split leaves: there the copying warp has three
-  // idle ones beside it, and the four hand theirs over (256 x 128 = 128 x 200 + 128 x 56).
-  static constexpr bool kSplit = NT > 1 || HD == 256;
+  // idle ones beside it, and the four hand theirs over (256 x 128 = 128 x 200 + 128 x 56), two CTAs
+  // an SM, not three.  (64 sequences of 4,503 positions, split and even: 16 rows a key head at
+  // head_dim 128 106 and 128 us; at 64, 16 rows 78 and 66, 24 rows 109 and 92, 32 rows 115 and 153.)
+  static constexpr bool kSplit = HD == 256 || (NT > 1 && HD == 128) || NT == 4;
   static constexpr int kThreads = (kWarps + (kSplit ? 4 : 1)) * 32;
   static constexpr int kCtas = kSplit ? 2 : 3;         // per SM
   static constexpr int kSteps = HD / 16;               // products of 16 along the head
-  static constexpr bool kQShared = NT > 2;             // query fragments in shared memory
+  static constexpr bool kQShared = NT > 2 || (NT == 2 && HD == 64);   // query fragments in shared memory
   static constexpr int kPitch = HD + 4;                // floats per row of the joining buffer
   static constexpr int kOffJoin = kSlots * kSlotBytes;
   static constexpr int kOffMl = kOffJoin + kWarps * 8 * kPitch * 4;
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     uint32_t qf[S::kQShared ? 1 : NT][S::kQShared ? 1 : S::kSteps][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      if (S::kQShared && nt != warp) continue;  // the warps share the work (NT == kWarps)
+      if (S::kQShared && nt != warp) continue;  // the warps share the work
       const int rho = nt * 8 + g;
       const int tok = (tile_row0 + rho) / a.group;
       uint32_t w[HD / 8];
@@ -574,7 +576,7 @@ template <int HD, int NT>
 cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   using S = Shape<HD, NT>;
   static_assert(S::kSmem <= 227 * 1024, "shared memory");
-  static_assert(!S::kQShared || NT == kWarps, "a warp loads one 8-row tile of queries");
+  static_assert(!S::kQShared || NT <= kWarps, "a warp loads at most one 8-row tile of queries");
   int blocks = 0;
   cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_kernel<HD, NT>), S::kThreads,
                                       S::kSmem, kCacheAttentionMaxCtas, &blocks);
@@ -586,9 +588,11 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   return launch_join<HD, S::kRows, S::kKeys>(a, blocks, stream);
 }
 
-// Rows that share a key head are taken 8, 16 or 32 at a time: the fewest that hold them
+// Rows that share a key head are taken 8, 16, 24 or 32 at a time: the fewest that hold them
 // all, so the cache is read once for up to 32 rows (16 at head_dim 256, where the
-// outputs of 32 would not fit the registers).  More than kWideRows go to the tcgen05 kernel.
+// outputs of 32 would not fit the registers).  64 sequences of 4,503 positions at head_dim 128: 70, 106,
+// 148 and 214 us (20 rows as 32: 192).  More than kWideRows go to the tcgen05 kernel, which takes 224 us
+// for these 32 and 217 for 20.
 constexpr int kWideRows = 32;
 template <int HD>
 cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {
@@ -597,6 +601,7 @@ cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {
   if constexpr (HD == 256) return launch<HD, 2>(a, workspace, stream);
   else
     return rows <= 16          ? launch<HD, 2>(a, workspace, stream)
+           : rows <= 24        ? launch<HD, 3>(a, workspace, stream)
            : rows <= kWideRows ? launch<HD, 4>(a, workspace, stream)
                                : launch_cache_attention_wide(a, workspace, stream);
 }

@@ -342,3 +342,11 @@ def test_pages_past_2_32_bytes(dev, new, heads):
     assert far[0].numel() > 2 ** 32
     got = _run({**c, "cache": tuple(far), "table": c["table"] + shift})
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def test_more_whole_groups_than_ctas(dev):
+    """Tables of one tile a sequence: a CTA takes several groups, and nothing is joined."""
+    c = _case(dev, [(b % 3, 2 + b % 254) for b in range(420)], 12, 3, 128, 64, seed=27)
+    c["table"] = c["table"][:, :4].contiguous()   # (256 positions)
+    out, lse = _run(c)
+    _check(c, out, lse)
