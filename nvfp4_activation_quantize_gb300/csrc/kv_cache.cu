@@ -15,10 +15,11 @@
 // step of 64 rows x 8 heads has only 16 units if each warp takes them all, so heads
 // are dealt out until every SM has its warps.
 //
-// Measured: 65,280 rows x 56 heads x 128 written in 0.356 ms (0.354 is the bytes' time at the
+// Measured: 65,280 rows x 56 heads x 128 written in 0.355 ms (0.354 is the bytes' time at the
 // copy rate; heads per warp at most 4: 0.361, 16: 0.369 ms); the 160,272 rows x 8 heads x 128 of 32
-// prefixes read in 0.148 ms (0.124; two heads' loads in flight, not four: 0.158, occupancy 4 CTAs
-// a SM instead of 5), where the scattered table lookups are what is left (0.142 without them).
+// prefixes read in 0.144 ms (0.124; heads per warp at most 8: 0.146, 2: 0.154; four heads' loads in
+// flight, not two: 0.158, occupancy 4 CTAs a SM instead of 5).  Units go round the warps: with a
+// contiguous range for each, 0.370 and 0.171 ms.
 #include "h3q_cache.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
@@ -30,7 +31,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kWriteUnroll = 4;   // heads whose loads are in flight
 constexpr int kReadUnroll = 2;
-constexpr int kMaxHeads = 8;      // heads of a unit, at most
+constexpr int kWriteHeads = 8;    // heads of a unit, at most
+constexpr int kReadHeads = 4;
 
 struct RowsArgs {
   PagedCache cache;
@@ -216,11 +218,11 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const RowsArgs a) 
 }
 
 // Heads per warp and the units that follow: as many heads as keep 16 warps on each of
-// 152 SMs busy, at most 16.
-void plan_units(RowsArgs& a, int rows_per_warp) {
+// 152 SMs busy, at most `most`.
+void plan_units(RowsArgs& a, int rows_per_warp, int most) {
   const int64_t groups = (a.rows + rows_per_warp - 1) / rows_per_warp;
   int64_t per = groups * a.cache.kv_heads / (152 * 16);
-  per = per < 1 ? 1 : per > kMaxHeads ? kMaxHeads : per;
+  per = per < 1 ? 1 : per > most ? most : per;
   if (per > a.cache.kv_heads) per = a.cache.kv_heads;
   a.heads_per_unit = static_cast<int>(per);
   a.head_units = (a.cache.kv_heads + per - 1) / per;
@@ -229,7 +231,7 @@ void plan_units(RowsArgs& a, int rows_per_warp) {
 
 template <int HD>
 cudaError_t launch_rows(RowsArgs a, bool write, cudaStream_t stream) {
-  plan_units(a, 512 / HD);
+  plan_units(a, 512 / HD, write ? kWriteHeads : kReadHeads);
   const void* kernel = write ? reinterpret_cast<const void*>(&cache_write_kernel<HD>)
                              : reinterpret_cast<const void*>(&cache_read_kernel<HD>);
   int blocks = 0;
