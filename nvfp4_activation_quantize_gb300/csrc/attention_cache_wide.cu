@@ -22,12 +22,17 @@
 //   warp 12           copies pages of codes and scales into a raw ring, a lane each
 //   warp 13           the products
 // Work is dealt out and joined as in attention_cache.cu, in tiles of 128 keys, one CTA per SM.
+// Where no sequence has more than 64 rows a key head (FEW) they fill both halves of the 128, so that two
+// threads share a row's softmax, the keys of the tile's lower and of its upper half: each has zeros for
+// weights of the other's keys, and an output of its own, joined as the streams' are.
+//
 // Measured, 32 query heads over 8 key heads of 128: 16 trees of 9 to 16 tokens (36 to 64 rows a
-// key head) over 1,000 to 8,000 positions in 72 us, where the bytes take 13.  A tile of 128 keys
-// takes about 2,400 clocks; 1,530 of them shared memory is busy (queries, keys and values read by
-// the products 96 KB, fp16 tiles written 64 KB, codes in and out 36 KB, at 128 bytes a clock).
-// Without the conversions 65 us, without the products 68, without the copies 69.  (Keys converted
-// a tile ahead of values: 71; fewer rows for the converting warps beside the softmax: 85.)
+// key head) over 1,000 to 8,000 positions in 69 us (72 with one thread a row), where the bytes take 13.  A
+// tile of 128 keys takes about 2,400 clocks; 1,530 of them shared memory is busy (queries, keys and values
+// read by the products 96 KB, fp16 tiles written 64 KB, codes in and out 36 KB, at 128 bytes a clock), and 20 us
+// are launch, plan, queries, first tile, outputs and the joining kernel.  Without the conversions it was 65 us
+// of 72, without the products 68, without the copies 69.  (Keys converted a tile ahead of values, fewer rows
+// for the converting warps beside the softmax: no faster, and 85 us.)
 // Every wait is bounded: one that runs out sets a device flag and tells the other roles to stop.
 #include "attention_cache.cuh"
 #include "h3q_tcgen05.cuh"
@@ -45,13 +50,16 @@ constexpr int kRows = 128;             // rows per tile
 constexpr int kKeys = 128;             // keys per tile
 constexpr int kMaxCtas = 152;          // the workspace holds the parts of so many (608 of 32 rows)
 constexpr int kGroupCost = 6;          // the time of a group's start and end, in tiles
+constexpr int kFewRegs0 = 160, kFewRegs1 = 104, kFewRegs2 = 88;
 constexpr float kInShift = 6.0f;       // weights are held as 2^6 e^(x - reference)
 constexpr float kSlack = 8.0f;         // how far (log2) a row's maximum may pass its reference
 
 __device__ int g_wide_fault;
 
-template <int HD>
+template <int HD, bool FEW>
 struct Shape {
+  static constexpr int kTileRows = FEW ? 64 : kRows;          // rows that are different
+  static constexpr int kCols = FEW ? kKeys / 2 : kKeys;       // keys of a thread's row
   static constexpr int kTileBytes = kKeys * HD * 2;           // a tile of keys or values in fp16
   static constexpr int kCodeBytes = kKeys * HD / 2;
   static constexpr int kRawBytes = kCodeBytes + kKeys * HD / 16;
@@ -90,9 +98,10 @@ __device__ __forceinline__ void weights16(const uint32_t* s, float2 c2, float2 b
   }
 }
 
-template <int HD>
+template <int HD, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const Args a) {
-  using S = Shape<HD>;
+  using S = Shape<HD, FEW>;
+  constexpr int kTileRows = S::kTileRows;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   __shared__ PlanScratch<kThreads / 32> scratch;
@@ -132,20 +141,22 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     mbar_init_fence();
   }
   Range w;
-  if (!plan<kThreads / 32, kGroupCost>(a, kRows, kKeys, scratch, w)) return;
+  if (!plan<kThreads / 32, kGroupCost>(a, kTileRows, kKeys, scratch, w)) return;
 
   auto wait = [&](uint32_t bar, uint32_t parity) {   // the whole warp: one decision
     return static_cast<bool>(__all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_wide_fault)));
   };
 
   // Registers: 8 softmax warps 200, 4 converting warps 72, the other four 40 (512 x 128 in all); with 168,
-  // 96 and 80 the scores did not fit, 80 us for 16 trees.
+  // 96 and 80 a thread's 128 scores did not fit, 80 us for 16 trees, not 72.  Half the scores: 160, 104 and 88 (69
+  // us; 144, 112, 112: 74, and 200, 72, 40: 73).
   if (warp < kConvertWarp0) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FEW ? kFewRegs0 : 200));
     // ---- softmax of one stream
     const int x = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;   // the TMEM of all 512 columns begins at 0
+    const uint32_t col0 = FEW ? row / 64 * 64 : 0;   // of the thread's keys
     const uint32_t taddr = lane_base + x * kKeys, taddr_o = lane_base + S::kO + x * HD;
     float* join = reinterpret_cast<float*>(smem + S::kOffJoin) + row;          // [column][row]
     float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl) + row;
@@ -159,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       const int count = w.here();
       const bool whole = w.tile == 0 && count == w.s.tiles;
       const int kv_head = w.kv_head(), row_tile = w.group - kv_head * w.s.row_tiles;
-      const int rho = row_tile * kRows + row;
+      const int rho = row_tile * kTileRows + row % kTileRows;
       const bool valid = rho < w.s.n * a.group;
       const bool rows = rho - lane < w.s.n * a.group;   // any of the warp's
       {
@@ -171,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         uint4 q[kSteps];
         uint32_t m[kSteps];
         {
-          int t = (row_tile * kRows + r0) / a.group;
-          int h = row_tile * kRows + r0 - t * a.group;
+          const int first = row_tile * kTileRows + r0 % kTileRows;   // (16 rows of a warp: no end of a tile inside)
+          int t = first / a.group;
+          int h = first - t * a.group;
 #pragma unroll
           for (int i = 0; i < kSteps; ++i) {
             q[i] = make_uint4(0, 0, 0, 0);
@@ -262,26 +274,27 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           hi &= ones(w.s.len - static_cast<int64_t>(key0) - 64);
           see[0] = static_cast<uint32_t>(lo), see[1] = static_cast<uint32_t>(lo >> 32);
           see[2] = static_cast<uint32_t>(hi), see[3] = static_cast<uint32_t>(hi >> 32);
+          if (FEW && col0 != 0) see[0] = see[2], see[1] = see[3];
         }
         const float2 c2 = make_float2(c, c);
-        uint32_t s[4][32];
+        uint32_t s[S::kCols / 32][32];
         uint32_t wt[32];
         float2 sum;
         bool fresh = i < 2;   // no reference yet: only the maximum is formed
         for (;;) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tc_load32(taddr + 32 * k, s[k]);
+          for (int k = 0; k < S::kCols / 32; ++k) tc_load32(taddr + col0 + 32 * k, s[k]);
           tc_wait_load(s[0]);
 #pragma unroll
-          for (int k = 1; k < 4; ++k) tc_loaded(s[k]);
+          for (int k = 1; k < S::kCols / 32; ++k) tc_loaded(s[k]);
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < 128; ++k)
+            for (int k = 0; k < S::kCols; ++k)
               if (!(see[k / 32] >> (k % 32) & 1)) s[k / 32][k % 32] = 0xff800000u;
           }
           float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 128; k += 8)
+          for (int k = 0; k < S::kCols; k += 8)
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               m[h] = max3(m[h], __uint_as_float(s[k / 32][k % 32 + 2 * h]), __uint_as_float(s[k / 32][k % 32 + 2 * h + 1]));
@@ -303,16 +316,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         }
         const float shift = m_ref == -INFINITY ? kInShift : __fadd_rn(kInShift, -__fmul_rn(m_ref, c));
         const float2 b2 = make_float2(shift, shift);
-        store_weights<32>(taddr, wt);
-        tc_wait_store();
-        tc_fence_before();
-        mbar_arrive(bar_p + 8 * x);
+        if constexpr (FEW) {   // the weights of this thread's half, and none of the other's
+          store_weights<32>(taddr + col0 / 2, wt);
+          uint32_t none[32] = {};
+          store_weights<32>(taddr + (32 - col0 / 2), none);
+          l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
+          tc_wait_store();
+          tc_fence_before();
+          mbar_arrive(bar_p + 8 * x);
+        } else {
+          store_weights<32>(taddr, wt);
+          tc_wait_store();
+          tc_fence_before();
+          mbar_arrive(bar_p + 8 * x);
 #pragma unroll
-        for (int k = 0; k < 64; k += 16) weights16(s[2 + k / 32] + k % 32, c2, b2, sum, wt + k / 2);
-        store_weights<32>(taddr + 32, wt);
-        l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
-        tc_wait_store();
-        tc_fence_before();
+          for (int k = 0; k < 64; k += 16) weights16(s[S::kCols / 64 + k / 32] + k % 32, c2, b2, sum, wt + k / 2);
+          store_weights<32>(taddr + 32, wt);
+          l = __fadd_rn(l, __fadd_rn(sum.x, sum.y));
+          tc_wait_store();
+          tc_fence_before();
+        }
         mbar_arrive(bar_p2 + 8 * x);
       }
       if (ok && x < count) {
@@ -336,12 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         l = __fmul_rn(l, f0);
         if (two) l = __fmaf_rn(other.y, f1, l);
       }
+      float g0 = 1.0f, g1 = 0.0f;   // the lower and the upper keys' share
+      if constexpr (FEW) {
+        sync_both();
+        if (x == 0 && col0 != 0) *join_ml = make_float2(m, l);
+        sync_both();
+        if (x == 0 && col0 == 0) {
+          const float2 other = join_ml[64];
+          const float top = fmaxf(m, other.x), use = top == -INFINITY ? 0.0f : top;
+          g0 = ex2(__fadd_rn(m, -use));
+          g1 = ex2(__fadd_rn(other.x, -use));
+          l = __fmaf_rn(other.y, g1, __fmul_rn(l, g0));
+          m = top;
+        }
+      }
       const float inv = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
       int rho_out = rho;
       asm volatile("" : "+r"(rho_out));   // (where it goes is formed here, not kept over the tiles)
       const int tok = rho_out / a.group, head = kv_head * a.group + rho_out - tok * a.group;
       const int64_t out_row = w.s.row0 + tok;
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * kRows + row;
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (first_segment ? 0 : 1)) * kTileRows + row % kTileRows;
 #pragma unroll 1
       for (int i = 0; i < HD; i += 32) {
         uint32_t o[32];
@@ -355,13 +392,26 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           for (int k = 0; k < 32; ++k) join[k * kRows] = __uint_as_float(o[k]);
         }
         if (two) sync_both();
-        if (x == 0 && valid && ok) {
-          float v[32];
+        float v[32];
+        if (x == 0 && rows) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             v[k] = __fmul_rn(__uint_as_float(o[k]), f0);
             if (two) v[k] = __fmaf_rn(join[k * kRows], f1, v[k]);
           }
+        }
+        if constexpr (FEW) {
+          if (x == 0 && rows && col0 != 0) {   // (its own places, which it has just read)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) join[k * kRows] = v[k];
+          }
+          sync_both();
+          if (x == 0 && rows && col0 == 0) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = __fmaf_rn(join[k * kRows + 64], g1, __fmul_rn(v[k], g0));
+          }
+        }
+        if (x == 0 && col0 == 0 && valid && ok) {
           if (whole) {
             uint16_t* dst = a.o + (out_row * a.heads + head) * HD + i;
 #pragma unroll
@@ -382,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
                                                                 __fmul_rn(v[k + 2], kUp), __fmul_rn(v[k + 3], kUp));
           }
         }
-        if (two) sync_both();
+        if (two || FEW) sync_both();
       }
-      if (x == 0 && valid && ok) {
+      if (x == 0 && col0 == 0 && valid && ok) {
         if (!whole)
           reinterpret_cast<float2*>(a.part_ml)[part] = make_float2(m, __fmul_rn(l, 256.0f));
         else if (a.lse != nullptr)
@@ -393,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       }
       tc_fence_before();   // O has been read before the next segment's first weights are announced
       first_segment = false;
-      w.advance(a, count, kRows, kKeys);
+      w.advance(a, count, kTileRows, kKeys);
     }
   } else if (warp < kCopyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW ? kFewRegs1 : 72));
     // ---- codes and scales -> fp16.  A lane takes 32 codes of a row (16 bytes), a row's lanes
     // side by side; it writes four 16-byte pieces.  Lanes of the upper 64 columns take theirs in
     // another order, so that eight lanes' pieces fall into eight banks.
@@ -454,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       if (!ok) break;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FEW ? kFewRegs2 : 40));
     if (warp == kCopyWarp) {
       // ---- copies: lane 2 i has the codes of page i of the tile, lane 2 i + 1 its scales
       const int page_shift = a.cache.page_shift;
@@ -476,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         const int64_t row = (static_cast<int64_t>(page) * a.cache.kv_heads + w.kv_head()) << page_shift;
         const uint32_t live = __ballot_sync(0xffffffffu, page >= 0);
         const bool mine = page >= 0;
-        w.advance(a, 1, kRows, kKeys);   // the next tile's pages, before this one's slots are waited for
+        w.advance(a, 1, kTileRows, kKeys);   // the next tile's pages, before this one's slots are waited for
         if (w.count > 0) page = page_number();
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -576,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           }
         }
         n0 += 2 * count;
-        w.advance(a, count, kRows, kKeys);
+        w.advance(a, count, kTileRows, kKeys);
       }
       if (*abort) {   // let what is issued finish before the TMEM is freed
         __syncwarp();
@@ -597,25 +647,32 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
   }
 }
 
-template <int HD>
+template <int HD, bool FEW>
 cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
-  using S = Shape<HD>;
+  using S = Shape<HD, FEW>;
   static_assert(S::kSmem <= 227 * 1024, "shared memory");
+  static_assert(256 * kFewRegs0 + 128 * kFewRegs1 + 128 * kFewRegs2 <= 65536, "registers");
   int blocks = 0;
-  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_wide_kernel<HD>), kThreads, S::kSmem,
-                                      kMaxCtas, &blocks);
+  cudaError_t err = persistent_blocks(reinterpret_cast<const void*>(&cache_attention_wide_kernel<HD, FEW>), kThreads,
+                                      S::kSmem, kMaxCtas, &blocks);
   if (err != cudaSuccess) return err;
-  place_workspace(a, workspace, kMaxCtas, kRows);
-  a.whole = whole_groups(a, blocks, kRows, kKeys);
-  cache_attention_wide_kernel<HD><<<blocks, kThreads, S::kSmem, stream>>>(a);
+  place_workspace(a, workspace, kMaxCtas, S::kTileRows);
+  a.whole = whole_groups(a, blocks, S::kTileRows, kKeys);
+  cache_attention_wide_kernel<HD, FEW><<<blocks, kThreads, S::kSmem, stream>>>(a);
   if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2 || a.whole) return err;
-  return launch_join<HD, kRows, kKeys>(a, blocks, stream);
+  return launch_join<HD, S::kTileRows, kKeys>(a, blocks, stream);
+}
+
+template <int HD>
+cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {
+  return static_cast<int64_t>(a.max_rows) * a.group <= 64 ? launch<HD, true>(a, workspace, stream)
+                                                           : launch<HD, false>(a, workspace, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attention_wide(const cached::Args& a, uint8_t* workspace, cudaStream_t stream) {
-  return a.cache.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
+  return a.cache.head_dim == 64 ? dispatch<64>(a, workspace, stream) : dispatch<128>(a, workspace, stream);
 }
 
 cudaError_t cache_attention_wide_error_flag(int* flag) {
