@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     *abort = 0;
     mbar_init_fence();
   }
+  after_stream();
   Range r;
   if (!plan<S::kThreads / 32, kGroupCost>(a, S::kRows, S::kKeys, scratch, r)) return;
 
@@ -583,8 +584,8 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   place_workspace(a, workspace, kCacheAttentionMaxCtas, S::kRows);
   a.whole = whole_groups(a, blocks, S::kRows, S::kKeys);
-  cache_attention_kernel<HD, NT><<<blocks, S::kThreads, S::kSmem, stream>>>(a);
-  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2 || a.whole) return err;
+  err = launch_early(&cache_attention_kernel<HD, NT>, blocks, S::kThreads, S::kSmem, stream, a);
+  if (err != cudaSuccess || blocks < 2 || a.whole) return err;
   return launch_join<HD, S::kRows, S::kKeys>(a, blocks, stream);
 }
 

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args
   constexpr int kPer = HD / 32;
   __shared__ float sum[kMergeWarps][kMergeRows][HD];
   __shared__ float sum_l[kMergeWarps][kMergeRows];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts are written
+  after_stream();   // the parts are written
   const int c = blockIdx.x + 1;
   const Cut cut = a.cut[c];
   if (!cut.valid) return;
@@ -367,16 +367,8 @@ inline bool whole_groups(const Args& a, int blocks, int tile_rows, int tile_keys
 // The kernel that joins the parts, after the one before it on the stream.
 template <int HD, int ROWS, int KEYS>
 cudaError_t launch_join(const Args& a, int blocks, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks - 1), ROWS / kMergeRows, 1);
-  cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_parts_kernel<HD, ROWS, KEYS>, a);
+  return launch_early(&join_parts_kernel<HD, ROWS, KEYS>, dim3(static_cast<unsigned>(blocks - 1), ROWS / kMergeRows, 1),
+                      kMergeWarps * 32, 0, stream, a);
 }
 
 // Addresses of the workspace's regions for CTAs of `rows` rows.

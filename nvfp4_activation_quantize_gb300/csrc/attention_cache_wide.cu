@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     *abort = 0;
     mbar_init_fence();
   }
+  after_stream();
   Range w;
   if (!plan<kThreads / 32, kGroupCost>(a, kTileRows, kKeys, scratch, w)) return;
 
@@ -658,8 +659,8 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   place_workspace(a, workspace, kMaxCtas, S::kTileRows);
   a.whole = whole_groups(a, blocks, S::kTileRows, kKeys);
-  cache_attention_wide_kernel<HD, FEW><<<blocks, kThreads, S::kSmem, stream>>>(a);
-  if ((err = cudaGetLastError()) != cudaSuccess || blocks < 2 || a.whole) return err;
+  err = launch_early(&cache_attention_wide_kernel<HD, FEW>, blocks, kThreads, S::kSmem, stream, a);
+  if (err != cudaSuccess || blocks < 2 || a.whole) return err;
   return launch_join<HD, S::kTileRows, kKeys>(a, blocks, stream);
 }
 

@@ -52,4 +52,25 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
   return static_cast<int64_t>(cu[lo]) <= r && r < static_cast<int64_t>(cu[lo + 1]) ? lo : -1;
 }
 
+// A launch that may begin while the stream's work before it ends: its CTAs are there when that is done.
+// Every thread of the kernel calls after_stream() before it reads or writes memory.  (A token's write and
+// attention at 777 positions, from a graph: 12.3 us, with plain launches 12.8; with the kernels letting the next
+// one in as they begin 12.5.)
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+__device__ __forceinline__ void after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace h3q

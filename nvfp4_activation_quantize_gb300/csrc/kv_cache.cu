@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const RowsArgs a)
   __shared__ float inv_table[2][128];
   const int lane = threadIdx.x & 31;
   const int mine = lane / kBlocks, blk = lane % kBlocks;
+  after_stream();
   const float gsf[2] = {*a.gsf[0], *a.gsf[1]};
   fill_inverse_scales(inv_table[0], gsf[0]);
   fill_inverse_scales(inv_table[1], gsf[1]);
@@ -171,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const RowsArgs a) 
   __shared__ uint4 tab[2][128];
   const int lane = threadIdx.x & 31;
   const int mine = lane / kBlocks, blk = lane % kBlocks;
+  after_stream();
   fill_magnitudes(tab[0], *a.gsf[0]);
   fill_magnitudes(tab[1], *a.gsf[1]);
   __syncthreads();
@@ -237,11 +239,7 @@ cudaError_t launch_rows(RowsArgs a, bool write, cudaStream_t stream) {
   int blocks = 0;
   cudaError_t err = persistent_blocks(kernel, kThreads, 0, (a.units + kWarps - 1) / kWarps, &blocks);
   if (err != cudaSuccess) return err;
-  if (write)
-    cache_write_kernel<HD><<<blocks, kThreads, 0, stream>>>(a);
-  else
-    cache_read_kernel<HD><<<blocks, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(write ? &cache_write_kernel<HD> : &cache_read_kernel<HD>, blocks, kThreads, 0, stream, a);
 }
 
 cudaError_t dispatch(const RowsArgs& a, bool write, cudaStream_t stream) {

@@ -350,3 +350,51 @@ def test_more_whole_groups_than_ctas(dev):
     c["table"] = c["table"][:, :4].contiguous()   # (256 positions)
     out, lse = _run(c)
     _check(c, out, lse)
+
+
+def test_captured_behind_copies_and_other_streams(dev):
+    """The calls as the first of a graph, behind copies from the host, fills, and work of another stream."""
+    heads, kv, dim, page, batch = 16, 4, 128, 16, 3
+    cache = h3q.kv_cache_nvfp4(64, kv, page, dim, dev)
+    table = torch.randperm(64, device=dev)[:60].to(torch.int32).view(batch, 20).contiguous()
+    cu, kv_len = cc.ints([0, 1, 2, 3], dev), cc.ints([5, 6, 7], dev)
+    new = [torch.tensor(n, dtype=torch.int32).pin_memory() for n in ([300, 17, 1], [20, 301, 64])]
+    host = torch.empty_like(new[0]).pin_memory()
+    kg, vg = _scales(dev, (448.0, 300.0))
+    x = torch.randn((batch, heads + 2 * kv, dim), device=dev).bfloat16()
+    for t in cache:
+        t.random_(0, 128)
+    lse = torch.zeros((heads, batch), device=dev)
+    other, y = torch.cuda.Stream(), torch.zeros_like(x)
+
+    def step():
+        kv_len.copy_(host, non_blocking=True)
+        h3q.h3q_kv_cache_write_nvfp4(y[:, heads:heads + kv], y[:, heads + kv:], cache, cu, kv_len, table, kg, vg)
+        lse.zero_()
+        out = h3q.h3q_attention_cache_nvfp4(y[:, :heads], cache, cu, kv_len, table, kg, vg, lse=lse)
+        return out, h3q.h3q_kv_cache_read_nvfp4(cache, cu, kv_len, table, kg, vg, rows=batch)
+
+    host.copy_(new[0])
+    y.copy_(x)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        other.wait_stream(main)
+        with torch.cuda.stream(other):
+            y.copy_(x)
+        kv_len.zero_()
+        main.wait_stream(other)
+        out, back = step()
+    for n in new:
+        host.copy_(n)
+        x.copy_(torch.randn_like(x))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (out, lse, *back, *cache)]
+        y.copy_(x)
+        want, rows = step()
+        for a, b in zip(got, (want, lse, *rows, *cache)):
+            assert torch.equal(a, b)
+        c = {"q": x[:, :heads], "cache": cache, "cu": cu, "len": kv_len, "table": table, "gs": (448.0, 300.0), "mask": None, "page": page}
+        _check(c, want, lse)
