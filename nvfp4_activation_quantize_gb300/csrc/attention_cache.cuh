@@ -132,26 +132,36 @@ __device__ __forceinline__ uint32_t magnitude_bits(const uint32_t (&w)[N]) {
   return m;
 }
 
-// A sum over the CTA of one value a thread, and the exclusive prefix of this thread.
+// a / b of numbers that are not negative, which mostly have 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// Sums over the CTA of two values a thread, and the exclusive prefixes of this thread.
+struct Pair {
+  int64_t tiles, groups;
+};
 template <int WARPS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* prefix) {
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* scratch, Pair* prefix) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+  Pair x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int64_t y = __shfl_up_sync(0xffffffffu, x.tiles, o), z = __shfl_up_sync(0xffffffffu, x.groups, o);
+    if (lane >= o) x.tiles += y, x.groups += z;
   }
   if (lane == 31) scratch[warp] = x;
   __syncthreads();
-  int64_t before = 0, total = 0;
+  Pair before{0, 0}, total{0, 0};
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
+    const Pair y = scratch[w];
+    if (w < warp) before.tiles += y.tiles, before.groups += y.groups;
+    total.tiles += y.tiles, total.groups += y.groups;
   }
   __syncthreads();
-  *prefix = before + x - v;
+  prefix->tiles = before.tiles + x.tiles - v.tiles;
+  prefix->groups = before.groups + x.groups - v.groups;
   return total;
 }
 
@@ -160,7 +170,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
 __device__ __forceinline__ int64_t tiles_before(const Seq& s, int64_t unit, int cost, int64_t x) {
   if (x <= 0) return 0;
   if (x >= unit * s.groups) return tiles_of(s);
-  const int64_t q = x / unit, r = x - q * unit - cost;
+  const int64_t q = quotient(x, unit), r = x - q * unit - cost;
   return q * s.tiles + (r > 0 ? r : 0);
 }
 
@@ -190,8 +200,9 @@ struct Range {
 
 template <int WARPS>
 struct PlanScratch {
-  int64_t scan[WARPS];
-  int64_t base;
+  Pair scan[WARPS];
+  int64_t base;            // units before the first range's sequence
+  int64_t first, last;     // tiles before the range, and before its end
   int b;
 };
 
@@ -201,53 +212,52 @@ struct PlanScratch {
 // tiles than CTAs each takes one.  With a.whole groups are counted instead.  The whole CTA calls it.
 template <int WARPS, int COST>
 __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys, PlanScratch<WARPS>& sh, Range& r) {
-  int64_t tiles = 0, groups = 0, prefix;
-  for (int b0 = 0; b0 < a.at.batch; b0 += WARPS * 32) {
+  const bool once = a.at.batch <= WARPS * 32;   // a sequence a thread
+  Seq s;
+  Pair mine, prefix, sum{0, 0};
+  auto count = [&](int b0) {
     const int b = b0 + threadIdx.x;
-    int64_t t = 0, g = 0;
+    mine = Pair{0, 0};
     if (b < a.at.batch) {
-      const Seq s = sequence(a, b, tile_rows, tile_keys);
-      t = tiles_of(s);
-      g = s.groups;
+      s = sequence(a, b, tile_rows, tile_keys);
+      mine = Pair{tiles_of(s), s.groups};
     }
-    tiles += block_scan<WARPS>(t, sh.scan, &prefix);
-    groups += block_scan<WARPS>(g, sh.scan, &prefix);
+    return block_scan<WARPS>(mine, sh.scan, &prefix);
+  };
+  for (int b0 = 0; b0 < a.at.batch; b0 += WARPS * 32) {
+    const Pair here = count(b0);
+    sum.tiles += here.tiles, sum.groups += here.groups;
   }
+  const int64_t tiles = sum.tiles, groups = sum.groups;
   const int cost = a.whole || tiles <= gridDim.x ? 0 : COST;
   const int64_t total = a.whole ? groups : tiles + cost * groups;
-  auto unit_of = [&](const Seq& s) { return a.whole ? int64_t{1} : static_cast<int64_t>(s.tiles) + cost; };
+  auto unit_of = [&](const Seq& q) { return a.whole ? int64_t{1} : static_cast<int64_t>(q.tiles) + cost; };
+  auto units_of = [&](const Pair& p) { return a.whole ? p.groups : p.tiles + cost * p.groups; };
   const int64_t most = total / (cost + 1);   // (a range has a tile: it is longer than cost)
   const int ctas = static_cast<int>(most < gridDim.x ? most : gridDim.x);
   if (static_cast<int>(blockIdx.x) >= ctas) {
     if (threadIdx.x == 0) a.cut[blockIdx.x].valid = 0;
     return false;
   }
-  const int64_t t0 = total * blockIdx.x / ctas, t1 = total * (blockIdx.x + 1) / ctas;
-  int64_t base = 0;
-  int64_t count = 0;
-  for (int b0 = 0; b0 < a.at.batch && base < t1; b0 += WARPS * 32) {
-    const int b = b0 + threadIdx.x;
-    int64_t mine = 0;
-    Seq s;
-    if (b < a.at.batch) {
-      s = sequence(a, b, tile_rows, tile_keys);
-      mine = unit_of(s) * s.groups;
-    }
-    const int64_t sum = block_scan<WARPS>(mine, sh.scan, &prefix);
-    const int64_t at = base + prefix;
-    if (at <= t0 && t0 < at + mine) {
-      sh.b = b;
+  const int64_t t0 = quotient(total * blockIdx.x, ctas), t1 = quotient(total * (blockIdx.x + 1), ctas);
+  Pair base{0, 0};
+  for (int b0 = 0; b0 < a.at.batch && units_of(base) < t1; b0 += WARPS * 32) {
+    const Pair here = once ? sum : count(b0);
+    const int64_t first = base.tiles + prefix.tiles, at = units_of(base) + units_of(prefix), end = at + units_of(mine);
+    if (at <= t0 && t0 < end) {
+      sh.b = b0 + threadIdx.x;
       sh.base = at;
+      sh.first = first + tiles_before(s, unit_of(s), cost, t0 - at);
     }
-    const int64_t part = mine == 0 ? 0 : tiles_before(s, unit_of(s), cost, t1 - at) - tiles_before(s, unit_of(s), cost, t0 - at);
-    count += block_scan<WARPS>(part, sh.scan, &prefix);   // (its barriers publish sh.b and sh.base too)
-    base += sum;
+    if (at < t1 && t1 <= end) sh.last = first + tiles_before(s, unit_of(s), cost, t1 - at);
+    base.tiles += here.tiles, base.groups += here.groups;
   }
-  r.count = static_cast<int>(count);
+  __syncthreads();
+  r.count = static_cast<int>(sh.last - sh.first);
   r.b = sh.b;
   r.s = sequence(a, r.b, tile_rows, tile_keys);
   const int64_t unit = unit_of(r.s);
-  r.group = static_cast<int>((t0 - sh.base) / unit);
+  r.group = static_cast<int>(quotient(t0 - sh.base, unit));
   const int64_t begin = sh.base + r.group * unit;
   r.tile = t0 - begin > cost ? static_cast<int>(t0 - begin) - cost : 0;
   if (threadIdx.x == 0) {
@@ -259,7 +269,7 @@ __device__ __forceinline__ bool plan(const Args& a, int tile_rows, int tile_keys
     c.b = r.b;
     c.kv_head = r.kv_head();
     c.row_tile = r.group % r.s.row_tiles;
-    c.valid = r.tile > 0 && total * (blockIdx.x - 1) / ctas <= begin + cost;   // blockIdx.x > 0 where tile > 0
+    c.valid = r.tile > 0 && quotient(total * (blockIdx.x - 1), ctas) <= begin + cost;   // blockIdx.x > 0 where tile > 0
     c.pad = 0;
     a.cut[blockIdx.x] = c;
   }
@@ -284,10 +294,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args
   const int row0 = cut.row_tile * ROWS + rho0;
   if (row0 >= s.n * a.group) return;
   // the first range's part is its last segment: slot 0 if the range began in this group too
-  const int64_t prev0 = cut.total * (c - 1) / cut.ctas;
+  const int64_t prev0 = quotient(cut.total * (c - 1), cut.ctas);
   const int64_t first = static_cast<int64_t>(c - 1) * 2 + (prev0 >= cut.begin ? 0 : 1);
   // one past the last range that starts inside the group: total * last / ctas < end
-  const int64_t past = (cut.end * cut.ctas + cut.total - 1) / cut.total;
+  const int64_t past = quotient(cut.end * cut.ctas + cut.total - 1, cut.total);
   const int last = static_cast<int>(past < cut.ctas ? past : cut.ctas);
   auto slot = [&](int k) { return (k == c - 1 ? first : static_cast<int64_t>(k) * 2) * ROWS + rho0; };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
