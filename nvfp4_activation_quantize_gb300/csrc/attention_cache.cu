@@ -43,8 +43,9 @@
 // grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
 //
 // Measured, 32 query heads over 8 key heads of 128: 64 tokens over 500 to 8,191 positions each in
-// 70 us (49 is the bytes' time at the copy rate; 63 with the copies alone, 64 with the
-// arithmetic alone), two tokens over 120,000 to 131,071 in 64 us (44).
+// 67 us (49 is the bytes' time at the copy rate), two tokens over 120,000 to 131,071 in 61 us (44).
+// Longer contexts cost the copy rate's time, 6.7 TB/s; 11 us are launch, plan, first tiles and join.  At 70
+// us it was 63 with the copies alone and 64 with the arithmetic alone.
 #include <cmath>
 
 #include "attention_cache.cuh"

@@ -17,7 +17,7 @@
 //
 // Measured: 65,280 rows x 56 heads x 128 written in 0.355 ms (0.354 is the bytes' time at the
 // copy rate; heads per warp at most 4: 0.361, 16: 0.369 ms); the 160,272 rows x 8 heads x 128 of 32
-// prefixes read in 0.144 ms (0.124; heads per warp at most 8: 0.146, 2: 0.154; four heads' loads in
+// prefixes read in 0.142 ms (0.124; heads per warp at most 8: 0.144, 2: 0.152; four heads' loads in
 // flight, not two: 0.158, occupancy 4 CTAs a SM instead of 5).  Units go round the warps: with a
 // contiguous range for each, 0.370 and 0.171 ms.
 #include "h3q_cache.cuh"
