@@ -499,7 +499,7 @@ int h3q_rmsnorm_adaln_nvfp4_host(const void *x_host, int64_t rows, int64_t cols,
  *                positions, kv_len[b] - n .. kv_len[b] - 1.
  *   block_table  int32 [batch, max_pages]: position p of sequence b is row
  *                p % page_size of page block_table[b][p / page_size].
- * batch >= 0, max_pages >= 1; batch * max_pages <= 2^40.  Lists are 4-byte aligned.
+ * batch 0 .. 2^24, max_pages >= 1; batch * max_pages <= 2^40.  Lists are 4-byte aligned.
  * Their entries are not checked on the host (that would need a synchronisation); no
  * entry makes a kernel touch memory outside the buffers.
  */
@@ -552,7 +552,7 @@ int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, con
  *   cu_q, cu_k  int32 [batch + 1] on the device, not decreasing: sequence b has queries
  *               cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1.  Not checked on the
  *               host; no contents make the kernel touch memory outside the buffers.
- *   rows_q      0 .. 2^31 - 512.   rows_k  0 .. 2^25.
+ *   batch       0 .. 2^24.   rows_q  0 .. 2^31 - 512.   rows_k  0 .. 2^25.
  *   heads       a multiple of kv_heads; heads * head_dim <= 2^24.
  *   head_dim    64, 128 or 256.        scale  finite, > 0 (e.g. head_dim^-0.5).
  *   causal      0 or 1.

@@ -41,6 +41,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int64_t kMaxCols = int64_t(1) << 24;
 constexpr int64_t kMaxRows = int64_t(1) << 40;
+// Sequences of a call: the kernels count them in 32 bits, up to a thousand past the last, and the prompt
+// kernel looks a unit's up 32 at a time while its other warps wait for it, at most 2 s.
+constexpr int64_t kMaxBatch = int64_t(1) << 24;
 
 // Byte range [p, p + n) of a buffer, for overlap checks.
 struct Span {
@@ -738,7 +741,7 @@ int check_cache_buffers(const char* fn, CacheShape& c) {
 
 int check_lists(const char* fn, const int32_t* cu_rows, const int32_t* kv_len, const int32_t* block_table,
                 int64_t batch, int64_t max_pages) {
-  if (batch < 0 || batch >= (int64_t(1) << 31)) return invalid(fn, "batch must be in [0, 2^31)");
+  if (batch < 0 || batch > kMaxBatch) return invalid(fn, "batch must be in [0, 2^24]");
   if (max_pages < 1) return invalid(fn, "max_pages must be >= 1");
   if (batch > 0 && max_pages > (int64_t(1) << 40) / batch) return invalid(fn, "batch * max_pages exceeds 2^40");
   if (batch == 0) return 0;
@@ -858,7 +861,7 @@ int h3q_attention_varlen(const void* q, int64_t ld_q, const void* k, int64_t ld_
   if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
   if (rows_q < 0 || rows_q > kMaxPacked) return invalid(fn, "rows_q must be in [0, 2^31 - 512]");
   if (rows_k < 0 || rows_k > kMaxKeys) return invalid(fn, "rows_k must be in [0, 2^25]");
-  if (batch < 0 || batch >= (int64_t(1) << 31)) return invalid(fn, "batch must be in [0, 2^31)");
+  if (batch < 0 || batch > kMaxBatch) return invalid(fn, "batch must be in [0, 2^24]");
   if (causal != 0 && causal != 1) return invalid(fn, "causal must be 0 or 1");
   if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
   if (rows_q == 0 || batch == 0) return H3Q_OK;
