@@ -49,6 +49,7 @@
 #include <cmath>
 
 #include "attention_cache.cuh"
+#include "h3q_ring.h"
 
 namespace h3q {
 namespace {
@@ -178,15 +179,10 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
       if (r.count > 0) page = page_number();
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        const uint32_t slot = n % S::kSlots, bar = bar_full + 8 * slot;
-        if (!__all_sync(0xffffffffu, wait_bounded(bar_empty + 8 * slot, ((n / S::kSlots) & 1) ^ 1u))) {
-          ok = false;   // a computing warp never came: nothing more is copied (it gives up by itself)
-          if (lane == 0) {
-            *abort = 1;
-            atomicExch(&g_cache_attention_fault, 1);
-          }
-          break;
-        }
+        const uint32_t slot = fill_slot(n, S::kSlots), bar = bar_full + 8 * slot;
+        ok = __all_sync(0xffffffffu, wait_or_abort(bar_empty + 8 * slot, fill_parity(n, S::kSlots) ^ 1u, abort,
+                                                   &g_cache_attention_fault));
+        if (!ok) break;
         if (lane == 0) mbar_expect_tx(bar, __popc(live) / 2 * piece_keys * (HD / 2 + HD / 16));
         __syncwarp();
         if (mine)
@@ -195,6 +191,9 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         ++n;
       }
     }
+    // computing warps that give up do not wait for the copies: they have landed before the CTA goes
+    for (uint32_t k = first_fill_under_way(n, S::kSlots); k < n; ++k)
+      (void)wait_bounded(bar_full + 8 * fill_slot(k, S::kSlots), fill_parity(k, S::kSlots));
     return;
   }
 
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
   const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
   const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
   uint32_t slot = 0, parity = 0;   // of the slot that is taken next
-  bool alive = true;     // false: a wait ran out; the rest is computed from whatever is there
+  bool alive = true;     // false: a wait ran out; no further tile is computed, and no output stored
   auto take = [&]() {    // the slot, once it is full
     const uint32_t bar = bar_full + 8 * slot;
     if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) && alive)
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
     }
 
     const uint32_t seen_by_all = s.ctx < 0 ? 0 : min(s.ctx, s.len);
-    for (int tile = r.tile; tile < seg_end; ++tile) {
+    for (int tile = r.tile; alive && tile < seg_end; ++tile) {
       // this warp's keys of the tile; -1: none of them is in the sequence
       const uint32_t first_key = static_cast<uint32_t>(tile) * S::kKeys + warp * S::kWarpKeys;
       const bool work = first_key < static_cast<uint32_t>(s.len);
@@ -515,7 +514,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         constexpr int kPer = HD / 16;        // columns per thread, 16 threads a row
         const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
         const int rho = nt * 8 + row;
-        if (rho < live_rows) {
+        if (rho < live_rows && *abort == 0) {   // (a warp that has given up raised it before the barrier above)
           float m = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_ml[w * 8 + row].x);

@@ -35,6 +35,7 @@
 // for the converting warps beside the softmax: no faster, and 85 us.)
 // Every wait is bounded: one that runs out sets a device flag and tells the other roles to stop.
 #include "attention_cache.cuh"
+#include "h3q_ring.h"
 #include "h3q_tcgen05.cuh"
 
 namespace h3q {
@@ -531,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         if (w.count > 0) page = page_number();
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const uint32_t raw = n % S::kRaw, bar = bar_raw + 8 * raw;
-          if (!(ok = wait(bar_used + 8 * raw, ((n / S::kRaw) & 1) ^ 1u))) break;
+          const uint32_t raw = fill_slot(n, S::kRaw), bar = bar_raw + 8 * raw;
+          if (!(ok = wait(bar_used + 8 * raw, fill_parity(n, S::kRaw) ^ 1u))) break;
           if (lane == 0) mbar_expect_tx(bar, __popc(live) / 2 * piece_keys * (HD / 2 + HD / 16));
           __syncwarp();
           if (mine)
@@ -541,9 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           ++n;
         }
       }
-      if (!ok)   // every copy issued has landed before the CTA goes
-        for (uint32_t k = n < S::kRaw ? 0 : n - S::kRaw; k < n; ++k)
-          (void)wait_bounded(bar_raw + 8 * (k % S::kRaw), (k / S::kRaw) & 1);
+      // converting warps that give up do not wait for the copies: they have landed before the CTA goes
+      for (uint32_t k = first_fill_under_way(n, S::kRaw); k < n; ++k)
+        (void)wait_bounded(bar_raw + 8 * fill_slot(k, S::kRaw), fill_parity(k, S::kRaw));
     } else if (warp == kMmaWarp) {
       // ---- products.  The whole warp allocates the CTA's TMEM: all 512 columns, so they begin at 0.
       asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
