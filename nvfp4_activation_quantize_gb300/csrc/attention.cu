@@ -530,9 +530,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     // here); after an abort, every copy issued has landed.
     if (lane == 0) {
       const uint32_t first = pos < S::kStages ? 0 : pos - S::kStages;
-      for (uint32_t i = first; i < pos && !*abort; ++i)
+      for (uint32_t i = first; i < pos && !raised_here(abort); ++i)
         (void)wait_or_abort(bar_empty + 8 * (i % S::kStages), (i / S::kStages) & 1, abort);
-      if (*abort) {
+      if (raised_here(abort)) {
         for (uint32_t i = first; i < pos; ++i) {
           const uint32_t stage = i % S::kStages;
           const bool raw = last_raw >> stage & 1;
@@ -575,7 +575,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             *abort = 1;
             atomicExch(&g_attention_fault, 1);
           }
-          if (__any_sync(0xffffffffu, late || *abort)) return false;
+          if (__any_sync(0xffffffffu, late || raised_here(abort))) return false;
         }
       }
     };
@@ -701,11 +701,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       }
       pos0 += 2 * tiles;
     }
-    if (*abort) {   // let what is issued finish before the TMEM is freed
-      __syncwarp();
-      commit_elected(bar_drain);
-      (void)wait_bounded(bar_drain, 0);
-    }
+    // what is issued finishes before the TMEM is freed, whoever gave up and when
+    commit_elected(bar_drain);
+    (void)wait_bounded(bar_drain, 0);
     __syncwarp();
   } else if (warp == kCheckWarp) {
     uint32_t pos0 = 0, raw_phase = 0;

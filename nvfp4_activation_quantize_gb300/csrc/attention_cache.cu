@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         constexpr int kPer = HD / 16;        // columns per thread, 16 threads a row
         const int row = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
         const int rho = nt * 8 + row;
-        if (rho < live_rows && *abort == 0) {   // (a warp that has given up raised it before the barrier above)
+        if (rho < live_rows && !raised_here(abort)) {   // (a warp that has given up raised it before the barrier above)
           float m = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) m = fmaxf(m, join_ml[w * 8 + row].x);

@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         ++o_count;
         tc_fence_after();
       }
-      if (*abort) ok = false;
+      if (raised(abort)) ok = false;
       // ---- join the streams, 32 columns at a time; write the outputs or leave the part
       const float m_mine = m_ref == -INFINITY ? -INFINITY : __fmul_rn(m_ref, c);
       if (x == 1) *join_ml = make_float2(m_mine, l);
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
               *abort = 1;
               atomicExch(&g_wide_fault, 1);
             }
-            if (__any_sync(0xffffffffu, late || *abort)) return false;
+            if (__any_sync(0xffffffffu, late || raised_here(abort))) return false;
           }
         }
       };
@@ -630,11 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         n0 += 2 * count;
         w.advance(a, count, kTileRows, kKeys);
       }
-      if (*abort) {   // let what is issued finish before the TMEM is freed
-        __syncwarp();
-        commit_elected(bar_drain);
-        (void)wait_bounded(bar_drain, 0);
-      }
+      // what is issued finishes before the TMEM is freed, whoever gave up and when
+      commit_elected(bar_drain);
+      (void)wait_bounded(bar_drain, 0);
+      __syncwarp();
       // the commits to the empty barriers arrive before the CTA goes
       for (uint32_t k = n0 < S::kSlots ? 0 : n0 - S::kSlots; ok && k < n0; ++k)
         ok = wait(bar_empty + 8 * (k % S::kSlots), (k / S::kSlots) & 1);
