@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
       for (int i = 0; i < HD; i += 32) {
         uint32_t o[32];
         __syncwarp();
-        if (rows && (x == 0 || two)) {
+        if (ok && rows && (x == 0 || two)) {   // (given up: the TMEM may not even be this CTA's yet)
           tc_load32(taddr_o + i, o);
           tc_wait_load(o);
         }

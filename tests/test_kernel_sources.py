@@ -30,3 +30,11 @@ def test_products_are_drained_on_every_way_out(name):
     text = _source(name)
     at = text.index("commit_elected(bar_drain)")
     assert text[:at].rstrip().endswith("}") and "wait_bounded(bar_drain, 0)" in text[at:at + 120]
+
+
+def test_outputs_are_read_only_after_their_products():
+    """A role that gave up touches no TMEM: another may still write it, or not have been given it yet."""
+    text = _source("attention_cache_wide.cu")
+    reads = [m.start() for m in re.finditer(r"tc_load32\(taddr_o \+ i, o\)", text)]
+    assert len(reads) == 2   # the rescaling, inside a tile whose wait was met, and the join
+    assert re.search(r"if \(ok && rows && [^{]*\{\s*$", text[:reads[1]])
