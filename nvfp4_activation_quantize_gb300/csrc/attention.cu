@@ -54,6 +54,7 @@
 #include "h3q_internal.h"
 #include "h3q_softmax.cuh"
 #include "h3q_tcgen05.cuh"
+#include "h3q_units.h"
 
 namespace h3q {
 namespace {
@@ -231,7 +232,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
   const uint32_t bar_drain = bar_want + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kOffMisc + 4);
-  const uint32_t next_block = base + S::kOffMisc + 16;
+  const uint32_t next_block_at = base + S::kOffMisc + 16;
   Unit* units = reinterpret_cast<Unit*>(smem + S::kOffSlots);
   static_assert(sizeof(Unit) <= 96, "slots");
   constexpr int kReaders = 4 * S::kTiles + 3;   // warps that read a slot: softmax, TMA, products, check
@@ -769,14 +770,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       if (it >= kSlots && slot.redo != 0) from = it % kSlots;
       int found = -1;
       int64_t rank = 0;
-      if (from < 0 && block >= 0) {
+      // (a block past the last unit has none, but the one that the CTA is given in its place may)
+      bool asking = true;
+      while (from < 0 && block >= 0 && found < 0 && asking) {
         __syncwarp();
         if (lane == 0) {   // ask for the next while this one is looked up
           mbar_expect_tx(bar_next, 16);
           asm volatile(
               "fence.proxy.async.shared::cta;\n\t"
               "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                  next_block),
+                  next_block_at),
               "r"(bar_next)
               : "memory");
         }
@@ -804,7 +807,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
           write_unit<HD>(a, found, rank, slot);
           mbar_arrive(bar_unit + 8 * (it % kSlots));
         }
-        if (!__all_sync(0xffffffffu, wait_or_abort(bar_next, asked & 1, abort))) {
+        asking = __all_sync(0xffffffffu, wait_or_abort(bar_next, asked & 1, abort));
+        if (!asking) {
           (void)wait_bounded(bar_next, asked & 1);
           break;
         }
@@ -817,11 +821,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
             "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
             : "=r"(taken), "=r"(x)
-            : "r"(next_block)
+            : "r"(next_block_at)
             : "memory");
-        block = taken && found >= 0 ? static_cast<int64_t>(x) : -1;   // (blocks past the last unit have none)
-        if (found >= 0) continue;
+        block = next_block(taken != 0, static_cast<int64_t>(x), found >= 0, before);
       }
+      if (!asking) break;
+      if (found >= 0) continue;
       // No block left: the units under way may still have to be taken again.
       bool ok = true;
       for (int k = it - 1; from < 0 && ok && k >= 0 && k > it - kSlots; --k) {
