@@ -895,8 +895,9 @@ cudaError_t launch(const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t l
   err = persistent_blocks(reinterpret_cast<const void*>(&attention_kernel<HD>), kThreads, S::kSmem, 1, &one);
   if (err != cudaSuccess) return err;
   const int64_t span = static_cast<int64_t>(a.tokens) * S::kTiles;
-  // at most this many pairs of row tiles, however the rows fall into sequences
-  const int64_t pairs = (a.rows_q + a.batch * (span - 1)) / span;
+  // at most this many pairs of row tiles, however the rows fall into sequences (each has a row)
+  const int64_t most = (a.rows_q + a.batch * (span - 1)) / span;
+  const int64_t pairs = most < a.rows_q ? most : a.rows_q;
   const int64_t blocks = pairs * a.tile_groups;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   attention_kernel<HD><<<static_cast<unsigned>(blocks), kThreads, S::kSmem, stream>>>(map_q, map_k, map_v, a);
