@@ -8,7 +8,9 @@ fallback: if the library is missing or no GPU is present the calls raise.
 
 Outputs that are not passed in are allocated here with ``torch.empty`` in the
 shapes of the ABI (codes ``[rows, cols/2]`` uint8, scales
-``[pad128(rows), cols/16]`` uint8 in the 128x4 swizzled layout).
+``[pad128(rows), cols/16]`` uint8 in the 128x4 swizzled layout).  With a ``stream``
+other than the current one, that stream first waits for what the current one has queued
+(whose memory such an output may be made of) and the output is recorded on it.
 """
 from __future__ import annotations
 
@@ -166,13 +168,17 @@ def _contiguous(name, t, dtype, shape, device):
     return t
 
 
-def _outputs(device, rows, cols, codes, scales):
+def _outputs(device, rows, cols, codes, scales, stream):
     import torch
 
+    fresh = []
     if codes is None:
         codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
+        fresh.append(codes)
     if scales is None:
         scales = torch.empty((padded_rows(rows), cols // 16), dtype=torch.uint8, device=device)
+        fresh.append(scales)
+    _lend(stream, device, fresh)
     _contiguous("codes", codes, torch.uint8, (rows, cols // 2), device)
     _contiguous("scales", scales, torch.uint8, (padded_rows(rows), cols // 16), device)
     return codes, scales
@@ -199,13 +205,39 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _lend(stream, device, fresh) -> None:
+    """Tensors that the binding has just allocated, which torch does on the current stream, made ready for a
+    kernel on the stream argument: it waits for the current stream's work (which may still use the memory, or
+    fill it), and the memory is not given away before the kernel has ended."""
+    if stream is None or not fresh:
+        return
+    import torch
+
+    handle = _stream(stream, device)
+    if handle == _stream(None, device):
+        return
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):   # a number, or another library's object (1: the legacy default)
+        stream = (torch.cuda.default_stream(device) if handle <= 1
+                  else torch.cuda.ExternalStream(handle, device=device))
+
+    def capturing(s):
+        with torch.cuda.stream(s):
+            return torch.cuda.is_current_stream_capturing()
+
+    if capturing(stream) == capturing(current):   # (a graph cannot wait for work outside it, nor such work for it)
+        stream.wait_stream(current)
+    for t in fresh:
+        t.record_stream(stream)
+
+
 def h3q_quantize_nvfp4(x, global_scale, codes=None, scales=None, stream=None):
     """Standalone NVFP4 quantize of bf16 x [rows, cols]; returns (codes, scales)."""
     import torch
 
     x, rows, cols, ld = _rows_view("x", x, torch.bfloat16)
     dev = x.device
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_quantize_nvfp4(x.data_ptr(), ld, rows, cols, gsf.data_ptr(),
@@ -244,7 +276,7 @@ def h3q_rmsnorm_adaln_nvfp4(x, gamma, mod_table, global_scale, *, row_frame=None
     if row_rstd is not None:
         _contiguous("row_rstd", row_rstd, torch.float32, (rows,), dev)
         rstd_ptr = row_rstd.data_ptr()
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_rmsnorm_adaln_nvfp4(
@@ -264,7 +296,7 @@ def h3q_swiglu_nvfp4(gate, up, global_scale, codes=None, scales=None, stream=Non
     up, rows_u, cols_u, ldu = _rows_view("up", up, torch.bfloat16, dev)
     if (rows_u, cols_u) != (rows, cols):
         raise ValueError("gate and up must have the same shape")
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_swiglu_nvfp4(gate.data_ptr(), ldg, up.data_ptr(), ldu, rows, cols,
@@ -286,6 +318,7 @@ def h3q_dequantize_nvfp4(codes, scales, global_scale, out=None, stream=None):
     _contiguous("scales", scales, torch.uint8, (padded_rows(rows), cols // 16), dev)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.float32, device=dev)
+        _lend(stream, dev, [out])
     _contiguous("out", out, torch.float32, (rows, cols), dev)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
@@ -299,11 +332,12 @@ def h3q_dequantize_nvfp4(codes, scales, global_scale, out=None, stream=None):
 # dynamic and calibrated global scales                                          #
 # --------------------------------------------------------------------------- #
 
-def _amax_buffer(amax, device):
+def _amax_buffer(amax, device, stream):
     import torch
 
     if amax is None:
         amax = torch.zeros(1, dtype=torch.float32, device=device)
+        _lend(stream, device, [amax])
     _cuda_tensor("amax", amax, torch.float32, device)
     if amax.numel() != 1:
         raise ValueError("amax must hold one fp32 value")
@@ -316,7 +350,7 @@ def h3q_amax_bf16(x, amax=None, stream=None):
     import torch
 
     x, rows, cols, ld = _rows_view("x", x, torch.bfloat16)
-    amax = _amax_buffer(amax, x.device)
+    amax = _amax_buffer(amax, x.device, stream)
     with torch.cuda.device(x.device):
         rc = library().h3q_amax_bf16(x.data_ptr(), ld, rows, cols, amax.data_ptr(),
                                      _stream(stream, x.device))
@@ -344,7 +378,7 @@ def h3q_rmsnorm_adaln_amax(x, gamma, mod_table, *, row_frame=None, rows_per_fram
         rows_per_frame = 0
     elif rows_per_frame is None:
         raise ValueError("give row_frame or rows_per_frame")
-    amax = _amax_buffer(amax, dev)
+    amax = _amax_buffer(amax, dev, stream)
     rstd_ptr = None
     if row_rstd is not None:
         _contiguous("row_rstd", row_rstd, torch.float32, (rows,), dev)
@@ -378,7 +412,7 @@ def h3q_rmsnorm_adaln_nvfp4_from_rstd(x, gamma, mod_table, row_rstd, global_scal
         rows_per_frame = 0
     elif rows_per_frame is None:
         raise ValueError("give row_frame or rows_per_frame")
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_rmsnorm_adaln_nvfp4_from_rstd(
@@ -398,7 +432,7 @@ def h3q_swiglu_amax(gate, up, amax=None, stream=None):
     up, rows_u, cols_u, ldu = _rows_view("up", up, torch.bfloat16, dev)
     if (rows_u, cols_u) != (rows, cols):
         raise ValueError("gate and up must have the same shape")
-    amax = _amax_buffer(amax, dev)
+    amax = _amax_buffer(amax, dev, stream)
     with torch.cuda.device(dev):
         rc = library().h3q_swiglu_amax(gate.data_ptr(), ldg, up.data_ptr(), ldu, rows, cols,
                                        amax.data_ptr(), _stream(stream, dev))
@@ -415,6 +449,7 @@ def h3q_global_scale_from_amax(amax, global_scale=None, stream=None):
     dev = amax.device
     if global_scale is None:
         global_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        _lend(stream, dev, [global_scale])
     _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_global_scale_from_amax(amax.data_ptr(), global_scale.data_ptr(),
@@ -432,9 +467,10 @@ def h3q_quantize_nvfp4_dynamic(x, global_scale=None, codes=None, scales=None, st
 
     x, rows, cols, ld = _rows_view("x", x, torch.bfloat16)
     dev = x.device
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     if global_scale is None:
         global_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        _lend(stream, dev, [global_scale])
     _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_quantize_nvfp4_dynamic(x.data_ptr(), ld, rows, cols,
@@ -485,7 +521,7 @@ def h3q_residual_rmsnorm_adaln_nvfp4(h, o, gate_table, gamma, mod_table, global_
     if row_rstd is not None:
         _contiguous("row_rstd", row_rstd, torch.float32, (rows,), dev)
         rstd_ptr = row_rstd.data_ptr()
-    codes, scales = _outputs(dev, rows, cols, codes, scales)
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_residual_rmsnorm_adaln_nvfp4(
@@ -511,7 +547,7 @@ def h3q_swiglu_packed_nvfp4(o, global_scale, bias=None, codes=None, scales=None,
     if bias is not None:
         _contiguous("bias", bias, torch.bfloat16, (two_f,), dev)
         bias_ptr = bias.data_ptr()
-    codes, scales = _outputs(dev, rows, f, codes, scales)
+    codes, scales = _outputs(dev, rows, f, codes, scales, stream)
     gsf = _gsf(global_scale, dev)
     with torch.cuda.device(dev):
         rc = library().h3q_swiglu_packed_nvfp4(o.data_ptr(), ld, bias_ptr, rows, f, gsf.data_ptr(),
@@ -546,6 +582,7 @@ def h3q_qkv_epilogue(q, k, v, biases, cos, sin, heads, eps, outs=None, interleav
         cos_ptr, sin_ptr = cos.data_ptr(), sin.data_ptr()
     if outs is None:
         outs = [torch.empty((rows, heads, hd), dtype=torch.bfloat16, device=dev) for _ in range(3)]
+        _lend(stream, dev, outs)
     outs = [_contiguous(n, t, torch.bfloat16, (rows, heads, hd), dev)
             for n, t in zip(("q_out", "k_out", "v_out"), outs)]
     with torch.cuda.device(dev):
@@ -631,7 +668,7 @@ def h3q_gemm_swiglu_nvfp4(a_codes, a_scales, b_codes, b_scales, alpha, global_sc
             raise ValueError(f"{name} must be contiguous with {rows} x {k // 16} bytes")
     _gsf(alpha, dev)
     gsf = _gsf(global_scale, dev)
-    codes, scales = _outputs(dev, m, f, codes, scales)
+    codes, scales = _outputs(dev, m, f, codes, scales, stream)
     y_ptr = acc_ptr = None
     if y is not None:
         _contiguous("y", y, torch.bfloat16, (m, f), dev)
@@ -833,6 +870,7 @@ def h3q_kv_cache_read_nvfp4(cache, cu_rows, kv_len, block_table, k_global_scale,
         shape, dev = (rows, codes[1], 2 * codes[3]), cache[0].device
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        _lend(stream, dev, (k_out, v_out))
     else:
         k_out, v_out = outs
     rc = _native.read(cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, k_out, v_out,
@@ -860,23 +898,16 @@ def attention_cache_workspace_bytes(max_rows: int, heads: int, kv_heads: int, he
     return 608 * (64 + 2 * tile * (head_dim + 2) * 4)
 
 
-def _workspace(workspace, nbytes, stream, device):
-    """The caller's workspace, or one of torch's allocator that outlives the work on the stream."""
+def _workspace(workspace, nbytes, device, fresh):
+    """The caller's workspace, or one that joins the fresh tensors."""
     torch = _torch or _load_torch()
     if workspace is not None:
         _cuda_tensor("workspace", workspace, torch.uint8, device)
         if not workspace.is_contiguous() or workspace.numel() < nbytes:
             raise ValueError(f"workspace must be contiguous with at least {nbytes} bytes")
         return workspace
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        # allocated on the current stream: the kernels wait for what used the block there before,
-        # and the block is not given away before they are done
-        stream.wait_stream(torch.cuda.current_stream(device))
-        workspace.record_stream(stream)
-    return workspace
+    fresh.append(torch.empty(nbytes, dtype=torch.uint8, device=device))
+    return fresh[-1]
 
 
 def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, *, max_rows=1,
@@ -899,14 +930,17 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
     dev = q.device
     max_rows = int(max_rows)
     scale = float(dim ** -0.5 if scale is None else scale)
+    fresh = []
     if out is None:
         out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+        fresh.append(out)
     if len(cache) != 4 or len(getattr(cache[0], "shape", ())) != 4:
         _cache(cache)
     kv_heads = cache[0].shape[1]
     # (a number of heads that the call refuses needs no workspace to be refused)
     nbytes = attention_cache_workspace_bytes(max_rows, heads, kv_heads, dim) if kv_heads and heads >= kv_heads else 256
-    workspace = _workspace(workspace, nbytes, stream, dev)
+    workspace = _workspace(workspace, nbytes, dev, fresh)
+    _lend(stream, dev, fresh)
     rc = _native.cached(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, max_rows, tree_mask,
                         scale, out, lse, workspace, dev, _handle(stream))
     if rc is not None:
@@ -943,6 +977,7 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     scale = float(q_shape[2] ** -0.5 if scale is None else scale)
     if out is None:
         out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+        _lend(stream, dev, [out])
     causal = bool(causal)
     rc = _native.varlen(q, k, v, cu_q, cu_k, causal, scale, out, lse, dev, _handle(stream))
     if rc is not None:
