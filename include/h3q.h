@@ -543,9 +543,10 @@ int h3q_kv_cache_read_nvfp4(const uint8_t *k_codes, const uint8_t *k_scales, con
  * over the sequence's keys j, with `causal` those with j <= i + (keys - queries): the
  * last query sees the last key.  lse = m + log(sum_j e^(x_j - m)), natural.  A query that
  * sees no key gets o = 0 and lse = -inf.  Products are of bf16 values with fp32 sums, the
- * weights are rounded to bf16, everything else is fp32.  A key or value that is no
- * number reaches only the rows that see it (an infinite value as if its weight were
- * positive).
+ * weights are rounded to bf16, everything else is fp32.  The sums are formed before they
+ * are divided, so finite values give finite outputs up to a magnitude of 2^86.  A key or
+ * value that is no number reaches only the rows that see it (an infinite value as if its
+ * weight were positive).
  *
  *   q           bf16 [rows_q, heads * head_dim], row stride ld_q; k, v bf16 [rows_k,
  *               kv_heads * head_dim], row strides ld_k, ld_v.  32-byte aligned.

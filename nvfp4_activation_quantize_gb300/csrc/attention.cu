@@ -67,7 +67,8 @@ constexpr int kPlanWarp = 11;
 constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
 constexpr float kSlack = 8.0f;  // a row's reference moves when its maximum has passed it by 2^8,
-constexpr float kJump = 64.0f;  // at once when a tile passes it by 2^64 (sums then stay far below 2^127)
+constexpr float kJump = 16.0f;  // at once when a tile passes it by 2^16: over 2^25 keys the sums of weights stay
+                                // below 2^41, those of weights and values finite for values up to 2^86
 
 __device__ int g_attention_fault;
 
