@@ -15,8 +15,8 @@
 // goes into the softmax scale and into the output: keys and values enter the tensor
 // cores without a rounding.  A query row is scaled by the power of two that brings its
 // largest magnitude into [2^14, 2^15), where every bf16 value down to 2^-29 of it is
-// exact in fp16.  Weights e^(x - m) are scaled by 2^14 and rounded to fp16 (11 bits),
-// their sum is formed in fp32 from the unrounded ones; all accumulators are fp32.
+// exact in fp16.  Weights are held as 2^6 e^(x - reference), below 2^14, and rounded to fp16
+// once (11 bits), their sum is formed in fp32 from the unrounded ones; all accumulators are fp32.
 //
 // Products with mma.sync m16n8k16 (16 keys or 16 value columns by 8 rows): a
 // decoding step has 8 to 32 rows where a tcgen05 tile has 128.  S^T = K Q^T takes the
@@ -39,8 +39,8 @@
 // warp, four copies of 256 bytes and 2 KB a tile: 103 us for 64 tokens over 4,503 positions
 // each, 68 of them in the copies alone.)
 //
-// A row's weights are taken against a reference that follows its maximum only where that has
-// grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
+// A row's weights are taken against a reference, a power of two, that follows its maximum only where that
+// has grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
 //
 // Measured, 32 query heads over 8 key heads of 128: 64 tokens over 500 to 8,191 positions each in
 // 67 us (49 is the bytes' time at the copy rate), two tokens over 120,000 to 131,071 in 61 us (44).
@@ -119,6 +119,9 @@ struct Shape {
   static constexpr int kOffBar = kOffFactor + kRows * 4;
   static constexpr int kSmem = kOffBar + 2 * kSlots * 8 + 8;
 };
+
+// 2^e for e <= 0 (0 below 2^-126).
+__device__ __forceinline__ float power(int e) { return e < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // The computing warps' barrier (the copying warp runs ahead).
 __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -386,26 +389,31 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
               top[i] = __fmul_rn(m, cf[nt][i]);
             }
             if (__any_sync(0xffffffffu, top[0] > m_run[nt][0] + kSlack || top[1] > m_run[nt][1] + kSlack)) {
+              // The reference is a whole number (in units of log2), so what is taken to a new one is multiplied
+              // by a power of two: weights that are fp16 already are not rounded again.
               float alpha[2];
+              int down[2];   // log2 of alpha, as far as it matters
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 float m = top[i];
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                m = fmaxf(m_run[nt][i], m);
-                alpha[i] = ex2(__fadd_rn(m_run[nt][i], m == -INFINITY ? 0.0f : -m));
+                m = fmaxf(m_run[nt][i], ceilf(m));
+                down[i] = max(__float2int_rz(__fadd_rn(m_run[nt][i], m == -INFINITY ? 0.0f : -m)), -127);
+                alpha[i] = power(down[i]);
                 l_run[nt][i] = __fmul_rn(l_run[nt][i], alpha[i]);
                 m_run[nt][i] = m;
               }
               if constexpr (S::kMt * 16 < S::kWarpKeys) {   // weights of this tile that were formed before
-                const uint32_t other = half2_of(__shfl_sync(0xffffffffu, alpha[0], g >> 1),
-                                                __shfl_sync(0xffffffffu, alpha[1], g >> 1));
-                const uint32_t al = __byte_perm(other, other, g & 1 ? 0x3232 : 0x1010);   // row g's factor, twice
+                // row g's factor as two that fp16 holds (below 2^-48 it leaves nothing of a weight)
+                const int of0 = __shfl_sync(0xffffffffu, down[0], g >> 1), of1 = __shfl_sync(0xffffffffu, down[1], g >> 1);
+                const int e = max(g & 1 ? of1 : of0, -48), half = e / 2;
+                const uint32_t a0 = half2_of(power(half), power(half)), a1 = half2_of(power(e - half), power(e - half));
 #pragma unroll
                 for (int mt = 0; mt < sub; ++mt) {
-                  pf[mt][nt][0] = hmul2(pf[mt][nt][0], al);
-                  pf[mt][nt][1] = hmul2(pf[mt][nt][1], al);
+                  pf[mt][nt][0] = hmul2(hmul2(pf[mt][nt][0], a0), a1);
+                  pf[mt][nt][1] = hmul2(hmul2(pf[mt][nt][1], a0), a1);
                 }
               }
 #pragma unroll
