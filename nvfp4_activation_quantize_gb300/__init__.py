@@ -910,13 +910,14 @@ def _workspace(workspace, nbytes, device, fresh):
     return fresh[-1]
 
 
-def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, *, max_rows=1,
+def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_scale, v_global_scale, *, max_rows=None,
                               tree_mask=None, scale=None, out=None, lse=None, workspace=None, stream=None):
     """Attention of new tokens over the paged NVFP4 cache that holds their context and, at its
     end, themselves (written before with the same lists).
 
     ``q`` is bf16 [rows, heads, head_dim] (contiguous rows of any stride), heads a multiple of the
-    cache's.  Every sequence has at most ``max_rows`` (1 .. 64) new tokens.  ``tree_mask`` (int64
+    cache's.  Every sequence has at most ``max_rows`` (1 .. 64) new tokens; more of one are not computed.
+    It need not be given for one token a sequence, that is, for no more rows than sequences.  ``tree_mask`` (int64
     [rows]): bit j says that the token sees token j of its sequence; without it a token sees itself
     and those before.  ``scale`` defaults to head_dim ** -0.5.  ``lse`` (fp32 [heads, rows], optional)
     receives the log of the sums of exponentials.  ``workspace`` (uint8, at least
@@ -928,6 +929,11 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
     q_shape = q.shape
     rows, heads, dim = q_shape
     dev = q.device
+    if max_rows is None:
+        if isinstance(kv_len, torch.Tensor) and kv_len.dim() == 1 and rows > kv_len.shape[0]:
+            raise ValueError(f"q has {rows} rows for {kv_len.shape[0]} sequences: give max_rows, the most new tokens "
+                             "that one has")
+        max_rows = 1
     max_rows = int(max_rows)
     scale = float(dim ** -0.5 if scale is None else scale)
     fresh = []
