@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
         const uint16_t* src = a.q + (s.row0 + tok) * a.ld_q + static_cast<int64_t>(head) * HD + t * (HD / 4);
 #pragma unroll
         for (int i = 0; i < HD / 32; ++i) {
-          const uint4 v = load16_reused(src + 8 * i);
+          const uint4 v = load16_fresh(src + 8 * i);
           w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
         }
       } else {

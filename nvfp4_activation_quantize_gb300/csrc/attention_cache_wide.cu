@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           for (int i = 0; i < kSteps; ++i) {
             q[i] = make_uint4(0, 0, 0, 0);
             if (t < w.s.n)
-              q[i] = load16_reused(a.q + (w.s.row0 + t) * a.ld_q + static_cast<int64_t>(kv_head * a.group + h) * HD + col * 8);
+              q[i] = load16_fresh(a.q + (w.s.row0 + t) * a.ld_q + static_cast<int64_t>(kv_head * a.group + h) * HD + col * 8);
             for (h += kStep; h >= a.group; h -= a.group) ++t;
           }
         }

@@ -53,7 +53,8 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
 }
 
 // A launch that may begin while the stream's work before it ends: its CTAs are there when that is done.
-// Every thread of the kernel calls after_stream() before it reads or writes memory.  (A token's write and
+// Every thread of the kernel calls after_stream() before it reads or writes memory, and no load is .nc: memory may
+// change while the kernel is resident.  (A token's write and
 // attention at 777 positions, from a graph: 12.3 us, with plain launches 12.8; with the kernels letting the next
 // one in as they begin 12.5.)
 template <class... P, class... A>

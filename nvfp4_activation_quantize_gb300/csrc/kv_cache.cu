@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const RowsArgs a)
 #pragma unroll
         for (int i = 0; i < kWriteUnroll; ++i) {
           if (slot >= 0 && h + i < h1) {
-            load_stream(src + static_cast<int64_t>(h + i) * HD, x[i]);
+            load_fresh(src + static_cast<int64_t>(h + i) * HD, x[i]);
           } else {
 #pragma unroll
             for (int w = 0; w < 8; ++w) x[i].w[w] = 0;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const RowsArgs a) 
           lo[i] = hi[i] = sf[i] = 0;  // a row that the cache does not hold reads as zero
           if (slot >= 0 && h + i < h1) {
             const int64_t at = slot + (static_cast<int64_t>(h + i) << a.cache.page_shift);
-            asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
+            asm volatile("ld.global.L1::no_allocate.v2.b32 {%0,%1}, [%2];"
                          : "=r"(lo[i]), "=r"(hi[i])
                          : "l"(codes + at * (HD / 2) + blk * 8));
             sf[i] = scales[at * kBlocks + blk] & 0x7fu;

@@ -38,3 +38,11 @@ def test_outputs_are_read_only_after_their_products():
     reads = [m.start() for m in re.finditer(r"tc_load32\(taddr_o \+ i, o\)", text)]
     assert len(reads) == 2   # the rescaling, inside a tile whose wait was met, and the join
     assert re.search(r"if \(ok && rows && [^{]*\{\s*$", text[:reads[1]])
+
+
+@pytest.mark.parametrize("name", ["kv_cache.cu", "attention_cache.cu", "attention_cache_wide.cu", "attention_cache.cuh"])
+def test_kernels_launched_early_read_coherently(name):
+    """A kernel that is resident while the one before it still writes makes no load that promises constant data."""
+    text = _source(name)
+    assert "after_stream()" in text
+    assert not re.search(r"ld\.global\.nc|load_stream\(|load_reused\(|load16_stream\(|load16_reused\(|__ldg|__restrict__", text)
