@@ -52,6 +52,7 @@
 #include "h3q_async.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
+#include "h3q_roles.cuh"
 #include "h3q_softmax.cuh"
 #include "h3q_tcgen05.cuh"
 #include "h3q_units.h"

@@ -15,6 +15,7 @@
 #include "h3q_cache.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
+#include "h3q_roles.cuh"
 #include "h3q_softmax.cuh"
 
 namespace h3q {

@@ -84,13 +84,6 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
   return false;
 }
 
-// Whether a role has raised *abort: as this lane sees it now (another may see it a moment later), and as one
-// answer for a converged warp, whose next steps are the whole warp's (votes, elections, TMEM).
-__device__ __forceinline__ bool raised_here(const volatile int* abort) { return *abort != 0; }
-__device__ __forceinline__ bool raised(const volatile int* abort) {
-  return __any_sync(0xffffffffu, raised_here(abort));
-}
-
 // 1-D bulk copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
 // from global to shared memory, completing on the barrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {

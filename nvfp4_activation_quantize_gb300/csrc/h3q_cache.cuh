@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "h3q_device.cuh"
 #include "h3q_pages.h"
 
 namespace h3q {
@@ -54,9 +55,8 @@ __device__ __forceinline__ int warp_find_sequence(const int32_t* cu, int batch, 
 
 // A launch that may begin while the stream's work before it ends: its CTAs are there when that is done.
 // Every thread of the kernel calls after_stream() before it reads or writes memory, and no load is .nc: memory may
-// change while the kernel is resident.  (A token's write and
-// attention at 777 positions, from a graph: 12.3 us, with plain launches 12.8; with the kernels letting the next
-// one in as they begin 12.5.)
+// change while the kernel is resident.  (A token's write and attention at 777 positions, from a graph: 12.3 us,
+// with plain launches 12.8; with the kernels letting the next one in as they begin 12.5.)
 template <class... P, class... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
@@ -73,5 +73,22 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 }
 
 __device__ __forceinline__ void after_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// load_stream and load16_reused (h3q_device.cuh) for such kernels: what they read may change while they are
+// resident, which .nc promises it does not.
+__device__ __forceinline__ void load_fresh(const void* p, Block16& b) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3]), "=r"(b.w[4]),
+                 "=r"(b.w[5]), "=r"(b.w[6]), "=r"(b.w[7])
+               : "l"(p));
+}
+
+__device__ __forceinline__ uint4 load16_fresh(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 }  // namespace h3q

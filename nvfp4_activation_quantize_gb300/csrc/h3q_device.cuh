@@ -64,23 +64,6 @@ __device__ __forceinline__ uint4 load16_reused(const void* p) {
   return v;
 }
 
-// The same two for kernels that are launched before the work ahead of them on the stream has ended
-// (launch_early): what they read may change while they are resident, which .nc promises it does not.
-__device__ __forceinline__ void load_fresh(const void* p, Block16& b) {
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(b.w[0]), "=r"(b.w[1]), "=r"(b.w[2]), "=r"(b.w[3]), "=r"(b.w[4]),
-                 "=r"(b.w[5]), "=r"(b.w[6]), "=r"(b.w[7])
-               : "l"(p));
-}
-
-__device__ __forceinline__ uint4 load16_fresh(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 __device__ __forceinline__ void store16(void* p, uint4 v) {
   asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
