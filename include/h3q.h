@@ -426,12 +426,12 @@ int h3q_gemm_swiglu_nvfp4(const uint8_t *a_codes, const uint8_t *a_scales, int64
                           uint8_t *scales, void *y, float *acc, void *stream);
 
 /*
- * *flag = 1 if a kernel launched since the last call had one of its bounded
- * waits run out, else 0; the flag is cleared.  The kernels that wait on
+ * *flag = 1 if a kernel launched on the current device since the last call had one of
+ * its bounded waits run out, else 0; the flag is cleared.  The kernels that wait on
  * mbarriers between their warps (the GEMM of h3q_gemm_swiglu_nvfp4, and those of
  * h3q_attention_varlen and h3q_attention_cache_nvfp4) bound every wait (2 s) and
  * then stop early, leaving that call's outputs unspecified.  Synchronous: it waits
- * for the device.  Not on any page; a diagnostic of this library.
+ * for the device, all streams.  Not on any page; a diagnostic of this library.
  */
 int h3q_kernel_error_flag(int *flag);
 

@@ -540,7 +540,9 @@ int h3q_kernel_error_flag(int* flag) {
   g_last_error.clear();
   if (flag == nullptr) return invalid(fn, "flag must not be NULL");
   int gemm = 0, cache = 0, attention = 0;
-  cudaError_t err = h3q::gemm_error_flag(&gemm);
+  // (the copies below wait for the legacy default stream alone, which streams made non-blocking do not join)
+  cudaError_t err = cudaDeviceSynchronize();
+  if (err == cudaSuccess) err = h3q::gemm_error_flag(&gemm);
   if (err == cudaSuccess) err = h3q::cache_attention_error_flag(&cache);
   if (err == cudaSuccess) err = h3q::attention_error_flag(&attention);
   *flag = gemm | cache | attention;
