@@ -3,8 +3,10 @@
 Each translation unit under ``csrc/`` is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a``, then linked into
 ``_build/libh3q.so`` (CUDA runtime linked statically, so the library loads
-without a GPU); the Python binding's C part (``binding.c``, gcc) becomes
-``_build/h3q_binding.so``.  ``-fmad=false`` and the absence of fast-math keep every
+without a GPU).  The Python binding's C part (``binding.c``, gcc) becomes
+``_build/h3q_binding`` with the interpreter's extension suffix, so each interpreter has its
+own; where gcc or Python's headers are missing it is left out, and the binding checks
+its arguments in Python.  ``-fmad=false`` and the absence of fast-math keep every
 binary32 operation a separately rounded IEEE operation, which the kernels'
 bit-exactness relies on.  ptxas resource usage is kept in
 ``_build/ptxas.log``.
@@ -22,7 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libh3q.so")
-BINDING_PATH = os.path.join(BUILD_DIR, "h3q_binding.so")
+BINDING_PATH = os.path.join(BUILD_DIR, "h3q_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 HEADER = os.path.join(os.path.dirname(HERE), "include", "h3q.h")
 
 SOURCES = ["h3q_api.cu", "quantize.cu", "adaln.cu", "swiglu.cu", "dequantize.cu", "amax.cu",
@@ -45,16 +47,42 @@ def _inputs():
     return [p for p in deps if os.path.isfile(p)]
 
 
+def _newer_than_inputs(path) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in _inputs())
+
+
+def _binding_compiler():
+    """gcc with Python's headers, as a command's beginning; None where either is missing."""
+    gcc, include = shutil.which("gcc"), sysconfig.get_paths()["include"]
+    if gcc is None or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    return [gcc, "-O2", "-Wall", "-shared", "-fPIC", "-I", include]
+
+
 def is_fresh() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+    return _newer_than_inputs(LIB_PATH) and (_binding_compiler() is None or _newer_than_inputs(BINDING_PATH))
+
+
+def build_binding(force: bool = False) -> bool:
+    """Compile the binding's C part where that can be done; whether it is there."""
+    compiler = _binding_compiler()
+    if compiler is None:
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    if force or not _newer_than_inputs(BINDING_PATH):
+        os.makedirs(BUILD_DIR, exist_ok=True)
+        tmp = BINDING_PATH + f".{os.getpid()}.tmp"
+        res = subprocess.run([*compiler, os.path.join(CSRC, "binding.c"), "-o", tmp], capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"gcc failed on binding.c:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, BINDING_PATH)
+    return True
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libh3q.so unless it is already newer than its sources."""
-    if not force and is_fresh():
+    """Compile and link libh3q.so, and the binding's C part, unless they are newer than the sources."""
+    if not build_binding(force) and verbose:
+        print("gcc or Python.h is missing: the binding checks its arguments in Python", file=sys.stderr)
+    if not force and _newer_than_inputs(LIB_PATH):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -67,19 +95,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{res.stdout}\n{res.stderr}")
         return obj, res.stderr
 
-    def compile_binding():
-        tmp = BINDING_PATH + f".{os.getpid()}.tmp"
-        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
-               os.path.join(CSRC, "binding.c"), "-o", tmp]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"gcc failed on binding.c:\n{res.stdout}\n{res.stderr}")
-        os.replace(tmp, BINDING_PATH)
-
-    with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
-        binding = pool.submit(compile_binding)
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
         results = list(pool.map(compile_one, SOURCES))
-        binding.result()
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as log:
         for (_, err), src in zip(results, SOURCES):
             log.write(f"== {src}\n{err}\n")
