@@ -548,11 +548,12 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
           const int head = kv_head * a.group + (tile_row0 + rho) - tok * a.group;
           const int64_t out_row = s.row0 + tok;
           if (whole) {
-            const float f = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
+            const float f = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);   // (v_factor / l may be too small for fp32)
             uint32_t w[kPer / 2];
 #pragma unroll
             for (int i = 0; i < kPer / 2; ++i)
-              w[i] = float2_to_bf16x2(make_float2(__fmul_rn(v[2 * i], f), __fmul_rn(v[2 * i + 1], f)));
+              w[i] = float2_to_bf16x2(make_float2(__fmul_rn(__fmul_rn(v[2 * i], f), v_factor),
+                                                  __fmul_rn(__fmul_rn(v[2 * i + 1], f), v_factor)));
             uint16_t* dst = a.o + (out_row * a.heads + head) * HD + c0;
             if constexpr (kPer == 4) {
               *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);

@@ -354,12 +354,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) join_parts_kernel(const Args
   const int tok = (row0 + warp) / a.group;
   const int head = cut.kv_head * a.group + (row0 + warp) - tok * a.group;
   const int64_t out_row = s.row0 + tok;
-  const float f = lw == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(256.0f, *a.v_gsf), lw);
+  const float f = lw == 0.0f ? 0.0f : __fdiv_rn(1.0f, lw);
+  const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);   // (their product may be too small for fp32)
   uint16_t* dst = a.o + (out_row * a.heads + head) * HD + lane * kPer;
 #pragma unroll
   for (int i = 0; i < kPer; i += 2)
     *reinterpret_cast<uint32_t*>(dst + i) =
-        float2_to_bf16x2(make_float2(__fmul_rn(o[i], f), __fmul_rn(o[i + 1], f)));
+        float2_to_bf16x2(make_float2(__fmul_rn(__fmul_rn(o[i], f), v_factor), __fmul_rn(__fmul_rn(o[i + 1], f), v_factor)));
   if (a.lse != nullptr && lane == 0)
     a.lse[head * a.rows + out_row] =
         lw == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(mw, __fadd_rn(log2f(lw), -kPShift)), kLn2);

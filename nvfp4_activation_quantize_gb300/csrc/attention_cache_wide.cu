@@ -164,7 +164,6 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
     float2* join_ml = reinterpret_cast<float2*>(smem + S::kOffMl) + row;
     float* factors = reinterpret_cast<float*>(smem + S::kOffFactor);
     const float k_factor = __fmul_rn(__fdiv_rn(__fmul_rn(a.scale, kLog2e), *a.k_gsf), 256.0f);
-    const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
     auto sync_both = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     bool first_segment = true, ok = true;
     uint32_t s_count = 0, o_count = 0;
@@ -375,7 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
           m = top;
         }
       }
-      const float inv = l == 0.0f ? 0.0f : __fdiv_rn(v_factor, l);
+      // outputs are divided by the sum here, and scaled as they are stored: both at once may be too small for fp32
+      const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+      if constexpr (FEW) {
+        g0 = __fmul_rn(g0, inv);
+        g1 = __fmul_rn(g1, inv);
+      } else {
+        f0 = __fmul_rn(f0, inv);
+        f1 = __fmul_rn(f1, inv);
+      }
+      const float v_factor = __fdiv_rn(256.0f, *a.v_gsf);
       int rho_out = rho;
       asm volatile("" : "+r"(rho_out));   // (where it goes is formed here, not kept over the tiles)
       const int tok = rho_out / a.group, head = kv_head * a.group + rho_out - tok * a.group;
@@ -422,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
 #pragma unroll
               for (int h = 0; h < 4; ++h)
                 p[h] = l == 0.0f ? 0u
-                                 : float2_to_bf16x2(make_float2(__fmul_rn(v[k + 2 * h], inv), __fmul_rn(v[k + 2 * h + 1], inv)));
+                                 : float2_to_bf16x2(make_float2(__fmul_rn(v[k + 2 * h], v_factor),
+                                                                __fmul_rn(v[k + 2 * h + 1], v_factor)));
               store16(dst + k, make_uint4(p[0], p[1], p[2], p[3]));
             }
           } else {

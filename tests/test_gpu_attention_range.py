@@ -44,3 +44,26 @@ def test_large_values_and_rising_scores(dev, causal, dim, step, size):
     out = h3q.h3q_attention_varlen(q.bfloat16(), k.bfloat16(), v, cu, cu, causal=causal, scale=0.6931471805599453)
     err = (out.double() - column.double()).abs() / column.double()
     assert float(err.max()) <= 2 * 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -19
+
+
+@pytest.mark.parametrize("v_scale", [3.0e38, 1.0e36, 1.0, 1.0e-34])
+@pytest.mark.parametrize("new, heads, keys", [(1, 8, 6000), (1, 8, 40), (9, 8, 3000), (2, 16, 900)])
+def test_values_near_the_ends_of_fp32(dev, v_scale, new, heads, keys):
+    """Global scales of very small and of very large values: what the cache stands for is a number of fp32's range,
+    and so is the mean, whatever the sum of the weights is."""
+    page, kv_heads, dim = 64, 2, 128
+    table, pages = cc.paged(dev, [keys], page, 3)
+    cache = cc.random_cache(dev, pages, kv_heads, page, dim, 4)
+    cache[2].fill_(0x77)           # values of 6 ...
+    cache[3].copy_(cache[3] % 16 + 0x6f)   # ... under scales of 120 to 448: the mean is far above fp32's smallest
+    g = torch.Generator(device=dev)
+    g.manual_seed(6)
+    q = torch.randn((new, heads, dim), generator=g, device=dev).bfloat16()
+    lse = torch.empty((heads, new), device=dev)
+    gs = (2688.0, float(torch.tensor(v_scale)))
+    out = h3q.h3q_attention_cache_nvfp4(q, cache, cc.ints([0, new], dev), cc.ints([keys], dev), table,
+                                        *(torch.tensor([x], device=dev) for x in gs), max_rows=new, lse=lse)
+    k, v = cc.cache_values64(cache, gs, table[0], keys, page)
+    seen = torch.ones((new, keys), dtype=torch.bool, device=dev).tril(keys - new)
+    cc.check_attention(out, lse, cc.attention64(q, k, v, seen, dim ** -0.5), keys, 2.0 ** -11, f"scale {v_scale}")
+    assert bool((out != 0).any())
