@@ -483,6 +483,8 @@ int h3q_rmsnorm_adaln_nvfp4_host(const void *x_host, int64_t rows, int64_t cols,
  *           E2M1 codes a byte, the even element in the low nibble.  16-byte aligned.
  *   scales  k_scales, v_scales  uint8 [num_pages, kv_heads, page_size, head_dim/16]:
  *           one E4M3 scale per 16 elements, in order (not swizzled).  16-byte aligned.
+ *           Its low seven bits are read; all of them set (what a NaN leaves in the cache)
+ *           count as 480, in reading rows back as in attention.
  *   k_global_scale, v_global_scale  device fp32, finite and > 0 (not checked): the
  *           static per-tensor scales, one for keys and one for values.
  *   num_pages  1 .. 2^31 - 1.    page_size  16, 32, 64 or 128.
@@ -595,9 +597,8 @@ int h3q_attention_varlen(const void *q, int64_t ld_q, const void *k, int64_t ld_
  *               passed this call (two calls that may run at once need one each).
  * The cache and the lists as above.  A page that is not in [0, num_pages) is read as
  * page 0, and the outputs of its sequence are unspecified; kv_len counts at most
- * max_pages * page_size positions.  A scale byte of all ones (which a NaN leaves in the
- * cache) counts as 480.  Launches one or two kernels.  The result does not depend
- * on what else runs.
+ * max_pages * page_size positions.  Launches one or two kernels.  The result does not
+ * depend on what else runs.
  */
 static inline int64_t h3q_attention_cache_workspace_bytes(int64_t max_rows, int64_t heads, int64_t kv_heads,
                                                           int64_t head_dim)

@@ -64,7 +64,6 @@ constexpr int kThreads = 384;
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kCheckWarp = 10;
-constexpr int kPlanWarp = 11;
 constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
 constexpr float kSlack = 8.0f;  // a row's reference moves when its maximum has passed it by 2^8,
