@@ -39,9 +39,9 @@
 //   warp 11           the plan: which unit is next.  The CTA's own block first, then those of
 //                     blocks that have not started, which it takes over from the launch
 //
-// Measured: four frames of 2,040 tokens, 56 heads of 128, 1.28 ms (1.50 PFLOP/s at the power
+// Measured: four frames of 2,040 tokens, 56 heads of 128, 1.26 ms (1.52 PFLOP/s at the power
 // limit, where the library's products alone reach 1.70); 16 packed causal prompts, 32 heads over
-// 8, 0.218 ms; four chunks over their prefixes 0.205 ms (2.6 units a CTA, so a third of it is
+// 8, 0.218 ms; four chunks over their prefixes 0.203 ms (2.6 units a CTA, so a third of it is
 // the last ones' time).  A pair of tiles takes about 2,750 clocks: 1,235 from S to the weights,
 // the products' own, and the two warps' notices to each other.
 //

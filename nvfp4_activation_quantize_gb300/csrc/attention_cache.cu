@@ -600,9 +600,9 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
 
 // Rows that share a key head are taken 8, 16, 24 or 32 at a time: the fewest that hold them
 // all, so the cache is read once for up to 32 rows (16 at head_dim 256, where the
-// outputs of 32 would not fit the registers).  64 sequences of 4,503 positions at head_dim 128: 70, 106,
-// 148 and 214 us (20 rows as 32: 192).  More than kWideRows go to the tcgen05 kernel, which takes 206 us
-// for 28 and for 32 of them where this one takes 199 and 214 (148 to 153 against 115 at head_dim 64).
+// outputs of 32 would not fit the registers).  64 sequences of 4,503 positions at head_dim 128: 65, 104,
+// 141 and 213 us (20 rows as 32: 192).  More than kWideRows go to the tcgen05 kernel, which takes 201 and 200 us
+// for 28 and for 32 of them where this one takes 196 and 213 (148 and 141 against 113 at head_dim 64).
 constexpr int kWideRows = 32;
 template <int HD>
 cudaError_t dispatch(const Args& a, uint8_t* workspace, cudaStream_t stream) {

@@ -27,8 +27,8 @@
 // weights of the other's keys, and an output of its own, joined as the streams' are.
 //
 // Measured, 32 query heads over 8 key heads of 128: 16 trees of 9 to 16 tokens (36 to 64 rows a
-// key head) over 1,000 to 8,000 positions in 68 us (3 more with one thread a row), where the bytes take 13.  A
-// tile of 128 keys takes about 2,550 clocks; 1,530 of them shared memory is busy (queries, keys and values
+// key head) over 1,000 to 8,000 positions in 67 us (3 more with one thread a row), where the bytes take 13.  A
+// tile of 128 keys takes about 2,530 clocks; 1,530 of them shared memory is busy (queries, keys and values
 // read by the products 96 KB, fp16 tiles written 64 KB, codes in and out 36 KB, at 128 bytes a clock), and 17 us
 // are launch, plan, queries, first tile, outputs and the joining kernel.  Without the conversions it was 65 us
 // of 72, without the products 68, without the copies 69.  (Keys converted a tile ahead of values, fewer rows

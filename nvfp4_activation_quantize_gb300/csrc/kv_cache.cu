@@ -15,7 +15,7 @@
 // step of 64 rows x 8 heads has only 16 units if each warp takes them all, so heads
 // are dealt out until every SM has its warps.
 //
-// Measured: 65,280 rows x 56 heads x 128 written in 0.355 ms (0.354 is the bytes' time at the
+// Measured: 65,280 rows x 56 heads x 128 written in 0.354 ms (0.354 is the bytes' time at the
 // copy rate; heads per warp at most 4: 0.361, 16: 0.369 ms); the 160,272 rows x 8 heads x 128 of 32
 // prefixes read in 0.142 ms (0.124; heads per warp at most 8: 0.144, 2: 0.152; four heads' loads in
 // flight, not two: 0.158, occupancy 4 CTAs a SM instead of 5).  Units go round the warps: with a
