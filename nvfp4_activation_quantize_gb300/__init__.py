@@ -903,6 +903,11 @@ def attention_cache_workspace_bytes(max_rows: int, heads: int, kv_heads: int, he
     return 608 * (64 + 2 * tile * (head_dim + 2) * 4)
 
 
+def _softmax_scale(scale, dim) -> float:
+    """The scale, head_dim ** -0.5 when not given (any for a head_dim that the call refuses)."""
+    return float(scale) if scale is not None else dim ** -0.5 if dim else 1.0
+
+
 def _workspace(workspace, nbytes, device, fresh):
     """The caller's workspace, or one that joins the fresh tensors."""
     torch = _torch or _load_torch()
@@ -940,7 +945,7 @@ def h3q_attention_cache_nvfp4(q, cache, cu_rows, kv_len, block_table, k_global_s
                              "that one has")
         max_rows = 1
     max_rows = int(max_rows)
-    scale = float(dim ** -0.5 if scale is None else scale)
+    scale = _softmax_scale(scale, dim)
     fresh = []
     if out is None:
         out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
@@ -985,7 +990,7 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     if len(getattr(q, "shape", ())) != 3:
         _head_rows("q", q)
     q_shape, dev = q.shape, q.device
-    scale = float(q_shape[2] ** -0.5 if scale is None else scale)
+    scale = _softmax_scale(scale, q_shape[2])
     if out is None:
         out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
         _lend(stream, dev, [out])

@@ -17,7 +17,7 @@ def pytest_configure(config):
 
 # Host tests that make accepted calls with addresses of no memory: without a GPU such a call ends with the
 # library's CUDA error; on one it would launch a kernel that reads them.
-NO_MEMORY = ("test_abi.py", "test_attention_abi.py")
+NO_MEMORY = ("test_abi.py", "test_attention_abi.py", "test_attention_limits.py")
 
 
 def reaches_no_gpu(items, cuda_available):
