@@ -218,9 +218,9 @@ __global__ void __launch_bounds__(Shape<HD, NT>::kThreads, Shape<HD, NT>::kCtas)
       alive = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, &g_cache_attention_fault));
     return smem + slot * S::kSlotBytes;
   };
-  auto give = [&]() {    // every lane has read it
+  auto give = [&]() {    // every lane has read it; a warp that gave up keeps it, its copy may be under way
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_empty + 8 * slot);
+    if (lane < static_cast<int>(alive)) mbar_arrive(bar_empty + 8 * slot);
     if (++slot == S::kSlots) slot = 0, parity ^= 1u;
   };
 

@@ -46,3 +46,10 @@ def test_kernels_launched_early_read_coherently(name):
     text = _source(name)
     assert "after_stream()" in text
     assert not re.search(r"ld\.global\.nc|load_stream\(|load_reused\(|load16_stream\(|load16_reused\(|__ldg|__restrict__", text)
+
+
+def test_a_warp_that_gave_up_gives_no_slot_back():
+    """A slot whose copy was not waited for may still be written: it is not filled again."""
+    text = _source("attention_cache.cu")
+    gives = re.findall(r"if \(([^;]*?)\) mbar_arrive\(bar_empty", text)
+    assert len(gives) == 1 and "alive" in gives[0]
