@@ -571,8 +571,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
       for (uint32_t i = 1;; ++i) {
         if (!done) done = mbar_try_wait(bar, parity);
         if (__all_sync(0xffffffffu, done)) return true;
-        if ((i & 255u) == 0) {
-          const bool late = now_ns() - start > kWaitNs;
+        if ((i & (kPolls - 1)) == 0) {
+          const bool late = now_ns() - start >= kWaitNs;
           if (late && lane == 0) {
             *abort = 1;
             atomicExch(&g_attention_fault, 1);

@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) cache_attention_wide_kernel(const
         for (uint32_t i = 1;; ++i) {
           if (!done) done = mbar_try_wait(bar, parity);
           if (__all_sync(0xffffffffu, done)) return true;
-          if ((i & 255u) == 0) {
-            const bool late = now_ns() - start > kWaitNs;
+          if ((i & (kPolls - 1)) == 0) {
+            const bool late = now_ns() - start >= kWaitNs;
             if (late && lane == 0) {
               *abort = 1;
               atomicExch(&g_wide_fault, 1);

@@ -1,9 +1,13 @@
 // h3q_async.cuh -- mbarriers and bulk copies (sm_100+ asynchronous copies into
 // shared memory), shared by the kernels that stage their inputs with them.
 //
-// Every wait in the library's kernels is bounded in time: wait_bounded gives up
+// Every wait in the library's kernels is bounded in time: wait_or_abort gives up
 // after kWaitNs of the global timer, so a copy that never lands cannot keep a
 // kernel (and the GPU) waiting forever; the caller decides what to do then.
+// wait_bounded is for what is under way when a role has given up, and has its own limit.
+//
+// A test compiles the attention kernels with H3Q_SHORT_WAITS, a limit in nanoseconds that ordinary
+// waits pass (polls do not suspend then, and each looks at the clock), to see what they leave.
 #pragma once
 
 #include <cstdint>
@@ -11,7 +15,16 @@
 
 namespace h3q {
 
-constexpr uint64_t kWaitNs = 2000000000ull;  // a wait gives up after 2 s
+constexpr uint64_t kDrainNs = 2000000000ull;  // 2 s
+#ifdef H3Q_SHORT_WAITS
+constexpr uint64_t kWaitNs = H3Q_SHORT_WAITS;
+constexpr uint32_t kPolls = 1;
+#define H3Q_POLL "mbarrier.test_wait"
+#else
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kPolls = 256;              // between two looks at the clock (a power of two)
+#define H3Q_POLL "mbarrier.try_wait"
+#endif
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -41,7 +54,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      H3Q_POLL ".parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -56,14 +69,14 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 
 // Wait for the phase of parity `parity` of the barrier to complete; false if
-// kWaitNs went by first.
+// kDrainNs went by first.
 // The timer is read only once the first poll has failed: reading it costs more
 // than a poll, and most waits find the phase complete.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t start = now_ns();
   for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
-    if ((i & 255u) == 0 && now_ns() - start > kWaitNs) return false;
+    if ((i & 255u) == 0 && now_ns() - start > kDrainNs) return false;
   return true;
 }
 
@@ -74,9 +87,9 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
   const uint64_t start = now_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0) {
+    if ((i & (kPolls - 1)) == 0) {
       if (*abort) return false;
-      if (now_ns() - start > kWaitNs) break;
+      if (now_ns() - start >= kWaitNs) break;
     }
   }
   *abort = 1;
