@@ -43,7 +43,7 @@
 // has grown by more than 2^8, so most tiles need one vote and no exchange between lanes.
 //
 // Measured, 32 query heads over 8 key heads of 128: 64 tokens over 500 to 8,191 positions each in
-// 67 us (49 is the bytes' time at the copy rate), two tokens over 120,000 to 131,071 in 61 us (44).
+// 68 us (49 is the bytes' time at the copy rate), two tokens over 120,000 to 131,071 in 61 us (44).
 // Longer contexts cost the copy rate's time, 6.7 TB/s; 11 us are launch, plan, first tiles and join.  At 70
 // us it was 63 with the copies alone and 64 with the arithmetic alone.
 #include <cmath>
@@ -600,7 +600,7 @@ cudaError_t launch(Args a, uint8_t* workspace, cudaStream_t stream) {
 
 // Rows that share a key head are taken 8, 16, 24 or 32 at a time: the fewest that hold them
 // all, so the cache is read once for up to 32 rows (16 at head_dim 256, where the
-// outputs of 32 would not fit the registers).  64 sequences of 4,503 positions at head_dim 128: 65, 104,
+// outputs of 32 would not fit the registers).  64 sequences of 4,503 positions at head_dim 128: 66, 104,
 // 141 and 213 us (20 rows as 32: 192).  More than kWideRows go to the tcgen05 kernel, which takes 201 and 200 us
 // for 28 and for 32 of them where this one takes 196 and 213 (148 and 141 against 113 at head_dim 64).
 constexpr int kWideRows = 32;
