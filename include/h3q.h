@@ -616,6 +616,140 @@ int h3q_attention_cache_nvfp4(const void *q, int64_t ld_q, int64_t rows, int64_t
                               const float *v_global_scale, float scale, void *o, float *lse,
                               void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * QKV epilogue with rotary positions of several axes (the time, height and width of a video's
+ * or an image's tokens): bias, RMSNorm of each head with its weight, and a rotation by
+ * angles made here from the rows' positions; grouped heads.  Per row and head, in fp32
+ * with one rounding to bf16 at the end:
+ *   x' = x + b;  n = x' * rsqrt(mean(x'^2) + eps) * w  (q and k; n = x' without the norm);
+ *   for pair j = 0 .. ROT/2 - 1, of axis a(j): angle = positions[row][a(j)] * f[j],
+ *   (n_a, n_b) -> (n_a cos - n_b sin, n_a sin + n_b cos); the values beyond ROT = the sum of
+ *   axis_dims stay.  v: out = bf16(x').
+ * The pairs are (j, j + ROT/2), or with `interleaved` (2j, 2j + 1); the axes take them in order,
+ * axis_dims[i] / 2 each.  f of pair i of an axis of d values is scale * theta^(-2i/d); with
+ * `sections` it is scale * theta^(-2j/ROT) of the pair's number j in all of ROT.  The angle is
+ * reduced to a turn in integers before it becomes fp32, so it is as exact for a position of a million
+ * as for one of ten (off by at most 2^-50 of the position, and 2^-23 of a turn).
+ *
+ *   q              bf16 [rows, heads * head_dim], k and v [rows, kv_heads * head_dim], row
+ *                  strides ld_q, ld_k, ld_v (multiples of 16), 32-byte aligned.
+ *   bias_q/k/v     bf16 [columns of it], 32-byte aligned, or NULL: none.
+ *   weight_q/k     bf16 [head_dim], 32-byte aligned, or NULL: ones; NULL where norm = 0.
+ *   positions      int32 [rows, axes] contiguous, 4-byte aligned (any values).
+ *   axes           1 .. 4.   axis_dims, theta, scale: HOST arrays of that length, read during the
+ *                  call; axis_dims even and > 0, their sum ROT a multiple of 16, at most head_dim;
+ *                  theta finite, > 0; scale finite (a position's unit: a frame rate, an
+ *                  interpolation).  With `sections` the first axis's theta serves all.
+ *   norm           1, or 0: no norm (weights NULL).   sections, interleaved: 0 or 1.
+ *   heads          a multiple of kv_heads; heads * head_dim <= 2^24.  head_dim 64, 128 or 256.
+ *   eps            finite, >= 0 (with eps = 0 an all-zero head gives NaN values).
+ *   q_out          bf16 [rows, heads, head_dim], k_out and v_out [rows, kv_heads, head_dim],
+ *                  contiguous, 16-byte aligned; no output overlaps an input or another.
+ * rows = 0 returns H3Q_OK with no launch.  No page has a counterpart; the pages' own epilogue
+ * is h3q_qkv_epilogue.
+ */
+int h3q_qkv_epilogue_axes(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v,
+                          int64_t ld_v, const void *bias_q, const void *bias_k, const void *bias_v,
+                          const void *weight_q, const void *weight_k, const int32_t *positions,
+                          int64_t axes, const int64_t *axis_dims, const double *theta, const double *scale,
+                          int sections, int interleaved, int norm, int64_t rows, int64_t heads,
+                          int64_t kv_heads, int64_t head_dim, float eps, void *q_out, void *k_out,
+                          void *v_out, void *stream);
+
+/*
+ * Norms on both sides of a block with its gate and scaled residual, and NVFP4 of the result:
+ *   u  = bf16(fl(o + bias))                       (u = o without a bias)
+ *   n  = fl(fl(u * rstd(u)) * gamma_post),        then fl(n * gate[t]) with a gate table
+ *   h' = fl(fl(residual_scale * h) + n)           written back to h
+ *   y  = bf16(m), m = fl(fl(h' * rstd(h')) * gamma), with a modulation table
+ *        m = fl(fl(m * fl(1 + scale[t])) + shift[t])
+ * and the NVFP4 quantize of y.  t is the row's frame; both rstd have the canonical order and
+ * the eps of h3q_rmsnorm_adaln_nvfp4, so results are bit-exact.  Without tables it is the sandwich
+ * norm of language models.  h3q_residual_rmsnorm_adaln_nvfp4 is the same without the first norm.
+ *
+ *   h           fp32 [rows, cols], row stride ld_h (a multiple of 8), 32-byte aligned, updated.
+ *   o           bf16 [rows, cols], row stride ld_o.   bias  bf16 [cols] or NULL.
+ *   gamma_post, gamma  bf16 [cols].                   residual_scale  finite.
+ *   gate_table  bf16 [num_frames, cols] or NULL.      mod_table  bf16 [num_frames, 2, cols]
+ *               ([t, 0] shift, [t, 1] scale) or NULL.  32-byte aligned.
+ *   num_frames, row_frame, rows_per_frame: as h3q_rmsnorm_adaln_nvfp4; not looked at where there
+ *               is no table.
+ *   cols        at most 8,192.   codes, scales, row_rstd (of h'; may be NULL): as there.
+ * Other preconditions and status codes as h3q_residual_rmsnorm_adaln_nvfp4.
+ */
+int h3q_postnorm_residual_adaln_nvfp4(float *h, int64_t ld_h, const void *o, int64_t ld_o, const void *bias,
+                                      const void *gamma_post, const void *gate_table, float residual_scale,
+                                      const void *gamma, const void *mod_table, int64_t num_frames,
+                                      const int32_t *row_frame, int64_t rows_per_frame, float eps,
+                                      int64_t rows, int64_t cols, const float *global_scale,
+                                      uint8_t *codes, uint8_t *scales, float *row_rstd, void *stream);
+
+/*
+ * Sparse attention over blocks: each block of block_q consecutive queries of a sequence
+ * attends, for each key head, to a list of blocks of block_k consecutive keys of the sequence.
+ * h3q_select_blocks makes the lists, h3q_attention_blocks attends over them (or over any others).
+ *
+ *   cu_q, cu_k, batch, rows_q, rows_k, heads, kv_heads: packed sequences as in
+ *                h3q_attention_varlen.  head_dim 64 or 128.  `causal`: query i of a sequence sees
+ *                its keys j <= i + (keys - queries).
+ *   block_q, block_k  64, 128 or 256.  The last block of a sequence may be shorter.
+ *   blocks       int32 [kv_heads, h3q_block_rows(rows_q, batch, block_q), top]: query block i
+ *                of sequence b has row cu_q[b] / block_q + b + i.  Rows of no query block are
+ *                there too.
+ *   top          1 .. 4,096.
+ */
+static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
+{
+    return rows / block + batch;
+}
+
+/*
+ * The blocks that a query block attends to, by a cheap score: the mean of its query rows
+ * (over the heads of the group too) times the mean of the block's keys.  Each list holds
+ * the numbers of the `top` blocks with the highest scores (of equal ones those with the
+ * lowest numbers) in ascending order, then -1 where there are fewer blocks.  Always among them,
+ * whatever their scores: the first `first` blocks, and with `causal` those that hold the query
+ * block's own positions (keys - queries + i of query i); causal blocks of later keys alone are
+ * not candidates.  The choice is that of the exact scores: where fp32 is too coarse to tell,
+ * they are formed again in 64 bits.  A score that is no number counts as the lowest.
+ *
+ *   q            bf16 [rows_q, heads * head_dim], row stride ld_q; k bf16 [rows_k, kv_heads *
+ *                head_dim], row stride ld_k; 32-byte aligned.
+ *   first        0 .. top.  With causal, top >= first + ceil(block_q / block_k) + 1.
+ *   blocks       out, 4-byte aligned; rows of no query block get -1.
+ *   scores       out, fp32 of the same shape: the entries' scores, -inf beside -1; or NULL.
+ *   workspace    device memory of h3q_select_blocks_workspace_bytes bytes, 256-byte aligned, any
+ *                contents; not touched by other work until the stream has passed this call.
+ * rows_k / block_k <= 16,000.  rows_q <= 2^31 - 512.  Two launches.
+ */
+static inline int64_t h3q_select_blocks_workspace_bytes(int64_t rows_q, int64_t rows_k, int64_t batch,
+                                                        int64_t kv_heads, int64_t head_dim, int64_t block_q,
+                                                        int64_t block_k)
+{
+    int64_t rows = h3q_block_rows(rows_q, batch, block_q) + h3q_block_rows(rows_k, batch, block_k);
+    return rows * kv_heads * (head_dim + 1) * 8 + 256;
+}
+int h3q_select_blocks(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const int32_t *cu_q,
+                      const int32_t *cu_k, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads,
+                      int64_t kv_heads, int64_t head_dim, int64_t block_q, int64_t block_k, int64_t top,
+                      int causal, int64_t first, int32_t *blocks, float *scores, void *workspace,
+                      int64_t workspace_bytes, void *stream);
+
+/*
+ * Softmax attention as h3q_attention_varlen's over the keys of the listed blocks alone: prompts,
+ * video, and single new tokens (a sequence of one query).  An entry of a list counts
+ * if it is the number of a block of the sequence and above all entries before it that count
+ * (so a block named twice counts once); all others are passed over.  A query that sees no key gets
+ * o = 0 and lse = -inf.  Rounding, magnitudes, numbers that are none, o and lse as there.
+ * The kernel's waits are bounded (2 s): if one runs out it stops early, the outputs are
+ * unspecified, and h3q_kernel_error_flag reports it.
+ */
+int h3q_attention_blocks(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const void *v, int64_t ld_v,
+                         const int32_t *cu_q, const int32_t *cu_k, int64_t batch, int64_t rows_q,
+                         int64_t rows_k, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t block_q,
+                         int64_t block_k, const int32_t *blocks, int64_t top, int causal, float scale,
+                         void *o, float *lse, void *stream);
+
 /* Message for the calling thread's most recent failed call ("" if none). */
 const char *h3q_last_error(void);
 

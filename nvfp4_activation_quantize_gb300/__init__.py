@@ -31,6 +31,8 @@ __all__ = [
     "h3q_gemm_swiglu_nvfp4", "h3q_kernel_error_flag",
     "kv_cache_nvfp4", "h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4",
     "h3q_attention_cache_nvfp4", "attention_cache_workspace_bytes", "h3q_attention_varlen",
+    "h3q_qkv_epilogue_axes", "h3q_postnorm_residual_adaln_nvfp4",
+    "block_rows", "select_blocks_workspace_bytes", "h3q_select_blocks", "h3q_attention_blocks",
 ]
 
 H3Q_OK = 0
@@ -68,6 +70,14 @@ _SIGNATURES = {
                              ctypes.c_float, _P, _P, _P],
     "h3q_attention_cache_nvfp4": [_P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I64,
                                   _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _P, _I64, _P],
+    "h3q_qkv_epilogue_axes": [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P, ctypes.c_int,
+                              ctypes.c_int, ctypes.c_int, _I64, _I64, _I64, _I64, ctypes.c_float, _P, _P, _P, _P],
+    "h3q_postnorm_residual_adaln_nvfp4": [_P, _I64, _P, _I64, _P, _P, _P, ctypes.c_float, _P, _P, _I64, _P, _I64,
+                                          ctypes.c_float, _I64, _I64, _P, _P, _P, _P, _P],
+    "h3q_select_blocks": [_P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, ctypes.c_int,
+                          _I64, _P, _P, _P, _I64, _P],
+    "h3q_attention_blocks": [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P,
+                             _I64, ctypes.c_int, ctypes.c_float, _P, _P, _P],
 }
 
 _lock = threading.Lock()
@@ -1018,4 +1028,193 @@ def h3q_attention_varlen(q, k, v, cu_q, cu_k, *, causal=True, scale=None, out=No
     _invoke("h3q_attention_varlen", dev, stream,
             (qp, ld_q, kp, ld_k, vp, ld_v, cu_q_ptr, cu_k_ptr, lists[0] - 1, rows_q, rows_k, heads, kv_heads, dim,
              int(causal), scale, out_ptr, lse_ptr))
+    return out
+
+
+def _per_axis(name, value, axes):
+    """A number for all axes, or one for each, as a C array of doubles."""
+    values = [float(x) for x in value] if isinstance(value, (list, tuple)) else [float(value)] * axes
+    if len(values) != axes:
+        raise ValueError(f"{name} must be a number, or one for each axis")
+    return (ctypes.c_double * axes)(*values)
+
+
+def h3q_qkv_epilogue_axes(q, k, v, positions, axis_dims, heads, *, kv_heads=None, theta=10000.0, scale=1.0, sections=False,
+                          biases=None, weights=None, norm=True, eps=1e-6, interleaved=False, outs=None, stream=None):
+    """QKV epilogue with rotary positions of several axes: projected q [rows, heads * HD] and k, v
+    [rows, kv_heads * HD] bf16 (contiguous rows of any stride; ``kv_heads`` defaults to ``heads``) ->
+    (q_out, k_out, v_out), bf16 [rows, heads or kv_heads, HD].  q and k are biased, RMS-normed
+    per head (``norm``) and turned by the angles of ``positions`` (int32 [rows, axes], e.g. time, height,
+    width), v is biased.  ``axis_dims`` are the values of a head that turn with each axis, in order; pair i of
+    an axis of d values turns by scale * theta ** (-2 i / d) a step (``theta`` and ``scale``: a number, or one
+    per axis), or with ``sections`` pair j of all by scale * theta ** (-2 j / sum(axis_dims)).  Pairs are
+    (j, j + sum / 2), or (2j, 2j + 1) with ``interleaved``.  ``biases`` (of q, k and v) and ``weights`` (of
+    q's and k's norm, [HD]) are tuples of bf16 tensors, any of them None."""
+    torch = _torch or _load_torch()
+    kv_heads = heads if kv_heads is None else kv_heads
+    q, rows, d, ld_q = _rows_view("q", q, torch.bfloat16)
+    dev = q.device
+    k, rows_k, d_k, ld_k = _rows_view("k", k, torch.bfloat16, dev)
+    v, rows_v, d_v, ld_v = _rows_view("v", v, torch.bfloat16, dev)
+    if heads < 1 or kv_heads < 1 or d % heads:
+        raise ValueError("the columns of q must split into heads")
+    hd = d // heads
+    if (rows_k, d_k) != (rows, kv_heads * hd) or (rows_v, d_v) != (rows, kv_heads * hd):
+        raise ValueError("k and v must have q's rows and kv_heads heads of q's size")
+    axes = len(axis_dims)
+    positions_ptr = _dense("positions", positions, torch.int32, (rows, axes), dev)
+    b = [None if t is None else _dense(n, t, torch.bfloat16, (c,), dev)
+         for n, t, c in zip(("bias_q", "bias_k", "bias_v"), biases or (None,) * 3, (d, d_k, d_k))]
+    w = [None if t is None else _dense(n, t, torch.bfloat16, (hd,), dev)
+         for n, t in zip(("weight_q", "weight_k"), weights or (None,) * 2)]
+    if outs is None:
+        outs = [torch.empty((rows, h, hd), dtype=torch.bfloat16, device=dev) for h in (heads, kv_heads, kv_heads)]
+        _lend(stream, dev, outs)
+    o = [_dense(n, t, torch.bfloat16, (rows, h, hd), dev)
+         for n, t, h in zip(("q_out", "k_out", "v_out"), outs, (heads, kv_heads, kv_heads))]
+    _invoke("h3q_qkv_epilogue_axes", dev, stream,
+            (q.data_ptr(), ld_q, k.data_ptr(), ld_k, v.data_ptr(), ld_v, *b, *w, positions_ptr, axes,
+             (_I64 * axes)(*axis_dims), _per_axis("theta", theta, axes), _per_axis("scale", scale, axes),
+             int(bool(sections)), int(bool(interleaved)), int(bool(norm)), rows, heads, kv_heads, hd, float(eps), *o))
+    return outs[0], outs[1], outs[2]
+
+
+def h3q_postnorm_residual_adaln_nvfp4(h, o, gamma_post, gamma, global_scale, *, bias=None, gate_table=None,
+                                      mod_table=None, residual_scale=1.0, row_frame=None, rows_per_frame=None, eps=1e-6,
+                                      codes=None, scales=None, row_rstd=None, stream=None):
+    """The norm after a block, its gate and scaled residual, the norm before the next block -> NVFP4:
+    h (fp32 [rows, cols], updated in place) = residual_scale * h + gate_table[frame] * RMSNorm(bf16(o + bias)) *
+    gamma_post, then RMSNorm(h) * gamma with the modulation of ``mod_table`` (bf16 [frames, 2, cols]: [t, 0] shift,
+    [t, 1] scale).  ``gate_table`` (bf16 [frames, cols]), ``mod_table`` and ``bias`` may be None; with a
+    table the frame of a row is ``row_frame[row]`` (int32 CUDA tensor) or ``row // rows_per_frame``.
+    ``row_rstd`` (fp32 [rows], optional) receives the rstd of the new h.  Returns (codes, scales)."""
+    torch = _torch or _load_torch()
+    _cuda_tensor("h", h, torch.float32)
+    dev = h.device
+    if h.dim() != 2 or (h.shape[1] > 1 and h.stride(1) != 1):
+        raise ValueError("h must be 2-D with contiguous rows")
+    rows, cols = h.shape
+    ld_h = h.stride(0) if rows > 1 else cols
+    o, rows_o, cols_o, ld_o = _rows_view("o", o, torch.bfloat16, dev)
+    if (rows_o, cols_o) != (rows, cols):
+        raise ValueError("o must have the shape of h")
+    vector = (cols,)
+    bias_ptr = _dense("bias", bias, torch.bfloat16, vector, dev) if bias is not None else None
+    post_ptr = _dense("gamma_post", gamma_post, torch.bfloat16, vector, dev)
+    gamma_ptr = _dense("gamma", gamma, torch.bfloat16, vector, dev)
+    frames, gate_ptr, table_ptr, rf_ptr = 0, None, None, None
+    if gate_table is not None:
+        _cuda_tensor("gate_table", gate_table, torch.bfloat16, dev)
+        if gate_table.dim() != 2 or gate_table.shape[1] != cols or not gate_table.is_contiguous():
+            raise ValueError("gate_table must be contiguous [frames, cols]")
+        frames, gate_ptr = gate_table.shape[0], gate_table.data_ptr()
+    if mod_table is not None:
+        _cuda_tensor("mod_table", mod_table, torch.bfloat16, dev)
+        if (mod_table.dim() != 3 or mod_table.shape[1:] != (2, cols) or not mod_table.is_contiguous()
+                or (gate_table is not None and mod_table.shape[0] != frames)):
+            raise ValueError("mod_table must be contiguous [frames, 2, cols], frames as gate_table")
+        frames, table_ptr = mod_table.shape[0], mod_table.data_ptr()
+    if gate_ptr is not None or table_ptr is not None:
+        if row_frame is not None:
+            rf_ptr = _dense("row_frame", row_frame, torch.int32, (rows,), dev)
+            rows_per_frame = 0
+        elif rows_per_frame is None:
+            raise ValueError("give row_frame or rows_per_frame")
+    rstd_ptr = _dense("row_rstd", row_rstd, torch.float32, (rows,), dev) if row_rstd is not None else None
+    codes, scales = _outputs(dev, rows, cols, codes, scales, stream)
+    _invoke("h3q_postnorm_residual_adaln_nvfp4", dev, stream,
+            (h.data_ptr(), ld_h, o.data_ptr(), ld_o, bias_ptr, post_ptr, gate_ptr, float(residual_scale), gamma_ptr,
+             table_ptr, frames, rf_ptr, int(rows_per_frame or 0), float(eps), rows, cols, _scale_ptr(global_scale, dev),
+             codes.data_ptr(), scales.data_ptr(), rstd_ptr))
+    return codes, scales
+
+
+def block_rows(rows: int, batch: int, block: int) -> int:
+    """Rows of the lists of blocks (h3q_block_rows in include/h3q.h): query block i of sequence b has row
+    cu[b] // block + b + i."""
+    return rows // block + batch
+
+
+def select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, head_dim, block_q, block_k) -> int:
+    """Device workspace bytes of h3q_select_blocks (h3q_select_blocks_workspace_bytes in include/h3q.h)."""
+    rows = block_rows(rows_q, batch, block_q) + block_rows(rows_k, batch, block_k)
+    return rows * kv_heads * (head_dim + 1) * 8 + 256
+
+
+def _block_sequences(q, k, cu_q, cu_k):
+    """Checks what the calls over blocks share; returns (q, ld_q, k, ld_k, cu_q, cu_k, batch, rows_q, rows_k, heads,
+    kv_heads, dim, device)."""
+    torch = _torch
+    qp, (rows_q, heads, dim), ld_q = _head_rows("q", q)
+    dev = q.device
+    kp, (rows_k, kv_heads, dim_k), ld_k = _head_rows("k", k, dev)
+    if dim_k != dim:
+        raise ValueError("k must have q's head_dim")
+    if not (isinstance(cu_q, torch.Tensor) and cu_q.dim() == 1 and cu_q.shape[0] >= 1):
+        _cuda_tensor("cu_q", cu_q, torch.int32, dev)
+        raise ValueError("cu_q must be contiguous [batch + 1]")
+    lists = cu_q.shape
+    return (qp, ld_q, kp, ld_k, _dense("cu_q", cu_q, torch.int32, lists, dev),
+            _dense("cu_k", cu_k, torch.int32, lists, dev), lists[0] - 1, rows_q, rows_k, heads, kv_heads, dim, dev)
+
+
+def h3q_select_blocks(q, k, cu_q, cu_k, top, *, block_q=128, block_k=128, causal=False, first=0, blocks=None, scores=None,
+                      workspace=None, stream=None):
+    """The key blocks that each query block of packed sequences attends to: int32 [kv_heads,
+    block_rows(rows_q, batch, block_q), top], ascending, then -1 -- the ``top`` blocks with the highest scores
+    mean(queries of the block and group) . mean(keys of the block), ties to the lowest numbers; always the
+    ``first`` blocks and, with ``causal``, those of the query block's own positions.  q bf16
+    [rows_q, heads, head_dim], k bf16 [rows_k, kv_heads, head_dim] and cu_q, cu_k as h3q_attention_varlen
+    takes them.  ``scores`` (fp32 of the lists' shape, optional) receives the entries' scores.  Where
+    ``workspace`` (uint8, select_blocks_workspace_bytes) is not given it is allocated.  Returns the lists."""
+    torch = _torch or _load_torch()
+    qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, dev = _block_sequences(
+        q, k, cu_q, cu_k)
+    if block_q < 1 or block_k < 1:
+        raise ValueError("block_q and block_k must be 64, 128 or 256")
+    shape = (kv_heads, block_rows(rows_q, batch, block_q), int(top))
+    fresh = []
+    if blocks is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=dev)
+        fresh.append(blocks)
+    nbytes = select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, dim, block_q, block_k)
+    workspace = _workspace(workspace, nbytes, dev, fresh)
+    _lend(stream, dev, fresh)
+    blocks_ptr = _dense("blocks", blocks, torch.int32, shape, dev)
+    scores_ptr = _dense("scores", scores, torch.float32, shape, dev) if scores is not None else None
+    _invoke("h3q_select_blocks", dev, stream,
+            (qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, block_q, block_k,
+             shape[2], int(bool(causal)), int(first), blocks_ptr, scores_ptr, workspace.data_ptr(),
+             workspace.numel()))
+    return blocks
+
+
+def h3q_attention_blocks(q, k, v, cu_q, cu_k, blocks, *, block_q=128, block_k=128, causal=False, scale=None, out=None,
+                         lse=None, stream=None):
+    """Softmax attention as h3q_attention_varlen's over the key blocks that ``blocks`` (int32 [kv_heads,
+    block_rows(rows_q, batch, block_q), top], as h3q_select_blocks makes them) lists for each query block: entries
+    that are no block of the sequence, or not above those before them, are passed over.  head_dim 64 or 128.
+    ``lse`` (fp32 [heads, rows_q], optional) receives the log of the sums of exponentials.  Returns out, bf16
+    [rows_q, heads, head_dim]; rows of no sequence are left as they were."""
+    torch = _torch or _load_torch()
+    qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, dev = _block_sequences(
+        q, k, cu_q, cu_k)
+    vp, v_shape, ld_v = _head_rows("v", v, dev)
+    if v_shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    if block_q < 1 or block_k < 1:
+        raise ValueError("block_q and block_k must be 64, 128 or 256")
+    _cuda_tensor("blocks", blocks, torch.int32, dev)
+    rows = block_rows(rows_q, batch, block_q)
+    if blocks.dim() != 3 or tuple(blocks.shape[:2]) != (kv_heads, rows) or not blocks.is_contiguous():
+        raise ValueError(f"blocks must be contiguous [{kv_heads}, {rows}, top], got {tuple(blocks.shape)}")
+    if out is None:
+        out = torch.empty((rows_q, heads, dim), dtype=torch.bfloat16, device=dev)
+        _lend(stream, dev, [out])
+    out_ptr = _dense("out", out, torch.bfloat16, (rows_q, heads, dim), dev)
+    lse_ptr = _dense("lse", lse, torch.float32, (heads, rows_q), dev) if lse is not None else None
+    _invoke("h3q_attention_blocks", dev, stream,
+            (qp, ld_q, kp, ld_k, vp, ld_v, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, block_q,
+             block_k, blocks.data_ptr(), blocks.shape[2], int(bool(causal)), _softmax_scale(scale, dim), out_ptr,
+             lse_ptr))
     return out

@@ -539,13 +539,14 @@ int h3q_kernel_error_flag(int* flag) {
   static const char* fn = "h3q_kernel_error_flag";
   g_last_error.clear();
   if (flag == nullptr) return invalid(fn, "flag must not be NULL");
-  int gemm = 0, cache = 0, attention = 0;
+  int gemm = 0, cache = 0, attention = 0, blocks = 0;
   // (the copies below wait for the legacy default stream alone, which streams made non-blocking do not join)
   cudaError_t err = cudaDeviceSynchronize();
   if (err == cudaSuccess) err = h3q::gemm_error_flag(&gemm);
   if (err == cudaSuccess) err = h3q::cache_attention_error_flag(&cache);
   if (err == cudaSuccess) err = h3q::attention_error_flag(&attention);
-  *flag = gemm | cache | attention;
+  if (err == cudaSuccess) err = h3q::attention_blocks_error_flag(&blocks);
+  *flag = gemm | cache | attention | blocks;
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 
@@ -940,6 +941,291 @@ int h3q_attention_cache_nvfp4(const void* q, int64_t ld_q, int64_t rows, int64_t
       paged_cache(c), at, static_cast<const uint16_t*>(q), ld_q, rows, static_cast<int>(heads),
       static_cast<int>(max_rows), tree_mask, k_global_scale, v_global_scale, scale, static_cast<uint16_t*>(o), lse,
       static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+// --- rotary positions with several axes, norms around a block, attention over blocks --
+
+int h3q_qkv_epilogue_axes(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                          const void* bias_q, const void* bias_k, const void* bias_v, const void* weight_q,
+                          const void* weight_k, const int32_t* positions, int64_t axes, const int64_t* axis_dims,
+                          const double* theta, const double* scale, int sections, int interleaved, int norm,
+                          int64_t rows, int64_t heads, int64_t kv_heads, int64_t head_dim, float eps, void* q_out,
+                          void* k_out, void* v_out, void* stream) {
+  static const char* fn = "h3q_qkv_epilogue_axes";
+  g_last_error.clear();
+  if (rows < 0) return invalid(fn, "rows must be >= 0");
+  if (rows > kMaxRows) return invalid(fn, "rows exceeds 2^40");
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return invalid(fn, "head_dim must be 64, 128 or 256");
+  if (kv_heads < 1) return invalid(fn, "kv_heads must be >= 1");
+  if (heads < 1 || heads % kv_heads != 0) return invalid(fn, "heads must be a positive multiple of kv_heads");
+  if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
+  if (axes < 1 || axes > 4) return invalid(fn, "axes must be in [1, 4]");
+  if (axis_dims == nullptr || theta == nullptr || scale == nullptr)
+    return invalid(fn, "axis_dims, theta and scale must not be NULL");
+  int64_t rot = 0;
+  for (int64_t i = 0; i < axes; ++i) {
+    if (axis_dims[i] < 2 || axis_dims[i] % 2 != 0 || axis_dims[i] > head_dim)
+      return invalid(fn, "axis_dims must be positive, even and at most head_dim");
+    if (!std::isfinite(theta[i]) || !(theta[i] > 0.0)) return invalid(fn, "theta must be finite and > 0");
+    if (!std::isfinite(scale[i])) return invalid(fn, "scale must be finite");
+    rot += axis_dims[i];
+  }
+  if (rot % 16 != 0 || rot > head_dim)
+    return invalid(fn, "the sum of axis_dims must be a multiple of 16 and at most head_dim");
+  for (int flag : {sections, interleaved, norm})
+    if (flag != 0 && flag != 1) return invalid(fn, "sections, interleaved and norm must be 0 or 1");
+  if (!norm && (weight_q != nullptr || weight_k != nullptr)) return invalid(fn, "weights need the norm");
+  if (!std::isfinite(eps) || eps < 0.0f) return invalid(fn, "eps must be finite and >= 0");
+  h3q::RopeTurns turns{};
+  int64_t j = 0;
+  for (int64_t i = 0; i < axes; ++i)
+    for (int64_t p = 0; p < axis_dims[i] / 2; ++p, ++j) {
+      const double f = scale[i] * (sections ? std::pow(theta[0], -2.0 * static_cast<double>(j) / static_cast<double>(rot))
+                                            : std::pow(theta[i], -2.0 * static_cast<double>(p) /
+                                                                     static_cast<double>(axis_dims[i])));
+      constexpr double kTurn = 6.283185307179586476925;
+      const double t = f / kTurn;
+      if (!std::isfinite(t)) return invalid(fn, "theta and scale give a frequency that is not finite");
+      const double part = t - std::floor(t);   // of a turn, in [0, 1]
+      turns.of_pair[j] = part >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(part, 64));
+      turns.axis[j] = static_cast<uint8_t>(i);
+    }
+  if (rows == 0) return H3Q_OK;
+  const void* xs[3] = {q, k, v};
+  const int64_t lds[3] = {ld_q, ld_k, ld_v};
+  const int64_t ds[3] = {heads * head_dim, kv_heads * head_dim, kv_heads * head_dim};
+  const void* bs[3] = {bias_q, bias_k, bias_v};
+  const void* ws[2] = {weight_q, weight_k};
+  void* outs[3] = {q_out, k_out, v_out};
+  static const char* xn[3] = {"q", "k", "v"};
+  static const char* bn[3] = {"bias_q", "bias_k", "bias_v"};
+  static const char* wn[2] = {"weight_q", "weight_k"};
+  Span ins[9], os[3];
+  int n_in = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (int e = check_input(fn, xn[i], xs[i], lds[i], rows, ds[i])) return e;
+    ins[n_in++] = span(xs[i], view_bytes(rows, ds[i], lds[i]));
+    if (bs[i] != nullptr) {
+      if (int e = check_input(fn, bn[i], bs[i], ds[i], 1, ds[i])) return e;
+      ins[n_in++] = span(bs[i], ds[i] * 2);
+    }
+    if (i < 2 && ws[i] != nullptr) {
+      if (int e = check_input(fn, wn[i], ws[i], head_dim, 1, head_dim)) return e;
+      ins[n_in++] = span(ws[i], head_dim * 2);
+    }
+    if (outs[i] == nullptr || !aligned(outs[i], 16))
+      return invalid(fn, "q_out, k_out and v_out must be 16-byte aligned and not NULL");
+    os[i] = span(outs[i], rows * ds[i] * 2);
+  }
+  if (positions == nullptr || !aligned(positions, 4))
+    return invalid(fn, "positions must be 4-byte aligned and not NULL");
+  ins[n_in++] = span(positions, rows * axes * 4);
+  for (int i = 0; i < 3; ++i) {
+    for (int m = 0; m < n_in; ++m)
+      if (overlap(os[i], ins[m])) return invalid(fn, "outputs overlap an input or each other");
+    for (int m = i + 1; m < 3; ++m)
+      if (overlap(os[i], os[m])) return invalid(fn, "outputs overlap an input or each other");
+  }
+  const uint16_t* x16[3];
+  const uint16_t* b16[3];
+  uint16_t* o16[3];
+  for (int i = 0; i < 3; ++i) {
+    x16[i] = static_cast<const uint16_t*>(xs[i]);
+    b16[i] = static_cast<const uint16_t*>(bs[i]);
+    o16[i] = static_cast<uint16_t*>(outs[i]);
+  }
+  const uint16_t* w16[2] = {static_cast<const uint16_t*>(weight_q), static_cast<const uint16_t*>(weight_k)};
+  cudaError_t err = h3q::launch_qkv_axes(x16, lds, b16, w16, o16, positions, static_cast<int>(axes), turns,
+                                         static_cast<int>(rot), interleaved, norm, rows, static_cast<int>(heads),
+                                         static_cast<int>(kv_heads), static_cast<int>(head_dim), eps,
+                                         static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+int h3q_postnorm_residual_adaln_nvfp4(float* h, int64_t ld_h, const void* o, int64_t ld_o, const void* bias,
+                                      const void* gamma_post, const void* gate_table, float residual_scale,
+                                      const void* gamma, const void* mod_table, int64_t num_frames,
+                                      const int32_t* row_frame, int64_t rows_per_frame, float eps, int64_t rows,
+                                      int64_t cols, const float* global_scale, uint8_t* codes, uint8_t* scales,
+                                      float* row_rstd, void* stream) {
+  static const char* fn = "h3q_postnorm_residual_adaln_nvfp4";
+  g_last_error.clear();
+  const bool tables = gate_table != nullptr || mod_table != nullptr;
+  if (int e = check_shape(fn, rows, cols)) return e;
+  if (cols > 8192) return invalid(fn, "cols exceeds 8,192");
+  if (!std::isfinite(eps) || eps < 0.0f) return invalid(fn, "eps must be finite and >= 0");
+  if (!std::isfinite(residual_scale)) return invalid(fn, "residual_scale must be finite");
+  if (tables) {
+    if (num_frames < 1) return invalid(fn, "num_frames must be >= 1");
+    if (num_frames > (int64_t(1) << 31)) return invalid(fn, "num_frames exceeds 2^31");
+  } else {
+    num_frames = 0;
+    row_frame = nullptr;
+  }
+  if (rows == 0) return H3Q_OK;
+  if (h == nullptr || !aligned(h, 32)) return invalid(fn, "h must be a 32-byte aligned pointer");
+  if (ld_h < cols || ld_h % 8 != 0) return invalid(fn, "ld of h must be >= cols and a multiple of 8");
+  if (ld_h > (int64_t(1) << 61) / rows) return invalid(fn, "h: rows * ld overflows");
+  if (int e = check_input(fn, "o", o, ld_o, rows, cols)) return e;
+  if (bias != nullptr)
+    if (int e = check_input(fn, "bias", bias, cols, 1, cols)) return e;
+  if (int e = check_input(fn, "gamma_post", gamma_post, cols, 1, cols)) return e;
+  if (int e = check_input(fn, "gamma", gamma, cols, 1, cols)) return e;
+  if (gate_table != nullptr)
+    if (int e = check_input(fn, "gate_table", gate_table, cols, num_frames, cols)) return e;
+  if (mod_table != nullptr)
+    if (int e = check_input(fn, "mod_table", mod_table, cols, 2 * num_frames, cols)) return e;
+  if (int e = check_outputs(fn, codes, scales, global_scale)) return e;
+  if (row_frame != nullptr) {
+    if (!aligned(row_frame, 4)) return invalid(fn, "row_frame must be 4-byte aligned");
+  } else if (tables) {
+    if (rows_per_frame < 1) return invalid(fn, "rows_per_frame must be >= 1 when row_frame is NULL");
+    if ((rows - 1) / rows_per_frame >= num_frames) return invalid(fn, "rows / rows_per_frame reaches past the tables");
+  }
+  if (row_rstd != nullptr && !aligned(row_rstd, 4)) return invalid(fn, "row_rstd must be 4-byte aligned");
+  const Span none{0, 0};
+  const Span outs[4] = {span(h, ((rows - 1) * ld_h + cols) * 4), span(codes, h3q_code_bytes(rows, cols)),
+                        span(scales, h3q_scale_bytes(rows, cols)), row_rstd ? span(row_rstd, rows * 4) : none};
+  const Span ins[8] = {span(o, view_bytes(rows, cols, ld_o)), bias ? span(bias, cols * 2) : none,
+                       span(gamma_post, cols * 2), span(gamma, cols * 2),
+                       gate_table ? span(gate_table, num_frames * 2 * cols) : none,
+                       mod_table ? span(mod_table, num_frames * 4 * cols) : none,
+                       row_frame ? span(row_frame, rows * 4) : none, span(global_scale, 4)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& in : ins)
+      if (overlap(outs[i], in)) return invalid(fn, "an output (h, codes, scales, row_rstd) overlaps an input");
+    for (int m = i + 1; m < 4; ++m)
+      if (overlap(outs[i], outs[m])) return invalid(fn, "outputs overlap each other");
+  }
+  const h3q::PostnormArgs a{h, ld_h, static_cast<const uint16_t*>(o), ld_o, static_cast<const uint16_t*>(bias),
+                            static_cast<const uint16_t*>(gamma_post), static_cast<const uint16_t*>(gate_table),
+                            residual_scale, static_cast<const uint16_t*>(gamma),
+                            static_cast<const uint16_t*>(mod_table), num_frames, row_frame, rows_per_frame, eps, rows,
+                            cols, global_scale, codes, scales, row_rstd};
+  cudaError_t err = h3q::launch_postnorm(a, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+namespace {
+constexpr int64_t kMaxPacked = (int64_t(1) << 31) - 512;   // tensor-copy coordinates are 32-bit
+constexpr int64_t kMaxKeys = int64_t(1) << 25;
+constexpr int64_t kMaxTop = 4096;
+constexpr int64_t kMaxBlocks = 16000;                      // key blocks of a sequence whose scores a CTA holds
+
+// The shapes of the calls that attend over blocks; returns 0 or an error code.
+int check_blocks(const char* fn, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads, int64_t kv_heads,
+                 int64_t head_dim, int64_t block_q, int64_t block_k, int64_t top, int causal) {
+  if (head_dim != 64 && head_dim != 128) return invalid(fn, "head_dim must be 64 or 128");
+  if (kv_heads < 1) return invalid(fn, "kv_heads must be >= 1");
+  if (heads < 1 || heads % kv_heads != 0) return invalid(fn, "heads must be a positive multiple of kv_heads");
+  if (heads > kMaxCols / head_dim) return invalid(fn, "heads * head_dim exceeds 2^24");
+  if (block_q != 64 && block_q != 128 && block_q != 256) return invalid(fn, "block_q must be 64, 128 or 256");
+  if (block_k != 64 && block_k != 128 && block_k != 256) return invalid(fn, "block_k must be 64, 128 or 256");
+  if (top < 1 || top > kMaxTop) return invalid(fn, "top must be in [1, 4096]");
+  if (rows_q < 0 || rows_q > kMaxPacked) return invalid(fn, "rows_q must be in [0, 2^31 - 512]");
+  if (rows_k < 0 || rows_k > kMaxKeys) return invalid(fn, "rows_k must be in [0, 2^25]");
+  if (batch < 0 || batch > kMaxBatch) return invalid(fn, "batch must be in [0, 2^24]");
+  if (causal != 0 && causal != 1) return invalid(fn, "causal must be 0 or 1");
+  return 0;
+}
+
+int check_offsets(const char* fn, const int32_t* cu_q, const int32_t* cu_k) {
+  if (cu_q == nullptr || cu_k == nullptr || !aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return invalid(fn, "cu_q and cu_k must be 4-byte aligned and not NULL");
+  return 0;
+}
+
+h3q::BlockShape block_shape(const int32_t* cu_q, const int32_t* cu_k, int64_t batch, int64_t rows_q, int64_t rows_k,
+                            int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t block_q, int64_t block_k,
+                            int64_t top, int causal) {
+  return {cu_q, cu_k, static_cast<int>(batch), rows_q, rows_k, static_cast<int>(heads), static_cast<int>(kv_heads),
+          static_cast<int>(head_dim), static_cast<int>(block_q), static_cast<int>(block_k), static_cast<int>(top),
+          causal};
+}
+}  // namespace
+
+int h3q_select_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const int32_t* cu_q,
+                      const int32_t* cu_k, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads,
+                      int64_t kv_heads, int64_t head_dim, int64_t block_q, int64_t block_k, int64_t top, int causal,
+                      int64_t first, int32_t* blocks, float* scores, void* workspace, int64_t workspace_bytes,
+                      void* stream) {
+  static const char* fn = "h3q_select_blocks";
+  g_last_error.clear();
+  if (int e = check_blocks(fn, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal)) return e;
+  if (rows_k / block_k > kMaxBlocks) return invalid(fn, "rows_k / block_k exceeds 16,000");
+  if (first < 0 || first > top) return invalid(fn, "first must be in [0, top]");
+  if (causal && top < first + (block_q + block_k - 1) / block_k + 1)
+    return invalid(fn, "top leaves no room for the first blocks and the queries' own");
+  const int64_t lists = h3q_block_rows(rows_q, batch, block_q);
+  if (lists * kv_heads > (int64_t(1) << 31) - 1 || (h3q_block_rows(rows_k, batch, block_k) + lists) * kv_heads >
+                                                       (int64_t(1) << 31) - 1)
+    return invalid(fn, "too many blocks: batch, rows and kv_heads give 2^31 lists or more");
+  if (lists == 0) return H3Q_OK;
+  const int64_t dq = heads * head_dim, dk = kv_heads * head_dim;
+  if (rows_q > 0)
+    if (int e = check_input(fn, "q", q, ld_q, rows_q, dq)) return e;
+  if (rows_k > 0)
+    if (int e = check_input(fn, "k", k, ld_k, rows_k, dk)) return e;
+  if (int e = check_offsets(fn, cu_q, cu_k)) return e;
+  if (blocks == nullptr || !aligned(blocks, 4)) return invalid(fn, "blocks must be 4-byte aligned and not NULL");
+  if (scores != nullptr && !aligned(scores, 4)) return invalid(fn, "scores must be 4-byte aligned");
+  if (workspace == nullptr || !aligned(workspace, 256)) return invalid(fn, "workspace must be 256-byte aligned");
+  if (workspace_bytes < h3q_select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, head_dim, block_q, block_k))
+    return invalid(fn, "workspace_bytes is below h3q_select_blocks_workspace_bytes");
+  const int64_t entries = lists * kv_heads * top;
+  const Span outs[3] = {span(blocks, entries * 4), scores ? span(scores, entries * 4) : Span{0, 0},
+                        span(workspace, workspace_bytes)};
+  const Span ins[] = {rows_q > 0 ? span(q, view_bytes(rows_q, dq, ld_q)) : Span{0, 0},
+                      rows_k > 0 ? span(k, view_bytes(rows_k, dk, ld_k)) : Span{0, 0}, span(cu_q, (batch + 1) * 4),
+                      span(cu_k, (batch + 1) * 4)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Span& in : ins)
+      if (overlap(outs[i], in)) return invalid(fn, "an output or the workspace overlaps an input");
+    for (int m = 0; m < i; ++m)
+      if (overlap(outs[i], outs[m])) return invalid(fn, "outputs and workspace overlap each other");
+  }
+  cudaError_t err = h3q::launch_select_blocks(
+      block_shape(cu_q, cu_k, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal),
+      static_cast<const uint16_t*>(q), ld_q, static_cast<const uint16_t*>(k), ld_k, static_cast<int>(first), blocks,
+      scores, static_cast<uint8_t*>(workspace), static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
+}
+
+int h3q_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                         const int32_t* cu_q, const int32_t* cu_k, int64_t batch, int64_t rows_q, int64_t rows_k,
+                         int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t block_q, int64_t block_k,
+                         const int32_t* blocks, int64_t top, int causal, float scale, void* o, float* lse,
+                         void* stream) {
+  static const char* fn = "h3q_attention_blocks";
+  g_last_error.clear();
+  if (int e = check_blocks(fn, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal)) return e;
+  if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
+  if (rows_q == 0 || batch == 0) return H3Q_OK;
+  const int64_t dq = heads * head_dim, dk = kv_heads * head_dim;
+  if (int e = check_input(fn, "q", q, ld_q, rows_q, dq)) return e;
+  if (rows_k > 0) {
+    if (int e = check_input(fn, "k", k, ld_k, rows_k, dk)) return e;
+    if (int e = check_input(fn, "v", v, ld_v, rows_k, dk)) return e;
+  }
+  if (int e = check_offsets(fn, cu_q, cu_k)) return e;
+  if (blocks == nullptr || !aligned(blocks, 4)) return invalid(fn, "blocks must be 4-byte aligned and not NULL");
+  if (o == nullptr || !aligned(o, 16)) return invalid(fn, "o must be 16-byte aligned and not NULL");
+  if (lse != nullptr && !aligned(lse, 4)) return invalid(fn, "lse must be 4-byte aligned");
+  const Span outs[2] = {span(o, rows_q * dq * 2), lse ? span(lse, heads * rows_q * 4) : Span{0, 0}};
+  const Span ins[] = {span(q, view_bytes(rows_q, dq, ld_q)),
+                      rows_k > 0 ? span(k, view_bytes(rows_k, dk, ld_k)) : Span{0, 0},
+                      rows_k > 0 ? span(v, view_bytes(rows_k, dk, ld_v)) : Span{0, 0},
+                      span(cu_q, (batch + 1) * 4), span(cu_k, (batch + 1) * 4),
+                      span(blocks, h3q_block_rows(rows_q, batch, block_q) * kv_heads * top * 4)};
+  for (const Span& out : outs)
+    for (const Span& in : ins)
+      if (overlap(out, in)) return invalid(fn, "an output overlaps an input");
+  if (overlap(outs[0], outs[1])) return invalid(fn, "o and lse overlap");
+  cudaError_t err = h3q::launch_attention_blocks(
+      block_shape(cu_q, cu_k, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal),
+      static_cast<const uint16_t*>(q), ld_q, static_cast<const uint16_t*>(k), ld_k, static_cast<const uint16_t*>(v),
+      ld_v, blocks, scale, static_cast<uint16_t*>(o), lse, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }
 

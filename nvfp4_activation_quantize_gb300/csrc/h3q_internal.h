@@ -135,6 +135,62 @@ cudaError_t launch_attention(const uint16_t* q, int64_t ld_q, const uint16_t* k,
                              uint16_t* o, float* lse, cudaStream_t stream);
 cudaError_t attention_error_flag(int* flag);
 
+// QKV epilogue with rotary positions of several axes: pair j of the rotated part belongs to
+// axis[j] and turns by of_pair[j] / 2^64 of a turn for each step of that position.
+struct RopeTurns {
+  unsigned long long of_pair[128];
+  uint8_t axis[128];
+};
+cudaError_t launch_qkv_axes(const uint16_t* const x[3], const int64_t ld[3], const uint16_t* const bias[3],
+                            const uint16_t* const weight[2], uint16_t* const out[3], const int32_t* positions, int axes,
+                            const RopeTurns& turns, int rot, int interleaved, int norm, int64_t rows, int heads,
+                            int kv_heads, int head_dim, float eps, cudaStream_t stream);
+
+// The norm after a block, gate and scaled residual, the next norm with its modulation -> NVFP4 (rows of
+// at most 8,192 columns).
+struct PostnormArgs {
+  float* h;
+  int64_t ld_h;
+  const uint16_t* o;
+  int64_t ld_o;
+  const uint16_t* bias;        // [cols] or nullptr
+  const uint16_t* gamma_post;  // [cols]
+  const uint16_t* gate;        // [num_frames, cols] or nullptr
+  float keep;                  // s
+  const uint16_t* gamma;       // [cols]
+  const uint16_t* table;       // [num_frames, 2, cols] ([t, 0] shift, [t, 1] scale) or nullptr
+  int64_t num_frames;
+  const int32_t* row_frame;    // or nullptr: row / rows_per_frame
+  int64_t rows_per_frame;
+  float eps;
+  int64_t rows;
+  int64_t cols;
+  const float* gsf;
+  uint8_t* codes;
+  uint8_t* scales;
+  float* row_rstd;             // or nullptr
+};
+cudaError_t launch_postnorm(const PostnormArgs& a, cudaStream_t stream);
+
+// Blocks of keys for each block of queries.  Row r of the lists belongs to sequence b where
+// cu_q[b] / block_q + b <= r (the last such b), as its query block r - cu_q[b] / block_q - b.
+struct BlockShape {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int batch;
+  int64_t rows_q, rows_k;
+  int heads, kv_heads, head_dim;
+  int block_q, block_k;
+  int top;      // entries of a list
+  int causal;
+};
+cudaError_t launch_select_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k,
+                                 int first, int32_t* blocks, float* scores, uint8_t* workspace, cudaStream_t stream);
+cudaError_t launch_attention_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k,
+                                    int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* blocks, float scale,
+                                    uint16_t* o, float* lse, cudaStream_t stream);
+cudaError_t attention_blocks_error_flag(int* flag);
+
 // RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
 // copies pipelined with the producer over chunk_rows-row chunks; `workspace`
 // holds h3q_host_workspace_bytes(chunk_rows, cols, rows, row_frame == nullptr)
