@@ -9,12 +9,11 @@
 // to 128 rows (tokens x heads of one group), so that one has its softmax while the other has the
 // tensor cores.  A tile of 128 keys is two runs of 64, each anywhere in the sequence: a block of 64,
 // or half of a larger one's part.
-//   Where a query block fills both tiles, or one that has no partner (grouped heads, 256 tokens), they share
-//   every key tile: a ring of two K and two V tiles.
+//   Where a query block fills both tiles (grouped heads, 256 tokens), they share every key tile.
 //   Where it fills one (128 tokens of a head of its own), the tiles are neighbouring query blocks
-//   with a list each: every key tile is loaded for one row tile, K and V of each in a stage of
-//   its own.  That is 64 KB from L2 for 1,024 clocks of products, 64 bytes a clock of an SM, where copies of
-//   32 KB alone get 80 (23 TB/s) and those in runs of 64 keys 60.
+//   with a list each, and every key tile is loaded for one row tile.  That is 64 KB from L2 for 1,024 clocks
+//   of products, 64 bytes a clock of an SM, where copies of 32 KB alone get 80 (23 TB/s) and those in
+//   runs of 64 keys 60.
 //
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns one row of S in TMEM, takes the weights against
 //                     a reference that follows the row's maximum when that has grown by more than
@@ -55,8 +54,8 @@ constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;       // of a tile: two runs of 64
 constexpr int kRun = 64;
-constexpr int kStages = 4;       // K and V tiles: of row tile 0 and of 1, or two of both
-constexpr int kTellRing = 4;     // key tiles whose first keys are told ahead (three may be unread)
+constexpr int kStages = 5;       // K and V tiles in the ring, in the order of their products
+constexpr int kTellRing = 8;     // key tiles whose first keys are told ahead (those in the ring, and one more unread)
 constexpr int kMostPartial = 4;  // tiles that some row does not see whole: runs that begin among 64 + 255 keys
 constexpr float kSlack = 8.0f;   // a row's reference moves when its maximum has passed it by 2^8,
 constexpr float kJump = 16.0f;   // at once when a tile passes it by 2^16 (sums stay finite, see attention.cu)
@@ -90,8 +89,7 @@ struct Shape {
   static constexpr int kQBytes = kTileRows * HD * 2;
   static constexpr int kKvBytes = kKeys * HD * 2;
   static constexpr int kOffKv = 2 * kQBytes;
-  static constexpr int kOffOut = kOffKv + kStages * kKvBytes;   // 32 rows x 64 columns of output per softmax warp
-  static constexpr int kOffBar = kOffOut + 8 * 4096;
+  static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
   static constexpr int kBars = 4 * kStages + 12 + 2 * kSlots + 4;   // named in the kernel
   static constexpr int kOffMisc = kOffBar + 8 * kBars;    // TMEM address, abort; a taken block's id (16-byte aligned)
   static constexpr int kOffTell = kOffMisc + 32;          // [row tile][kTellRing] first keys of a tile's runs
@@ -342,7 +340,6 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const uint32_t taddr_o = lane_base + S::kO + x * HD;
     const uint32_t taddr = lane_base + x * S::kS;
     const float c = fmaxf(__fmul_rn(a.scale, kLog2e), 0x1p-126f);   // never 0: a hidden key's -inf stays one
-    uint8_t* staged = smem + S::kOffOut + warp * 4096;
     uint32_t s_count = 0, o_count = 0;   // S tiles and outputs waited for
     bool ok = true;
     Unit* u;
@@ -444,9 +441,9 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         tc_fence_after();
       }
       if (ok) {
-        // The row of O, scaled, through shared memory (the 16-byte pieces of a row in the order of
-        // their number's exclusive or with the row's, so that no two rows' meet in a bank), 128
-        // bytes of a row at a time, and out eight lanes a row.
+        // The row of O, scaled, 128 bytes at a time.  Eight lanes hold eight rows of eight 16-byte pieces: they
+        // exchange them (three steps of a transposition), so that a store writes whole rows of 128 bytes, eight
+        // lanes each.  (No shared memory: a stage of the ring more is worth more there.)
         const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
         const int64_t out_row = u->q0 + tok;
         const int head = u->head0 + row_head;
@@ -485,31 +482,35 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
               }
             }
           }
+          uint32_t w[8][4];
 #pragma unroll
-          for (int piece = 0; piece < 8; ++piece) {
-            uint32_t w[4];
+          for (int k = 0; k < 32; ++k) {
+            const float2 y = make_float2(__uint_as_float(o[k / 16][k % 16 * 2]), __uint_as_float(o[k / 16][k % 16 * 2 + 1]));
+            w[k / 4][k % 4] = l == 0.0f ? 0u : float2_to_bf16x2(mul2(y, make_float2(inv, inv)));
+          }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t* pair = o[piece / 4] + piece % 4 * 8 + 2 * k;
-              const float2 y = make_float2(__uint_as_float(pair[0]), __uint_as_float(pair[1]));
-              w[k] = l == 0.0f ? 0u : float2_to_bf16x2(mul2(y, make_float2(inv, inv)));
+          for (int step = 1; step < 8; step <<= 1) {
+            const bool upper = lane & step;
+#pragma unroll
+            for (int piece = 0; piece < 8; ++piece) {
+              if (piece & step) continue;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[piece][k] : w[piece | step][k], step);
+                if (upper) {
+                  w[piece][k] = got;
+                } else {
+                  w[piece | step][k] = got;
+                }
+              }
             }
-            *reinterpret_cast<uint4*>(staged + lane * 128 + ((piece ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
-          uint4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int r = 4 * k + (lane >> 3), piece = lane & 7;
-            v[k] = *reinterpret_cast<const uint4*>(staged + r * 128 + ((piece ^ (r & 7)) << 4));
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const unsigned long long to = __shfl_sync(0xffffffffu, dst, 4 * k + (lane >> 3));
-            if (to != 0) store16(reinterpret_cast<uint16_t*>(to) + i + 8 * (lane & 7), v[k]);
+          for (int k = 0; k < 8; ++k) {   // row k of the eight lanes' rows, piece lane % 8
+            const unsigned long long to = __shfl_sync(0xffffffffu, dst, (lane & 24) + k);
+            if (to != 0)
+              store16(reinterpret_cast<uint16_t*>(to) + i + 8 * (lane & 7), make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]));
           }
-          __syncwarp();
         }
         if (valid && a.lse != nullptr)
           a.lse[head * a.rows_q + out_row] =
@@ -527,7 +528,8 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const int runs_each = 1 << (a.shift_k - 6);
     bool ok = true;
     uint32_t q_count[2] = {0, 0}, told[2] = {0, 0};   // Q tiles issued, K tiles told
-    uint32_t uses[kStages] = {0, 0, 0, 0};            // of each stage
+    uint32_t stage = 0;                               // the next one
+    uint32_t used = 0, use_phase = 0;                 // per stage: whether it has been filled, how often (its last bit)
     uint32_t full_phase = 0, raw_phase = 0;           // per stage: the phases of its full and v_raw barriers
     uint32_t last_raw = 0;                            // per stage: its last tile went to the check warp
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -575,12 +577,14 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         return true;
       };
-      auto load_tile = [&](uint32_t stage, const CUtensorMap* map, const int2& r, bool raw) {
-        if (!wait(bar_empty + 8 * stage, (uses[stage] & 1) ^ 1u)) return false;
-        ++uses[stage];
-        const uint32_t bar = (raw ? bar_vraw : bar_full) + 8 * stage;
-        last_raw = (last_raw & ~(1u << stage)) | static_cast<uint32_t>(raw) << stage;
-        (raw ? raw_phase : full_phase) ^= 1u << stage;
+      auto free_stage = [&]() { return wait(bar_empty + 8 * stage, (use_phase >> stage & 1) ^ 1u); };
+      // (blocks of 64 come in boxes of 64 keys; larger ones in boxes of a tile, whose runs follow each other)
+      auto load_tile = [&](const CUtensorMap* map, const int2& r, bool raw) {
+        const uint32_t bar = (raw ? bar_vraw : bar_full) + 8 * stage, bit = 1u << stage;
+        used |= bit;
+        use_phase ^= bit;
+        last_raw = (last_raw & ~bit) | static_cast<uint32_t>(raw) << stage;
+        (raw ? raw_phase : full_phase) ^= bit;
         if (lane == 0) {
           mbar_expect_tx(bar, S::kKvBytes);
           const int second = r.y < len ? r.y : r.x;   // (none: any keys, which are hidden, and cleaned from V)
@@ -590,28 +594,29 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             if (a.shift_k == 6) tma_load_3d(to + kRun * 128, map, 64 * h, kv_head, row_k0 + second, bar);
           }
         }
-        return true;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
       };
-      // (blocks of 64 come in boxes of 64 keys; larger ones in boxes of a tile, whose runs follow each other)
-      auto load_k = [&](int x, uint32_t stage) {
+      auto load_k = [&](int x) {
         runs[x].x = next_run(x);
         runs[x].y = next_run(x);
-        if (!wait(bar_empty + 8 * stage, (uses[stage] & 1) ^ 1u)) return false;   // (first: the ring of what is told)
-        if (lane == 0) {
+        if (!free_stage()) return false;
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            if (tiles[y] == 0 || (!shared && y != x)) continue;
-            const int place = y * kTellRing + told[y] % kTellRing;
+        for (int y = 0; y < 2; ++y) {
+          if (tiles[y] == 0 || (!shared && y != x)) continue;
+          const int place = y * kTellRing + told[y]++ % kTellRing;
+          if (lane == 0) {
             tell[place].x = runs[x].x;
             tell[place].y = runs[x].y;
           }
         }
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          if (tiles[y] > 0 && (shared || y == x)) ++told[y];
-        return load_tile(stage, &map_k, runs[x], false);
+        load_tile(&map_k, runs[x], false);
+        return true;
       };
-      auto load_v = [&](int x, int j, uint32_t stage) { return load_tile(stage, &map_v, runs[x], j >= partial[x]); };
+      auto load_v = [&](int x, int j) {
+        if (!free_stage()) return false;
+        load_tile(&map_v, runs[x], j >= partial[x]);
+        return true;
+      };
       auto want = [&]() {
         if (lane == 0) mbar_arrive(bar_want);
       };
@@ -621,21 +626,21 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       if (shared) {
         for (int j = 0; j < n && ok; ++j) {
           if (j == n - 1) want();
-          ok = load_k(0, 2 * (j & 1));
+          ok = load_k(0);
           if (ok && j == 0) ok = load_q(1);
-          if (ok) ok = load_v(0, j, 2 * (j & 1) + 1);
+          if (ok) ok = load_v(0, j);
         }
       } else {
-        if (ok && tiles[0] > 0) ok = load_k(0, 0);
+        if (ok && tiles[0] > 0) ok = load_k(0);
         if (ok) ok = load_q(1);
-        if (ok && tiles[1] > 0) ok = load_k(1, 2);
+        if (ok && tiles[1] > 0) ok = load_k(1);
         for (int j = 0; j < n && ok; ++j) {
           if (j == n - 1) want();
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || j >= tiles[x]) continue;
-            ok = load_v(x, j, 2 * x + 1);
-            if (ok && j + 1 < tiles[x]) ok = load_k(x, 2 * x);
+            ok = load_v(x, j);
+            if (ok && j + 1 < tiles[x]) ok = load_k(x);
           }
         }
       }
@@ -644,10 +649,10 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     // here); after an abort, every copy issued has landed.
     if (lane == 0) {
       for (uint32_t i = 0; i < kStages && !raised_here(abort); ++i)
-        if (uses[i] > 0) (void)wait_or_abort(bar_empty + 8 * i, (uses[i] - 1) & 1, abort);
+        if (used >> i & 1) (void)wait_or_abort(bar_empty + 8 * i, (use_phase >> i & 1) ^ 1u, abort);
       if (raised_here(abort)) {
         for (uint32_t i = 0; i < kStages; ++i)
-          if (uses[i] > 0) {
+          if (used >> i & 1) {
             const bool raw = last_raw >> i & 1;
             (void)wait_bounded((raw ? bar_vraw : bar_full) + 8 * i, ((raw ? raw_phase : full_phase) >> i & 1) ^ 1u);
           }
@@ -668,6 +673,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const uint32_t q_low = desc_low(base, 16);
     const uint32_t k_low = desc_low(base + S::kOffKv, 16);
     const uint32_t v_low = desc_low(base + S::kOffKv, kKeys * 128);   // 64 columns of V, then the next 64
+    uint32_t next_stage = 0;                // of the ring, as the tiles come
     uint32_t full_phase = 0, ok_phase = 0;  // per stage: phases of the full and v_ok barriers
     uint32_t p_count[2] = {0, 0}, q_count[2] = {0, 0};
     bool ok = true;
@@ -691,8 +697,10 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       }
     };
     auto wait = [&](uint32_t bar, uint32_t parity) { return wait_lanes(lane == 0 ? bar : 0u, parity); };
-    // The barrier of a stage's next tile and its parity, each tile once.
-    auto tile_bar = [&](uint32_t stage, bool checked, uint32_t& parity) {
+    // The next tile's stage, its barrier and parity.
+    auto next_tile = [&](bool checked, uint32_t& stage, uint32_t& parity) {
+      stage = next_stage;
+      next_stage = next_stage + 1 == kStages ? 0 : next_stage + 1;
       parity = (checked ? ok_phase : full_phase) >> stage & 1;
       (checked ? ok_phase : full_phase) ^= 1u << stage;
       return (checked ? bar_vok : bar_full) + 8 * stage;
@@ -723,25 +731,26 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       leave_unit(it);
       const int tiles = n0 > n1 ? n0 : n1;
       if (tiles == 0) continue;
+      uint32_t k_stage = 0, v_stage = 0;
       // the first S of each
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int n = x == 0 ? n0 : n1;
         if (!ok || n == 0) continue;
         uint32_t parity = 0;
-        const uint32_t stage = shared ? 0 : 2 * x;
-        const uint32_t k_bar = !shared || x == 0 ? tile_bar(stage, false, parity) : 0u;
+        const uint32_t k_bar = !shared || x == 0 ? next_tile(false, k_stage, parity) : 0u;
         const uint32_t bar = lane == 0 ? bar_q + 8 * x : lane == 1 ? k_bar : 0u;
         const uint32_t q_parity = q_count[x]++ & 1;
         if (!(ok = wait_lanes(bar, lane == 0 ? q_parity : parity))) continue;
         tc_fence_after();
-        s_product(x, stage);
+        s_product(x, k_stage);
         if (n == 1) commit_elected(bar_qfree + 8 * x);
-        if (!shared || x == 1 || n1 == 0) release(stage);
+        if (!shared || x == 1 || n1 == 0) release(k_stage);
       }
       // Commits go in where the queue of products is short (behind a full one they would keep the
-      // warp until it has run), so a turn leaves its stages to the next; but not to one that waits
-      // for what is loaded there.
+      // warp until it has run), so a turn leaves its stages to the next.  With a list for each tile
+      // the loads are the slower part and get their stages back at once (32,640 tokens of 56 heads over
+      // 32 of 255 blocks 3.04 ms, against 3.22).
       int held_v = -1, held_k = -1;
       auto release_held = [&]() {
         if (held_v >= 0) release(held_v);
@@ -752,14 +761,12 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         uint32_t v_parity = 0, k_parity = 0, v_bar = 0, k_bar = 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int n = x == 0 ? n0 : n1, other = x == 0 ? n1 : n0;
+          const int n = x == 0 ? n0 : n1;
           if (!ok || j >= n) continue;
-          const uint32_t v_stage = shared ? 2 * (j & 1) + 1 : 2 * x + 1;
-          const uint32_t k_stage = shared ? 2 * ((j + 1) & 1) : 2 * x;
           const bool first = !shared || x == 0, last = !shared || x == 1 || n1 == 0;
           if (first) {
-            v_bar = tile_bar(v_stage, j >= (x == 0 ? partial0 : partial1), v_parity);
-            k_bar = j + 1 < n ? tile_bar(k_stage, false, k_parity) : 0u;
+            v_bar = next_tile(j >= (x == 0 ? partial0 : partial1), v_stage, v_parity);
+            k_bar = j + 1 < n ? next_tile(false, k_stage, k_parity) : 0u;
           }
           // V[j], K[j + 1] and the first half of the weights, all at once
           const uint32_t parity = p_count[x]++ & 1;
@@ -778,7 +785,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           if (last) {
             held_v = v_stage;
             held_k = j + 1 < n ? static_cast<int>(k_stage) : -1;
-            if (!shared && (x == 0 ? j >= other : j + 1 >= other)) release_held();   // the next turn is this tile's too
+            if (!shared) release_held();
           }
         }
       }
@@ -790,6 +797,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     __syncwarp();
   } else if (warp == kCheckWarp) {
     uint32_t raw_phase = 0, count[2] = {0, 0};   // count: K tiles told of before this unit
+    uint32_t base_stage = 0;                     // of the unit's first tile
     bool ok = true;
     Unit* u;
     for (int it = 0; ok && (u = unit_at(it)) != nullptr; ++it) {
@@ -800,7 +808,12 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok || j >= tiles[x] || j < u->partial[x] || (shared && x == 1)) continue;
-          const uint32_t stage = shared ? 2 * (j & 1) + 1 : 2 * x + 1;
+          // tiles before this one: K V K V ..., or K0 K1, then V0 K0 V1 K1 a turn as far as each goes
+          const int n0 = tiles[0], n1 = tiles[1], t0 = max(n0 - 1, 0), t1 = max(n1 - 1, 0);
+          const int ahead = shared ? 2 * j + 1
+                                   : (n0 > 0) + (n1 > 0) + min(j, n0) + min(j, t0) + min(j, n1) + min(j, t1) +
+                                         (x == 1 ? (j < n0) + (j < t0) : 0);
+          const uint32_t stage = (base_stage + ahead) % kStages;
           if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, raw_phase >> stage & 1, abort)))) continue;
           raw_phase ^= 1u << stage;
           const int told = x * kTellRing + (count[x] + j) % kTellRing;
@@ -840,6 +853,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       }
       count[0] += tiles[0];
       count[1] += tiles[1];
+      base_stage = (base_stage + 2 * (shared ? tiles[0] : tiles[0] + tiles[1])) % kStages;
       leave_unit(it);
     }
   } else {
