@@ -6,22 +6,27 @@
 //
 // Two kernels.
 //   pool    sums the rows of each block of q and of k: every input byte is read once, which is
-//           the bound (DRAM).  A sum is kept as hi + lo, two fp32 that hold 48 bits of it (D. E.
-//           Knuth's two-sum, The Art of Computer Programming vol. 2, 4.2.2: the rounding error of
-//           an fp32 addition is itself an fp32): seven packed additions a pair of values, half of what
-//           the loads leave time for.
+//           the bound (DRAM).  The sums are kept as hi + lo, two fp32.  A running sum begins at a
+//           constant that is larger than all that can come (S. M. Rump, T. Ogita and S. Oishi,
+//           "Accurate floating-point summation part I", SIAM J. Sci. Comput. 31(1), 2008): what its
+//           rounding leaves of each value is exact and goes to a sum of its own, four packed
+//           additions a pair of values (65,280 rows of 56 + 56 heads of 128 in 299 us, 6.4 TB/s with what is
+//           written; with two-sums, seven additions, 331).  A sum of
+//           up to 256 values is exact where they lie within a factor of 2^18 of each other, and else off by
+//           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
 //   score   16 query blocks a CTA against all key blocks of their sequence: products of the hi
 //           parts in fp32 (the lo parts are below their rounding), 8 x 4 scores a thread
-//           from tiles in shared memory, then a warp per query block finds the top-th
-//           highest score by bisection.
+//           from tiles of 512 key blocks x 8 dimensions that bulk copies bring; then a warp per query
+//           block takes its scores into registers and bisects for the top-th highest.
 //
 // What fp32 cannot tell apart is told apart in 64 bits: a score is off by at most
-// delta = 2^-18 * sum|q_i| * max|k_i| (parts hi: 2 * 2^-24; chains of 16 fused products, and 8 sums of
-// them: 24 * 2^-24; the mean: 2^-23; less than 64 * 2^-24 in all).  Where the top-th score is more
+// delta = 80 * 2^-24 * sum|q_i| * max|k_i| (parts hi: 2 * 2^-24; chains of at most 64 fused products, and
+// the sum of two: 65 * 2^-24; the mean: 2 * 2^-24).  Where the top-th score is more
 // than 2 delta above the next, the choice is the exact one.  Where it is not (one list in a hundred
 // for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in fp64, and
 // the places that are left go to the highest of those.
 #include <cfloat>
+#include <cmath>
 
 #include "h3q_async.cuh"
 #include "h3q_blocks.cuh"
@@ -35,8 +40,9 @@ namespace {
 
 constexpr int kPoolThreads = 256;
 
-// The workspace: hi and lo parts [kv_heads][block rows][head_dim] of q and of k, then for each block sum |q|
-// and max |mean k|.
+// The workspace: hi and lo parts of q and of k, then for each block sum |q| and max |mean k|.  Those of q are
+// [kv_heads][block rows][head_dim], those of k [kv_heads][head_dim / 4][block rows][4]: four
+// dimensions of neighbouring blocks are one copy.
 struct Sums {
   float* hi[2];
   float* lo[2];
@@ -75,7 +81,8 @@ struct PoolArgs {
 
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.0f, -1.0f), a); }
 
-// (hi, lo) += x: hi + error = hi + x without rounding.
+// (hi, lo) += x: hi + error = hi + x without rounding (D. E. Knuth's two-sum, The Art of Computer Programming
+// vol. 2, 4.2.2).
 __device__ __forceinline__ void add_to(float2& hi, float2& lo, float2 x) {
   const float2 s = add2(hi, x);
   const float2 y = sub2(s, hi);
@@ -84,15 +91,17 @@ __device__ __forceinline__ void add_to(float2& hi, float2& lo, float2 x) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ PoolArgs a) {
-  constexpr int kLanes8 = HD / 8;           // lanes of a row of a head, 8 values each
-  constexpr int kRows = 32 / kLanes8;       // rows of a head that a load of the warp takes
-  constexpr int kUnroll = 8;
+__global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_constant__ PoolArgs a) {
+  constexpr int kLanes = HD / 8;            // lanes of a row of a head, 8 values each
+  constexpr int kRows = 32 / kLanes;        // rows of a head that a load of the warp takes
+  constexpr int kUnroll = 4;                // loads under way while as many are summed
   const int lane = threadIdx.x & 31;
-  const int c = lane % kLanes8;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kPoolThreads / 32) + (threadIdx.x >> 5);
-  int64_t r = unit / a.kv_heads;
-  const int head = static_cast<int>(unit - r * a.kv_heads);
+  const int c = lane % kLanes;
+  const uint32_t unit = blockIdx.x * (kPoolThreads / 32) + (threadIdx.x >> 5);   // (below 2^31, see the API)
+  const uint32_t row_of_unit = unit / static_cast<uint32_t>(a.kv_heads);
+  const int head = static_cast<int>(unit - row_of_unit * a.kv_heads);
+  int64_t r = row_of_unit;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (they wait for this kernel's end)
   if (r >= a.sums.rows[0] + a.sums.rows[1]) return;
   const int t = r >= a.sums.rows[0];
   if (t) r -= a.sums.rows[0];
@@ -101,31 +110,92 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constan
   const int group = a.group[t], items = p.rows * group;   // rows of single heads
   const int64_t ld = a.ld[t];
   const uint16_t* const x = a.x[t] + p.row0 * ld + static_cast<int64_t>(head) * group * HD + c * 8;
+  // hi: sums and `offset`, which is 1.5 * 2^k with 2^k at least 4 times what `items` values below `limit` can
+  // come to, so that all of them have the same last place.
   float2 hi[4], lo[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) hi[i] = lo[i] = make_float2(0.0f, 0.0f);
-  for (int i0 = lane / kLanes8; i0 < items; i0 += kRows * kUnroll) {
-    uint4 w[kUnroll];
+  float offset = 0.0f, limit = 0.0f;
+  const int growth = 36 - __clz(items);   // 2^growth > 16 * items: 4, and values up to 4 times the exponent's
+  bool finite = true;
+  // (seldom more than once: a larger value has come)
+  auto raise = [&](float most) {
+    const int e = max(static_cast<int>(__float_as_uint(most) >> 23), 1) + growth;
+    if (e >= 254) {
+      finite = false;
+      return;
+    }
+    const float to = __uint_as_float(static_cast<uint32_t>(max(e, 30)) << 23 | 0x400000u);
+    const float2 from2 = make_float2(offset, offset), to2 = make_float2(to, to);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = sub2(hi[i], from2);
+      hi[i] = add2(to2, v);
+      lo[i] = add2(lo[i], sub2(v, sub2(hi[i], to2)));
+    }
+    offset = to;
+    limit = __uint_as_float(static_cast<uint32_t>(max(e - growth + 2, 3)) << 23);
+  };
+  auto load = [&](int i0, uint4 (&w)[kUnroll]) {
 #pragma unroll
     for (int n = 0; n < kUnroll; ++n) {
       const int i = i0 + n * kRows;
       w[n] = make_uint4(0u, 0u, 0u, 0u);
       if (i < items) {
-        const int row = i / group;
+        const int row = group == 1 ? i : i / group;
         w[n] = load16_stream(x + row * ld + (i - row * group) * HD);
       }
     }
+  };
+  auto sum = [&](const uint4 (&w)[kUnroll]) {
+    uint32_t most = 0u;
+#pragma unroll
+    for (int n = 0; n < kUnroll; ++n)
+      most = absmax_bf16x2(most, absmax_bf16x2(absmax_bf16x2(w[n].x, w[n].y), absmax_bf16x2(w[n].z, w[n].w)));
+    const float largest = halves_amax(most);
+    if (!(largest < limit)) raise(largest);
 #pragma unroll
     for (int n = 0; n < kUnroll; ++n) {
-      add_to(hi[0], lo[0], bf16x2_to_float2(w[n].x));
-      add_to(hi[1], lo[1], bf16x2_to_float2(w[n].y));
-      add_to(hi[2], lo[2], bf16x2_to_float2(w[n].z));
-      add_to(hi[3], lo[3], bf16x2_to_float2(w[n].w));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 v = bf16x2_to_float2(i == 0 ? w[n].x : i == 1 ? w[n].y : i == 2 ? w[n].z : w[n].w);
+        const float2 s = add2(hi[i], v);
+        lo[i] = add2(lo[i], sub2(v, sub2(s, hi[i])));
+        hi[i] = s;
+      }
+    }
+  };
+  uint4 w0[kUnroll], w1[kUnroll];
+  constexpr int kStep = kRows * kUnroll;
+  load(lane / kLanes, w0);
+  for (int i0 = lane / kLanes; i0 < items; i0 += 2 * kStep) {   // (zeros past the last change nothing)
+    load(i0 + kStep, w1);
+    sum(w0);
+    load(i0 + 2 * kStep, w0);
+    sum(w1);
+  }
+  if (finite) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 rest = lo[i];
+      hi[i] = sub2(hi[i], make_float2(offset, offset));
+      lo[i] = make_float2(0.0f, 0.0f);
+      add_to(hi[i], lo[i], rest);
+    }
+  } else {   // infinities, values that are no numbers, or sums near fp32's end: as fp32 has them
+#pragma unroll
+    for (int i = 0; i < 4; ++i) hi[i] = lo[i] = make_float2(0.0f, 0.0f);
+    for (int i0 = lane / kLanes; i0 < items; i0 += kRows) {
+      const uint4 w = load16_stream(x + i0 / group * ld + (i0 % group) * HD);
+      hi[0] = add2(hi[0], bf16x2_to_float2(w.x));
+      hi[1] = add2(hi[1], bf16x2_to_float2(w.y));
+      hi[2] = add2(hi[2], bf16x2_to_float2(w.z));
+      hi[3] = add2(hi[3], bf16x2_to_float2(w.w));
     }
   }
   // the other rows' lanes
 #pragma unroll
-  for (int o = kLanes8; o < 32; o <<= 1) {
+  for (int o = kLanes; o < 32; o <<= 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 h = make_float2(__shfl_xor_sync(0xffffffffu, hi[i].x, o), __shfl_xor_sync(0xffffffffu, hi[i].y, o));
@@ -150,31 +220,34 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constan
   }
   if (t && !(size <= FLT_MAX)) size = 0.0f;   // (its scores are no numbers, or infinite, whatever fp32 makes of them)
 #pragma unroll
-  for (int o = 1; o < kLanes8; o <<= 1) {
+  for (int o = 1; o < kLanes; o <<= 1) {
     const float other = __shfl_xor_sync(0xffffffffu, size, o);
     size = t ? fmaxf(size, other) : __fadd_rn(size, other);
   }
-  const int64_t at = static_cast<int64_t>(head) * a.sums.rows[t] + r;
+  const int64_t rows = a.sums.rows[t], at = static_cast<int64_t>(head) * rows + r;
   if (lane == 0) a.sums.size[t][at] = t ? __fdiv_rn(size, static_cast<float>(p.rows)) : size;
-  if (lane < kLanes8) {
-    float4* const hd = reinterpret_cast<float4*>(a.sums.hi[t] + at * HD + c * 8);
-    float4* const ld4 = reinterpret_cast<float4*>(a.sums.lo[t] + at * HD + c * 8);
+  if (lane < kLanes) {
+    const int64_t to = t ? (static_cast<int64_t>(head) * (HD / 4) + 2 * c) * rows + r : at * (HD / 4) + 2 * c;
+    const int64_t step = t ? rows : 1;
+    float4* const hd = reinterpret_cast<float4*>(a.sums.hi[t]) + to;
+    float4* const ld4 = reinterpret_cast<float4*>(a.sums.lo[t]) + to;
     hd[0] = make_float4(h[0], h[1], h[2], h[3]);
-    hd[1] = make_float4(h[4], h[5], h[6], h[7]);
+    hd[step] = make_float4(h[4], h[5], h[6], h[7]);
     ld4[0] = make_float4(l[0], l[1], l[2], l[3]);
-    ld4[1] = make_float4(l[4], l[5], l[6], l[7]);
+    ld4[step] = make_float4(l[4], l[5], l[6], l[7]);
   }
 }
 
 // ---------------------------------------------------------------------------- score
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 16;         // query blocks of a CTA at most
-constexpr int kTile = 256;        // key blocks of a tile,
-constexpr int kDims = 16;         // and its dimensions
-constexpr int kStride = kDims + 4;   // floats between a tile's rows: eight rows' 16 bytes meet in no bank
-constexpr int kTileBytes = kTile * kStride * 4;
-// Scores that a CTA holds: 16 query blocks against 256, 512 or 1,024 key blocks, or fewer against more (one
+constexpr int kTile = 512;        // key blocks of a tile,
+constexpr int kDims = 8;          // and its dimensions: two copies of 8 KB
+constexpr int kStages = 4;
+constexpr int kStageBytes = kTile * kDims * 4;
+// Scores that a CTA holds: 16 query blocks against 512 or 1,024 key blocks, or fewer against more (one
 // against 16,384, see kMaxBlocks).
 constexpr int kMostScores = kRows * 1024;
 
@@ -198,59 +271,223 @@ __device__ __forceinline__ float value_of(uint32_t order) {
   return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
 }
 
-// The n-th highest of the orders that `get` gives for 0 .. count - 1 (1 <= n <= the count of those above 0 or
-// any), by bisection of the 32 bits; `above`: how many are higher.  Whole warp.
-template <typename Get>
-__device__ __forceinline__ uint32_t nth_highest(int count, int n, Get get, int& above) {
-  const int lane = threadIdx.x & 31;
-  uint32_t lowest = 0xffffffffu, highest = 0u;
-  for (int i = lane; i < count; i += 32) {
-    const uint32_t x = get(i);
-    lowest = min(lowest, x);
-    highest = max(highest, x);
-  }
-  uint32_t lo = __reduce_min_sync(0xffffffffu, lowest), hi = __reduce_max_sync(0xffffffffu, highest);
-  // at least n are >= lo; fewer than n are > hi
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2 + 1;
-    int mine = 0;
-    for (int i = lane; i < count; i += 32) mine += get(i) >= mid;
-    const int got = __reduce_add_sync(0xffffffffu, mine);
-    if (got >= n) {
-      lo = mid;
-      if (got == n) {   // exactly these: the lowest of them
-        uint32_t least = 0xffffffffu;
-        for (int i = lane; i < count; i += 32) {
-          const uint32_t x = get(i);
-          if (x >= mid) least = min(least, x);
-        }
-        lo = __reduce_min_sync(0xffffffffu, least);
-        break;
-      }
+// A query block's orders as the lanes of a warp have them, that of key block 32 r + lane in round r: in R
+// registers, or (R = 0) in shared memory.
+template <int R>
+struct Orders {
+  uint32_t held[R > 0 ? R : 1];
+  uint32_t* at;
+  int count;
+  template <typename F>
+  __device__ __forceinline__ void each(F f) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) f(32 * r + lane, held[r]);
     } else {
-      hi = mid - 1;
+      for (int j = lane; j < count; j += 32) f(j, at[j]);
     }
   }
-  int mine = 0;
-  for (int i = lane; i < count; i += 32) mine += get(i) > lo;
-  above = __reduce_add_sync(0xffffffffu, mine);
+  // each, in step: all lanes call f in every round
+  template <typename F>
+  __device__ __forceinline__ void in_step(F f) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (R > 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        if (32 * r < count) f(32 * r + lane, held[r]);
+    } else {
+      for (int j = lane; j < count + lane; j += 32) {
+        uint32_t x = j < count ? at[j] : 0u;
+        f(j, x);
+        if (j < count) at[j] = x;
+      }
+    }
+  }
+};
+
+// The n-th highest of the orders, 0 if fewer than n are above 0, how many are higher and how many it is.  Each
+// round halves the interval; the first ones by the share of the scores that are in it and above (which
+// finds a border that some hundred scores have between them in five or six), then by the values and
+// at last by the orders.  Whole warp.
+template <int R>
+__device__ __forceinline__ uint32_t nth_highest(Orders<R>& row, int n, int& above, int& same) {
+  uint32_t lowest = 0xffffffffu, highest = 0u;
+  int any = 0;
+  row.each([&](int, uint32_t x) {
+    if (x != 0u) lowest = min(lowest, x);
+    highest = max(highest, x);
+    any += x != 0u;
+  });
+  int at_lo = __reduce_add_sync(0xffffffffu, any), over_hi = 0;   // at least n are >= lo, fewer than n > hi
+  above = at_lo;
+  same = 0;
+  if (at_lo < n) return 0u;
+  uint32_t lo = __reduce_min_sync(0xffffffffu, lowest), hi = __reduce_max_sync(0xffffffffu, highest);
+  for (int round = 0; lo < hi; ++round) {
+    uint32_t mid = lo + (hi - lo) / 2 + 1;
+    if (round < 24) {
+      const float from = value_of(lo), width = __fsub_rn(value_of(hi), from);
+      const float share = round % 3 == 2 ? 0.5f
+                                         : __fdividef(static_cast<float>(at_lo - n) + 0.5f, static_cast<float>(at_lo - over_hi));
+      const uint32_t between = order_of(__fadd_rn(from, __fmul_rn(width, share)));
+      if (between > lo && between <= hi) mid = between;
+    }
+    int mine = 0;
+    row.each([&](int, uint32_t x) { mine += x >= mid; });
+    const int got = __reduce_add_sync(0xffffffffu, mine);
+    if (got < n) {
+      hi = mid - 1;
+      over_hi = got;
+    } else if (got > n) {
+      lo = mid;
+      at_lo = got;
+    } else {   // exactly these: the lowest of them
+      uint32_t least = 0xffffffffu;
+      row.each([&](int, uint32_t x) {
+        if (x >= mid) least = min(least, x);
+      });
+      lo = __reduce_min_sync(0xffffffffu, least);
+      break;
+    }
+  }
+  int more = 0;
+  any = 0;
+  row.each([&](int, uint32_t x) {
+    more += x > lo;
+    any += x == lo;
+  });
+  above = __reduce_add_sync(0xffffffffu, more);
+  same = __reduce_add_sync(0xffffffffu, any);
   return lo;
 }
 
 struct RowPlace {
   BlockPlace block;
   int candidates;    // key blocks that may be chosen: the first of them
-  int own;           // those from here on are (causal)
+  int own;           // those from here on always are (causal)
   float delta;       // how far a score may be off
 };
 
+// One query block's choice among the first p.candidates key blocks, whose scores' orders are at `scored`.
+// `q_at`, `k_at`: where its sums and those of its sequence's key blocks begin in a.sums; `len`: keys.  Whole warp.
+template <int HD, int R>
+__device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, uint32_t* scored, int64_t q_at,
+                                       int64_t k_at, int64_t len, int64_t list) {
+  const int lane = threadIdx.x & 31;
+  const int m = p.candidates, top = a.s.top;
+  auto kept = [&](int j) { return j < a.first || j >= p.own; };
+  Orders<R> row;
+  row.at = scored;
+  row.count = m;
+  if constexpr (R > 0) {   // those that are always chosen stand above all, those past m below
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int j = 32 * r + lane;
+      row.held[r] = j >= m ? 0u : kept(j) ? 0xffffffffu : scored[j];
+    }
+  } else {
+    row.in_step([&](int j, uint32_t& x) {
+      if (kept(j)) x = 0xffffffffu;
+    });
+    __syncwarp();
+  }
+  // The score of key block j from hi + lo, in 64 bits: a lane has 4 or 2 dimensions.
+  constexpr int kEach = HD / 32;
+  double q[kEach];
+  bool has_q = false;
+  auto exact = [&](int j) {
+    if (!has_q) {
+#pragma unroll
+      for (int z = 0; z < kEach; ++z)
+        q[z] = static_cast<double>(a.sums.hi[0][q_at + lane * kEach + z]) +
+               static_cast<double>(a.sums.lo[0][q_at + lane * kEach + z]);
+      has_q = true;
+    }
+    const int64_t at = k_at + (lane * kEach / 4 * a.sums.rows[1] + j) * 4 + lane * kEach % 4;
+    double sum = 0.0;
+#pragma unroll
+    for (int z = 0; z < kEach; ++z)
+      sum = fma(q[z], static_cast<double>(a.sums.hi[1][at + z]) + static_cast<double>(a.sums.lo[1][at + z]), sum);
+#pragma unroll
+    for (int z = 16; z >= 1; z >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+    const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
+    return sum / static_cast<double>(left < a.s.block_k ? left : static_cast<int64_t>(a.s.block_k));
+  };
+
+  uint32_t border = 0u;   // all above it are chosen, and the first `ties` of those at it
+  int ties = m, same = m;
+  if (m > top) {
+    int above;
+    border = nth_highest(row, top, above, same);
+    ties = top - above;
+    uint32_t next = 0u;   // the highest that would not be chosen
+    row.each([&](int, uint32_t x) {
+      if (x < border) next = max(next, x);
+    });
+    next = same > ties ? border : __reduce_max_sync(0xffffffffu, next);
+    const float t = value_of(border), reach = __fmul_rn(p.delta, 2.0f);
+    if (border != 0u && border != 0xffffffffu && next != 0u && reach <= FLT_MAX && __fsub_rn(t, value_of(next)) <= reach) {
+      // Those within reach of the border compete by their exact scores (less t, so that fp32 holds them to
+      // 2^-24 of delta) for the places that those above leave; what is beyond reach keeps its side.
+      row.in_step([&](int j, uint32_t& x) {
+        const bool may = x != 0u && x != 0xffffffffu;
+        const float from_t = may ? __fsub_rn(value_of(x), t) : 0.0f;
+        const bool close = may && fabsf(from_t) <= reach;
+        if (may && !close) x = from_t > reach ? 0xffffffffu : 0u;
+        uint32_t todo = __ballot_sync(0xffffffffu, close);
+        while (todo) {
+          const int i = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const double s = exact(j - lane + i);
+          if (lane == i) x = order_of(static_cast<float>(s - static_cast<double>(t)));
+        }
+      });
+      __syncwarp();
+      border = nth_highest(row, top, above, same);
+      ties = top - above;
+    }
+    if (border == 0u) same = ties + 1;   // (entries past m have that order too)
+  }
+  const bool all_same = same <= ties;   // all at the border are chosen
+  int written = 0, tied = 0;
+  const uint32_t before = (1u << lane) - 1u;
+  const float rows_f = static_cast<float>(p.block.rows) * static_cast<float>(a.s.heads / a.s.kv_heads);
+  const float per_row = __fdiv_rn(1.0f, rows_f);
+  row.in_step([&](int j, uint32_t& x) {
+    bool in = j < m && x >= border;
+    if (!all_same) {
+      const uint32_t at_border = __ballot_sync(0xffffffffu, j < m && x == border);
+      in = in && (x > border || tied + __popc(at_border & before) < ties);
+      tied += __popc(at_border);
+    }
+    uint32_t chosen = __ballot_sync(0xffffffffu, in);
+    const int place = written + __popc(chosen & before);
+    written += __popc(chosen);
+    if (in && place < top) a.blocks[list + place] = j;
+    if (a.scores == nullptr) return;
+    if constexpr (R > 0) {
+      if (in && place < top) a.scores[list + place] = __fmul_rn(value_of(scored[j]), per_row);
+    } else {   // (the scores are no longer there)
+      while (chosen) {
+        const int i = __ffs(chosen) - 1;
+        chosen &= chosen - 1;
+        const double s = exact(j - lane + i);
+        if (lane == i && place < top) a.scores[list + place] = static_cast<float>(s / static_cast<double>(rows_f));
+      }
+    }
+  });
+  for (int place = written + lane; place < top; place += 32) {
+    a.blocks[list + place] = -1;
+    if (a.scores != nullptr) a.scores[list + place] = -INFINITY;
+  }
+}
+
 template <int HD, int CAPACITY>
-__global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(kThreads, CAPACITY <= kRows * 512 ? 2 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  float* const tiles = reinterpret_cast<float*>(smem);                        // two
-  float* const q = reinterpret_cast<float*>(smem + 2 * kTileBytes);           // [kRows][HD]
-  float* const scores = q + kRows * HD;                                       // [rows of a pass][width]
-  uint32_t* const near_flags = reinterpret_cast<uint32_t*>(scores + CAPACITY);   // [rows of a pass][width / 32]
+  float* const q = reinterpret_cast<float*>(smem + kStages * kStageBytes);    // [kRows][HD]
+  uint32_t* const scored = reinterpret_cast<uint32_t*>(q + kRows * HD);       // orders [rows of a pass][width]
   __shared__ RowPlace places[kRows];
   __shared__ float most_k;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -260,6 +497,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
   const int64_t r0 = (blockIdx.x - head * chunks) * a.rows;
   const int rows = static_cast<int>(lists - r0 < a.rows ? lists - r0 : a.rows);
 
+  // (the lists of rows are older than the sums: they are looked at before those are there)
   if (threadIdx.x < rows) {
     RowPlace p{};
     p.block = block_at(a.s.cu_q, a.s.batch, a.s.rows_q, a.shift_q, r0 + threadIdx.x);
@@ -274,36 +512,54 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
     }
     places[threadIdx.x] = p;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
   __syncthreads();
 
   for (int seg = 0; seg < rows;) {
     // rows of one sequence, as many as the scores have room for
-    const RowPlace head_place = places[seg];
-    int most = head_place.candidates, n = 1;
-    const int width_of_one = (most + kTile - 1) / kTile * kTile;
-    int width = width_of_one;
-    while (seg + n < rows && places[seg + n].block.rows > 0 && head_place.block.rows > 0 &&
-           places[seg + n].block.sequence == head_place.block.sequence) {
-      const int other = places[seg + n].candidates > most ? places[seg + n].candidates : most;
-      const int w = (other + kTile - 1) / kTile * kTile;
+    const RowPlace first = places[seg];
+    int most = first.candidates, n = 1, width = (most + 31) / 32 * 32;
+    while (seg + n < rows && first.block.rows > 0 && places[seg + n].block.rows > 0 &&
+           places[seg + n].block.sequence == first.block.sequence) {
+      const int other = max(places[seg + n].candidates, most);
+      const int w = (other + 31) / 32 * 32;
       if ((n + 1) * w > CAPACITY) break;
       most = other;
       width = w;
       ++n;
     }
+    const int b = first.block.sequence;
+    const int64_t q_at = (static_cast<int64_t>(head) * lists + r0 + seg) * HD;
+    int64_t k_at = 0, len = 0;
     if (most > 0) {
-      const int b = head_place.block.sequence;
       const int64_t kb0 = (a.s.cu_k[b] >> a.shift_k) + static_cast<int64_t>(b);   // the sequence's key block rows
-      const int64_t len = rows_of(a.s.cu_k, b, a.s.rows_k);
-      const float* const k_hi = a.sums.hi[1] + (static_cast<int64_t>(head) * kb_rows + kb0) * HD;
+      len = rows_of(a.s.cu_k, b, a.s.rows_k);
+      k_at = static_cast<int64_t>(head) * kb_rows * HD + kb0 * 4;
       const float* const k_size = a.sums.size[1] + static_cast<int64_t>(head) * kb_rows + kb0;
-      const float* const q_hi = a.sums.hi[0] + (static_cast<int64_t>(head) * lists + r0 + seg) * HD;
       const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
+      constexpr int kSteps = HD / kDims;
+      const int steps = (most + kTile - 1) / kTile * kSteps;
+      auto fetch = [&](int step) {
+        if (step < steps) {
+          const int j0 = step / kSteps * kTile, quad0 = step % kSteps * (kDims / 4);
+          const uint32_t to = smem_u32(smem) + step % kStages * kStageBytes;
+#pragma unroll
+          for (int i = 0; i < kTile * kDims / 4 / kThreads; ++i) {
+            const int piece = threadIdx.x + i * kThreads;       // [quad][key block]
+            const int j = j0 + piece % kTile;
+            const float* from = a.sums.hi[1] + k_at + ((quad0 + piece / kTile) * kb_rows + (j < most ? j : most - 1)) * 4;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + piece * 16), "l"(from) : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) fetch(i);
       if (threadIdx.x == 0) most_k = 0.0f;
       for (int i = threadIdx.x; i < kRows * HD / 4; i += kThreads) {
         const bool there = i / (HD / 4) < n;
-        reinterpret_cast<float4*>(q)[i] =
-            there ? reinterpret_cast<const float4*>(q_hi)[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        reinterpret_cast<float4*>(q)[i] = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at)[i]
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       __syncthreads();
       {
@@ -313,197 +569,72 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) atomicMax(reinterpret_cast<int*>(&most_k), __float_as_int(m));   // (none is negative)
       }
-
-      // ---- scores: 16 query blocks by tiles of 256 key blocks, 16 dimensions at a time
-      constexpr int kSteps = HD / kDims;
-      const int steps = width / kTile * kSteps;
-      auto fetch = [&](int step) {
-        const int j0 = step / kSteps * kTile, d0 = step % kSteps * kDims;
-        float* const to = tiles + (step & 1) * (kTileBytes / 4);
-#pragma unroll
-        for (int i = 0; i < kTile * kDims / 4 / kThreads; ++i) {
-          const int piece = threadIdx.x + i * kThreads;
-          const int j = piece / (kDims / 4), d = piece % (kDims / 4) * 4;
-          const int from = j0 + j < most ? j0 + j : most - 1;   // (past the last: any)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + j * kStride + d)),
-                       "l"(k_hi + static_cast<int64_t>(from) * HD + d0 + d)
-                       : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-      // A thread's scores: query blocks 8 (warp / 2) .. + 7, key blocks (warp % 2) * 128 + lane + 32 x.
-      const int q_first = warp / 2 * 8, k_first = warp % 2 * 128 + lane;
-      float2 total[8][2];   // key blocks x = 0, 1 and 2, 3
-      fetch(0);
+      // A thread's scores: query blocks q_first .. + 7, key blocks k_first + 32 x of a tile, even dimensions
+      // in one half of a pair and odd ones in the other.
+      const int q_first = warp / 4 * 8, k_first = warp % 4 * 128 + lane;
+      float2 acc[8][4];
       for (int step = 0; step < steps; ++step) {
-        if (step + 1 < steps) {
-          fetch(step + 1);
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncthreads();
-        const float* const k = tiles + (step & 1) * (kTileBytes / 4) + k_first * kStride;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();   // the step's tile is there, and the last step's is no longer read
+        fetch(step + kStages - 1);
+        const int j0 = step / kSteps * kTile;
+        if (q_first >= n || j0 + warp % 4 * 128 >= most) continue;
+        const float4* const k = reinterpret_cast<const float4*>(smem + step % kStages * kStageBytes) + k_first;
         const float* const qd = q + q_first * HD + step % kSteps * kDims;
-        float2 part[8][2];
+        if (step % kSteps == 0) {
 #pragma unroll
-        for (int d = 0; d < kDims; d += 4) {
+          for (int y = 0; y < 8; ++y)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[y][x] = make_float2(0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int quad = 0; quad < kDims / 4; ++quad) {
           float4 kv[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kv[x] = *reinterpret_cast<const float4*>(k + 32 * x * kStride + d);
+          for (int x = 0; x < 4; ++x) kv[x] = k[quad * kTile + 32 * x];
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
-            const float4 qv = *reinterpret_cast<const float4*>(qd + y * HD + d);
+            const float4 qv = *reinterpret_cast<const float4*>(qd + y * HD + 4 * quad);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float4 k0 = kv[2 * x], k1 = kv[2 * x + 1];
-              float2 p = d == 0 ? mul2(make_float2(qv.x, qv.x), make_float2(k0.x, k1.x))
-                                : fma2(make_float2(qv.x, qv.x), make_float2(k0.x, k1.x), part[y][x]);
-              p = fma2(make_float2(qv.y, qv.y), make_float2(k0.y, k1.y), p);
-              p = fma2(make_float2(qv.z, qv.z), make_float2(k0.z, k1.z), p);
-              part[y][x] = fma2(make_float2(qv.w, qv.w), make_float2(k0.w, k1.w), p);
-            }
+            for (int x = 0; x < 4; ++x)
+              acc[y][x] = fma2(make_float2(qv.z, qv.w), make_float2(kv[x].z, kv[x].w),
+                               fma2(make_float2(qv.x, qv.y), make_float2(kv[x].x, kv[x].y), acc[y][x]));
           }
         }
-        const bool begins = step % kSteps == 0;
-#pragma unroll
-        for (int y = 0; y < 8; ++y)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) total[y][x] = begins ? part[y][x] : add2(total[y][x], part[y][x]);
         if (step % kSteps == kSteps - 1) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int j = step / kSteps * kTile + k_first + 32 * x;
+            const int j = j0 + k_first + 32 * x;
+            if (j >= most) continue;
             const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
-            const int keys = left < 1 ? 1 : left < a.s.block_k ? static_cast<int>(left) : a.s.block_k;
-            const float per_key = __fdiv_rn(1.0f, static_cast<float>(keys));
+            const float per_key = __fdiv_rn(1.0f, static_cast<float>(left < a.s.block_k ? left : a.s.block_k));
 #pragma unroll
             for (int y = 0; y < 8; ++y)
-              if (q_first + y < n) {
-                const float2 z = total[y][x / 2];
-                scores[(q_first + y) * width + j] = __fmul_rn(x & 1 ? z.y : z.x, per_key);
-              }
+              if (q_first + y < n)
+                scored[(q_first + y) * width + j] = order_of(__fmul_rn(__fadd_rn(acc[y][x].x, acc[y][x].y), per_key));
           }
         }
-        __syncthreads();   // the tile may be filled again
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();
       if (threadIdx.x < n) places[seg + threadIdx.x].delta =
-          fmaxf(__fmul_rn(__fmul_rn(q_size[threadIdx.x], most_k), 0x1p-18f), 0x1p-140f);
+          fmaxf(__fmul_rn(__fmul_rn(q_size[threadIdx.x], most_k), 0x1.4p-18f), 0x1p-140f);
       __syncthreads();
     }
-
-    // ---- the choice: a warp for each query block
-    for (int y = warp; y < n; y += kThreads / 32) {
+    // the choice: a warp for each query block
+    for (int y = warp; y < n; y += kWarps) {
       const RowPlace p = places[seg + y];
       const int64_t list = (static_cast<int64_t>(head) * lists + r0 + seg + y) * a.s.top;
-      float* const row = scores + y * width;
-      uint32_t* const near = near_flags + y * (width / 32);
-      const int m = p.block.rows > 0 ? p.candidates : 0, top = a.s.top;
-      auto kept = [&](int j) { return j < a.first || j >= p.own; };
-      auto order = [&](int j) { return kept(j) ? 0xffffffffu : order_of(row[j]); };
-      uint32_t border = 0u;   // all above it are chosen, and the first `ties` of those at it
-      int ties = m;
-      bool again = false;     // those near the border are chosen by their exact scores
-      if (m > top) {
-        int above;
-        border = nth_highest(m, top, order, above);
-        ties = top - above;
-        uint32_t next = 0u;   // the highest that would not be chosen
-        int at_border = 0;
-        for (int j = lane; j < m; j += 32) {
-          const uint32_t x = order(j);
-          at_border += x == border;
-          if (x < border) next = max(next, x);
+      uint32_t* const row = scored + y * width;
+      const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
+      if (p.candidates <= 512) {
+        choose<HD, 16>(a, p, row, q_row, k_at, len, list);
+      } else if constexpr (CAPACITY > kRows * 512) {
+        if (p.candidates <= 1024) {
+          choose<HD, 32>(a, p, row, q_row, k_at, len, list);
+        } else {
+          choose<HD, 0>(a, p, row, q_row, k_at, len, list);
         }
-        next = __reduce_add_sync(0xffffffffu, at_border) > ties ? border : __reduce_max_sync(0xffffffffu, next);
-        const float t = value_of(border), below = next == 0u ? -INFINITY : value_of(next);
-        const float reach = __fmul_rn(p.delta, 2.0f);
-        again = border != 0xffffffffu && border != 0u && reach <= FLT_MAX && __fsub_rn(t, below) <= reach;
-        if (again) {
-          // The candidates within reach: their scores from hi + lo in 64 bits, less t (so that fp32 holds them
-          // to 2^-24 of delta); they compete for the places that those above leave.
-          const int b = p.block.sequence;
-          const int64_t len = rows_of(a.s.cu_k, b, a.s.rows_k);
-          const int64_t q_at = (static_cast<int64_t>(head) * lists + r0 + seg + y) * HD;
-          const int64_t k_at = (static_cast<int64_t>(head) * kb_rows + (a.s.cu_k[b] >> a.shift_k) + b) * HD;
-          constexpr int kEach = HD / 32;
-          double qd[kEach];
-#pragma unroll
-          for (int i = 0; i < kEach; ++i)
-            qd[i] = static_cast<double>(a.sums.hi[0][q_at + lane + 32 * i]) +
-                    static_cast<double>(a.sums.lo[0][q_at + lane + 32 * i]);
-          int higher = 0;
-          for (int j0 = 0; j0 < m; j0 += 32) {
-            const int j = j0 + lane;
-            const float x = j < m ? row[j] : 0.0f;
-            const bool over = j < m && (kept(j) || __fsub_rn(x, t) > reach);
-            const bool close = j < m && !over && fabsf(__fsub_rn(x, t)) <= reach;
-            higher += __popc(__ballot_sync(0xffffffffu, over));
-            uint32_t todo = __ballot_sync(0xffffffffu, close);
-            if (lane == 0) near[j0 / 32] = todo;
-            while (todo) {
-              const int i = __ffs(todo) - 1;
-              todo &= todo - 1;
-              const int64_t k_row = k_at + static_cast<int64_t>(j0 + i) * HD + lane;
-              double sum = 0.0;
-#pragma unroll
-              for (int z = 0; z < kEach; ++z)
-                sum = fma(qd[z], static_cast<double>(a.sums.hi[1][k_row + 32 * z]) +
-                                     static_cast<double>(a.sums.lo[1][k_row + 32 * z]), sum);
-#pragma unroll
-              for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              const int64_t left = len - (static_cast<int64_t>(j0 + i) << a.shift_k);
-              sum = sum / static_cast<double>(left < a.s.block_k ? left : a.s.block_k) - static_cast<double>(t);
-              if (lane == i) row[j] = static_cast<float>(sum);
-            }
-          }
-          __syncwarp();
-          const int places_left = top - higher;   // >= 1; those at t or above are either higher or among the near
-          auto exact = [&](int j) { return near[j / 32] >> (j % 32) & 1u ? order_of(row[j]) : 0u; };
-          int above_exact;
-          const uint32_t line = nth_highest(m, places_left, exact, above_exact);
-          int left_over = places_left - above_exact, written = 0;
-          const float rows_f = static_cast<float>(p.block.rows) * static_cast<float>(a.s.heads / a.s.kv_heads);
-          for (int j0 = 0; j0 < m; j0 += 32) {
-            const int j = j0 + lane;
-            const bool is_near = j < m && (near[j0 / 32] >> lane & 1u);
-            const float x = j < m ? row[j] : 0.0f;
-            const uint32_t e = is_near ? order_of(x) : 0u;
-            const uint32_t at_line = __ballot_sync(0xffffffffu, is_near && e == line);
-            const bool in = is_near ? e > line || (e == line && __popc(at_line & ((1u << lane) - 1u)) < left_over)
-                                    : j < m && (kept(j) || __fsub_rn(x, t) > reach);
-            left_over -= __popc(at_line);
-            left_over = left_over < 0 ? 0 : left_over;
-            const uint32_t chosen = __ballot_sync(0xffffffffu, in);
-            const int place = written + __popc(chosen & ((1u << lane) - 1u));
-            if (in && place < top) {
-              a.blocks[list + place] = j;
-              if (a.scores) a.scores[list + place] = __fdiv_rn(is_near ? __fadd_rn(t, x) : x, rows_f);
-            }
-            written += __popc(chosen);
-          }
-          continue;   // (top of them)
-        }
-      }
-      int written = 0, tied = 0;
-      const float rows_f = static_cast<float>(p.block.rows) * static_cast<float>(a.s.heads / a.s.kv_heads);
-      for (int j0 = 0; j0 < m; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t x = j < m ? order(j) : 0u;
-        const uint32_t at = __ballot_sync(0xffffffffu, j < m && x == border);
-        const bool in = j < m && (m <= top || x > border || (x == border && tied + __popc(at & ((1u << lane) - 1u)) < ties));
-        tied += __popc(at);
-        const uint32_t chosen = __ballot_sync(0xffffffffu, in);
-        const int place = written + __popc(chosen & ((1u << lane) - 1u));
-        if (in && place < top) {
-          a.blocks[list + place] = j;
-          if (a.scores) a.scores[list + place] = __fdiv_rn(row[j], rows_f);
-        }
-        written += __popc(chosen);
-      }
-      for (int place = written + lane; place < top; place += 32) {
-        a.blocks[list + place] = -1;
-        if (a.scores) a.scores[list + place] = -INFINITY;
       }
     }
     seg += n;
@@ -513,17 +644,26 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const __grid_constant__
 
 template <int HD, int CAPACITY>
 cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
-  const int smem = 2 * kTileBytes + kRows * HD * 4 + CAPACITY * 4 + CAPACITY / 8;
+  const int smem = kStages * kStageBytes + kRows * HD * 4 + CAPACITY * 4;
   int blocks = 0;
   const void* kernel = reinterpret_cast<const void*>(&score_kernel<HD, CAPACITY>);
   cudaError_t err = persistent_blocks(kernel, kThreads, smem, int64_t{1} << 30, &blocks);
   if (err != cudaSuccess) return err;
-  // query blocks of a CTA: 16, or fewer where the CTAs would not fill the GPU
-  const int64_t rows = score.sums.rows[0] * score.s.kv_heads / blocks;
+  // query blocks of a CTA: 16, or fewer where all CTAs run at once all the same
+  const int64_t rows = (score.sums.rows[0] * score.s.kv_heads + blocks - 1) / blocks;
   score.rows = static_cast<int>(rows < 1 ? 1 : rows > kRows ? kRows : rows);
   const int64_t chunks = (score.sums.rows[0] + score.rows - 1) / score.rows;
-  score_kernel<HD, CAPACITY><<<static_cast<unsigned>(chunks * score.s.kv_heads), kThreads, smem, stream>>>(score);
-  return cudaGetLastError();
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(chunks * score.s.kv_heads));
+  config.blockDim = dim3(kThreads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, score_kernel<HD, CAPACITY>, score);
 }
 
 template <int HD>
@@ -535,7 +675,6 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   if (err != cudaSuccess) return err;
   // room for the longest sequence that there can be
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
-  if (longest <= 256) return launch_score<HD, kRows * 256>(score, stream);
   if (longest <= 512) return launch_score<HD, kRows * 512>(score, stream);
   return launch_score<HD, kMostScores>(score, stream);
 }
