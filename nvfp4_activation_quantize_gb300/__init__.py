@@ -726,7 +726,7 @@ _native = None
 
 
 class _NoShortWay:
-    write = read = cached = varlen = staticmethod(lambda *args: None)
+    write = read = cached = varlen = axes = postnorm = select = blocks = staticmethod(lambda *args: None)
 
 
 def _load_torch():
@@ -750,6 +750,9 @@ def _load_torch():
                  *(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in
                    ("h3q_kv_cache_write_nvfp4", "h3q_kv_cache_read_nvfp4", "h3q_attention_cache_nvfp4",
                     "h3q_attention_varlen")))
+    native.setup_blocks(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in
+                          ("h3q_qkv_epilogue_axes", "h3q_postnorm_residual_adaln_nvfp4", "h3q_select_blocks",
+                           "h3q_attention_blocks")))
     _native = native
     _torch = torch
     return torch
@@ -1052,6 +1055,19 @@ def h3q_qkv_epilogue_axes(q, k, v, positions, axis_dims, heads, *, kv_heads=None
     q's and k's norm, [HD]) are tuples of bf16 tensors, any of them None."""
     torch = _torch or _load_torch()
     kv_heads = heads if kv_heads is None else kv_heads
+    shape = getattr(q, "shape", ())
+    if len(shape) == 2 and heads > 0 and kv_heads > 0:
+        dev, fresh = q.device, outs
+        if fresh is None:
+            size = shape[1] // heads
+            fresh = [torch.empty((shape[0], h, size), dtype=torch.bfloat16, device=dev) for h in (heads, kv_heads, kv_heads)]
+            _lend(stream, dev, fresh)
+        rc = _native.axes(q, k, v, positions, axis_dims, heads, kv_heads, theta, scale, sections, biases, weights, norm,
+                          eps, interleaved, fresh, dev, _handle(stream))
+        if rc is not None:
+            if rc != H3Q_OK:
+                raise H3QError("h3q_qkv_epilogue_axes", rc, h3q_last_error())
+            return fresh[0], fresh[1], fresh[2]
     q, rows, d, ld_q = _rows_view("q", q, torch.bfloat16)
     dev = q.device
     k, rows_k, d_k, ld_k = _rows_view("k", k, torch.bfloat16, dev)
@@ -1089,6 +1105,23 @@ def h3q_postnorm_residual_adaln_nvfp4(h, o, gamma_post, gamma, global_scale, *, 
     table the frame of a row is ``row_frame[row]`` (int32 CUDA tensor) or ``row // rows_per_frame``.
     ``row_rstd`` (fp32 [rows], optional) receives the rstd of the new h.  Returns (codes, scales)."""
     torch = _torch or _load_torch()
+    shape = getattr(h, "shape", ())
+    if len(shape) == 2:
+        dev, fresh = h.device, []
+        to_codes, to_scales = codes, scales
+        if to_codes is None:
+            to_codes = torch.empty((shape[0], shape[1] // 2), dtype=torch.uint8, device=dev)
+            fresh.append(to_codes)
+        if to_scales is None:
+            to_scales = torch.empty((padded_rows(shape[0]), shape[1] // 16), dtype=torch.uint8, device=dev)
+            fresh.append(to_scales)
+        _lend(stream, dev, fresh)
+        rc = _native.postnorm(h, o, gamma_post, gamma, global_scale, bias, gate_table, mod_table, residual_scale,
+                              row_frame, rows_per_frame, eps, to_codes, to_scales, row_rstd, dev, _handle(stream))
+        if rc is not None:
+            if rc != H3Q_OK:
+                raise H3QError("h3q_postnorm_residual_adaln_nvfp4", rc, h3q_last_error())
+            return to_codes, to_scales
     _cuda_tensor("h", h, torch.float32)
     dev = h.device
     if h.dim() != 2 or (h.shape[1] > 1 and h.stride(1) != 1):
@@ -1168,10 +1201,11 @@ def h3q_select_blocks(q, k, cu_q, cu_k, top, *, block_q=128, block_k=128, causal
     takes them.  ``scores`` (fp32 of the lists' shape, optional) receives the entries' scores.  Where
     ``workspace`` (uint8, select_blocks_workspace_bytes) is not given it is allocated.  Returns the lists."""
     torch = _torch or _load_torch()
-    qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, dev = _block_sequences(
-        q, k, cu_q, cu_k)
     if block_q < 1 or block_k < 1:
         raise ValueError("block_q and block_k must be 64, 128 or 256")
+    if len(getattr(q, "shape", ())) != 3 or len(getattr(k, "shape", ())) != 3 or len(getattr(cu_q, "shape", ())) != 1:
+        _block_sequences(q, k, cu_q, cu_k)
+    (rows_q, _, dim), (rows_k, kv_heads, _), batch, dev = q.shape, k.shape, cu_q.shape[0] - 1, q.device
     shape = (kv_heads, block_rows(rows_q, batch, block_q), int(top))
     fresh = []
     if blocks is None:
@@ -1180,6 +1214,14 @@ def h3q_select_blocks(q, k, cu_q, cu_k, top, *, block_q=128, block_k=128, causal
     nbytes = select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, dim, block_q, block_k)
     workspace = _workspace(workspace, nbytes, dev, fresh)
     _lend(stream, dev, fresh)
+    rc = _native.select(q, k, cu_q, cu_k, top, block_q, block_k, causal, first, blocks, scores, workspace, dev,
+                        _handle(stream))
+    if rc is not None:
+        if rc != H3Q_OK:
+            raise H3QError("h3q_select_blocks", rc, h3q_last_error())
+        return blocks
+    qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, dev = _block_sequences(
+        q, k, cu_q, cu_k)
     blocks_ptr = _dense("blocks", blocks, torch.int32, shape, dev)
     scores_ptr = _dense("scores", scores, torch.float32, shape, dev) if scores is not None else None
     _invoke("h3q_select_blocks", dev, stream,
@@ -1197,6 +1239,18 @@ def h3q_attention_blocks(q, k, v, cu_q, cu_k, blocks, *, block_q=128, block_k=12
     ``lse`` (fp32 [heads, rows_q], optional) receives the log of the sums of exponentials.  Returns out, bf16
     [rows_q, heads, head_dim]; rows of no sequence are left as they were."""
     torch = _torch or _load_torch()
+    shape = getattr(q, "shape", ())
+    if len(shape) == 3:
+        dev, fresh = q.device, out
+        if fresh is None:
+            fresh = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            _lend(stream, dev, [fresh])
+        rc = _native.blocks(q, k, v, cu_q, cu_k, blocks, block_q, block_k, causal, _softmax_scale(scale, shape[2]), fresh,
+                            lse, dev, _handle(stream))
+        if rc is not None:
+            if rc != H3Q_OK:
+                raise H3QError("h3q_attention_blocks", rc, h3q_last_error())
+            return fresh
     qp, ld_q, kp, ld_k, cu_q_ptr, cu_k_ptr, batch, rows_q, rows_k, heads, kv_heads, dim, dev = _block_sequences(
         q, k, cu_q, cu_k)
     vp, v_shape, ld_v = _head_rows("v", v, dev)
