@@ -11,13 +11,14 @@
 // Both rstd in the canonical order (chunk c on lane c % 128, eight fmaf partials per lane, the
 // lane total, a butterfly per warp, (T0+T1)+(T2+T3)).
 //
-// One CTA of 128 threads owns one row at a time (two CTAs per SM, persistent over a contiguous
-// range of rows): the second norm needs all of h', which needs all of u, so a row stays in
-// registers from its load to its codes, with two sums over the CTA between.  The next row's
-// loads are issued before a row is worked on.  The tables of the columns lie in shared memory as
-// bf16, 12 bytes a column: bias and both gammas for the launch, gate, scale and shift of the
-// current frame.  What is absent is a table of ones (gate), zeros (scale) or minus zeros (bias and
-// shift: x + -0 = x, zeros keeping their sign), so a launch has one path.
+// One CTA of 128 threads owns one row at a time, four CTAs an SM: the second norm needs all of h',
+// which needs all of u, so a row stays in registers from its load to its codes, with two sums over the
+// CTA between.  The other CTAs' rows fill the waits, and a row is asked for (a bulk prefetch into
+// L2) when the one before is begun.  Neighbouring rows go to different CTAs, so that all of them are in
+// the same frame or two and the tables, 12 bytes a column, are read through L1.  (Two CTAs with the
+// tables in shared memory and the next row in registers took 909 us for 65,280 x 7,168.)
+// What is absent is a value of one (gate), zero (scale) or minus zero (bias and shift: x + -0 = x, zeros
+// keeping their sign), so a launch has one path.
 //
 // Bound: 4 + 2 + 4 + 0.5 + 1/16 bytes of DRAM traffic an element.
 #include "h3q_device.cuh"
@@ -27,9 +28,6 @@ namespace h3q {
 namespace {
 
 constexpr int kThreads = 128;  // the lanes of the canonical order
-
-// Planes of 16-byte entries in shared memory, one entry per 8-column chunk.
-enum Plane { kBias, kGammaPost, kGamma, kGate, kScale, kShift, kPlanes };
 
 __device__ __forceinline__ int64_t frame_of(const PostnormArgs& a, int64_t row) {
   if (a.gate == nullptr && a.table == nullptr) return 0;
@@ -66,66 +64,52 @@ __device__ __forceinline__ float row_rstd_of(const float2 (&acc)[4], float* tota
 
 // Rows of up to 1,024 * C1 columns (FULL: exactly).
 template <int C1, bool FULL>
-__global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArgs a) {
-  constexpr int kSlots = kThreads * C1;
-  extern __shared__ uint4 planes[];   // [kPlanes][kSlots]
+__global__ void __launch_bounds__(kThreads, C1 > 4 ? 3 : 4) postnorm_kernel(const __grid_constant__ PostnormArgs a) {
   __shared__ float inv_table[128];
   __shared__ float totals[4][4];      // [row parity * 2 + norm]
   const float gsf = *a.gsf;
   fill_inverse_scales(inv_table, gsf);
+  __syncthreads();
 
   const int t = threadIdx.x;
   const int chunks = static_cast<int>(a.cols >> 3);
   const int64_t quads = a.cols >> 6;
   const float cols_f = static_cast<float>(a.cols);  // exact: cols <= 8,192
   constexpr uint32_t kOnes = 0x3f803f80u, kMinusZeros = 0x80008000u;
-  for (int c = t; c < chunks; c += kThreads) {  // the launch-wide planes, and what is absent
-    planes[kBias * kSlots + c] = a.bias ? load16_reused(a.bias + c * 8) : filled(kMinusZeros);
-    planes[kGammaPost * kSlots + c] = load16_reused(a.gamma_post + c * 8);
-    planes[kGamma * kSlots + c] = load16_reused(a.gamma + c * 8);
-    if (a.gate == nullptr) planes[kGate * kSlots + c] = filled(kOnes);
-    if (a.table == nullptr) {
-      planes[kScale * kSlots + c] = filled(0u);
-      planes[kShift * kSlots + c] = filled(kMinusZeros);
-    }
-  }
-  __syncthreads();
-  const int64_t r_begin = a.rows * blockIdx.x / gridDim.x;
-  const int64_t r_end = a.rows * (blockIdx.x + 1) / gridDim.x;
-  int64_t frame = -1;
+  const uint16_t* const bias = a.bias ? a.bias + t * 8 : nullptr;
+  auto entry = [&](const uint16_t* table, int j, uint32_t absent) {   // eight columns of a table
+    return table != nullptr && (FULL || t + j * kThreads < chunks) ? load16_reused(table + j * (kThreads * 8)) : filled(absent);
+  };
 
-  auto load = [&](int64_t r, float (&h)[C1][8], uint4 (&o)[C1]) {
-    if (r >= r_end) return;  // CTA-uniform
-    const float* hr = a.h + r * a.ld_h + t * 8;
-    const uint16_t* orow = a.o + r * a.ld_o + t * 8;
+  int parity = 0;
+  int64_t frame = frame_of(a, blockIdx.x);
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x, parity ^= 1) {
+    float h[C1][8];
+    uint4 o[C1];
+    const int64_t next = r + gridDim.x;
+    if (next < a.rows && t < 2) {
+      const void* from = t == 0 ? static_cast<const void*>(a.o + next * a.ld_o) : static_cast<const void*>(a.h + next * a.ld_h);
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(static_cast<uint32_t>(a.cols) * (t == 0 ? 2u : 4u))
+                   : "memory");
+    }
+    const int64_t next_frame = next < a.rows ? frame_of(a, next) : 0;
+    float* const hr = a.h + r * a.ld_h + t * 8;
+    const uint16_t* const orow = a.o + r * a.ld_o + t * 8;
+#pragma unroll
+    for (int j = 0; j < C1; ++j)
+      o[j] = FULL || t + j * kThreads < chunks ? load16_stream(orow + j * (kThreads * 8)) : filled(0u);
 #pragma unroll
     for (int j = 0; j < C1; ++j) {
       if (FULL || t + j * kThreads < chunks) {
-        o[j] = load16_stream(orow + j * (kThreads * 8));
         ld_h8(hr + j * (kThreads * 8), h[j]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[j][e] = 0.0f;
-        o[j] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
-  };
-
-  auto process = [&](int64_t r, float (&h)[C1][8], uint4 (&o)[C1], int parity) {
-    const int64_t f = frame_of(a, r);  // CTA-uniform
-    if (f != frame) {
-      __syncthreads();  // nobody reads the previous frame's planes any more
-      for (int c = t; c < chunks; c += kThreads) {
-        if (a.gate != nullptr) planes[kGate * kSlots + c] = load16_reused(a.gate + f * a.cols + c * 8);
-        if (a.table != nullptr) {
-          const uint16_t* shift = a.table + f * 2 * a.cols + c * 8;
-          planes[kShift * kSlots + c] = load16_reused(shift);
-          planes[kScale * kSlots + c] = load16_reused(shift + a.cols);
-        }
-      }
-      __syncthreads();
-      frame = f;
-    }
+    const uint16_t* const gate = a.gate ? a.gate + frame * a.cols + t * 8 : nullptr;
+    const uint16_t* const shift = a.table ? a.table + frame * 2 * a.cols + t * 8 : nullptr;
+    const uint16_t* const scale = a.table ? shift + a.cols : nullptr;
     // u, over o, and its squares (exact in fp32)
     float2 acc[4];
 #pragma unroll
@@ -134,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArg
     for (int j = 0; j < C1; ++j) {
       const int c = t + j * kThreads;
       if (FULL || c < chunks) {
-        const uint4 b = planes[kBias * kSlots + c];
+        const uint4 b = entry(bias, j, kMinusZeros);
         o[j] = make_uint4(add_bf16x2(o[j].x, b.x), add_bf16x2(o[j].y, b.y), add_bf16x2(o[j].z, b.z),
                           add_bf16x2(o[j].w, b.w));
         const uint32_t w[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
@@ -148,14 +132,13 @@ __global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArg
     const float rstd_u = row_rstd_of(acc, totals[2 * parity], cols_f, a.eps);
     // the residual, written back, and its squares
     const float2 rstd_u2 = make_float2(rstd_u, rstd_u), keep2 = make_float2(a.keep, a.keep);
-    float* hr = a.h + r * a.ld_h + t * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < C1; ++j) {
       const int c = t + j * kThreads;
       if (FULL || c < chunks) {
-        const uint4 p4 = planes[kGammaPost * kSlots + c], g4 = planes[kGate * kSlots + c];
+        const uint4 p4 = entry(a.gamma_post + t * 8, j, 0u), g4 = entry(gate, j, kOnes);
         const uint32_t w[4] = {o[j].x, o[j].y, o[j].z, o[j].w}, pw[4] = {p4.x, p4.y, p4.z, p4.w},
                        gw[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
@@ -183,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArg
     for (int j = 0; j < C1; ++j) {
       const int c = t + j * kThreads;
       const bool valid = FULL || c < chunks;
-      const uint4 g4 = planes[kGamma * kSlots + c], s4 = planes[kScale * kSlots + c], t4 = planes[kShift * kSlots + c];
+      const uint4 g4 = entry(a.gamma + t * 8, j, 0u), s4 = entry(scale, j, 0u), t4 = entry(shift, j, kMinusZeros);
       const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, sw[4] = {s4.x, s4.y, s4.z, s4.w},
                      tw[4] = {t4.x, t4.y, t4.z, t4.w};
       uint32_t y[4];
@@ -200,19 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArg
       if (valid) store_word(codes_at + j * (kThreads * 4), codes);
       if (valid && !(t & 1)) store_byte(scale_at + j * (kThreads / 8 * 512), sf);
     }
-  };
-
-  // Two register sets: the next row's loads are in flight while a row is worked on.
-  float hA[C1][8], hB[C1][8];
-  uint4 oA[C1], oB[C1];
-  load(r_begin, hA, oA);
-  for (int64_t r = r_begin; r < r_end; r += 2) {
-    load(r + 1, hB, oB);
-    process(r, hA, oA, 0);
-    if (r + 1 < r_end) {  // CTA-uniform
-      load(r + 2, hA, oA);
-      process(r + 1, hB, oB, 1);
-    }
+    frame = next_frame;
   }
 
   // zero the scale words of the padding rows rows..pad128(rows)-1
@@ -224,17 +195,16 @@ __global__ void __launch_bounds__(kThreads, 2) postnorm_kernel(const PostnormArg
 
 template <int C1>
 cudaError_t launch_c1(const PostnormArgs& a, cudaStream_t stream) {
-  const int smem = kPlanes * kThreads * C1 * 16;
   const bool full = a.cols == int64_t(1024) * C1;
   const void* kernel = full ? reinterpret_cast<const void*>(&postnorm_kernel<C1, true>)
                             : reinterpret_cast<const void*>(&postnorm_kernel<C1, false>);
   int blocks = 0;
-  cudaError_t err = persistent_blocks(kernel, kThreads, smem, a.rows, &blocks);
+  cudaError_t err = persistent_blocks(kernel, kThreads, 0, a.rows, &blocks);
   if (err != cudaSuccess) return err;
   if (full)
-    postnorm_kernel<C1, true><<<blocks, kThreads, smem, stream>>>(a);
+    postnorm_kernel<C1, true><<<blocks, kThreads, 0, stream>>>(a);
   else
-    postnorm_kernel<C1, false><<<blocks, kThreads, smem, stream>>>(a);
+    postnorm_kernel<C1, false><<<blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
