@@ -18,9 +18,12 @@
 // ROT/16 lanes away (a shuffle), an interleaved one in the same lane.
 //
 // Bound: every value is read and written once, 4 bytes, which is DRAM's time; the arithmetic, about
-// 80 instructions for 256 values, runs beside it.  A unit of work is a row's heads of q, k or v
-// (fewer of them where there are not rows enough to fill the GPU), four loads of 512 bytes a
-// warp in flight.
+// 80 instructions for 256 values, runs beside it.  A unit of work is a row's heads of q, k or v, or some of
+// them where there are few rows: all of q's, then k's, then v's, because DRAM reads and writes one
+// tensor faster than three at once (65,280 rows of 56 heads of 128: 883 us, 6.4 TB/s, with the rows' three
+// units together 929).  A warp's values land in a ring of its own in shared memory, a load of 1 KB ahead of
+// the one that it works on, also of its next unit.
+#include "h3q_async.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
 
@@ -29,7 +32,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;   // head groups whose loads are in flight together
+constexpr int kUnroll = 2;   // head groups that are loaded together
+constexpr int kRing = 2;     // such loads of a warp: of one it works, the other is under way
 constexpr int kMaxPairs = 128;
 
 struct AxesArgs {
@@ -62,12 +66,13 @@ constexpr uint32_t kMinusZeros = 0x80008000u;   // x + -0 = x, the sign of a zer
 
 // 8 * LPH values a head: LPH lanes each, 32 / LPH heads at a time.
 template <int LPH, bool ILV>
-__global__ void __launch_bounds__(kThreads, 3) qkv_axes_kernel(const __grid_constant__ AxesArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) qkv_axes_kernel(const __grid_constant__ AxesArgs a) {
   constexpr int kHd = 8 * LPH;
   constexpr int kHeadsPerWarp = 32 / LPH;
   __shared__ unsigned long long turns[kMaxPairs];
   __shared__ uint8_t axis[kMaxPairs];
   __shared__ __align__(16) float2 angles[kWarps][kHd / 2];   // cos, sin
+  __shared__ uint4 ring[kWarps][kRing][kUnroll][32];         // (each lane reads what it has loaded)
   const int pairs = a.rot / 2;
   for (int j = threadIdx.x; j < pairs; j += kThreads) {
     turns[j] = a.turns.of_pair[j];
@@ -80,74 +85,84 @@ __global__ void __launch_bounds__(kThreads, 3) qkv_axes_kernel(const __grid_cons
   const int rot_chunks = a.rot >> 3, half = rot_chunks >> 1;
   const bool rotated = c < rot_chunks;
   const int src = (lane - c) + (c < half ? c + half : rotated ? c - half : c);   // rotate-half partner
-  const int row_units = a.units[0] + a.units[1] + a.units[2];
-  const int64_t units = a.rows * row_units;
+  const int64_t units = a.rows * (a.units[0] + a.units[1] + a.units[2]);
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
 
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units; u += nwarps) {
-    const int64_t row = u / row_units;
-    int part = static_cast<int>(u - row * row_units), tensor = 0;
-    while (part >= a.units[tensor]) part -= a.units[tensor++];   // warp-uniform
-    const int heads = a.heads[tensor];
-    const uint16_t* const xrow = a.x[tensor] + row * a.ld[tensor];
-    uint16_t* const orow = a.out[tensor] + row * (static_cast<int64_t>(heads) * kHd);
-    const uint16_t* const bias = a.bias[tensor];
-    const int all = (heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
-    const int g_begin = part * a.unit_groups;
-    const int g_end = g_begin + a.unit_groups < all ? g_begin + a.unit_groups : all;
-    const int col0 = (lane / LPH) * kHd + c * 8;
+  const int col0 = (lane / LPH) * kHd + c * 8;
+  const int rounds = (pairs + 31) / 32;
 
-    auto load = [&](int g, uint4 (&xw)[kUnroll]) {
+  struct Unit {
+    int64_t row;
+    int tensor, g, g_end;   // head groups [g, g_end)
+  };
+  auto unit_of = [&](int64_t u) {
+    Unit w;
+    w.tensor = 0;
+    while (u >= a.rows * a.units[w.tensor]) u -= a.rows * a.units[w.tensor++];   // (all of q, then k, then v)
+    w.row = a.units[w.tensor] == 1 ? u : u / a.units[w.tensor];
+    const int part = static_cast<int>(u - w.row * a.units[w.tensor]);
+    const int all = (a.heads[w.tensor] + kHeadsPerWarp - 1) / kHeadsPerWarp;
+    w.g = part * a.unit_groups;
+    w.g_end = w.g + a.unit_groups < all ? w.g + a.unit_groups : all;
+    return w;
+  };
+
+  int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (u >= units) return;
+  Unit w = unit_of(u), f = w;   // worked on; loaded
+  int64_t fu = u;
+  int slot = 0, fslot = 0;
+  // The next load (zeros where there is no head), or none after the last unit's.
+  auto load = [&]() {
+    if (fu < units) {
+      const uint16_t* const x = a.x[f.tensor] + f.row * a.ld[f.tensor] + col0;
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        xw[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (g + j < g_end && (g + j) * kHeadsPerWarp + lane / LPH < heads)
-          xw[j] = load16_stream(xrow + static_cast<int64_t>(g + j) * (kHeadsPerWarp * kHd) + col0);
+        const bool there = f.g + j < f.g_end && (f.g + j) * kHeadsPerWarp + lane / LPH < a.heads[f.tensor];
+        const uint16_t* const from = there ? x + static_cast<int64_t>(f.g + j) * (kHeadsPerWarp * kHd) : a.x[f.tensor];
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(&ring[warp][fslot][j][lane])), "l"(from),
+                     "r"(there ? 16 : 0)
+                     : "memory");
       }
-    };
-    auto bias_of = [&](int g, bool mine) {
-      return mine && bias != nullptr ? load16_reused(bias + static_cast<int64_t>(g) * (kHeadsPerWarp * kHd) + col0)
-                                     : make_uint4(kMinusZeros, kMinusZeros, kMinusZeros, kMinusZeros);
-    };
-
-    uint4 xw[kUnroll];
-    load(g_begin, xw);
-    if (tensor == 2) {
-      for (int g = g_begin; g < g_end; g += kUnroll) {
-        if (g > g_begin) load(g, xw);
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-          const bool mine = g + j < g_end && (g + j) * kHeadsPerWarp + lane / LPH < heads;
-          const uint4 b = bias_of(g + j, mine);   // (one rounding: the sum of two bf16 values)
-          if (mine)
-            store16(orow + static_cast<int64_t>(g + j) * (kHeadsPerWarp * kHd) + col0,
-                    make_uint4(add_bf16x2(xw[j].x, b.x), add_bf16x2(xw[j].y, b.y), add_bf16x2(xw[j].z, b.z),
-                               add_bf16x2(xw[j].w, b.w)));
-        }
+      fslot = (fslot + 1) % kRing;
+      f.g += kUnroll;
+      if (f.g >= f.g_end) {
+        fu += nwarps;
+        if (fu < units) f = unit_of(fu);
       }
-      continue;
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) load();
+  for (;;) {
+    const int heads = a.heads[w.tensor];
+    uint16_t* const out = a.out[w.tensor] + w.row * (static_cast<int64_t>(heads) * kHd) + col0;
+    const uint16_t* const bias = a.bias[w.tensor] ? a.bias[w.tensor] + col0 : nullptr;
 
     // the row's angles, while its first values are on their way
-    __syncwarp();
-    for (int j = lane; j < pairs; j += 32) {
-      const long long p = a.positions[row * a.axes + axis[j]];
-      const long long t = static_cast<long long>(static_cast<unsigned long long>(p) * turns[j]);
-      float s, co;
-      sincospif(__fmul_rn(__ll2float_rn(t), 0x1p-63f), &s, &co);
-      angles[warp][j] = make_float2(co, s);
-    }
-    __syncwarp();
     float2 A[4], B[4];   // out_i = rstd * (x_i A_i + partner_i B_i)
-    {
-      const uint16_t* const weight = a.weight[tensor];
-      constexpr uint32_t kOnes = 0x3f803f80u;
-      uint4 w = make_uint4(kOnes, kOnes, kOnes, kOnes), wp = w;
-      if (weight != nullptr) {
-        w = load16_reused(weight + c * 8);
-        wp = ILV ? w : load16_reused(weight + (src % LPH) * 8);
+    if (w.tensor < 2) {
+      __syncwarp();
+      for (int i = 0; i < rounds; ++i) {
+        const int j = lane + 32 * i;
+        if (j < pairs) {
+          const long long p = a.positions[w.row * a.axes + axis[j]];
+          const long long t = static_cast<long long>(static_cast<unsigned long long>(p) * turns[j]);
+          float s, co;
+          sincospif(__fmul_rn(__ll2float_rn(t), 0x1p-63f), &s, &co);
+          angles[warp][j] = make_float2(co, s);
+        }
       }
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w}, wq[4] = {wp.x, wp.y, wp.z, wp.w};
+      __syncwarp();
+      const uint16_t* const weight = a.weight[w.tensor];
+      constexpr uint32_t kOnes = 0x3f803f80u;
+      uint4 wv = make_uint4(kOnes, kOnes, kOnes, kOnes), wp = wv;
+      if (weight != nullptr) {
+        wv = load16_reused(weight + c * 8);
+        wp = ILV ? wv : load16_reused(weight + (src % LPH) * 8);
+      }
+      const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w}, wq[4] = {wp.x, wp.y, wp.z, wp.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 wi = bf16x2_to_float2(ww[i]), wo = bf16x2_to_float2(wq[i]);
@@ -169,14 +184,28 @@ __global__ void __launch_bounds__(kThreads, 3) qkv_axes_kernel(const __grid_cons
       }
     }
 
-    for (int g = g_begin; g < g_end; g += kUnroll) {
-      if (g > g_begin) load(g, xw);
+    for (int g = w.g; g < w.g_end; g += kUnroll) {
+      load();
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      uint4 xw[kUnroll];
+#pragma unroll
+      for (int j = 0; j < kUnroll; ++j) xw[j] = ring[warp][slot][j][lane];
+      slot = (slot + 1) % kRing;
 #pragma unroll
       for (int j = 0; j < kUnroll; ++j) {
-        if (g + j >= g_end) break;  // warp-uniform
+        if (g + j >= w.g_end) break;  // warp-uniform
         const bool mine = (g + j) * kHeadsPerWarp + lane / LPH < heads;
+        const int64_t at = static_cast<int64_t>(g + j) * (kHeadsPerWarp * kHd);
+        const uint4 b = mine && bias != nullptr ? load16_reused(bias + at)
+                                                : make_uint4(kMinusZeros, kMinusZeros, kMinusZeros, kMinusZeros);
+        if (w.tensor == 2) {   // (one rounding: the sum of two bf16 values)
+          if (mine)
+            store16(out + at, make_uint4(add_bf16x2(xw[j].x, b.x), add_bf16x2(xw[j].y, b.y), add_bf16x2(xw[j].z, b.z),
+                                         add_bf16x2(xw[j].w, b.w)));
+          continue;
+        }
         float2 x[4];
-        biased(xw[j], bias_of(g + j, mine), x);
+        biased(xw[j], b, x);
         float rstd = 1.0f;
         if (a.norm) {
           const float2 s2 = fma2(x[3], x[3], fma2(x[2], x[2], fma2(x[1], x[1], mul2(x[0], x[0]))));
@@ -186,27 +215,23 @@ __global__ void __launch_bounds__(kThreads, 3) qkv_axes_kernel(const __grid_cons
           rstd = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / kHd), a.eps));
         }
         float2 y[4];
-        if constexpr (ILV) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[i] = mul2(x[i], A[i]);
-            if (rotated) y[i] = fma2(make_float2(x[i].y, x[i].x), B[i], y[i]);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 p = make_float2(__shfl_sync(0xffffffffu, x[i].x, src), __shfl_sync(0xffffffffu, x[i].y, src));
-            y[i] = mul2(x[i], A[i]);
-            if (rotated) y[i] = fma2(p, B[i], y[i]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          float2 p = make_float2(x[i].y, x[i].x);
+          if constexpr (!ILV)
+            p = make_float2(__shfl_sync(0xffffffffu, x[i].x, src), __shfl_sync(0xffffffffu, x[i].y, src));
+          y[i] = mul2(x[i], A[i]);
+          if (rotated) y[i] = fma2(p, B[i], y[i]);
         }
         const float2 r2 = make_float2(rstd, rstd);
         if (mine)
-          store16(orow + static_cast<int64_t>(g + j) * (kHeadsPerWarp * kHd) + col0,
-                  make_uint4(float2_to_bf16x2(mul2(y[0], r2)), float2_to_bf16x2(mul2(y[1], r2)),
-                             float2_to_bf16x2(mul2(y[2], r2)), float2_to_bf16x2(mul2(y[3], r2))));
+          store16(out + at, make_uint4(float2_to_bf16x2(mul2(y[0], r2)), float2_to_bf16x2(mul2(y[1], r2)),
+                                       float2_to_bf16x2(mul2(y[2], r2)), float2_to_bf16x2(mul2(y[3], r2))));
       }
     }
+    u += nwarps;
+    if (u >= units) break;
+    w = unit_of(u);
   }
 }
 
@@ -216,7 +241,8 @@ cudaError_t launch(AxesArgs& a, cudaStream_t stream) {
   int blocks = 0;
   cudaError_t err = persistent_blocks(kernel, kThreads, 0, int64_t{1} << 30, &blocks);
   if (err != cudaSuccess) return err;
-  // A unit takes all heads of a row where the rows alone fill the GPU, down to one batch of loads.
+  // A unit takes all heads of a row where the rows give every warp some eight units, down to one load's:
+  // its angles are made again for every unit of the row, but the warps end together.
   constexpr int kHeadsPerWarp = 32 / LPH;
   int most = 0;
   for (int t = 0; t < 3; ++t) {
@@ -224,9 +250,10 @@ cudaError_t launch(AxesArgs& a, cudaStream_t stream) {
     most = groups > most ? groups : most;
   }
   const int64_t warps = static_cast<int64_t>(blocks) * kWarps;
-  int64_t parts = (warps + 3 * a.rows - 1) / (3 * a.rows);
+  int64_t parts = 8 * warps / (3 * a.rows);
   const int64_t batches = (most + kUnroll - 1) / kUnroll;
   if (parts > batches) parts = batches;
+  if (parts < 1) parts = 1;
   a.unit_groups = static_cast<int>((batches + parts - 1) / parts) * kUnroll;
   int64_t units = 0;
   for (int t = 0; t < 3; ++t) {
