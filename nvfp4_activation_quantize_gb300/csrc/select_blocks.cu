@@ -249,7 +249,7 @@ constexpr int kStages = 4;
 constexpr int kStageBytes = kTile * kDims * 4;
 // Scores that a CTA holds: 16 query blocks against 512 or 1,024 key blocks, or fewer against more (one
 // against 16,384, see kMaxBlocks).
-constexpr int kMostScores = kRows * 1024;
+constexpr int kFewScores = kRows * 512, kMostScores = kRows * 1024;
 
 struct ScoreArgs {
   BlockShape s;
@@ -306,10 +306,9 @@ struct Orders {
   }
 };
 
-// The n-th highest of the orders, 0 if fewer than n are above 0, how many are higher and how many it is.  Each
-// round halves the interval; the first ones by the share of the scores that are in it and above (which
-// finds a border that some hundred scores have between them in five or six), then by the values and
-// at last by the orders.  Whole warp.
+// The n-th highest of the orders, 0 if fewer than n are above 0, how many are higher and how many it is.
+// Bisection: of the values where that narrows (nine rounds for 510 normally distributed scores), else of
+// the orders.  (By the share of the scores that an interval has, twelve rounds.)  Whole warp.
 template <int R>
 __device__ __forceinline__ uint32_t nth_highest(Orders<R>& row, int n, int& above, int& same) {
   uint32_t lowest = 0xffffffffu, highest = 0u;
@@ -319,18 +318,15 @@ __device__ __forceinline__ uint32_t nth_highest(Orders<R>& row, int n, int& abov
     highest = max(highest, x);
     any += x != 0u;
   });
-  int at_lo = __reduce_add_sync(0xffffffffu, any), over_hi = 0;   // at least n are >= lo, fewer than n > hi
-  above = at_lo;
+  above = __reduce_add_sync(0xffffffffu, any);
   same = 0;
-  if (at_lo < n) return 0u;
+  if (above < n) return 0u;
+  // at least n are >= lo, fewer than n are > hi
   uint32_t lo = __reduce_min_sync(0xffffffffu, lowest), hi = __reduce_max_sync(0xffffffffu, highest);
   for (int round = 0; lo < hi; ++round) {
     uint32_t mid = lo + (hi - lo) / 2 + 1;
     if (round < 24) {
-      const float from = value_of(lo), width = __fsub_rn(value_of(hi), from);
-      const float share = round % 3 == 2 ? 0.5f
-                                         : __fdividef(static_cast<float>(at_lo - n) + 0.5f, static_cast<float>(at_lo - over_hi));
-      const uint32_t between = order_of(__fadd_rn(from, __fmul_rn(width, share)));
+      const uint32_t between = order_of(__fmul_rn(0.5f, __fadd_rn(value_of(lo), value_of(hi))));
       if (between > lo && between <= hi) mid = between;
     }
     int mine = 0;
@@ -338,10 +334,8 @@ __device__ __forceinline__ uint32_t nth_highest(Orders<R>& row, int n, int& abov
     const int got = __reduce_add_sync(0xffffffffu, mine);
     if (got < n) {
       hi = mid - 1;
-      over_hi = got;
     } else if (got > n) {
       lo = mid;
-      at_lo = got;
     } else {   // exactly these: the lowest of them
       uint32_t least = 0xffffffffu;
       row.each([&](int, uint32_t x) {
@@ -484,7 +478,7 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
 }
 
 template <int HD, int CAPACITY>
-__global__ void __launch_bounds__(kThreads, CAPACITY <= kRows * 512 ? 2 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   float* const q = reinterpret_cast<float*>(smem + kStages * kStageBytes);    // [kRows][HD]
   uint32_t* const scored = reinterpret_cast<uint32_t*>(q + kRows * HD);       // orders [rows of a pass][width]
@@ -629,12 +623,10 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kRows * 512 ? 2 : 1) sco
       const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
       if (p.candidates <= 512) {
         choose<HD, 16>(a, p, row, q_row, k_at, len, list);
-      } else if constexpr (CAPACITY > kRows * 512) {
-        if (p.candidates <= 1024) {
-          choose<HD, 32>(a, p, row, q_row, k_at, len, list);
-        } else {
-          choose<HD, 0>(a, p, row, q_row, k_at, len, list);
-        }
+      } else if (CAPACITY > kFewScores && p.candidates <= 1024) {
+        choose<HD, (CAPACITY > kFewScores) ? 32 : 0>(a, p, row, q_row, k_at, len, list);
+      } else {
+        choose<HD, 0>(a, p, row, q_row, k_at, len, list);
       }
     }
     seg += n;
@@ -673,9 +665,13 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  // room for the longest sequence that there can be
+  // Many lists: two CTAs an SM, each with room for 16 query blocks against 512 key blocks, which is enough where
+  // sequences have so many on average (65,280 tokens 0.60 ms against 0.71 with one CTA).  Few: one
+  // CTA an SM, whose registers hold all that it works on (16 single tokens 64 us against 74, 4 chunks 88 against 103).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
-  if (longest <= 512) return launch_score<HD, kRows * 512>(score, stream);
+  const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
+  if (many && longest <= kFewScores && longest <= 512 * static_cast<int64_t>(score.s.batch))
+    return launch_score<HD, kFewScores>(score, stream);
   return launch_score<HD, kMostScores>(score, stream);
 }
 
