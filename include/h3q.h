@@ -629,7 +629,7 @@ int h3q_attention_cache_nvfp4(const void *q, int64_t ld_q, int64_t rows, int64_t
  * axis_dims[i] / 2 each.  f of pair i of an axis of d values is scale * theta^(-2i/d); with
  * `sections` it is scale * theta^(-2j/ROT) of the pair's number j in all of ROT.  The angle is
  * reduced to a turn in integers before it becomes fp32, so it is as exact for a position of a million
- * as for one of ten (off by at most 2^-50 of the position, and 2^-23 of a turn).
+ * as for one of ten (off by at most 2^-46 of the position, and 2^-23 of a turn).
  *
  *   q              bf16 [rows, heads * head_dim], k and v [rows, kv_heads * head_dim], row
  *                  strides ld_q, ld_k, ld_v (multiples of 16), 32-byte aligned.

@@ -1054,20 +1054,23 @@ def h3q_qkv_epilogue_axes(q, k, v, positions, axis_dims, heads, *, kv_heads=None
     (j, j + sum / 2), or (2j, 2j + 1) with ``interleaved``.  ``biases`` (of q, k and v) and ``weights`` (of
     q's and k's norm, [HD]) are tuples of bf16 tensors, any of them None."""
     torch = _torch or _load_torch()
-    kv_heads = heads if kv_heads is None else kv_heads
+    if kv_heads is None:
+        kv_heads = heads
     shape = getattr(q, "shape", ())
     if len(shape) == 2 and heads > 0 and kv_heads > 0:
         dev, fresh = q.device, outs
         if fresh is None:
-            size = shape[1] // heads
-            fresh = [torch.empty((shape[0], h, size), dtype=torch.bfloat16, device=dev) for h in (heads, kv_heads, kv_heads)]
-            _lend(stream, dev, fresh)
+            rows, size, empty, bf16 = shape[0], shape[1] // heads, torch.empty, torch.bfloat16
+            fresh = (empty((rows, heads, size), dtype=bf16, device=dev), empty((rows, kv_heads, size), dtype=bf16, device=dev),
+                     empty((rows, kv_heads, size), dtype=bf16, device=dev))
+            if stream is not None:
+                _lend(stream, dev, fresh)
         rc = _native.axes(q, k, v, positions, axis_dims, heads, kv_heads, theta, scale, sections, biases, weights, norm,
-                          eps, interleaved, fresh, dev, _handle(stream))
+                          eps, interleaved, fresh, dev, None if stream is None else _handle(stream))
+        if rc == H3Q_OK:
+            return fresh if outs is None else tuple(fresh)
         if rc is not None:
-            if rc != H3Q_OK:
-                raise H3QError("h3q_qkv_epilogue_axes", rc, h3q_last_error())
-            return fresh[0], fresh[1], fresh[2]
+            raise H3QError("h3q_qkv_epilogue_axes", rc, h3q_last_error())
     q, rows, d, ld_q = _rows_view("q", q, torch.bfloat16)
     dev = q.device
     k, rows_k, d_k, ld_k = _rows_view("k", k, torch.bfloat16, dev)
@@ -1107,21 +1110,21 @@ def h3q_postnorm_residual_adaln_nvfp4(h, o, gamma_post, gamma, global_scale, *, 
     torch = _torch or _load_torch()
     shape = getattr(h, "shape", ())
     if len(shape) == 2:
-        dev, fresh = h.device, []
-        to_codes, to_scales = codes, scales
+        dev, u8, to_codes, to_scales = h.device, torch.uint8, codes, scales
+        rows, cols = shape
         if to_codes is None:
-            to_codes = torch.empty((shape[0], shape[1] // 2), dtype=torch.uint8, device=dev)
-            fresh.append(to_codes)
+            to_codes = torch.empty((rows, cols // 2), dtype=u8, device=dev)
         if to_scales is None:
-            to_scales = torch.empty((padded_rows(shape[0]), shape[1] // 16), dtype=torch.uint8, device=dev)
-            fresh.append(to_scales)
-        _lend(stream, dev, fresh)
+            to_scales = torch.empty(((rows + 127) // 128 * 128, cols // 16), dtype=u8, device=dev)
+        if stream is not None:
+            _lend(stream, dev, [t for t, given in ((to_codes, codes), (to_scales, scales)) if given is None])
         rc = _native.postnorm(h, o, gamma_post, gamma, global_scale, bias, gate_table, mod_table, residual_scale,
-                              row_frame, rows_per_frame, eps, to_codes, to_scales, row_rstd, dev, _handle(stream))
-        if rc is not None:
-            if rc != H3Q_OK:
-                raise H3QError("h3q_postnorm_residual_adaln_nvfp4", rc, h3q_last_error())
+                              row_frame, rows_per_frame, eps, to_codes, to_scales, row_rstd, dev,
+                              None if stream is None else _handle(stream))
+        if rc == H3Q_OK:
             return to_codes, to_scales
+        if rc is not None:
+            raise H3QError("h3q_postnorm_residual_adaln_nvfp4", rc, h3q_last_error())
     _cuda_tensor("h", h, torch.float32)
     dev = h.device
     if h.dim() != 2 or (h.shape[1] > 1 and h.stride(1) != 1):

@@ -73,16 +73,21 @@ static int attr_is(PyObject *o, PyObject *name, PyObject *want)
     return same;
 }
 
+/* Whether the tensor is on this device. */
+static int on_device(PyObject *t, PyObject *device)
+{
+    PyObject *d = PyObject_GetAttr(t, s_device);
+    if (d == NULL) return 0;
+    int same = d == device || PyObject_RichCompareBool(d, device, Py_EQ) == 1;
+    Py_DECREF(d);
+    return same;
+}
+
 /* The tensor's dimensions, if it is one of this dtype with nd of them on this device. */
 static int look(PyObject *t, PyObject *dtype, PyObject *device, int nd, View *v)
 {
     if (Py_TYPE(t) != (PyTypeObject *)g_tensor && !PyType_IsSubtype(Py_TYPE(t), (PyTypeObject *)g_tensor)) return 0;
-    if (!attr_is(t, s_dtype, dtype)) return 0;
-    PyObject *d = PyObject_GetAttr(t, s_device);
-    if (d == NULL) return 0;
-    int same = PyObject_RichCompareBool(d, device, Py_EQ);
-    Py_DECREF(d);
-    if (same != 1) return 0;
+    if (!attr_is(t, s_dtype, dtype) || !on_device(t, device)) return 0;
     PyObject *shape = PyObject_GetAttr(t, s_shape);
     if (shape == NULL || !PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != nd) {
         Py_XDECREF(shape);

@@ -979,11 +979,11 @@ int h3q_qkv_epilogue_axes(const void* q, int64_t ld_q, const void* k, int64_t ld
   if (!std::isfinite(eps) || eps < 0.0f) return invalid(fn, "eps must be finite and >= 0");
   h3q::RopeTurns turns{};
   int64_t j = 0;
-  for (int64_t i = 0; i < axes; ++i)
+  for (int64_t i = 0; i < axes; ++i) {
+    // theta^(-2 p / d) as a power of two (half of pow's time, which is a tenth of a small call's)
+    const double step = -2.0 * std::log2(theta[sections ? 0 : i]) / static_cast<double>(sections ? rot : axis_dims[i]);
     for (int64_t p = 0; p < axis_dims[i] / 2; ++p, ++j) {
-      const double f = scale[i] * (sections ? std::pow(theta[0], -2.0 * static_cast<double>(j) / static_cast<double>(rot))
-                                            : std::pow(theta[i], -2.0 * static_cast<double>(p) /
-                                                                     static_cast<double>(axis_dims[i])));
+      const double f = scale[i] * std::exp2(step * static_cast<double>(sections ? j : p));
       constexpr double kTurn = 6.283185307179586476925;
       const double t = f / kTurn;
       if (!std::isfinite(t)) return invalid(fn, "theta and scale give a frequency that is not finite");
@@ -991,6 +991,7 @@ int h3q_qkv_epilogue_axes(const void* q, int64_t ld_q, const void* k, int64_t ld
       turns.of_pair[j] = part >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(part, 64));
       turns.axis[j] = static_cast<uint8_t>(i);
     }
+  }
   if (rows == 0) return H3Q_OK;
   const void* xs[3] = {q, k, v};
   const int64_t lds[3] = {ld_q, ld_k, ld_v};
