@@ -306,54 +306,82 @@ struct Orders {
   }
 };
 
-// The n-th highest of the orders, 0 if fewer than n are above 0, how many are higher and how many it is.
-// Bisection: of the values where that narrows (nine rounds for 510 normally distributed scores), else of
-// the orders.  (By the share of the scores that an interval has, twelve rounds.)  Whole warp.
+// Where a row is cut: `border` is the n-th highest of its orders (0 if fewer than n are above 0), `next` the
+// highest that is not among the n, border itself where more than those have it (`tied`: then `above` are higher).
+struct Cut {
+  uint32_t border, next;
+  bool tied;
+  int above;
+};
+
+// Rounds of counting what is at least some value: the first ones at the place that normally distributed scores of
+// the row's mean and deviation would have it, corrected by what was counted (four for 510 such scores, where
+// halves of the interval take nine), then halves of the interval of values, at last of orders.  Whole warp.
 template <int R>
-__device__ __forceinline__ uint32_t nth_highest(Orders<R>& row, int n, int& above, int& same) {
+__device__ __forceinline__ Cut cut_at(Orders<R>& row, int n) {
   uint32_t lowest = 0xffffffffu, highest = 0u;
-  int any = 0;
+  int any = 0, over = 0;   // above 0; of the highest order, which is no score
+  float sum = 0.0f, squares = 0.0f;
   row.each([&](int, uint32_t x) {
-    if (x != 0u) lowest = min(lowest, x);
-    highest = max(highest, x);
     any += x != 0u;
+    over += x == 0xffffffffu;
+    lowest = min(lowest, x - 1u);   // (0 last)
+    highest = max(highest, x);
+    const float v = x + 1u > 1u ? value_of(x) : 0.0f;
+    sum = __fadd_rn(sum, v);
+    squares = __fmaf_rn(v, v, squares);
   });
-  above = __reduce_add_sync(0xffffffffu, any);
-  same = 0;
-  if (above < n) return 0u;
+  any = __reduce_add_sync(0xffffffffu, any);
+  if (any < n) return {0u, 0u, true, any};
+  over = __reduce_add_sync(0xffffffffu, over);
+  uint32_t lo = __reduce_min_sync(0xffffffffu, lowest) + 1u, hi = __reduce_max_sync(0xffffffffu, highest);
   // at least n are >= lo, fewer than n are > hi
-  uint32_t lo = __reduce_min_sync(0xffffffffu, lowest), hi = __reduce_max_sync(0xffffffffu, highest);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+    squares = __fadd_rn(squares, __shfl_xor_sync(0xffffffffu, squares, o));
+  }
+  const float per = __fdividef(1.0f, static_cast<float>(max(any - over, 1))), mean = __fmul_rn(sum, per);
+  const float deviation = sqrtf(fmaxf(__fmaf_rn(-mean, mean, __fmul_rn(squares, per)), 0.0f));
+  float guess;   // (the normal quantile to 3e-3: C. Hastings, "Approximations for Digital Computers", 1955)
+  {
+    const float share = __fmul_rn(static_cast<float>(n - over), per), tail = fminf(share, __fsub_rn(1.0f, share));
+    const float r = sqrtf(__fmul_rn(-2.0f, __logf(fmaxf(tail, 1e-6f))));
+    const float z = __fsub_rn(r, __fdividef(__fmaf_rn(0.27061f, r, 2.30753f),
+                                            __fmaf_rn(__fmaf_rn(0.04481f, r, 0.99229f), r, 1.0f)));
+    guess = __fmaf_rn(share < 0.5f ? z : -z, deviation, mean);
+  }
   for (int round = 0; lo < hi; ++round) {
     uint32_t mid = lo + (hi - lo) / 2 + 1;
     if (round < 24) {
-      const uint32_t between = order_of(__fmul_rn(0.5f, __fadd_rn(value_of(lo), value_of(hi))));
-      if (between > lo && between <= hi) mid = between;
+      const uint32_t at = order_of(round < 6 ? guess : __fmul_rn(0.5f, __fadd_rn(value_of(lo), value_of(hi))));
+      if (at > lo && at <= hi) mid = at;
     }
     int mine = 0;
     row.each([&](int, uint32_t x) { mine += x >= mid; });
     const int got = __reduce_add_sync(0xffffffffu, mine);
+    if (got == n) {   // exactly these: the lowest of them, and the highest of the others
+      uint32_t least = 0xffffffffu, most = 0u;
+      row.each([&](int, uint32_t x) {
+        least = min(least, x >= mid ? x : 0xffffffffu);
+        most = max(most, x >= mid ? 0u : x);
+      });
+      return {__reduce_min_sync(0xffffffffu, least), __reduce_max_sync(0xffffffffu, most), false, 0};
+    }
     if (got < n) {
       hi = mid - 1;
-    } else if (got > n) {
+    } else {
       lo = mid;
-    } else {   // exactly these: the lowest of them
-      uint32_t least = 0xffffffffu;
-      row.each([&](int, uint32_t x) {
-        if (x >= mid) least = min(least, x);
-      });
-      lo = __reduce_min_sync(0xffffffffu, least);
-      break;
+    }
+    if (round < 5) {   // a score more is sqrt(2 pi) e^(z^2 / 2) deviations over the scores further down
+      const float z = __fdividef(__fsub_rn(guess, mean), deviation);
+      const float step = __fmul_rn(__fmul_rn(2.5066f * per, deviation), __expf(fminf(__fmul_rn(0.5f * z, z), 20.0f)));
+      guess = __fmaf_rn(static_cast<float>(got - n), step, guess);
     }
   }
   int more = 0;
-  any = 0;
-  row.each([&](int, uint32_t x) {
-    more += x > lo;
-    any += x == lo;
-  });
-  above = __reduce_add_sync(0xffffffffu, more);
-  same = __reduce_add_sync(0xffffffffu, any);
-  return lo;
+  row.each([&](int, uint32_t x) { more += x > lo; });
+  return {lo, lo, true, static_cast<int>(__reduce_add_sync(0xffffffffu, more))};
 }
 
 struct RowPlace {
@@ -378,7 +406,8 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int j = 32 * r + lane;
-      row.held[r] = j >= m ? 0u : kept(j) ? 0xffffffffu : scored[j];
+      const uint32_t x = scored[j < m ? j : 0];
+      row.held[r] = j >= m ? 0u : kept(j) ? 0xffffffffu : x;
     }
   } else {
     row.in_step([&](int j, uint32_t& x) {
@@ -409,19 +438,12 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
     return sum / static_cast<double>(left < a.s.block_k ? left : static_cast<int64_t>(a.s.block_k));
   };
 
-  uint32_t border = 0u;   // all above it are chosen, and the first `ties` of those at it
-  int ties = m, same = m;
+  Cut cut{0u, 0u, false, 0};   // all at least at the border are chosen (tied: all above it, and the first of those at it)
   if (m > top) {
-    int above;
-    border = nth_highest(row, top, above, same);
-    ties = top - above;
-    uint32_t next = 0u;   // the highest that would not be chosen
-    row.each([&](int, uint32_t x) {
-      if (x < border) next = max(next, x);
-    });
-    next = same > ties ? border : __reduce_max_sync(0xffffffffu, next);
-    const float t = value_of(border), reach = __fmul_rn(p.delta, 2.0f);
-    if (border != 0u && border != 0xffffffffu && next != 0u && reach <= FLT_MAX && __fsub_rn(t, value_of(next)) <= reach) {
+    cut = cut_at(row, top);
+    const float t = value_of(cut.border), reach = __fmul_rn(p.delta, 2.0f);
+    if (cut.border != 0u && cut.border != 0xffffffffu && cut.next != 0u && reach <= FLT_MAX &&
+        __fsub_rn(t, value_of(cut.next)) <= reach) {
       // Those within reach of the border compete by their exact scores (less t, so that fp32 holds them to
       // 2^-24 of delta) for the places that those above leave; what is beyond reach keeps its side.
       row.in_step([&](int j, uint32_t& x) {
@@ -438,39 +460,69 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
         }
       });
       __syncwarp();
-      border = nth_highest(row, top, above, same);
-      ties = top - above;
+      cut = cut_at(row, top);
     }
-    if (border == 0u) same = ties + 1;   // (entries past m have that order too)
   }
-  const bool all_same = same <= ties;   // all at the border are chosen
-  int written = 0, tied = 0;
+  int written = 0, ties = cut.tied ? top - cut.above : m;   // places; of those at the border
   const uint32_t before = (1u << lane) - 1u;
   const float rows_f = static_cast<float>(p.block.rows) * static_cast<float>(a.s.heads / a.s.kv_heads);
-  const float per_row = __fdiv_rn(1.0f, rows_f);
-  row.in_step([&](int j, uint32_t& x) {
-    bool in = j < m && x >= border;
-    if (!all_same) {
-      const uint32_t at_border = __ballot_sync(0xffffffffu, j < m && x == border);
-      in = in && (x > border || tied + __popc(at_border & before) < ties);
-      tied += __popc(at_border);
+  int32_t* const blocks = a.blocks + list;
+  float* const scores = a.scores != nullptr ? a.scores + list : nullptr;
+  auto is_chosen = [&](int j, uint32_t x) {
+    bool in = j < m && x >= cut.border;
+    if (cut.tied) {
+      const uint32_t at_border = __ballot_sync(0xffffffffu, j < m && x == cut.border);
+      in = in && (x > cut.border || __popc(at_border & before) < ties);
+      ties -= __popc(at_border);
     }
-    uint32_t chosen = __ballot_sync(0xffffffffu, in);
-    const int place = written + __popc(chosen & before);
-    written += __popc(chosen);
-    if (in && place < top) a.blocks[list + place] = j;
-    if (a.scores == nullptr) return;
-    if constexpr (R > 0) {
-      if (in && place < top) a.scores[list + place] = __fmul_rn(value_of(scored[j]), per_row);
-    } else {   // (the scores are no longer there)
-      while (chosen) {
+    return in;
+  };
+  if constexpr (R > 0) {
+    // Which are chosen, a bit for each round; lane r has round r's lanes, and how many were chosen before.  Then
+    // each lane writes its own: two of 32 rounds' bits, mostly.
+    static_assert(R <= 32, "a lane for each round");
+    const float per_row = __fdiv_rn(1.0f, rows_f);
+    uint32_t mine = 0u, lanes = 0u;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (32 * r >= m) break;   // (uniform)
+      const bool in = is_chosen(32 * r + lane, row.held[r]);
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      if (lane == r) lanes = all;
+      mine |= static_cast<uint32_t>(in) << r;
+    }
+    int upto = __popc(lanes);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    written = __shfl_sync(0xffffffffu, upto, 31);
+    upto -= __popc(lanes);
+    while (__any_sync(0xffffffffu, mine != 0u)) {
+      const int r = mine != 0u ? __ffs(mine) - 1 : 0;
+      const int place = __shfl_sync(0xffffffffu, upto, r) + __popc(__shfl_sync(0xffffffffu, lanes, r) & before);
+      if (mine != 0u && place < top) {
+        blocks[place] = 32 * r + lane;
+        if (scores != nullptr) scores[place] = __fmul_rn(value_of(scored[32 * r + lane]), per_row);
+      }
+      mine &= mine - 1u;
+    }
+  } else {
+    row.in_step([&](int j, uint32_t& x) {
+      const bool in = is_chosen(j, x);
+      uint32_t chosen = __ballot_sync(0xffffffffu, in);
+      const int place = written + __popc(chosen & before);
+      written += __popc(chosen);
+      if (in && place < top) blocks[place] = j;
+      while (scores != nullptr && chosen) {   // (the scores are no longer there)
         const int i = __ffs(chosen) - 1;
         chosen &= chosen - 1;
         const double s = exact(j - lane + i);
-        if (lane == i && place < top) a.scores[list + place] = static_cast<float>(s / static_cast<double>(rows_f));
+        if (lane == i && place < top) scores[place] = static_cast<float>(s / static_cast<double>(rows_f));
       }
-    }
-  });
+    });
+  }
   for (int place = written + lane; place < top; place += 32) {
     a.blocks[list + place] = -1;
     if (a.scores != nullptr) a.scores[list + place] = -INFINITY;
@@ -533,22 +585,36 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
       const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
       constexpr int kSteps = HD / kDims;
       const int steps = (most + kTile - 1) / kTile * kSteps;
-      auto fetch = [&](int step) {
-        if (step < steps) {
-          const int j0 = step / kSteps * kTile, quad0 = step % kSteps * (kDims / 4);
-          const uint32_t to = smem_u32(smem) + step % kStages * kStageBytes;
-#pragma unroll
-          for (int i = 0; i < kTile * kDims / 4 / kThreads; ++i) {
-            const int piece = threadIdx.x + i * kThreads;       // [quad][key block]
-            const int j = j0 + piece % kTile;
-            const float* from = a.sums.hi[1] + k_at + ((quad0 + piece / kTile) * kb_rows + (j < most ? j : most - 1)) * 4;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + piece * 16), "l"(from) : "memory");
+      // (Addresses are kept from step to step: made anew they took 700 clocks of each.)
+      static_assert(kTile == 2 * kThreads && kDims == 8, "a thread copies two key blocks' two quads");
+      const int64_t quad_step = kb_rows * 4;   // floats from four dimensions to the next
+      const float *from0 = nullptr, *from1 = nullptr;   // of its key blocks, where the next step begins
+      const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
+      uint32_t fill = 0;
+      int fetched = 0;
+      auto fetch = [&]() {
+        if (fetched < steps) {
+          if (fetched % kSteps == 0) {   // (past the last key block: any)
+            const int j = fetched / kSteps * kTile + threadIdx.x;
+            from0 = a.sums.hi[1] + k_at + (j < most ? j : most - 1) * 4;
+            from1 = a.sums.hi[1] + k_at + (j + kThreads < most ? j + kThreads : most - 1) * 4;
           }
+          auto copy = [&](uint32_t to, const float* from) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+          };
+          copy(ring + fill, from0);
+          copy(ring + fill + kThreads * 16, from1);
+          copy(ring + fill + kTile * 16, from0 + quad_step);
+          copy(ring + fill + kTile * 16 + kThreads * 16, from1 + quad_step);
+          from0 += 2 * quad_step;
+          from1 += 2 * quad_step;
+          ++fetched;
+          fill = fill == (kStages - 1) * kStageBytes ? 0u : fill + kStageBytes;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
 #pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fetch(i);
+      for (int i = 0; i < kStages - 1; ++i) fetch();
       if (threadIdx.x == 0) most_k = 0.0f;
       for (int i = threadIdx.x; i < kRows * HD / 4; i += kThreads) {
         const bool there = i / (HD / 4) < n;
@@ -570,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
       for (int step = 0; step < steps; ++step) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncthreads();   // the step's tile is there, and the last step's is no longer read
-        fetch(step + kStages - 1);
+        fetch();
         const int j0 = step / kSteps * kTile;
         if (q_first >= n || j0 + warp % 4 * 128 >= most) continue;
         const float4* const k = reinterpret_cast<const float4*>(smem + step % kStages * kStageBytes) + k_first;
