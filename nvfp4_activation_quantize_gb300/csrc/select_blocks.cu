@@ -16,15 +16,17 @@
 //           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
 //   score   16 query blocks a CTA against all key blocks of their sequence: products of the hi
 //           parts in fp32 (the lo parts are below their rounding), 8 x 4 scores a thread
-//           from tiles of 512 key blocks x 8 dimensions that bulk copies bring; then a warp per query
-//           block takes its scores into registers and bisects for the top-th highest.
+//           from tiles of 512 key blocks x 8 dimensions that asynchronous copies bring; then a warp per
+//           query block takes its scores into registers and looks for the top-th highest.  65,280 tokens'
+//           510 x 510 scores of 56 heads, of which 64 a row are kept: 284 us.  Bound: instructions, half of them the
+//           products', and the latency of a CTA's steps with 16 warps an SM.
 //
 // What fp32 cannot tell apart is told apart in 64 bits: a score is off by at most
 // delta = 80 * 2^-24 * sum|q_i| * max|k_i| (parts hi: 2 * 2^-24; chains of at most 64 fused products, and
 // the sum of two: 65 * 2^-24; the mean: 2 * 2^-24).  Where the top-th score is more
 // than 2 delta above the next, the choice is the exact one.  Where it is not (one list in a hundred
-// for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in fp64, and
-// the places that are left go to the highest of those.
+// for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in pairs of fp32 (to
+// 2^-40 and better), and the places that are left go to the highest of those.
 #include <cfloat>
 #include <cmath>
 
@@ -415,34 +417,64 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
     });
     __syncwarp();
   }
-  // The score of key block j from hi + lo, in 64 bits: a lane has 4 or 2 dimensions.
+  // The score of key block j from hi + lo, less `from`: a lane has 4 or 2 dimensions.  In pairs of fp32, whose
+  // products and sums keep their rounding errors (T. J. Dekker, "A floating-point technique for extending the
+  // available precision", Numer. Math. 18, 1971), as far as those cannot underflow; else in fp64, of which an
+  // SM does two a clock.  (The worst, 65,280 tokens of equal blocks, all of which tie: 10.8 ms, in fp64 27.8.)
   constexpr int kEach = HD / 32;
-  double q[kEach];
+  float qh[kEach], ql[kEach];
   bool has_q = false;
-  auto exact = [&](int j) {
+  const bool pairs = p.delta > 0x1p-80f && p.delta < 0x1p80f;
+  auto exact = [&](int j, float from) {
     if (!has_q) {
 #pragma unroll
-      for (int z = 0; z < kEach; ++z)
-        q[z] = static_cast<double>(a.sums.hi[0][q_at + lane * kEach + z]) +
-               static_cast<double>(a.sums.lo[0][q_at + lane * kEach + z]);
+      for (int z = 0; z < kEach; ++z) {
+        qh[z] = a.sums.hi[0][q_at + lane * kEach + z];
+        ql[z] = a.sums.lo[0][q_at + lane * kEach + z];
+      }
       has_q = true;
     }
     const int64_t at = k_at + (lane * kEach / 4 * a.sums.rows[1] + j) * 4 + lane * kEach % 4;
+    const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
+    const int keys = left < a.s.block_k ? static_cast<int>(left) : a.s.block_k;
+    if (pairs) {
+      float s = 0.0f, rest = 0.0f;
+      auto add = [&](float x) {   // s + rest += x
+        const float sum = __fadd_rn(s, x), y = __fsub_rn(sum, s);
+        rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(sum, y)), __fsub_rn(x, y)));
+        s = sum;
+      };
+#pragma unroll
+      for (int z = 0; z < kEach; ++z) {
+        const float kh = a.sums.hi[1][at + z], kl = a.sums.lo[1][at + z];
+        const float product = __fmul_rn(qh[z], kh);
+        rest = __fadd_rn(rest, __fadd_rn(__fmaf_rn(qh[z], kh, -product), __fmaf_rn(qh[z], kl, __fmul_rn(ql[z], kh))));
+        add(product);
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, s, o), its = __shfl_xor_sync(0xffffffffu, rest, o);
+        rest = __fadd_rn(rest, its);
+        add(other);
+      }
+      const float n = static_cast<float>(keys), mean = __fdiv_rn(s, n);
+      return __fadd_rn(__fsub_rn(mean, from), __fdiv_rn(__fadd_rn(__fmaf_rn(-mean, n, s), rest), n));
+    }
     double sum = 0.0;
 #pragma unroll
     for (int z = 0; z < kEach; ++z)
-      sum = fma(q[z], static_cast<double>(a.sums.hi[1][at + z]) + static_cast<double>(a.sums.lo[1][at + z]), sum);
+      sum = fma(static_cast<double>(qh[z]) + static_cast<double>(ql[z]),
+                static_cast<double>(a.sums.hi[1][at + z]) + static_cast<double>(a.sums.lo[1][at + z]), sum);
 #pragma unroll
     for (int z = 16; z >= 1; z >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
-    const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
-    return sum / static_cast<double>(left < a.s.block_k ? left : static_cast<int64_t>(a.s.block_k));
+    return static_cast<float>(sum / static_cast<double>(keys) - static_cast<double>(from));
   };
 
   Cut cut{0u, 0u, false, 0};   // all at least at the border are chosen (tied: all above it, and the first of those at it)
   if (m > top) {
     cut = cut_at(row, top);
     const float t = value_of(cut.border), reach = __fmul_rn(p.delta, 2.0f);
-    if (cut.border != 0u && cut.border != 0xffffffffu && cut.next != 0u && reach <= FLT_MAX &&
+    if (cut.border != 0u && cut.border != 0xffffffffu && cut.next != 0u && reach > 0.0f && reach <= FLT_MAX &&
         __fsub_rn(t, value_of(cut.next)) <= reach) {
       // Those within reach of the border compete by their exact scores (less t, so that fp32 holds them to
       // 2^-24 of delta) for the places that those above leave; what is beyond reach keeps its side.
@@ -455,8 +487,8 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
         while (todo) {
           const int i = __ffs(todo) - 1;
           todo &= todo - 1;
-          const double s = exact(j - lane + i);
-          if (lane == i) x = order_of(static_cast<float>(s - static_cast<double>(t)));
+          const float s = exact(j - lane + i, t);
+          if (lane == i) x = order_of(s);
         }
       });
       __syncwarp();
@@ -518,8 +550,8 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
       while (scores != nullptr && chosen) {   // (the scores are no longer there)
         const int i = __ffs(chosen) - 1;
         chosen &= chosen - 1;
-        const double s = exact(j - lane + i);
-        if (lane == i && place < top) scores[place] = static_cast<float>(s / static_cast<double>(rows_f));
+        const float s = exact(j - lane + i, 0.0f);
+        if (lane == i && place < top) scores[place] = __fdiv_rn(s, rows_f);
       }
     });
   }
@@ -677,8 +709,11 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
-      if (threadIdx.x < n) places[seg + threadIdx.x].delta =
-          fmaxf(__fmul_rn(__fmul_rn(q_size[threadIdx.x], most_k), 0x1.4p-18f), 0x1p-140f);
+      if (threadIdx.x < n) {   // (0: queries or keys of zeros, whose scores are exact)
+        const float q_sum = q_size[threadIdx.x];
+        const float off = fmaxf(__fmul_rn(__fmul_rn(q_sum, most_k), 0x1.4p-18f), 0x1p-140f);
+        places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
+      }
       __syncthreads();
     }
     // the choice: a warp for each query block
