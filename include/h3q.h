@@ -10,7 +10,9 @@
  * for checking, and what takes the epilogue's outputs on to the next projection:
  * a paged key/value cache that holds its rows in NVFP4 (write, read), attention of
  * packed sequences over bf16 keys and values, and attention of a few new tokens a
- * sequence over that cache.  Every NVFP4 producer writes:
+ * sequence over that cache; the epilogue with rotary positions of several axes, the norms on
+ * both sides of a block with its gate and residual, and sparse attention over blocks of keys that a
+ * cheap score selects.  Every NVFP4 producer writes:
  *
  *   codes   uint8 [rows, cols/2]: E2M1 codes, two per byte, the even column in
  *           the low nibble (FastVideo compare "fasth3-spark-exact-perf",
@@ -429,8 +431,8 @@ int h3q_gemm_swiglu_nvfp4(const uint8_t *a_codes, const uint8_t *a_scales, int64
  * *flag = 1 if a kernel launched on the current device since the last call had one of
  * its bounded waits run out, else 0; the flag is cleared.  The kernels that wait on
  * mbarriers between their warps (the GEMM of h3q_gemm_swiglu_nvfp4, and those of
- * h3q_attention_varlen and h3q_attention_cache_nvfp4) bound every wait (2 s) and
- * then stop early, leaving that call's outputs unspecified.  Synchronous: it waits
+ * h3q_attention_varlen, h3q_attention_cache_nvfp4 and h3q_attention_blocks) bound every wait
+ * (2 s) and then stop early, leaving that call's outputs unspecified.  Synchronous: it waits
  * for the device, all streams.  Not on any page; a diagnostic of this library.
  */
 int h3q_kernel_error_flag(int *flag);
@@ -711,7 +713,9 @@ static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
  * whatever their scores: the first `first` blocks, and with `causal` those that hold the query
  * block's own positions (keys - queries + i of query i); causal blocks of later keys alone are
  * not candidates.  The choice is that of the exact scores: where fp32 is too coarse to tell,
- * they are formed again in 64 bits.  A score that is no number counts as the lowest.
+ * they are formed again from sums held in pairs of fp32.  (Those are exact where the values
+ * of a block's columns lie within a factor of 2^18 of each other, up to 256 of them, and else off by
+ * 2^-20 of the largest at most; sums have to fit fp32.)  A score that is no number counts as the lowest.
  *
  *   q            bf16 [rows_q, heads * head_dim], row stride ld_q; k bf16 [rows_k, kv_heads *
  *                head_dim], row stride ld_k; 32-byte aligned.

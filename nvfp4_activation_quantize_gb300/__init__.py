@@ -1206,7 +1206,10 @@ def h3q_select_blocks(q, k, cu_q, cu_k, top, *, block_q=128, block_k=128, causal
     torch = _torch or _load_torch()
     if block_q < 1 or block_k < 1:
         raise ValueError("block_q and block_k must be 64, 128 or 256")
-    if len(getattr(q, "shape", ())) != 3 or len(getattr(k, "shape", ())) != 3 or len(getattr(cu_q, "shape", ())) != 1:
+    if not 1 <= top <= 4096:
+        raise ValueError("top must be in [1, 4096]")
+    if (len(getattr(q, "shape", ())) != 3 or len(getattr(k, "shape", ())) != 3 or len(getattr(cu_q, "shape", ())) != 1
+            or cu_q.shape[0] < 1):
         _block_sequences(q, k, cu_q, cu_k)
     (rows_q, _, dim), (rows_k, kv_heads, _), batch, dev = q.shape, k.shape, cu_q.shape[0] - 1, q.device
     shape = (kv_heads, block_rows(rows_q, batch, block_q), int(top))

@@ -11,16 +11,18 @@
 // Both rstd in the canonical order (chunk c on lane c % 128, eight fmaf partials per lane, the
 // lane total, a butterfly per warp, (T0+T1)+(T2+T3)).
 //
-// One CTA of 128 threads owns one row at a time, four CTAs an SM: the second norm needs all of h',
-// which needs all of u, so a row stays in registers from its load to its codes, with two sums over the
-// CTA between.  The other CTAs' rows fill the waits, and a row is asked for (a bulk prefetch into
-// L2) when the one before is begun.  Neighbouring rows go to different CTAs, so that all of them are in
-// the same frame or two and the tables, 12 bytes a column, are read through L1.  (Two CTAs with the
-// tables in shared memory and the next row in registers took 909 us for 65,280 x 7,168.)
+// One CTA of 128 threads owns one row at a time, three CTAs an SM (four up to 4,096 columns): the
+// second norm needs all of h', which needs all of u, so a row stays in registers from its load to its
+// codes, with two sums over the CTA between.  The other CTAs' rows fill the waits, and a row is asked
+// for (a bulk prefetch into L2) when the one before is begun.  Neighbouring rows go to different CTAs, so
+// that all of them are in the same frame or two and the tables, 12 bytes a column, are read through L1.
+// 65,280 x 7,168 take 827 us, 5.9 TB/s.  (Two CTAs with the tables in shared memory and the next row
+// in registers took 909, four with spills 957, no prefetch 841, one two rows ahead 1,000.)
 // What is absent is a value of one (gate), zero (scale) or minus zero (bias and shift: x + -0 = x, zeros
 // keeping their sign), so a launch has one path.
 //
-// Bound: 4 + 2 + 4 + 0.5 + 1/16 bytes of DRAM traffic an element.
+// Bound: 4 + 2 + 4 + 0.5 + 1/16 bytes of DRAM traffic an element, and the latency of a row's chain of two
+// sums with 12 warps an SM (168 registers a thread hold a row).
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
 

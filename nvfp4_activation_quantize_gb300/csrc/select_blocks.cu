@@ -458,6 +458,7 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
         add(other);
       }
       const float n = static_cast<float>(keys), mean = __fdiv_rn(s, n);
+      if (!(fabsf(mean) <= FLT_MAX)) return __fsub_rn(mean, from);   // (an infinity has no rest)
       return __fadd_rn(__fsub_rn(mean, from), __fdiv_rn(__fadd_rn(__fmaf_rn(-mean, n, s), rest), n));
     }
     double sum = 0.0;

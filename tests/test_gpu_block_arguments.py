@@ -108,5 +108,10 @@ def test_outputs_that_do_not_fit(args):
     with pytest.raises(h3q.H3QError, match="overlap"):
         h3q.h3q_attention_blocks(a["q"], a["k"], a["v"], a["cu_q"], a["cu_k"], a["lists"], block_q=64, block_k=64,
                                  out=a["q"])
+    for top in (-1, 0, 4097):
+        with pytest.raises(ValueError, match="top"):
+            h3q.h3q_select_blocks(a["q"], a["k"], a["cu_q"], a["cu_k"], top, block_q=64, block_k=64)
+    with pytest.raises(ValueError, match="cu_q"):
+        h3q.h3q_select_blocks(a["q"], a["k"], a["cu_q"][:0], a["cu_k"], 4, block_q=64, block_k=64)
     with pytest.raises(h3q.H3QError, match="no room"):
         h3q.h3q_select_blocks(a["q"], a["k"], a["cu_q"], a["cu_k"], 2, block_q=64, block_k=64, causal=True, first=1)

@@ -111,6 +111,24 @@ def test_numbers_that_are_none(dev):
     _check(c, 6, 64, 64, False, 0, scores=False)
 
 
+@pytest.mark.parametrize("blocks", [40, 1500])   # scores kept in registers, formed again
+def test_scores_that_are_infinite(dev, blocks):
+    c = bc.sequences(dev, [(64, 64 * blocks)], 1, 1, 64, seed=29, tail=0)
+    c["q"][:, :, 0] = 1.0                                 # (the mean of ones: the infinities' sign is the score's)
+    c["k"][64 * 3 + 5, 0, 0], c["k"][64 * 30, 0, 0] = float("inf"), float("-inf")
+    c["k"][64 * 9, 0, 0], c["k"][64 * 9 + 1, 0, 0] = float("inf"), float("-inf")
+    s = torch.empty((1, 1 + 1, blocks), device=dev)
+    lists = h3q.h3q_select_blocks(c["q"], c["k"], c["cu_q"], c["cu_k"], blocks, block_q=64, block_k=64, scores=s)
+    want, want_scores = bc.selected(c, blocks, 64, 64, False, 0)
+    assert (lists.cpu().numpy() == want).all()
+    got = s.cpu().numpy()
+    assert got[0, 0, 3] == np.inf and got[0, 0, 30] == -np.inf and np.isnan(got[0, 0, 9])
+    rest = np.isfinite(want_scores[0, 0])
+    assert rest.sum() == blocks - 3 and np.isfinite(got[0, 0][rest]).all()
+    top = h3q.h3q_select_blocks(c["q"], c["k"], c["cu_q"], c["cu_k"], 5, block_q=64, block_k=64)
+    assert 3 in top[0, 0].tolist() and 30 not in top[0, 0].tolist() and 9 not in top[0, 0].tolist()
+
+
 def test_no_sequences_and_no_rows(dev):
     for seqs in ([], [(0, 0)], [(0, 100), (0, 0)]):
         c = bc.sequences(dev, seqs, 2, 1, 64, seed=23, tail=200)
