@@ -731,7 +731,8 @@ static inline int64_t h3q_select_blocks_workspace_bytes(int64_t rows_q, int64_t 
                                                         int64_t block_k)
 {
     int64_t rows = h3q_block_rows(rows_q, batch, block_q) + h3q_block_rows(rows_k, batch, block_k);
-    return rows * kv_heads * (head_dim + 1) * 8 + 256;
+    return rows * kv_heads * (head_dim + 1) * 8 +
+           (h3q_block_rows(rows_k, batch, block_k) * kv_heads + 7) / 8 * 8 * head_dim * 4 + 256;
 }
 int h3q_select_blocks(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const int32_t *cu_q,
                       const int32_t *cu_k, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads,

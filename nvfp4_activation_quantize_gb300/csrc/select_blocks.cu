@@ -14,19 +14,24 @@
 //           written; with two-sums, seven additions, 331).  A sum of
 //           up to 256 values is exact where they lie within a factor of 2^18 of each other, and else off by
 //           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
-//   score   16 query blocks a CTA against all key blocks of their sequence: products of the hi
-//           parts in fp32 (the lo parts are below their rounding), 8 x 4 scores a thread
-//           from tiles of 512 key blocks x 8 dimensions that asynchronous copies bring; then a warp per
-//           query block takes its scores into registers and looks for the top-th highest.  65,280 tokens'
-//           510 x 510 scores of 56 heads, of which 64 a row are kept: 284 us.  Bound: instructions, half of them the
-//           products', and the latency of a CTA's steps with 16 warps an SM.
+//   score   16 query blocks a CTA against all key blocks of their sequence, with mma.sync m16n8k16 (16 rows are
+//           what there is; scores go straight to the choice), on two fp16 parts of each sum, scaled: three
+//           products are as good as fp32's.  q's operands stay in registers, k's come from L2 in the order
+//           that a lane wants, a load of 16 bytes for three products.  Then a warp per query block takes its
+//           scores into registers and looks for the top-th highest.  (In fp32, from tiles of key blocks that
+//           asynchronous copies brought: 284 us for 65,280 tokens' 510 x 510 scores of 56 heads, of which 64 a row are kept.)
+//           Bound: the choice's instructions, about 3,000 a list and warp.
 //
-// What fp32 cannot tell apart is told apart in 64 bits: a score is off by at most
-// delta = 80 * 2^-24 * sum|q_i| * max|k_i| (parts hi: 2 * 2^-24; chains of at most 64 fused products, and
-// the sum of two: 65 * 2^-24; the mean: 2 * 2^-24).  Where the top-th score is more
-// than 2 delta above the next, the choice is the exact one.  Where it is not (one list in a hundred
-// for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in pairs of fp32 (to
-// 2^-40 and better), and the places that are left go to the highest of those.
+// What these products cannot tell apart is told apart by fp32 pairs: a score is off by at most
+// delta = 176 * 2^-24 * sum|q_i| * max|k_i|.  (Parts and the product of two second parts: 3 * 2^-22.  A product of 16
+// values adds 17 terms, of each of which it may cut what is below 2^-23 of the largest, and rounds, 36 * 2^-24 at most: M.
+// Fasi, N. J. Higham, M. Mikaitis and S. Pranesh, "Numerical behavior of NVIDIA tensor cores", PeerJ Comput. Sci. 7,
+// 2021; four of them follow each other in each of two sums, 144; in the third, of second parts, they are 2^-10 of that.
+// Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the choice is the exact one.  Where it is
+// not (one list in fifty for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in
+// pairs of fp32 (to 2^-40 and better), and the places that are left go to the highest of those.
+#include <cuda_fp16.h>
+
 #include <cfloat>
 #include <cmath>
 
@@ -42,13 +47,15 @@ namespace {
 
 constexpr int kPoolThreads = 256;
 
-// The workspace: hi and lo parts of q and of k, then for each block sum |q| and max |mean k|.  Those of q are
-// [kv_heads][block rows][head_dim], those of k [kv_heads][head_dim / 4][block rows][4]: four
-// dimensions of neighbouring blocks are one copy.
+// The workspace: hi and lo parts of q and of k, [kv_heads][block rows][head_dim], for each block sum |q| and max |k|
+// of its sums (infinity where one is no number), and k once more as two fp16 parts for the products, scaled by
+// a power of two that takes the block's size to 2^14: [8 rows of all heads'][16 dimensions][row][4 dimensions], for
+// these the first parts and the second ones, so that a load of 16 bytes a lane is an operand of the products.
 struct Sums {
   float* hi[2];
   float* lo[2];
   float* size[2];
+  uint4* parts;
   int64_t rows[2];   // block rows
 };
 
@@ -63,6 +70,8 @@ Sums carve(const BlockShape& s, uint8_t* workspace) {
     w.lo[t] = at + n;
     at += 2 * n;
   }
+  w.parts = reinterpret_cast<uint4*>(at);   // (16-byte aligned: head_dim is a multiple of 4)
+  at += (w.rows[1] * s.kv_heads + 7) / 8 * 8 * s.head_dim;
   for (int t = 0; t < 2; ++t) {
     w.size[t] = at;
     at += w.rows[t] * s.kv_heads;
@@ -90,6 +99,29 @@ __device__ __forceinline__ void add_to(float2& hi, float2& lo, float2 x) {
   const float2 y = sub2(s, hi);
   lo = add2(lo, add2(sub2(hi, sub2(s, y)), sub2(x, y)));
   hi = s;
+}
+
+// The power of two that takes numbers up to `size` below 2^15, in two factors (2^140 is none), and its exponent's
+// negative.
+struct Scale {
+  float a, b;
+  int down;
+};
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
+}
+__device__ __forceinline__ Scale scale_of(float size) {
+  const int up = 141 - max(static_cast<int>(__float_as_uint(size) >> 23), 1);   // 14 less the exponent
+  return {power_of_two(up >> 1), power_of_two(up - (up >> 1)), -up};
+}
+
+// x, scaled, as two fp16 parts: to 2^-22 of it (and 2^-25).
+__device__ __forceinline__ void halves_of(float2 x, const Scale& s, uint32_t& first, uint32_t& second) {
+  x = mul2(mul2(x, make_float2(s.a, s.a)), make_float2(s.b, s.b));
+  const __half2 h = __float22half2_rn(x);
+  const __half2 rest = __float22half2_rn(sub2(x, __half22float2(h)));
+  first = *reinterpret_cast<const uint32_t*>(&h);
+  second = *reinterpret_cast<const uint32_t*>(&rest);
 }
 
 template <int HD>
@@ -220,23 +252,36 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
     }
     size = t ? fmaxf(size, fabsf(h[i])) : __fadd_rn(size, fabsf(h[i]));
   }
-  if (t && !(size <= FLT_MAX)) size = 0.0f;   // (its scores are no numbers, or infinite, whatever fp32 makes of them)
 #pragma unroll
   for (int o = 1; o < kLanes; o <<= 1) {
     const float other = __shfl_xor_sync(0xffffffffu, size, o);
     size = t ? fmaxf(size, other) : __fadd_rn(size, other);
   }
+  // (a maximum passes over what is no number)
+  bool odd = !(size <= FLT_MAX);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) odd = odd || h[i] != h[i];
+  if (__any_sync(0xffffffffu, odd)) size = INFINITY;
   const int64_t rows = a.sums.rows[t], at = static_cast<int64_t>(head) * rows + r;
-  if (lane == 0) a.sums.size[t][at] = t ? __fdiv_rn(size, static_cast<float>(p.rows)) : size;
+  if (lane == 0) a.sums.size[t][at] = size;
   if (lane < kLanes) {
-    const int64_t to = t ? (static_cast<int64_t>(head) * (HD / 4) + 2 * c) * rows + r : at * (HD / 4) + 2 * c;
-    const int64_t step = t ? rows : 1;
-    float4* const hd = reinterpret_cast<float4*>(a.sums.hi[t]) + to;
-    float4* const ld4 = reinterpret_cast<float4*>(a.sums.lo[t]) + to;
+    float4* const hd = reinterpret_cast<float4*>(a.sums.hi[t] + at * HD) + 2 * c;
+    float4* const ld4 = reinterpret_cast<float4*>(a.sums.lo[t] + at * HD) + 2 * c;
     hd[0] = make_float4(h[0], h[1], h[2], h[3]);
-    hd[step] = make_float4(h[4], h[5], h[6], h[7]);
+    hd[1] = make_float4(h[4], h[5], h[6], h[7]);
     ld4[0] = make_float4(l[0], l[1], l[2], l[3]);
-    ld4[step] = make_float4(l[4], l[5], l[6], l[7]);
+    ld4[1] = make_float4(l[4], l[5], l[6], l[7]);
+    if (t) {
+      const Scale s = scale_of(size <= FLT_MAX ? size : 1.0f);
+      uint4* const to = a.sums.parts + (at / 8 * (HD / 16) + c / 2) * 32 + at % 8 * 4 + c % 2 * 2;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4 w;
+        halves_of(make_float2(h[4 * i], h[4 * i + 1]), s, w.x, w.z);
+        halves_of(make_float2(h[4 * i + 2], h[4 * i + 3]), s, w.y, w.w);
+        to[i] = w;
+      }
+    }
   }
 }
 
@@ -244,14 +289,12 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 16;         // query blocks of a CTA at most
-constexpr int kTile = 512;        // key blocks of a tile,
-constexpr int kDims = 8;          // and its dimensions: two copies of 8 KB
-constexpr int kStages = 4;
-constexpr int kStageBytes = kTile * kDims * 4;
-// Scores that a CTA holds: 16 query blocks against 512 or 1,024 key blocks, or fewer against more (one
-// against 16,384, see kMaxBlocks).
-constexpr int kFewScores = kRows * 512, kMostScores = kRows * 1024;
+constexpr int kRows = 16;         // query blocks of a CTA at most: the rows of a product
+// Scores that a CTA holds: 16 query blocks against 1,016 key blocks, or fewer against more (one against 16,376, see
+// kMaxBlocks).
+constexpr int kScores = kRows * 1024;
+// A row of scores begins so much past a multiple of 32 words: the eight rows that a warp stores to are in other banks.
+constexpr int kRowPad = 8;
 
 struct ScoreArgs {
   BlockShape s;
@@ -434,7 +477,7 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
       }
       has_q = true;
     }
-    const int64_t at = k_at + (lane * kEach / 4 * a.sums.rows[1] + j) * 4 + lane * kEach % 4;
+    const int64_t at = k_at + static_cast<int64_t>(j) * HD + lane * kEach;
     const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
     const int keys = left < a.s.block_k ? static_cast<int>(left) : a.s.block_k;
     if (pairs) {
@@ -562,13 +605,19 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
   }
 }
 
-template <int HD, int CAPACITY>
-__global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* const q = reinterpret_cast<float*>(smem + kStages * kStageBytes);    // [kRows][HD]
-  uint32_t* const scored = reinterpret_cast<uint32_t*>(q + kRows * HD);       // orders [rows of a pass][width]
+// acc += A B: 16 query blocks by 8 key blocks over 16 dimensions.
+__device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&x)[4], uint32_t y0, uint32_t y1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y0), "r"(y1));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ __align__(16) uint32_t scored[];       // orders [rows of a pass][width]
   __shared__ RowPlace places[kRows];
   __shared__ float most_k;
+  __shared__ int odd;          // some sums are no numbers
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t lists = a.sums.rows[0], kb_rows = a.sums.rows[1];
   const int64_t chunks = (lists + a.rows - 1) / a.rows;
@@ -597,12 +646,12 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
   for (int seg = 0; seg < rows;) {
     // rows of one sequence, as many as the scores have room for
     const RowPlace first = places[seg];
-    int most = first.candidates, n = 1, width = (most + 31) / 32 * 32;
+    int most = first.candidates, n = 1, width = (most + 31) / 32 * 32 + kRowPad;
     while (seg + n < rows && first.block.rows > 0 && places[seg + n].block.rows > 0 &&
            places[seg + n].block.sequence == first.block.sequence) {
       const int other = max(places[seg + n].candidates, most);
-      const int w = (other + 31) / 32 * 32;
-      if ((n + 1) * w > CAPACITY) break;
+      const int w = (other + 31) / 32 * 32 + kRowPad;
+      if ((n + 1) * w > kScores) break;
       most = other;
       width = w;
       ++n;
@@ -613,106 +662,106 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
     if (most > 0) {
       const int64_t kb0 = (a.s.cu_k[b] >> a.shift_k) + static_cast<int64_t>(b);   // the sequence's key block rows
       len = rows_of(a.s.cu_k, b, a.s.rows_k);
-      k_at = static_cast<int64_t>(head) * kb_rows * HD + kb0 * 4;
-      const float* const k_size = a.sums.size[1] + static_cast<int64_t>(head) * kb_rows + kb0;
+      const int64_t k_row = static_cast<int64_t>(head) * kb_rows + kb0;   // among all heads'
+      k_at = k_row * HD;
+      const float* const k_size = a.sums.size[1] + k_row;
       const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
-      constexpr int kSteps = HD / kDims;
-      const int steps = (most + kTile - 1) / kTile * kSteps;
-      // (Addresses are kept from step to step: made anew they took 700 clocks of each.)
-      static_assert(kTile == 2 * kThreads && kDims == 8, "a thread copies two key blocks' two quads");
-      const int64_t quad_step = kb_rows * 4;   // floats from four dimensions to the next
-      const float *from0 = nullptr, *from1 = nullptr;   // of its key blocks, where the next step begins
-      const uint32_t ring = smem_u32(smem) + threadIdx.x * 16;
-      uint32_t fill = 0;
-      int fetched = 0;
-      auto fetch = [&]() {
-        if (fetched < steps) {
-          if (fetched % kSteps == 0) {   // (past the last key block: any)
-            const int j = fetched / kSteps * kTile + threadIdx.x;
-            from0 = a.sums.hi[1] + k_at + (j < most ? j : most - 1) * 4;
-            from1 = a.sums.hi[1] + k_at + (j + kThreads < most ? j + kThreads : most - 1) * 4;
-          }
-          auto copy = [&](uint32_t to, const float* from) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-          };
-          copy(ring + fill, from0);
-          copy(ring + fill + kThreads * 16, from1);
-          copy(ring + fill + kTile * 16, from0 + quad_step);
-          copy(ring + fill + kTile * 16 + kThreads * 16, from1 + quad_step);
-          from0 += 2 * quad_step;
-          from1 += 2 * quad_step;
-          ++fetched;
-          fill = fill == (kStages - 1) * kStageBytes ? 0u : fill + kStageBytes;
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) fetch();
-      if (threadIdx.x == 0) most_k = 0.0f;
-      for (int i = threadIdx.x; i < kRows * HD / 4; i += kThreads) {
-        const bool there = i / (HD / 4) < n;
-        reinterpret_cast<float4*>(q)[i] = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at)[i]
-                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (threadIdx.x == 0) {
+        most_k = 0.0f;
+        odd = 0;
       }
       __syncthreads();
+      auto keys_of = [&](int j) {
+        const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
+        return static_cast<float>(left < a.s.block_k ? left : a.s.block_k);
+      };
       {
         float m = 0.0f;
-        for (int i = threadIdx.x; i < most; i += kThreads) m = fmaxf(m, k_size[i]);
+        for (int i = threadIdx.x; i < most; i += kThreads) {
+          const float size = k_size[i];
+          if (size <= FLT_MAX) {
+            m = fmaxf(m, __fdiv_rn(size, keys_of(i)));
+          } else {
+            odd = 1;
+          }
+        }
+        if (threadIdx.x < n && !(q_size[threadIdx.x] <= FLT_MAX)) odd = 1;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) atomicMax(reinterpret_cast<int*>(&most_k), __float_as_int(m));   // (none is negative)
       }
-      // A thread's scores: query blocks q_first .. + 7, key blocks k_first + 32 x of a tile, even dimensions
-      // in one half of a pair and odd ones in the other.
-      const int q_first = warp / 4 * 8, k_first = warp % 4 * 128 + lane;
-      float2 acc[8][4];
-      for (int step = 0; step < steps; ++step) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();   // the step's tile is there, and the last step's is no longer read
-        fetch();
-        const int j0 = step / kSteps * kTile;
-        if (q_first >= n || j0 + warp % 4 * 128 >= most) continue;
-        const float4* const k = reinterpret_cast<const float4*>(smem + step % kStages * kStageBytes) + k_first;
-        const float* const qd = q + q_first * HD + step % kSteps * kDims;
-        if (step % kSteps == 0) {
+      // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, kept
+      // for all key blocks; a warp takes every eighth group of 8 key blocks.
+      constexpr int kSteps = HD / 16;
+      uint32_t q_first[kSteps][4], q_second[kSteps][4];
+      int q_down[2];
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
+      for (int y = 0; y < 2; ++y) {
+        const int block = lane / 4 + 8 * y;
+        const float size = block < n ? q_size[block] : INFINITY;
+        const bool there = size <= FLT_MAX;
+        const Scale s = scale_of(there ? size : 1.0f);
+        q_down[y] = s.down;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) acc[y][x] = make_float2(0.0f, 0.0f);
+        for (int z = 0; z < kSteps; ++z) {
+          const float4 v = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at + block * HD)[4 * z + lane % 4]
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          halves_of(make_float2(v.x, v.y), s, q_first[z][y], q_second[z][y]);
+          halves_of(make_float2(v.z, v.w), s, q_first[z][2 + y], q_second[z][2 + y]);
+        }
+      }
+      const int last = static_cast<int>((len - 1) >> a.shift_k);   // the sequence's last block, which may be shorter
+      const float per_full = __fdiv_rn(1.0f, static_cast<float>(a.s.block_k)), per_last = __fdiv_rn(1.0f, keys_of(last));
+      const int64_t group0 = k_row / 8;
+      const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
+      const int groups = (before + most + 7) / 8;
+      for (int g = warp; g < groups; g += kWarps) {
+        const uint4* const from = a.sums.parts + (group0 + g) * (HD / 16 * 32) + lane;
+        uint4 k[kSteps];
+#pragma unroll
+        for (int z = 0; z < kSteps; ++z) k[z] = from[z * 32];
+        const int j = 8 * g - before + lane % 4 * 2;
+        float size[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) size[x] = j + x >= 0 && j + x < most ? k_size[j + x] : 0.0f;
+        // (three sums, so that none is long: first parts of even and odd steps, the rest)
+        float even[4] = {}, uneven[4] = {}, rest[4] = {};
+#pragma unroll
+        for (int z = 0; z < kSteps; ++z) {
+          product(z & 1 ? uneven : even, q_first[z], k[z].x, k[z].y);
+          product(rest, q_first[z], k[z].z, k[z].w);
+          product(rest, q_second[z], k[z].x, k[z].y);
         }
 #pragma unroll
-        for (int quad = 0; quad < kDims / 4; ++quad) {
-          float4 kv[4];
+        for (int x = 0; x < 2; ++x) {
+          if (j + x < 0 || j + x >= most) continue;
+          const float per_key = j + x == last ? per_last : per_full;
+          const int k_down = scale_of(size[x] <= FLT_MAX ? size[x] : 1.0f).down;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) kv[x] = k[quad * kTile + 32 * x];
-#pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const float4 qv = *reinterpret_cast<const float4*>(qd + y * HD + 4 * quad);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              acc[y][x] = fma2(make_float2(qv.z, qv.w), make_float2(kv[x].z, kv[x].w),
-                               fma2(make_float2(qv.x, qv.y), make_float2(kv[x].x, kv[x].y), acc[y][x]));
-          }
-        }
-        if (step % kSteps == kSteps - 1) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int j = j0 + k_first + 32 * x;
-            if (j >= most) continue;
-            const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
-            const float per_key = __fdiv_rn(1.0f, static_cast<float>(left < a.s.block_k ? left : a.s.block_k));
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              if (q_first + y < n)
-                scored[(q_first + y) * width + j] = order_of(__fmul_rn(__fadd_rn(acc[y][x].x, acc[y][x].y), per_key));
+          for (int y = 0; y < 2; ++y) {
+            const int block = lane / 4 + 8 * y, i = 2 * y + x, down = q_down[y] + k_down;
+            if (block >= n) continue;
+            const float sum = __fmul_rn(__fadd_rn(__fadd_rn(even[i], uneven[i]), rest[i]), per_key);
+            scored[block * width + j + x] =
+                order_of(__fmul_rn(__fmul_rn(sum, power_of_two(down >> 1)), power_of_two(down - (down >> 1))));
           }
         }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncthreads();
+      if (odd) {   // scores with sums that are no numbers: as fp32 has them
+        for (int i = threadIdx.x; i < n * most; i += kThreads) {
+          const int y = i / most, j = i - y * most;
+          if (q_size[y] <= FLT_MAX && k_size[j] <= FLT_MAX) continue;
+          const float* const qv = a.sums.hi[0] + q_at + y * HD;
+          const float* const kv = a.sums.hi[1] + k_at + static_cast<int64_t>(j) * HD;
+          float s = 0.0f;
+          for (int d = 0; d < HD; ++d) s = __fmaf_rn(qv[d], kv[d], s);
+          scored[y * width + j] = order_of(__fdiv_rn(s, keys_of(j)));
+        }
+      }
       if (threadIdx.x < n) {   // (0: queries or keys of zeros, whose scores are exact)
         const float q_sum = q_size[threadIdx.x];
-        const float off = fmaxf(__fmul_rn(__fmul_rn(q_sum, most_k), 0x1.4p-18f), 0x1p-140f);
+        const float off = fmaxf(__fmul_rn(__fmul_rn(q_sum, most_k), 0x1.6p-17f), 0x1p-140f);
         places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
       }
       __syncthreads();
@@ -725,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
       const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
       if (p.candidates <= 512) {
         choose<HD, 16>(a, p, row, q_row, k_at, len, list);
-      } else if (CAPACITY > kFewScores && p.candidates <= 1024) {
-        choose<HD, (CAPACITY > kFewScores) ? 32 : 0>(a, p, row, q_row, k_at, len, list);
+      } else if (p.candidates <= 1024) {
+        choose<HD, 32>(a, p, row, q_row, k_at, len, list);
       } else {
         choose<HD, 0>(a, p, row, q_row, k_at, len, list);
       }
@@ -736,12 +785,16 @@ __global__ void __launch_bounds__(kThreads, CAPACITY <= kFewScores ? 2 : 1) scor
   }
 }
 
-template <int HD, int CAPACITY>
-cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
-  const int smem = kStages * kStageBytes + kRows * HD * 4 + CAPACITY * 4;
+template <int HD>
+cudaError_t launch(const PoolArgs& pool, ScoreArgs score, cudaStream_t stream) {
+  const int64_t warps = (pool.sums.rows[0] + pool.sums.rows[1]) * pool.kv_heads;
+  const int64_t pool_blocks = (warps + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
+  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  constexpr int kSmem = kScores * 4;
   int blocks = 0;
-  const void* kernel = reinterpret_cast<const void*>(&score_kernel<HD, CAPACITY>);
-  cudaError_t err = persistent_blocks(kernel, kThreads, smem, int64_t{1} << 30, &blocks);
+  err = persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD>), kThreads, kSmem, int64_t{1} << 30, &blocks);
   if (err != cudaSuccess) return err;
   // query blocks of a CTA: 16, or fewer where all CTAs run at once all the same
   const int64_t rows = (score.sums.rows[0] * score.s.kv_heads + blocks - 1) / blocks;
@@ -750,31 +803,14 @@ cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(chunks * score.s.kv_heads));
   config.blockDim = dim3(kThreads);
-  config.dynamicSmemBytes = smem;
+  config.dynamicSmemBytes = kSmem;
   config.stream = stream;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   config.attrs = &early;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, score_kernel<HD, CAPACITY>, score);
-}
-
-template <int HD>
-cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t stream) {
-  const int64_t warps = (pool.sums.rows[0] + pool.sums.rows[1]) * pool.kv_heads;
-  const int64_t pool_blocks = (warps + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
-  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  // Many lists: two CTAs an SM, each with room for 16 query blocks against 512 key blocks, which is enough where
-  // sequences have so many on average (65,280 tokens 0.60 ms against 0.71 with one CTA).  Few: one
-  // CTA an SM, whose registers hold all that it works on (16 single tokens 64 us against 74, 4 chunks 88 against 103).
-  const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
-  const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
-  if (many && longest <= kFewScores && longest <= 512 * static_cast<int64_t>(score.s.batch))
-    return launch_score<HD, kFewScores>(score, stream);
-  return launch_score<HD, kMostScores>(score, stream);
+  return cudaLaunchKernelEx(&config, score_kernel<HD>, score);
 }
 
 }  // namespace
