@@ -57,8 +57,7 @@ constexpr int kSlots = 3;        // units known ahead
 constexpr int kTileRows = 128;
 constexpr int kKeys = 128;       // of a tile: two runs of 64
 constexpr int kRun = 64;
-constexpr int kStages = 5;       // K and V tiles in the ring, in the order of their products
-constexpr int kTellRing = 8;     // key tiles whose first keys are told ahead (those in the ring, and one more unread)
+constexpr int kTellRing = 16;    // key tiles whose first keys are told ahead (those in the ring, and two more unread)
 constexpr int kMostPartial = 4;  // tiles that some row does not see whole: runs that begin among 64 + 255 keys
 constexpr float kSlack = 8.0f;   // a row's reference moves when its maximum has passed it by 2^8,
 constexpr float kJump = 16.0f;   // at once when a tile passes it by 2^16 (sums stay finite, see attention.cu)
@@ -91,6 +90,7 @@ struct Shape {
   static constexpr int kHalves = HD / 64;               // 64-element (128-byte) column blocks of a row
   static constexpr int kQBytes = kTileRows * HD * 2;
   static constexpr int kKvBytes = kKeys * HD * 2;
+  static constexpr int kStages = 5 * 128 / HD;          // K and V tiles in the ring, in the order of their products
   static constexpr int kOffKv = 2 * kQBytes;
   static constexpr int kOffBar = kOffKv + kStages * kKvBytes;
   static constexpr int kBars = 4 * kStages + 12 + 2 * kSlots + 4;   // named in the kernel
@@ -273,10 +273,10 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t{1023});
   const uint32_t base = smem_u32(smem);
   const uint32_t bar_full = base + S::kOffBar;             // + 8 * stage
-  const uint32_t bar_empty = bar_full + 8 * kStages;
-  const uint32_t bar_vraw = bar_empty + 8 * kStages;       // a V tile that the check warp looks at first ...
-  const uint32_t bar_vok = bar_vraw + 8 * kStages;         // ... and has passed on
-  const uint32_t bar_q = bar_vok + 8 * kStages;            // + 8 * row tile: Q has landed,
+  const uint32_t bar_empty = bar_full + 8 * S::kStages;
+  const uint32_t bar_vraw = bar_empty + 8 * S::kStages;       // a V tile that the check warp looks at first ...
+  const uint32_t bar_vok = bar_vraw + 8 * S::kStages;         // ... and has passed on
+  const uint32_t bar_q = bar_vok + 8 * S::kStages;            // + 8 * row tile: Q has landed,
   const uint32_t bar_qfree = bar_q + 16;                   // is no longer read
   const uint32_t bar_s = bar_qfree + 16;                   // + 8 * row tile
   const uint32_t bar_p = bar_s + 16;
@@ -297,7 +297,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       mbar_init(bar_full + 8 * i, 1);
       mbar_init(bar_empty + 8 * i, 1);
       mbar_init(bar_vraw + 8 * i, 1);
@@ -597,7 +597,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             if (a.shift_k == 6) tma_load_3d(to + kRun * 128, map, 64 * h, kv_head, row_k0 + second, bar);
           }
         }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        stage = stage + 1 == S::kStages ? 0 : stage + 1;
       };
       auto load_k = [&](int x) {
         runs[x].x = next_run(x);
@@ -651,10 +651,10 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     // Before the CTA goes: every stage's last tile is released (the products' commits arrive
     // here); after an abort, every copy issued has landed.
     if (lane == 0) {
-      for (uint32_t i = 0; i < kStages && !raised_here(abort); ++i)
+      for (uint32_t i = 0; i < S::kStages && !raised_here(abort); ++i)
         if (used >> i & 1) (void)wait_or_abort(bar_empty + 8 * i, (use_phase >> i & 1) ^ 1u, abort);
       if (raised_here(abort)) {
-        for (uint32_t i = 0; i < kStages; ++i)
+        for (uint32_t i = 0; i < S::kStages; ++i)
           if (used >> i & 1) {
             const bool raw = last_raw >> i & 1;
             (void)wait_bounded((raw ? bar_vraw : bar_full) + 8 * i, ((raw ? raw_phase : full_phase) >> i & 1) ^ 1u);
@@ -703,7 +703,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     // The next tile's stage, its barrier and parity.
     auto next_tile = [&](bool checked, uint32_t& stage, uint32_t& parity) {
       stage = next_stage;
-      next_stage = next_stage + 1 == kStages ? 0 : next_stage + 1;
+      next_stage = next_stage + 1 == S::kStages ? 0 : next_stage + 1;
       parity = (checked ? ok_phase : full_phase) >> stage & 1;
       (checked ? ok_phase : full_phase) ^= 1u << stage;
       return (checked ? bar_vok : bar_full) + 8 * stage;
@@ -816,7 +816,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           const int ahead = shared ? 2 * j + 1
                                    : (n0 > 0) + (n1 > 0) + min(j, n0) + min(j, t0) + min(j, n1) + min(j, t1) +
                                          (x == 1 ? (j < n0) + (j < t0) : 0);
-          const uint32_t stage = (base_stage + ahead) % kStages;
+          const uint32_t stage = (base_stage + ahead) % S::kStages;
           if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar_vraw + 8 * stage, raw_phase >> stage & 1, abort)))) continue;
           raw_phase ^= 1u << stage;
           const int told = x * kTellRing + (count[x] + j) % kTellRing;
@@ -856,7 +856,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       }
       count[0] += tiles[0];
       count[1] += tiles[1];
-      base_stage = (base_stage + 2 * (shared ? tiles[0] : tiles[0] + tiles[1])) % kStages;
+      base_stage = (base_stage + 2 * (shared ? tiles[0] : tiles[0] + tiles[1])) % S::kStages;
       leave_unit(it);
     }
   } else {
