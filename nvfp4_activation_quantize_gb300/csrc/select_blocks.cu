@@ -606,15 +606,18 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
 }
 
 // acc += A B: 16 query blocks by 8 key blocks over 16 dimensions.
-__device__ __forceinline__ void product(float (&acc)[4], const uint32_t (&x)[4], uint32_t y0, uint32_t y1) {
+__device__ __forceinline__ void product(float (&acc)[4], const uint4& x, uint32_t y0, uint32_t y1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
-      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(y0), "r"(y1));
+      : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y0), "r"(y1));
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ ScoreArgs a) {
-  extern __shared__ __align__(16) uint32_t scored[];       // orders [rows of a pass][width]
+template <int HD, int R>
+__global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const __grid_constant__ ScoreArgs a) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  constexpr int kSteps = HD / 16;
+  uint4* const q_parts = reinterpret_cast<uint4*>(smem);   // [step][first, second][lane]
+  uint32_t* const scored = smem + kSteps * 2 * 32 * 4;     // orders [rows of a pass][width]
   __shared__ RowPlace places[kRows];
   __shared__ float most_k;
   __shared__ int odd;          // some sums are no numbers
@@ -690,10 +693,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) atomicMax(reinterpret_cast<int*>(&most_k), __float_as_int(m));   // (none is negative)
       }
-      // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, kept
-      // for all key blocks; a warp takes every eighth group of 8 key blocks.
-      constexpr int kSteps = HD / 16;
-      uint32_t q_first[kSteps][4], q_second[kSteps][4];
+      // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, which
+      // the warps make together; a warp takes every eighth group of 8 key blocks.
       int q_down[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -702,14 +703,15 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         const bool there = size <= FLT_MAX;
         const Scale s = scale_of(there ? size : 1.0f);
         q_down[y] = s.down;
-#pragma unroll
-        for (int z = 0; z < kSteps; ++z) {
+        for (int z = warp; z < kSteps; z += kWarps) {
           const float4 v = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at + block * HD)[4 * z + lane % 4]
                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          halves_of(make_float2(v.x, v.y), s, q_first[z][y], q_second[z][y]);
-          halves_of(make_float2(v.z, v.w), s, q_first[z][2 + y], q_second[z][2 + y]);
+          uint32_t* const to = reinterpret_cast<uint32_t*>(q_parts + 2 * z * 32 + lane) + y;
+          halves_of(make_float2(v.x, v.y), s, to[0], to[32 * 4]);
+          halves_of(make_float2(v.z, v.w), s, to[2], to[32 * 4 + 2]);
         }
       }
+      __syncthreads();
       const int last = static_cast<int>((len - 1) >> a.shift_k);   // the sequence's last block, which may be shorter
       const float per_full = __fdiv_rn(1.0f, static_cast<float>(a.s.block_k)), per_last = __fdiv_rn(1.0f, keys_of(last));
       const int64_t group0 = k_row / 8;
@@ -728,9 +730,10 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         float even[4] = {}, uneven[4] = {}, rest[4] = {};
 #pragma unroll
         for (int z = 0; z < kSteps; ++z) {
-          product(z & 1 ? uneven : even, q_first[z], k[z].x, k[z].y);
-          product(rest, q_first[z], k[z].z, k[z].w);
-          product(rest, q_second[z], k[z].x, k[z].y);
+          const uint4 first = q_parts[2 * z * 32 + lane], second = q_parts[(2 * z + 1) * 32 + lane];
+          product(z & 1 ? uneven : even, first, k[z].x, k[z].y);
+          product(rest, first, k[z].z, k[z].w);
+          product(rest, second, k[z].x, k[z].y);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -774,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
       if (p.candidates <= 512) {
         choose<HD, 16>(a, p, row, q_row, k_at, len, list);
-      } else if (p.candidates <= 1024) {
-        choose<HD, 32>(a, p, row, q_row, k_at, len, list);
+      } else if (R > 16 && p.candidates <= 1024) {
+        choose<HD, (R > 16 ? 32 : 0)>(a, p, row, q_row, k_at, len, list);
       } else {
         choose<HD, 0>(a, p, row, q_row, k_at, len, list);
       }
@@ -785,16 +788,12 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   }
 }
 
-template <int HD>
-cudaError_t launch(const PoolArgs& pool, ScoreArgs score, cudaStream_t stream) {
-  const int64_t warps = (pool.sums.rows[0] + pool.sums.rows[1]) * pool.kv_heads;
-  const int64_t pool_blocks = (warps + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
-  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  constexpr int kSmem = kScores * 4;
+template <int HD, int R>
+cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
+  constexpr int kSmem = HD / 16 * 2 * 512 + kScores * 4;
   int blocks = 0;
-  err = persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD>), kThreads, kSmem, int64_t{1} << 30, &blocks);
+  cudaError_t err =
+      persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R>), kThreads, kSmem, int64_t{1} << 30, &blocks);
   if (err != cudaSuccess) return err;
   // query blocks of a CTA: 16, or fewer where all CTAs run at once all the same
   const int64_t rows = (score.sums.rows[0] * score.s.kv_heads + blocks - 1) / blocks;
@@ -810,7 +809,21 @@ cudaError_t launch(const PoolArgs& pool, ScoreArgs score, cudaStream_t stream) {
   early.val.programmaticStreamSerializationAllowed = 1;
   config.attrs = &early;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, score_kernel<HD>, score);
+  return cudaLaunchKernelEx(&config, score_kernel<HD, R>, score);
+}
+
+template <int HD>
+cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t stream) {
+  const int64_t warps = (pool.sums.rows[0] + pool.sums.rows[1]) * pool.kv_heads;
+  const int64_t pool_blocks = (warps + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
+  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  // Three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key blocks on
+  // average; else two, whose warps hold 1,024.
+  const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
+  return longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
+                                                               : launch_score<HD, 32>(score, stream);
 }
 
 }  // namespace
