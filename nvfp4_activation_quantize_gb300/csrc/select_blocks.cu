@@ -643,6 +643,10 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
     }
     places[threadIdx.x] = p;
   }
+  if (threadIdx.x == 0) {
+    most_k = 0.0f;
+    odd = 0;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
   __syncthreads();
 
@@ -669,11 +673,6 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
       k_at = k_row * HD;
       const float* const k_size = a.sums.size[1] + k_row;
       const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
-      if (threadIdx.x == 0) {
-        most_k = 0.0f;
-        odd = 0;
-      }
-      __syncthreads();
       auto keys_of = [&](int j) {
         const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
         return static_cast<float>(left < a.s.block_k ? left : a.s.block_k);
@@ -711,14 +710,14 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
           halves_of(make_float2(v.z, v.w), s, to[2], to[32 * 4 + 2]);
         }
       }
-      __syncthreads();
       const int last = static_cast<int>((len - 1) >> a.shift_k);   // the sequence's last block, which may be shorter
       const float per_full = __fdiv_rn(1.0f, static_cast<float>(a.s.block_k)), per_last = __fdiv_rn(1.0f, keys_of(last));
       const int64_t group0 = k_row / 8;
       const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
       const int groups = (before + most + 7) / 8;
+      __syncthreads();
       for (int g = warp; g < groups; g += kWarps) {
-        const uint4* const from = a.sums.parts + (group0 + g) * (HD / 16 * 32) + lane;
+        const uint4* const from = a.sums.parts + (group0 + g) * (kSteps * 32) + lane;
         uint4 k[kSteps];
 #pragma unroll
         for (int z = 0; z < kSteps; ++z) k[z] = from[z * 32];
@@ -726,14 +725,14 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
         float size[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) size[x] = j + x >= 0 && j + x < most ? k_size[j + x] : 0.0f;
-        // (three sums, so that none is long: first parts of even and odd steps, the rest)
-        float even[4] = {}, uneven[4] = {}, rest[4] = {};
+        // (four sums, so that none is long: first parts of even and odd steps, the rest)
+        float even[4] = {}, uneven[4] = {}, rest[4] = {}, other[4] = {};
 #pragma unroll
         for (int z = 0; z < kSteps; ++z) {
           const uint4 first = q_parts[2 * z * 32 + lane], second = q_parts[(2 * z + 1) * 32 + lane];
           product(z & 1 ? uneven : even, first, k[z].x, k[z].y);
           product(rest, first, k[z].z, k[z].w);
-          product(rest, second, k[z].x, k[z].y);
+          product(other, second, k[z].x, k[z].y);
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -744,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
           for (int y = 0; y < 2; ++y) {
             const int block = lane / 4 + 8 * y, i = 2 * y + x, down = q_down[y] + k_down;
             if (block >= n) continue;
-            const float sum = __fmul_rn(__fadd_rn(__fadd_rn(even[i], uneven[i]), rest[i]), per_key);
+            const float sum = __fmul_rn(__fadd_rn(__fadd_rn(even[i], uneven[i]), __fadd_rn(rest[i], other[i])), per_key);
             scored[block * width + j + x] =
                 order_of(__fmul_rn(__fmul_rn(sum, power_of_two(down >> 1)), power_of_two(down - (down >> 1))));
           }
@@ -768,6 +767,10 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
         places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
       }
       __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      most_k = 0.0f;
+      odd = 0;
     }
     // the choice: a warp for each query block
     for (int y = warp; y < n; y += kWarps) {
