@@ -23,12 +23,12 @@
 //           Bound: the choice's instructions, about 3,000 a list and warp.
 //
 // What these products cannot tell apart is told apart by fp32 pairs: a score is off by at most
-// delta = 176 * 2^-24 * sum|q_i| * max|k_i|.  (Parts and the product of two second parts: 3 * 2^-22.  A product of 16
+// delta = 176 * 2^-24 * |q| |k|, of the largest |k|.  (Parts and the product of two second parts: 3 * 2^-22.  A product of 16
 // values adds 17 terms, of each of which it may cut what is below 2^-23 of the largest, and rounds, 36 * 2^-24 at most: M.
 // Fasi, N. J. Higham, M. Mikaitis and S. Pranesh, "Numerical behavior of NVIDIA tensor cores", PeerJ Comput. Sci. 7,
 // 2021; four of them follow each other in each of two sums, 144; in the third, of second parts, they are 2^-10 of that.
 // Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the choice is the exact one.  Where it is
-// not (one list in fifty for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in
+// not (one list in forty for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in
 // pairs of fp32 (to 2^-40 and better), and the places that are left go to the highest of those.
 #include <cuda_fp16.h>
 
@@ -47,8 +47,8 @@ namespace {
 
 constexpr int kPoolThreads = 256;
 
-// The workspace: hi and lo parts of q and of k, [kv_heads][block rows][head_dim], for each block sum |q| and max |k|
-// of its sums (infinity where one is no number), and k once more as two fp16 parts for the products, scaled by
+// The workspace: hi and lo parts of q and of k, [kv_heads][block rows][head_dim], for each block the length of its sums
+// as a vector (infinity where one is no number), and k once more as two fp16 parts for the products, scaled by
 // a power of two that takes the block's size to 2^14: [8 rows of all heads'][16 dimensions][row][4 dimensions], for
 // these the first parts and the second ones, so that a load of 16 bytes a lane is an operand of the products.
 struct Sums {
@@ -101,23 +101,14 @@ __device__ __forceinline__ void add_to(float2& hi, float2& lo, float2 x) {
   hi = s;
 }
 
-// The power of two that takes numbers up to `size` below 2^15, in two factors (2^140 is none), and its exponent's
-// negative.
-struct Scale {
-  float a, b;
-  int down;
-};
-__device__ __forceinline__ float power_of_two(int e) {
-  return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
-}
-__device__ __forceinline__ Scale scale_of(float size) {
-  const int up = 141 - max(static_cast<int>(__float_as_uint(size) >> 23), 1);   // 14 less the exponent
-  return {power_of_two(up >> 1), power_of_two(up - (up >> 1)), -up};
-}
+// Powers of two that take numbers up to `size` (and not above 2^-112) below 2^15, and back.
+__device__ __forceinline__ uint32_t exponent_of(float size) { return max(__float_as_uint(size) >> 23, 15u); }
+__device__ __forceinline__ float scale_up(float size) { return __uint_as_float((268u - exponent_of(size)) << 23); }
+__device__ __forceinline__ float scale_down(float size) { return __uint_as_float((exponent_of(size) - 14u) << 23); }
 
 // x, scaled, as two fp16 parts: to 2^-22 of it (and 2^-25).
-__device__ __forceinline__ void halves_of(float2 x, const Scale& s, uint32_t& first, uint32_t& second) {
-  x = mul2(mul2(x, make_float2(s.a, s.a)), make_float2(s.b, s.b));
+__device__ __forceinline__ void halves_of(float2 x, float scale, uint32_t& first, uint32_t& second) {
+  x = mul2(x, make_float2(scale, scale));
   const __half2 h = __float22half2_rn(x);
   const __half2 rest = __float22half2_rn(sub2(x, __half22float2(h)));
   first = *reinterpret_cast<const uint32_t*>(&h);
@@ -250,18 +241,28 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
       h[i] = a0;
       l[i] = 0.0f;
     }
-    size = t ? fmaxf(size, fabsf(h[i])) : __fadd_rn(size, fabsf(h[i]));
-  }
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) {
-    const float other = __shfl_xor_sync(0xffffffffu, size, o);
-    size = t ? fmaxf(size, other) : __fadd_rn(size, other);
+    size = fmaxf(size, fabsf(h[i]));
   }
   // (a maximum passes over what is no number)
   bool odd = !(size <= FLT_MAX);
 #pragma unroll
   for (int i = 0; i < 8; ++i) odd = odd || h[i] != h[i];
-  if (__any_sync(0xffffffffu, odd)) size = INFINITY;
+#pragma unroll
+  for (int o = 1; o < kLanes; o <<= 1) size = fmaxf(size, __shfl_xor_sync(0xffffffffu, size, o));
+  {   // the length of the sums, and a little more
+    const float up = scale_up(size);
+    float squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __fmul_rn(h[i], up);
+      squares = __fmaf_rn(y, y, squares);
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) squares = __fadd_rn(squares, __shfl_xor_sync(0xffffffffu, squares, o));
+    const float length = __fmul_rn(__fmul_rn(__fsqrt_rn(squares), 1.0f + 0x1p-18f), scale_down(size));
+    size = fmaxf(size, length);
+  }
+  if (__any_sync(0xffffffffu, odd || !(size <= FLT_MAX))) size = INFINITY;
   const int64_t rows = a.sums.rows[t], at = static_cast<int64_t>(head) * rows + r;
   if (lane == 0) a.sums.size[t][at] = size;
   if (lane < kLanes) {
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
     ld4[0] = make_float4(l[0], l[1], l[2], l[3]);
     ld4[1] = make_float4(l[4], l[5], l[6], l[7]);
     if (t) {
-      const Scale s = scale_of(size <= FLT_MAX ? size : 1.0f);
+      const float s = scale_up(size <= FLT_MAX ? size : 1.0f);
       uint4* const to = a.sums.parts + (at / 8 * (HD / 16) + c / 2) * 32 + at % 8 * 4 + c % 2 * 2;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -307,11 +308,11 @@ struct ScoreArgs {
 };
 
 // A float's place in the order of all, as an unsigned number; no number is the lowest.
-__device__ __forceinline__ uint32_t order_of(float x) {
-  if (x != x) return 0u;
+__device__ __forceinline__ uint32_t order_of_number(float x) {
   const uint32_t u = __float_as_uint(__fadd_rn(x, 0.0f));   // (-0 counts as 0)
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t order_of(float x) { return x != x ? 0u : order_of_number(x); }
 __device__ __forceinline__ float value_of(uint32_t order) {
   return __uint_as_float(order & 0x80000000u ? order & 0x7fffffffu : ~order);
 }
@@ -522,19 +523,37 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
         __fsub_rn(t, value_of(cut.next)) <= reach) {
       // Those within reach of the border compete by their exact scores (less t, so that fp32 holds them to
       // 2^-24 of delta) for the places that those above leave; what is beyond reach keeps its side.
-      row.in_step([&](int j, uint32_t& x) {
+      auto sort_out = [&](uint32_t& x) {   // whether it is within reach; else above or below all
         const bool may = x != 0u && x != 0xffffffffu;
         const float from_t = may ? __fsub_rn(value_of(x), t) : 0.0f;
         const bool close = may && fabsf(from_t) <= reach;
         if (may && !close) x = from_t > reach ? 0xffffffffu : 0u;
-        uint32_t todo = __ballot_sync(0xffffffffu, close);
-        while (todo) {
-          const int i = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const float s = exact(j - lane + i, t);
-          if (lane == i) x = order_of(s);
+        return close;
+      };
+      if constexpr (R > 0) {
+        uint32_t near = 0u;   // a bit for each round
+#pragma unroll
+        for (int r = 0; r < R; ++r) near |= static_cast<uint32_t>(sort_out(row.held[r])) << r;
+        for (uint32_t lanes; (lanes = __ballot_sync(0xffffffffu, near != 0u)) != 0u;) {
+          const int i = __ffs(lanes) - 1, r = __shfl_sync(0xffffffffu, __ffs(near) - 1, i);
+          const uint32_t x = order_of(exact(32 * r + i, t));
+          if (lane != i) continue;
+          near &= near - 1;
+#pragma unroll
+          for (int z = 0; z < R; ++z)
+            if (z == r) row.held[z] = x;
         }
-      });
+      } else {
+        row.in_step([&](int j, uint32_t& x) {
+          uint32_t todo = __ballot_sync(0xffffffffu, sort_out(x));
+          while (todo) {
+            const int i = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const float s = exact(j - lane + i, t);
+            if (lane == i) x = order_of(s);
+          }
+        });
+      }
       __syncwarp();
       cut = cut_at(row, top);
     }
@@ -694,14 +713,14 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
       }
       // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, which
       // the warps make together; a warp takes every eighth group of 8 key blocks.
-      int q_down[2];
+      float q_down[2];
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int block = lane / 4 + 8 * y;
         const float size = block < n ? q_size[block] : INFINITY;
         const bool there = size <= FLT_MAX;
-        const Scale s = scale_of(there ? size : 1.0f);
-        q_down[y] = s.down;
+        const float s = scale_up(there ? size : 1.0f);
+        q_down[y] = scale_down(there ? size : 1.0f);
         for (int z = warp; z < kSteps; z += kWarps) {
           const float4 v = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at + block * HD)[4 * z + lane % 4]
                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -716,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
       const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
       const int groups = (before + most + 7) / 8;
       __syncthreads();
+      uint32_t* const my_scores = scored + lane / 4 * width;
       for (int g = warp; g < groups; g += kWarps) {
         const uint4* const from = a.sums.parts + (group0 + g) * (kSteps * 32) + lane;
         uint4 k[kSteps];
@@ -724,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
         const int j = 8 * g - before + lane % 4 * 2;
         float size[2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) size[x] = j + x >= 0 && j + x < most ? k_size[j + x] : 0.0f;
+        for (int x = 0; x < 2; ++x) size[x] = static_cast<uint32_t>(j + x) < static_cast<uint32_t>(most) ? k_size[j + x] : 0.0f;
         // (four sums, so that none is long: first parts of even and odd steps, the rest)
         float even[4] = {}, uneven[4] = {}, rest[4] = {}, other[4] = {};
 #pragma unroll
@@ -736,16 +756,15 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (j + x < 0 || j + x >= most) continue;
-          const float per_key = j + x == last ? per_last : per_full;
-          const int k_down = scale_of(size[x] <= FLT_MAX ? size[x] : 1.0f).down;
+          if (static_cast<uint32_t>(j + x) >= static_cast<uint32_t>(most)) continue;
+          const float per_key = j + x == last ? per_last : per_full, k_down = scale_down(size[x]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const int block = lane / 4 + 8 * y, i = 2 * y + x, down = q_down[y] + k_down;
-            if (block >= n) continue;
-            const float sum = __fmul_rn(__fadd_rn(__fadd_rn(even[i], uneven[i]), __fadd_rn(rest[i], other[i])), per_key);
-            scored[block * width + j + x] =
-                order_of(__fmul_rn(__fmul_rn(sum, power_of_two(down >> 1)), power_of_two(down - (down >> 1))));
+            const int i = 2 * y + x;
+            const float sum = __fadd_rn(__fadd_rn(even[i], uneven[i]), __fadd_rn(rest[i], other[i]));
+            // (the smaller factor first: nothing is too large on the way that is not so at the end)
+            const float s = __fmul_rn(__fmul_rn(__fmul_rn(sum, per_key), fminf(q_down[y], k_down)), fmaxf(q_down[y], k_down));
+            if (lane / 4 + 8 * y < n) my_scores[8 * y * width + j + x] = order_of_number(s);
           }
         }
       }
@@ -763,7 +782,9 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
       }
       if (threadIdx.x < n) {   // (0: queries or keys of zeros, whose scores are exact)
         const float q_sum = q_size[threadIdx.x];
-        const float off = fmaxf(__fmul_rn(__fmul_rn(q_sum, most_k), 0x1.6p-17f), 0x1p-140f);
+        // (2^-145: what scaled sums below 2^-112 may lose)
+        const float off = fmaxf(fmaxf(__fmul_rn(q_sum, fmaxf(__fmul_rn(most_k, 0x1.6p-17f), 0x1p-145f)),
+                                      __fmul_rn(most_k, 0x1p-145f)), 0x1p-140f);
         places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
       }
       __syncthreads();
