@@ -734,13 +734,20 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
       const int64_t group0 = k_row / 8;
       const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
       const int groups = (before + most + 7) / 8;
+      // Steps whose operands are asked for before the group is begun: half, where there are registers for them.
+      constexpr int kAhead = R > 16 ? kSteps / 2 : 0;
+      const uint4* from = a.sums.parts + (group0 + warp) * (kSteps * 32) + lane;
+      uint4 k[kSteps];
+      if (warp < groups) {
+#pragma unroll
+        for (int z = 0; z < kAhead; ++z) k[z] = from[z * 32];
+      }
       __syncthreads();
       uint32_t* const my_scores = scored + lane / 4 * width;
       for (int g = warp; g < groups; g += kWarps) {
-        const uint4* const from = a.sums.parts + (group0 + g) * (kSteps * 32) + lane;
-        uint4 k[kSteps];
 #pragma unroll
-        for (int z = 0; z < kSteps; ++z) k[z] = from[z * 32];
+        for (int z = kAhead; z < kSteps; ++z) k[z] = from[z * 32];
+        if (g + kWarps < groups) from += kWarps * kSteps * 32;
         const int j = 8 * g - before + lane % 4 * 2;
         float size[2];
 #pragma unroll
@@ -753,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
           product(z & 1 ? uneven : even, first, k[z].x, k[z].y);
           product(rest, first, k[z].z, k[z].w);
           product(other, second, k[z].x, k[z].y);
+          if (z < kAhead) k[z] = from[z * 32];   // (after the last group: any)
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -843,10 +851,12 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  // Three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key blocks on
-  // average; else two, whose warps hold 1,024.
+  // Many lists: three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key
+  // blocks on average (65,280 tokens 486 us against 525 with two).  Else two, whose warps hold 1,024 and ask
+  // for operands ahead (16 single tokens 47 us against 49).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
-  return longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
+  const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
+  return many && longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
                                                                : launch_score<HD, 32>(score, stream);
 }
 
