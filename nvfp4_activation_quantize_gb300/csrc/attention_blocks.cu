@@ -73,6 +73,7 @@ struct Args {
   int heads_per_tile, tokens, tile_groups;  // a row tile: tokens x heads_per_tile; tile_groups of heads
   int head_chunk;            // tile groups that are swept together (their keys and values stay in L2)
   int shift_q, shift_k;      // log2 of the blocks' sizes
+  int split_sms;             // the last units are split where they leave half of so many CTAs idle; 0: never
   int block_pairs;           // pairs of row tiles of a query block; 0: a block is one tile, two blocks a pair
   const int32_t* lists;      // [kv_heads][list_rows][top]
   int64_t list_rows;
@@ -173,9 +174,9 @@ __device__ __forceinline__ bool entry_counts(int v, int blocks, int& above) {
   return w > before;
 }
 
-// Fills in unit number `rank` of sequence b: every lane the same.  Whole warp.
+// Fills in unit number `rank` of sequence b, or its row tile number `half` alone: every lane the same.  Whole warp.
 template <int HD>
-__device__ __forceinline__ void write_unit(const Args& a, int b, int64_t rank, Unit& u) {
+__device__ __forceinline__ void write_unit(const Args& a, int b, int64_t rank, int half, Unit& u) {
   const int lane = threadIdx.x & 31;
   const int64_t q0 = a.cu_q[b];
   const int64_t n = rows_of(a.cu_q, b, a.rows_q);
@@ -194,18 +195,19 @@ __device__ __forceinline__ void write_unit(const Args& a, int b, int64_t rank, U
   const int32_t* list[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int64_t block = shared ? pair / a.block_pairs : 2 * pair + x;
-    const int64_t from = (block << a.shift_q) + (shared ? (2 * (pair % a.block_pairs) + x) * a.tokens : 0);
+    const int tile = half < 0 ? x : half;
+    const int64_t block = shared ? pair / a.block_pairs : 2 * pair + tile;
+    const int64_t from = (block << a.shift_q) + (shared ? (2 * (pair % a.block_pairs) + tile) * a.tokens : 0);
     int64_t end = (block + 1) << a.shift_q;   // of the block's tokens
     if (end > n) end = n;
     const int64_t count = end - from < a.tokens ? end - from : a.tokens;
-    toks[x] = count < 0 ? 0 : static_cast<int>(count);
+    toks[x] = count < 0 || (half >= 0 && x == 1) ? 0 : static_cast<int>(count);
     tok[x] = toks[x] > 0 ? static_cast<int>(from) : 0;
     least[x] = a.causal ? clamp_keys(tok[x] + shift, len) : len;
     most[x] = toks[x] == 0 ? 0 : a.causal ? clamp_keys(tok[x] + toks[x] - 1 + shift, len) : len;
     list[x] = a.lists + (static_cast<int64_t>(head0 / a.group) * a.list_rows + first_list + (toks[x] > 0 ? block : 0)) * a.top;
   }
-  if (shared) {   // one plan for both (tile 0 has rows: a pair's first tile always has)
+  if (shared) {   // one plan for both (the first has rows, or neither)
     most[0] = most[1] = max(most[0], most[1]);
     least[1] = least[0];
   }
@@ -875,6 +877,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       Unit& slot = *unit_slot(it);
       int found = -1;
       int64_t rank = 0;
+      int half = -1;
       // (a block past the last unit has none, but the one that the CTA is given in its place may)
       bool asking = true;
       while (block >= 0 && found < 0 && asking) {
@@ -888,7 +891,7 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
               "r"(bar_next)
               : "memory");
         }
-        // the sequences' units are counted 32 at a time
+        // the sequences' units are counted 32 at a time (units are split only where there are no more sequences)
         int64_t before = 0;
         for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
           const int b = b0 + lane;
@@ -899,16 +902,23 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
           }
-          const int64_t r = block - before;
+          int64_t unit = block, launched = __shfl_sync(0xffffffffu, upto, 31);
+          if (a.split_sms > 0) {
+            const UnitPart part = part_of(block, launched, a.split_sms);
+            unit = part.unit;
+            half = part.half;
+            launched = part.blocks;
+          }
+          const int64_t r = unit - before;
           const uint32_t hit = __ballot_sync(0xffffffffu, r >= upto - mine && r < upto);
           if (hit) {
             found = b0 + __ffs(hit) - 1;
             rank = __shfl_sync(0xffffffffu, r - (upto - mine), __ffs(hit) - 1);
           }
-          before += __shfl_sync(0xffffffffu, upto, 31);
+          before += launched;
         }
         if (found >= 0) {
-          write_unit<HD>(a, found, rank, slot);
+          write_unit<HD>(a, found, rank, half, slot);
           if (lane == 0) mbar_arrive(bar_unit + 8 * (it % kSlots));
         }
         asking = __all_sync(0xffffffffu, wait_or_abort(bar_next, asked & 1, abort));
@@ -966,7 +976,7 @@ cudaError_t head_map(CUtensorMap* map, const void* p, int64_t rows, int64_t head
 }
 
 template <int HD>
-cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k, const Args& a,
+cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k, Args a,
                    cudaStream_t stream) {
   using S = Shape<HD>;
   static_assert(S::kSmem <= 227 * 1024, "shared memory");
@@ -982,13 +992,22 @@ cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const u
     err = keys ? head_map(&map_v, a.v, a.rows_k, b.kv_heads, HD, a.ld_v, 1, box)
                : head_map(&map_v, q, a.rows_q, a.heads, HD, ld_q, 1, box);
   if (err != cudaSuccess) return err;
-  int one = 0;
-  err = persistent_blocks(reinterpret_cast<const void*>(&attention_blocks_kernel<HD>), kThreads, S::kSmem, 1, &one);
+  int sms = 0;
+  err = persistent_blocks(reinterpret_cast<const void*>(&attention_blocks_kernel<HD>), kThreads, S::kSmem,
+                          int64_t{1} << 30, &sms);
   if (err != cudaSuccess) return err;
   // at most this many pairs of row tiles, however the rows fall into sequences (each has a row)
   const int64_t most = a.block_pairs > 0 ? a.list_rows * a.block_pairs : (a.list_rows + a.batch + 1) / 2;
   const int64_t pairs = most < a.rows_q ? most : a.rows_q;
-  const int64_t blocks = pairs * a.tile_groups;
+  // The last units may be split in their row tiles where sequences have more than one of these on average (2,040
+  // tokens of 8 heads, 64 units: 35 us, 43 without; 4 chunks, 640: 160 and 162), unless a CTA has so many units
+  // that the last hardly matters.
+  int64_t halves = 0;
+  if (a.batch <= 32 && a.rows_q > static_cast<int64_t>(a.batch) * a.tokens && pairs * a.tile_groups < int64_t{16} * sms) {
+    halves = most_halves((a.rows_q + 2 * a.tokens - 1) / (2 * a.tokens) * a.tile_groups, pairs * a.tile_groups, sms);
+    if (halves > 0) a.split_sms = sms;
+  }
+  const int64_t blocks = pairs * a.tile_groups + halves;
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
   attention_blocks_kernel<HD><<<static_cast<unsigned>(blocks), kThreads, S::kSmem, stream>>>(map_q, map_k, map_v, a);
   return cudaGetLastError();
