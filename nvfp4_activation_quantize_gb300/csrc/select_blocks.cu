@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
 
 // ---------------------------------------------------------------------------- score
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// R = 16: 256 threads a CTA, three CTAs an SM.  R = 32: 512, one.
+template <int R>
+constexpr int kScoreThreads = R <= 16 ? 256 : 512;
 constexpr int kRows = 16;         // query blocks of a CTA at most: the rows of a product
 // Scores that a CTA holds: 16 query blocks against 1,016 key blocks, or fewer against more (one against 16,376, see
 // kMaxBlocks).
@@ -632,7 +633,8 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint4& x, uint32_
 }
 
 template <int HD, int R>
-__global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const __grid_constant__ ScoreArgs a) {
+__global__ void __launch_bounds__(kScoreThreads<R>, R <= 16 ? 3 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
+  constexpr int kThreads = kScoreThreads<R>, kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t smem[];
   constexpr int kSteps = HD / 16;
   uint4* const q_parts = reinterpret_cast<uint4*>(smem);   // [step][first, second][lane]
@@ -822,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, R <= 16 ? 3 : 2) score_kernel(const 
 
 template <int HD, int R>
 cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
-  constexpr int kSmem = HD / 16 * 2 * 512 + kScores * 4;
+  constexpr int kThreads = kScoreThreads<R>, kSmem = HD / 16 * 2 * 512 + kScores * 4;
   int blocks = 0;
   cudaError_t err =
       persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R>), kThreads, kSmem, int64_t{1} << 30, &blocks);
@@ -852,8 +854,8 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   // Many lists: three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key
-  // blocks on average (65,280 tokens 486 us against 525 with two).  Else two, whose warps hold 1,024 and ask
-  // for operands ahead (16 single tokens 47 us against 49).
+  // blocks on average (65,280 tokens 486 us against 525 with two).  Else one of twice the threads, whose warps hold 1,024 and ask
+  // for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
   const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
   return many && longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
