@@ -45,7 +45,7 @@ namespace {
 
 // ---------------------------------------------------------------------------- pool
 
-constexpr int kPoolThreads = 256;
+constexpr int kPoolThreads = 128;
 
 // The workspace: hi and lo parts of q and of k, [kv_heads][block rows][head_dim], for each block the length of its sums
 // as a vector (infinity where one is no number), and k once more as two fp16 parts for the products, scaled by
@@ -77,6 +77,30 @@ Sums carve(const BlockShape& s, uint8_t* workspace) {
     at += w.rows[t] * s.kv_heads;
   }
   return w;
+}
+
+// block_at for up to 32 sequences, a lane for each: one wait for memory, where halving waits for every step.  Whole warp.
+__device__ __forceinline__ BlockPlace block_at_once(const int32_t* cu, int batch, int64_t total, int shift, int64_t r) {
+  const int lane = threadIdx.x & 31;
+  BlockPlace p{0, 0, 0, 0};
+  if (batch == 0) return p;
+  int first = 0, end = 0;
+  if (lane < batch) {
+    first = cu[lane];
+    end = cu[lane + 1];
+  }
+  const uint32_t upto = __ballot_sync(0xffffffffu, lane < batch && (first >> shift) + static_cast<int64_t>(lane) <= r);
+  p.sequence = upto != 0u ? 31 - __clz(upto) : 0;
+  first = __shfl_sync(0xffffffffu, first, p.sequence);
+  end = __shfl_sync(0xffffffffu, end, p.sequence);
+  int64_t n = static_cast<int64_t>(end) - first;
+  if (n > total - first) n = total - first;
+  const int64_t i = r - (first >> shift) - p.sequence, left = n - (i << shift);
+  if (first < 0 || i < 0 || left <= 0) return p;
+  p.index = static_cast<int>(i);
+  p.row0 = first + (i << shift);
+  p.rows = static_cast<int>(left < (int64_t{1} << shift) ? left : int64_t{1} << shift);
+  return p;
 }
 
 struct PoolArgs {
@@ -116,7 +140,7 @@ __device__ __forceinline__ void halves_of(float2 x, float scale, uint32_t& first
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_constant__ PoolArgs a) {
+__global__ void __launch_bounds__(kPoolThreads, 6) pool_kernel(const __grid_constant__ PoolArgs a) {
   constexpr int kLanes = HD / 8;            // lanes of a row of a head, 8 values each
   constexpr int kRows = 32 / kLanes;        // rows of a head that a load of the warp takes
   constexpr int kUnroll = 4;                // loads under way while as many are summed
@@ -130,7 +154,8 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
   if (r >= a.sums.rows[0] + a.sums.rows[1]) return;
   const int t = r >= a.sums.rows[0];
   if (t) r -= a.sums.rows[0];
-  const BlockPlace p = block_at(a.cu[t], a.batch, a.total[t], a.shift[t], r);
+  const BlockPlace p = a.batch <= 32 ? block_at_once(a.cu[t], a.batch, a.total[t], a.shift[t], r)
+                                     : block_at(a.cu[t], a.batch, a.total[t], a.shift[t], r);
   if (p.rows == 0) return;   // (never read)
   const int group = a.group[t], items = p.rows * group;   // rows of single heads
   const int64_t ld = a.ld[t];
@@ -161,16 +186,33 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
     offset = to;
     limit = __uint_as_float(static_cast<uint32_t>(max(e - growth + 2, 3)) << 23);
   };
-  auto load = [&](int i0, uint4 (&w)[kUnroll]) {
+  // The lane's next item: row item / group, head item % group.
+  int item = lane / kLanes, item_head = item % group;
+  const uint16_t* from = x + item / group * ld + item_head * HD;
+  const int heads_on = kRows % group;
+  const int64_t step = kRows / group * ld + heads_on * HD, wrap = ld - group * HD;
+  auto one = [&]() {
+    const uint4 w = load16_stream(from);
+    from += step;
+    item_head += heads_on;
+    if (item_head >= group) {
+      item_head -= group;
+      from += wrap;
+    }
+    return w;
+  };
+  auto load = [&](uint4 (&w)[kUnroll]) {
+    if (item + (kUnroll - 1) * kRows < items) {
 #pragma unroll
-    for (int n = 0; n < kUnroll; ++n) {
-      const int i = i0 + n * kRows;
-      w[n] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < items) {
-        const int row = group == 1 ? i : i / group;
-        w[n] = load16_stream(x + row * ld + (i - row * group) * HD);
+      for (int n = 0; n < kUnroll; ++n) w[n] = one();
+    } else {   // the last, or past them
+#pragma unroll
+      for (int n = 0; n < kUnroll; ++n) {
+        w[n] = make_uint4(0u, 0u, 0u, 0u);
+        if (item + n * kRows < items) w[n] = one();
       }
     }
+    item += kUnroll * kRows;
   };
   auto sum = [&](const uint4 (&w)[kUnroll]) {
     uint32_t most = 0u;
@@ -192,11 +234,11 @@ __global__ void __launch_bounds__(kPoolThreads, 3) pool_kernel(const __grid_cons
   };
   uint4 w0[kUnroll], w1[kUnroll];
   constexpr int kStep = kRows * kUnroll;
-  load(lane / kLanes, w0);
+  load(w0);
   for (int i0 = lane / kLanes; i0 < items; i0 += 2 * kStep) {   // (zeros past the last change nothing)
-    load(i0 + kStep, w1);
+    load(w1);
     sum(w0);
-    load(i0 + 2 * kStep, w0);
+    load(w0);
     sum(w1);
   }
   if (finite) {
