@@ -16,18 +16,18 @@
 //           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
 //   score   16 query blocks a CTA against all key blocks of their sequence, with mma.sync m16n8k16 (16 rows are
 //           what there is; scores go straight to the choice), on two fp16 parts of each sum, scaled: three
-//           products are as good as fp32's.  q's operands stay in registers, k's come from L2 in the order
+//           products are as good as fp32's.  q's operands are in shared memory, k's come from L2 in the order
 //           that a lane wants, a load of 16 bytes for three products.  Then a warp per query block takes its
-//           scores into registers and looks for the top-th highest.  (In fp32, from tiles of key blocks that
-//           asynchronous copies brought: 284 us for 65,280 tokens' 510 x 510 scores of 56 heads, of which 64 a row are kept.)
-//           Bound: the choice's instructions, about 3,000 a list and warp.
+//           scores into registers and looks for the top-th highest.  65,280 tokens' 510 x 510 scores of 56
+//           heads, of which 64 a row are kept: 140 us (284 with fp32 products from tiles in shared memory).
+//           Bound: latency with 24 warps an SM, of the products' loads (80 us) and the choice's steps (55).
 //
 // What these products cannot tell apart is told apart by fp32 pairs: a score is off by at most
-// delta = 176 * 2^-24 * |q| |k|, of the largest |k|.  (Parts and the product of two second parts: 3 * 2^-22.  A product of 16
-// values adds 17 terms, of each of which it may cut what is below 2^-23 of the largest, and rounds, 36 * 2^-24 at most: M.
-// Fasi, N. J. Higham, M. Mikaitis and S. Pranesh, "Numerical behavior of NVIDIA tensor cores", PeerJ Comput. Sci. 7,
-// 2021; four of them follow each other in each of two sums, 144; in the third, of second parts, they are 2^-10 of that.
-// Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the choice is the exact one.  Where it is
+// delta = 176 * 2^-24 * |q| |k|, of the largest |k|.  (Parts and the product of two second parts: 3 * 2^-22.  A
+// product of 16 values adds 17 terms, of each of which it may cut what is below 2^-23 of the largest, and rounds,
+// 36 * 2^-24 at most: M. Fasi, N. J. Higham, M. Mikaitis and S. Pranesh, "Numerical behavior of NVIDIA tensor
+// cores", PeerJ Comput. Sci. 7, 2021.  Four of them follow each other in each of two sums, 144; in the other two, of
+// second parts, they are 2^-10 of that.  Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the choice is the exact one.  Where it is
 // not (one list in forty for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in
 // pairs of fp32 (to 2^-40 and better), and the places that are left go to the highest of those.
 #include <cuda_fp16.h>

@@ -111,6 +111,27 @@ def test_numbers_that_are_none(dev):
     _check(c, 6, 64, 64, False, 0, scores=False)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_are_as_near_as_the_choice_takes_them(dev, dim):
+    """Large products that cancel beside small ones: each score within 176 * 2^-24 of |q| |k|, and the two roundings of
+    what is stored."""
+    c = bc.sequences(dev, [(64 * 20, 64 * 200)], 1, 1, dim, seed=31, tail=0)
+    g = torch.Generator(device=dev)
+    g.manual_seed(31)
+    for name in "qk":
+        size = torch.randint(-9, 10, (1, 1, dim // 2), generator=g, device=dev).float().exp2()
+        c[name][:] = (c[name].float() * size.repeat_interleave(2, 2)).bfloat16()
+    c["q"][:, :, 1::2] = c["q"][:, :, 0::2]
+    c["k"][:, :, 1::2] = -c["k"][:, :, 0::2]
+    c["k"][3::7, :, 1::2] *= 0.99                         # the rest of some rows' cancellation
+    s = torch.empty((1, 20 + 1, 200), device=dev)
+    h3q.h3q_select_blocks(c["q"], c["k"], c["cu_q"], c["cu_k"], 200, block_q=64, block_k=64, scores=s)
+    q = c["q"].double().view(20, 64, dim).mean(1)
+    k = c["k"].double().view(200, 64, dim).mean(1)
+    off = (s[0, :20].double() - q @ k.T).abs()
+    assert bool((off <= 2.0 ** -24 * (176 * q.norm(dim=1)[:, None] * k.norm(dim=1) + 2 * (q @ k.T).abs())).all())
+
+
 @pytest.mark.parametrize("blocks", [40, 1500])   # scores kept in registers, formed again
 def test_scores_that_are_infinite(dev, blocks):
     c = bc.sequences(dev, [(64, 64 * blocks)], 1, 1, 64, seed=29, tail=0)
