@@ -10,8 +10,8 @@
 //           constant that is larger than all that can come (S. M. Rump, T. Ogita and S. Oishi,
 //           "Accurate floating-point summation part I", SIAM J. Sci. Comput. 31(1), 2008): what its
 //           rounding leaves of each value is exact and goes to a sum of its own, four packed
-//           additions a pair of values (65,280 rows of 56 + 56 heads of 128 in 299 us, 6.4 TB/s with what is
-//           written; with two-sums, seven additions, 331).  A sum of
+//           additions a pair of values (65,280 rows of 56 + 56 heads of 128 in 282 us, 6.8 TB/s with what is
+//           written).  A sum of
 //           up to 256 values is exact where they lie within a factor of 2^18 of each other, and else off by
 //           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
 //   score   16 query blocks a CTA against all key blocks of their sequence, with mma.sync m16n8k16 (16 rows are
@@ -35,7 +35,6 @@
 #include <cfloat>
 #include <cmath>
 
-#include "h3q_async.cuh"
 #include "h3q_blocks.cuh"
 #include "h3q_device.cuh"
 #include "h3q_internal.h"
@@ -507,7 +506,7 @@ __device__ __forceinline__ void choose(const ScoreArgs& a, const RowPlace& p, ui
   // The score of key block j from hi + lo, less `from`: a lane has 4 or 2 dimensions.  In pairs of fp32, whose
   // products and sums keep their rounding errors (T. J. Dekker, "A floating-point technique for extending the
   // available precision", Numer. Math. 18, 1971), as far as those cannot underflow; else in fp64, of which an
-  // SM does two a clock.  (The worst, 65,280 tokens of equal blocks, all of which tie: 10.8 ms, in fp64 27.8.)
+  // SM does two a clock.  (The worst, 65,280 tokens of equal blocks, all of which tie: 4.1 ms.)
   constexpr int kEach = HD / 32;
   float qh[kEach], ql[kEach];
   bool has_q = false;
@@ -896,8 +895,8 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   // Many lists: three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key
-  // blocks on average (65,280 tokens 486 us against 525 with two).  Else one of twice the threads, whose warps hold 1,024 and ask
-  // for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
+  // blocks on average (65,280 tokens 486 us against 525 with two).  Else one of twice the threads, whose warps
+  // hold 1,024 and ask for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
   const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
   return many && longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
