@@ -211,6 +211,21 @@ def test_wrong_offsets_touch_nothing_outside(dev):
         assert torch.equal(out[:200], want[:200])
 
 
+@pytest.mark.parametrize("heads, kv_heads, dim, block_q", [(8, 8, 128, 128), (8, 8, 64, 64), (6, 6, 128, 256), (16, 4, 128, 64)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_units_in_halves_give_the_same_bits(dev, heads, kv_heads, dim, block_q, causal):
+    """The last units run as two row tiles where there are few sequences, as one beside 32 empty sequences."""
+    c = bc.sequences(dev, [(1100, 1500)], heads, kv_heads, dim, seed=33)
+    lists = bc.random_lists(c, kv_heads, block_q, 64, 9, 33)
+    out, lse = _run(c, lists, block_q, 64, causal)
+    many = dict(c, cu_q=cc.ints([0] * 33 + [1100], dev), cu_k=cc.ints([0] * 33 + [1500], dev))
+    more = torch.full((kv_heads, lists.shape[1] + 32, 9), -1, dtype=torch.int32, device=dev)
+    more[:, 32:] = lists
+    again, lse_again = _run(many, more, block_q, 64, causal)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+    bc.check_blocks(c, lists, block_q, 64, causal, out, lse)
+
+
 def test_long_keys_past_32_bits(dev):
     """Keys whose place passes 2^31 elements."""
     heads, dim, keys = 8, 128, 2_200_000

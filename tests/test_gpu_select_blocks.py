@@ -184,6 +184,30 @@ def test_rows_of_a_workspace_are_its_own(dev):
         assert (lists.cpu().numpy() == want).all()
 
 
+def test_many_sequences_give_the_same_lists(dev):
+    """A sequence of its own, and behind 40 empty ones."""
+    c = bc.sequences(dev, [(900, 3000)], 4, 2, 128, seed=32)
+    want = _check(c, 9, 64, 64, True, 1)
+    many = dict(c, cu_q=cc.ints([0] * 41 + [900], dev), cu_k=cc.ints([0] * 41 + [3000], dev))
+    assert torch.equal(_check(many, 9, 64, 64, True, 1)[:, 40:], want)
+
+
+def test_long_keys_past_32_bits(dev):
+    """Keys whose place passes 2^31 elements."""
+    heads, keys = 64, 300_000
+    g = torch.Generator(device=dev)
+    g.manual_seed(34)
+    k = torch.empty((keys, heads, 128), dtype=torch.bfloat16, device=dev)
+    for part in k.split(keys // 10):
+        part.normal_(generator=g)
+    q = torch.randn((100, heads, 128), generator=g, device=dev).bfloat16()
+    got = h3q.h3q_select_blocks(q, k, cc.ints([0, 100], dev), cc.ints([0, keys], dev), 20)
+    for head in (0, heads - 1):
+        c = {"q": q[:, head:head + 1], "k": k[:, head:head + 1], "cu_q": cc.ints([0, 100], dev), "cu_k": cc.ints([0, keys], dev)}
+        want, _ = bc.selected(c, 20, 128, 128, False, 0)
+        assert (got[head].cpu().numpy() == want[0]).all()
+
+
 def test_wrong_offsets_touch_nothing_outside(dev):
     c = bc.sequences(dev, [(200, 300), (200, 300)], 2, 2, 128, seed=27, tail=0)
     for cu_q, cu_k in (([0, 200, 10_000], [0, 300, 20_000]), ([0, 200, -5], [0, 300, -7]), ([5, 3, 1], [9, 4, 2]),
