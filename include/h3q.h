@@ -715,7 +715,8 @@ static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
  * not candidates.  The choice is that of the exact scores: where fp32 is too coarse to tell,
  * they are formed again from sums held in pairs of fp32.  (Those are exact where the values
  * of a block's columns lie within a factor of 2^18 of each other, up to 256 of them, and else off by
- * 2^-20 of the largest at most; sums have to fit fp32.)  A score that is no number counts as the lowest.
+ * 2^-20 of the largest at most.  The length of a block's sums as a vector and the scores of sums have to fit
+ * fp32, not what comes up on the way.)  A score that is no number counts as the lowest.
  *
  *   q            bf16 [rows_q, heads * head_dim], row stride ld_q; k bf16 [rows_k, kv_heads *
  *                head_dim], row stride ld_k; 32-byte aligned.

@@ -240,7 +240,11 @@ __global__ void __launch_bounds__(kPoolThreads, 6) pool_kernel(const __grid_cons
     load(w0);
     sum(w1);
   }
-  if (finite) {
+  // Values near fp32's end, infinities or values that are no numbers, in any lane: by two-sums, at 2^-32 of their
+  // size, so that sums may pass fp32's end on the way.
+  constexpr float kDown = 0x1p-32f, kUp = 0x1p32f;
+  const bool scaled = !__all_sync(0xffffffffu, finite);
+  if (!scaled) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 rest = lo[i];
@@ -248,15 +252,16 @@ __global__ void __launch_bounds__(kPoolThreads, 6) pool_kernel(const __grid_cons
       lo[i] = make_float2(0.0f, 0.0f);
       add_to(hi[i], lo[i], rest);
     }
-  } else {   // infinities, values that are no numbers, or sums near fp32's end: as fp32 has them
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) hi[i] = lo[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
     for (int i0 = lane / kLanes; i0 < items; i0 += kRows) {
       const uint4 w = load16_stream(x + i0 / group * ld + (i0 % group) * HD);
-      hi[0] = add2(hi[0], bf16x2_to_float2(w.x));
-      hi[1] = add2(hi[1], bf16x2_to_float2(w.y));
-      hi[2] = add2(hi[2], bf16x2_to_float2(w.z));
-      hi[3] = add2(hi[3], bf16x2_to_float2(w.w));
+      add_to(hi[0], lo[0], mul2(bf16x2_to_float2(w.x), make_float2(kDown, kDown)));
+      add_to(hi[1], lo[1], mul2(bf16x2_to_float2(w.y), make_float2(kDown, kDown)));
+      add_to(hi[2], lo[2], mul2(bf16x2_to_float2(w.z), make_float2(kDown, kDown)));
+      add_to(hi[3], lo[3], mul2(bf16x2_to_float2(w.w), make_float2(kDown, kDown)));
     }
   }
   // the other rows' lanes
@@ -268,6 +273,13 @@ __global__ void __launch_bounds__(kPoolThreads, 6) pool_kernel(const __grid_cons
       const float2 l = make_float2(__shfl_xor_sync(0xffffffffu, lo[i].x, o), __shfl_xor_sync(0xffffffffu, lo[i].y, o));
       add_to(hi[i], lo[i], h);
       lo[i] = add2(lo[i], l);
+    }
+  }
+  if (scaled) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi[i] = mul2(hi[i], make_float2(kUp, kUp));
+      lo[i] = mul2(lo[i], make_float2(kUp, kUp));
     }
   }
   // hi = the sum rounded to fp32, lo = the rest (none where hi is no number)
