@@ -747,6 +747,7 @@ int h3q_select_blocks(const void *q, int64_t ld_q, const void *k, int64_t ld_k, 
  * if it is the number of a block of the sequence and above all entries before it that count
  * (so a block named twice counts once); all others are passed over.  A query that sees no key gets
  * o = 0 and lse = -inf.  Rounding, magnitudes, numbers that are none, o and lse as there.
+ * Fewer than 2^31 units of work, pairs of row tiles of up to 128 rows of a sequence's tokens and heads.
  * The kernel's waits are bounded (2 s): if one runs out it stops early, the outputs are
  * unspecified, and h3q_kernel_error_flag reports it.
  */

@@ -958,6 +958,46 @@ attention_blocks_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   }
 }
 
+// How the rows of a call are cut into tiles.
+Args tiles_of(const BlockShape& b) {
+  Args a{};
+  a.cu_q = b.cu_q;
+  a.cu_k = b.cu_k;
+  a.batch = b.batch;
+  a.rows_q = b.rows_q;
+  a.rows_k = b.rows_k;
+  a.heads = b.heads;
+  a.group = b.heads / b.kv_heads;
+  // heads of a row tile: the divisor of the group that fills the most of 128 rows, the
+  // largest of those
+  int best = 0;
+  for (int d = 1; d <= a.group && d <= kTileRows; ++d)
+    if (a.group % d == 0 && kTileRows / d * d >= best) {
+      best = kTileRows / d * d;
+      a.heads_per_tile = d;
+    }
+  a.tokens = kTileRows / a.heads_per_tile;
+  if (a.tokens > b.block_q) a.tokens = b.block_q;
+  a.tile_groups = b.heads / a.heads_per_tile;
+  const int block_tiles = (b.block_q + a.tokens - 1) / a.tokens;
+  a.block_pairs = block_tiles == 1 ? 0 : (block_tiles + 1) / 2;
+  // heads whose keys and values are swept together: as many as stay in half of the L2
+  const int64_t kv_bytes = b.rows_k * b.head_dim * 4;
+  int64_t kv_chunk = kv_bytes > 0 ? (int64_t{64} << 20) / kv_bytes : b.kv_heads;
+  kv_chunk = kv_chunk < 1 ? 1 : kv_chunk > b.kv_heads ? b.kv_heads : kv_chunk;
+  a.head_chunk = static_cast<int>(kv_chunk * (a.group / a.heads_per_tile));
+  a.shift_q = log2_of(b.block_q);
+  a.shift_k = log2_of(b.block_k);
+  a.list_rows = b.rows_q / b.block_q + b.batch;
+  return a;
+}
+
+// At most this many pairs of row tiles, however the rows fall into sequences (each has a row).
+int64_t most_pairs(const Args& a) {
+  const int64_t most = a.block_pairs > 0 ? a.list_rows * a.block_pairs : (a.list_rows + a.batch + 1) / 2;
+  return most < a.rows_q ? most : a.rows_q;
+}
+
 // bf16 [rows, heads, head_dim] in boxes of 64 elements x box_heads x box_rows, 128-byte swizzle; rows past
 // the end read as zero.
 cudaError_t head_map(CUtensorMap* map, const void* p, int64_t rows, int64_t heads, int64_t head_dim, int64_t ld,
@@ -996,9 +1036,7 @@ cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const u
   err = persistent_blocks(reinterpret_cast<const void*>(&attention_blocks_kernel<HD>), kThreads, S::kSmem,
                           int64_t{1} << 30, &sms);
   if (err != cudaSuccess) return err;
-  // at most this many pairs of row tiles, however the rows fall into sequences (each has a row)
-  const int64_t most = a.block_pairs > 0 ? a.list_rows * a.block_pairs : (a.list_rows + a.batch + 1) / 2;
-  const int64_t pairs = most < a.rows_q ? most : a.rows_q;
+  const int64_t pairs = most_pairs(a);
   // The last units may be split in their row tiles where sequences have more than one of these on average (2,040
   // tokens of 8 heads, 64 units: 35 us, 43 without; 4 chunks, 640: 160 and 162), unless a CTA has so many units
   // that the last hardly matters.
@@ -1007,8 +1045,7 @@ cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const u
     halves = most_halves((a.rows_q + 2 * a.tokens - 1) / (2 * a.tokens) * a.tile_groups, pairs * a.tile_groups, sms);
     if (halves > 0) a.split_sms = sms;
   }
-  const int64_t blocks = pairs * a.tile_groups + halves;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = pairs * a.tile_groups + halves;   // (below 2^31, see the API; halves only where there are few)
   attention_blocks_kernel<HD><<<static_cast<unsigned>(blocks), kThreads, S::kSmem, stream>>>(map_q, map_k, map_v, a);
   return cudaGetLastError();
 }
@@ -1018,36 +1055,8 @@ cudaError_t launch(const BlockShape& b, const uint16_t* q, int64_t ld_q, const u
 cudaError_t launch_attention_blocks(const BlockShape& b, const uint16_t* q, int64_t ld_q, const uint16_t* k,
                                     int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* blocks, float scale,
                                     uint16_t* o, float* lse, cudaStream_t stream) {
-  Args a{};
-  a.cu_q = b.cu_q;
-  a.cu_k = b.cu_k;
-  a.batch = b.batch;
-  a.rows_q = b.rows_q;
-  a.rows_k = b.rows_k;
-  a.heads = b.heads;
-  a.group = b.heads / b.kv_heads;
-  // heads of a row tile: the divisor of the group that fills the most of 128 rows, the
-  // largest of those
-  int best = 0;
-  for (int d = 1; d <= a.group && d <= kTileRows; ++d)
-    if (a.group % d == 0 && kTileRows / d * d >= best) {
-      best = kTileRows / d * d;
-      a.heads_per_tile = d;
-    }
-  a.tokens = kTileRows / a.heads_per_tile;
-  if (a.tokens > b.block_q) a.tokens = b.block_q;
-  a.tile_groups = b.heads / a.heads_per_tile;
-  const int block_tiles = (b.block_q + a.tokens - 1) / a.tokens;
-  a.block_pairs = block_tiles == 1 ? 0 : (block_tiles + 1) / 2;
-  // heads whose keys and values are swept together: as many as stay in half of the L2
-  const int64_t kv_bytes = b.rows_k * b.head_dim * 4;
-  int64_t kv_chunk = kv_bytes > 0 ? (int64_t{64} << 20) / kv_bytes : b.kv_heads;
-  kv_chunk = kv_chunk < 1 ? 1 : kv_chunk > b.kv_heads ? b.kv_heads : kv_chunk;
-  a.head_chunk = static_cast<int>(kv_chunk * (a.group / a.heads_per_tile));
-  a.shift_q = log2_of(b.block_q);
-  a.shift_k = log2_of(b.block_k);
+  Args a = tiles_of(b);
   a.lists = blocks;
-  a.list_rows = b.rows_q / b.block_q + b.batch;
   a.top = b.top;
   a.causal = b.causal;
   a.scale = scale;
@@ -1056,6 +1065,11 @@ cudaError_t launch_attention_blocks(const BlockShape& b, const uint16_t* q, int6
   a.o = o;
   a.lse = lse;
   return b.head_dim == 64 ? launch<64>(b, q, ld_q, k, ld_k, a, stream) : launch<128>(b, q, ld_q, k, ld_k, a, stream);
+}
+
+int64_t attention_blocks_units(const BlockShape& b) {
+  const Args a = tiles_of(b);
+  return most_pairs(a) * a.tile_groups;
 }
 
 cudaError_t attention_blocks_error_flag(int* flag) {

@@ -1203,6 +1203,10 @@ int h3q_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_
   if (int e = check_blocks(fn, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal)) return e;
   if (!std::isfinite(scale) || !(scale > 0.0f)) return invalid(fn, "scale must be finite and > 0");
   if (rows_q == 0 || batch == 0) return H3Q_OK;
+  const h3q::BlockShape shape =
+      block_shape(cu_q, cu_k, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal);
+  if (h3q::attention_blocks_units(shape) > (int64_t(1) << 31) - 1)
+    return invalid(fn, "too many rows: batch, rows_q and heads give 2^31 pairs of row tiles or more");
   const int64_t dq = heads * head_dim, dk = kv_heads * head_dim;
   if (int e = check_input(fn, "q", q, ld_q, rows_q, dq)) return e;
   if (rows_k > 0) {
@@ -1224,8 +1228,7 @@ int h3q_attention_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_
       if (overlap(out, in)) return invalid(fn, "an output overlaps an input");
   if (overlap(outs[0], outs[1])) return invalid(fn, "o and lse overlap");
   cudaError_t err = h3q::launch_attention_blocks(
-      block_shape(cu_q, cu_k, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal),
-      static_cast<const uint16_t*>(q), ld_q, static_cast<const uint16_t*>(k), ld_k, static_cast<const uint16_t*>(v),
+      shape, static_cast<const uint16_t*>(q), ld_q, static_cast<const uint16_t*>(k), ld_k, static_cast<const uint16_t*>(v),
       ld_v, blocks, scale, static_cast<uint16_t*>(o), lse, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? H3Q_OK : cuda_failed(fn, err);
 }

@@ -189,6 +189,7 @@ cudaError_t launch_select_blocks(const BlockShape& s, const uint16_t* q, int64_t
 cudaError_t launch_attention_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k,
                                     int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* blocks, float scale,
                                     uint16_t* o, float* lse, cudaStream_t stream);
+int64_t attention_blocks_units(const BlockShape& s);   // blocks of its launch, at most (and some halves where there are few)
 cudaError_t attention_blocks_error_flag(int* flag);
 
 // RMSNorm + AdaLN -> NVFP4 on host buffers (x in, codes and scales out), the
