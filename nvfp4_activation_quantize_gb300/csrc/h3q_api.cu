@@ -1112,7 +1112,6 @@ namespace {
 constexpr int64_t kMaxPacked = (int64_t(1) << 31) - 512;   // tensor-copy coordinates are 32-bit
 constexpr int64_t kMaxKeys = int64_t(1) << 25;
 constexpr int64_t kMaxTop = 4096;
-constexpr int64_t kMaxBlocks = 16000;                      // key blocks of a sequence whose scores a CTA holds
 
 // The shapes of the calls that attend over blocks; returns 0 or an error code.
 int check_blocks(const char* fn, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads, int64_t kv_heads,
@@ -1154,7 +1153,7 @@ int h3q_select_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k, 
   static const char* fn = "h3q_select_blocks";
   g_last_error.clear();
   if (int e = check_blocks(fn, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal)) return e;
-  if (rows_k / block_k > kMaxBlocks) return invalid(fn, "rows_k / block_k exceeds 16,000");
+  if (rows_k / block_k > h3q::kMaxKeyBlocks) return invalid(fn, "rows_k / block_k exceeds 16,000");
   if (first < 0 || first > top) return invalid(fn, "first must be in [0, top]");
   if (causal && top < first + (block_q + block_k - 1) / block_k + 1)
     return invalid(fn, "top leaves no room for the first blocks and the queries' own");

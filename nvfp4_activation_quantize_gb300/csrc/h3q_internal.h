@@ -184,6 +184,8 @@ struct BlockShape {
   int top;      // entries of a list
   int causal;
 };
+constexpr int64_t kMaxKeyBlocks = 16000;   // of a call that selects: a CTA holds a query block's scores (of rows_k / block_k
+                                           // full ones and a shorter one, where all are of one sequence)
 cudaError_t launch_select_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k,
                                  int first, int32_t* blocks, float* scores, uint8_t* workspace, cudaStream_t stream);
 cudaError_t launch_attention_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k,

@@ -345,11 +345,12 @@ __global__ void __launch_bounds__(kPoolThreads, 6) pool_kernel(const __grid_cons
 template <int R>
 constexpr int kScoreThreads = R <= 16 ? 256 : 512;
 constexpr int kRows = 16;         // query blocks of a CTA at most: the rows of a product
-// Scores that a CTA holds: 16 query blocks against 1,016 key blocks, or fewer against more (one against 16,376, see
-// kMaxBlocks).
-constexpr int kScores = kRows * 1024;
 // A row of scores begins so much past a multiple of 32 words: the eight rows that a warp stores to are in other banks.
 constexpr int kRowPad = 8;
+__host__ __device__ constexpr int width_of(int candidates) { return (candidates + 31) / 32 * 32 + kRowPad; }
+// Scores that a CTA holds: 16 query blocks against 1,024 key blocks, or fewer against more.
+constexpr int kScores = kRows * width_of(1024);
+static_assert(width_of(static_cast<int>(kMaxKeyBlocks) + 1) <= kScores, "one query block against the most key blocks");
 
 struct ScoreArgs {
   BlockShape s;
@@ -727,11 +728,11 @@ __global__ void __launch_bounds__(kScoreThreads<R>, R <= 16 ? 3 : 1) score_kerne
   for (int seg = 0; seg < rows;) {
     // rows of one sequence, as many as the scores have room for
     const RowPlace first = places[seg];
-    int most = first.candidates, n = 1, width = (most + 31) / 32 * 32 + kRowPad;
+    int most = first.candidates, n = 1, width = width_of(most);
     while (seg + n < rows && first.block.rows > 0 && places[seg + n].block.rows > 0 &&
            places[seg + n].block.sequence == first.block.sequence) {
       const int other = max(places[seg + n].candidates, most);
-      const int w = (other + 31) / 32 * 32 + kRowPad;
+      const int w = width_of(other);
       if ((n + 1) * w > kScores) break;
       most = other;
       width = w;
