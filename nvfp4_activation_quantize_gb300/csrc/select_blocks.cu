@@ -876,12 +876,19 @@ __global__ void __launch_bounds__(kScoreThreads<R>, R <= 16 ? 3 : 1) score_kerne
   }
 }
 
+// CTAs of the scores' kernel that the device holds.
+template <int HD>
+constexpr int kScoreSmem = HD / 16 * 2 * 512 + kScores * 4;
+template <int HD, int R>
+cudaError_t resident(int* blocks) {
+  return persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R>), kScoreThreads<R>, kScoreSmem<HD>,
+                           int64_t{1} << 30, blocks);
+}
+
 template <int HD, int R>
 cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
-  constexpr int kThreads = kScoreThreads<R>, kSmem = HD / 16 * 2 * 512 + kScores * 4;
   int blocks = 0;
-  cudaError_t err =
-      persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R>), kThreads, kSmem, int64_t{1} << 30, &blocks);
+  cudaError_t err = resident<HD, R>(&blocks);
   if (err != cudaSuccess) return err;
   // query blocks of a CTA: 16, or fewer where all CTAs run at once all the same
   const int64_t rows = (score.sums.rows[0] * score.s.kv_heads + blocks - 1) / blocks;
@@ -889,8 +896,8 @@ cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
   const int64_t chunks = (score.sums.rows[0] + score.rows - 1) / score.rows;
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(chunks * score.s.kv_heads));
-  config.blockDim = dim3(kThreads);
-  config.dynamicSmemBytes = kSmem;
+  config.blockDim = dim3(kScoreThreads<R>);
+  config.dynamicSmemBytes = kScoreSmem<HD>;
   config.stream = stream;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -904,14 +911,16 @@ template <int HD>
 cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t stream) {
   const int64_t warps = (pool.sums.rows[0] + pool.sums.rows[1]) * pool.kv_heads;
   const int64_t pool_blocks = (warps + kPoolThreads / 32 - 1) / (kPoolThreads / 32);
-  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
-  cudaError_t err = cudaGetLastError();
+  int single = 0;
+  cudaError_t err = resident<HD, 32>(&single);
   if (err != cudaSuccess) return err;
+  pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
+  if ((err = cudaGetLastError()) != cudaSuccess) return err;
   // Many lists: three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key
   // blocks on average (65,280 tokens 486 us against 525 with two).  Else one of twice the threads, whose warps
   // hold 1,024 and ask for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
-  const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * 152 * kRows;
+  const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * single * kRows;
   return many && longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
                                                                : launch_score<HD, 32>(score, stream);
 }
