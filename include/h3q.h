@@ -725,15 +725,22 @@ static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
  *   scores       out, fp32 of the same shape: the entries' scores, -inf beside -1; or NULL.
  *   workspace    device memory of h3q_select_blocks_workspace_bytes bytes, 256-byte aligned, any
  *                contents; not touched by other work until the stream has passed this call.
- * rows_k / block_k <= 16,000.  rows_q <= 2^31 - 512.  Two launches.
+ * rows_q <= 2^31 - 512.  Two launches.  Where rows_k / block_k is above 16,000 (of all sequences together) the
+ * workspace has room for rows of scores too: those of a sequence that has so many blocks by itself are kept
+ * there, and take longer to choose from.
  */
 static inline int64_t h3q_select_blocks_workspace_bytes(int64_t rows_q, int64_t rows_k, int64_t batch,
                                                         int64_t kv_heads, int64_t head_dim, int64_t block_q,
                                                         int64_t block_k)
 {
     int64_t rows = h3q_block_rows(rows_q, batch, block_q) + h3q_block_rows(rows_k, batch, block_k);
-    return rows * kv_heads * (head_dim + 1) * 8 +
-           (h3q_block_rows(rows_k, batch, block_k) * kv_heads + 7) / 8 * 8 * head_dim * 4 + 256;
+    int64_t bytes = rows * kv_heads * (head_dim + 1) * 8 +
+                    (h3q_block_rows(rows_k, batch, block_k) * kv_heads + 7) / 8 * 8 * head_dim * 4 + 256;
+    if (rows_k / block_k > 16000) {
+        int64_t lists = h3q_block_rows(rows_q, batch, block_q) * kv_heads;
+        bytes += (lists < 1024 ? lists : 1024) * ((rows_k / block_k + 32) / 32 * 32) * 4;
+    }
+    return bytes;
 }
 int h3q_select_blocks(const void *q, int64_t ld_q, const void *k, int64_t ld_k, const int32_t *cu_q,
                       const int32_t *cu_k, int64_t batch, int64_t rows_q, int64_t rows_k, int64_t heads,

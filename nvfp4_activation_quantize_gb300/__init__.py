@@ -1173,9 +1173,11 @@ def block_rows(rows: int, batch: int, block: int) -> int:
 
 def select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, head_dim, block_q, block_k) -> int:
     """Device workspace bytes of h3q_select_blocks (h3q_select_blocks_workspace_bytes in include/h3q.h)."""
-    rows_k = block_rows(rows_k, batch, block_k)
-    rows = block_rows(rows_q, batch, block_q) + rows_k
-    return rows * kv_heads * (head_dim + 1) * 8 + (rows_k * kv_heads + 7) // 8 * 8 * head_dim * 4 + 256
+    keys, lists = block_rows(rows_k, batch, block_k), block_rows(rows_q, batch, block_q)
+    nbytes = (lists + keys) * kv_heads * (head_dim + 1) * 8 + (keys * kv_heads + 7) // 8 * 8 * head_dim * 4 + 256
+    if rows_k // block_k > 16000:   # rows of scores
+        nbytes += min(lists * kv_heads, 1024) * ((rows_k // block_k + 32) // 32 * 32) * 4
+    return nbytes
 
 
 def _block_sequences(q, k, cu_q, cu_k):

@@ -1153,7 +1153,6 @@ int h3q_select_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k, 
   static const char* fn = "h3q_select_blocks";
   g_last_error.clear();
   if (int e = check_blocks(fn, batch, rows_q, rows_k, heads, kv_heads, head_dim, block_q, block_k, top, causal)) return e;
-  if (rows_k / block_k > h3q::kMaxKeyBlocks) return invalid(fn, "rows_k / block_k exceeds 16,000");
   if (first < 0 || first > top) return invalid(fn, "first must be in [0, top]");
   if (causal && top < first + (block_q + block_k - 1) / block_k + 1)
     return invalid(fn, "top leaves no room for the first blocks and the queries' own");
@@ -1172,7 +1171,10 @@ int h3q_select_blocks(const void* q, int64_t ld_q, const void* k, int64_t ld_k, 
   if (scores != nullptr && !aligned(scores, 4)) return invalid(fn, "scores must be 4-byte aligned");
   if (workspace == nullptr || !aligned(workspace, 256)) return invalid(fn, "workspace must be 256-byte aligned");
   if (workspace_bytes < h3q_select_blocks_workspace_bytes(rows_q, rows_k, batch, kv_heads, head_dim, block_q, block_k))
-    return invalid(fn, "workspace_bytes is below h3q_select_blocks_workspace_bytes");
+    return invalid(fn, rows_k / block_k > h3q::kNearBlocks
+                           ? "workspace_bytes is below h3q_select_blocks_workspace_bytes (rows of scores for more than "
+                             "16,000 key blocks included)"
+                           : "workspace_bytes is below h3q_select_blocks_workspace_bytes");
   const int64_t entries = lists * kv_heads * top;
   const Span outs[3] = {span(blocks, entries * 4), scores ? span(scores, entries * 4) : Span{0, 0},
                         span(workspace, workspace_bytes)};

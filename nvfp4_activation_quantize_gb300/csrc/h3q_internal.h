@@ -184,8 +184,9 @@ struct BlockShape {
   int top;      // entries of a list
   int causal;
 };
-constexpr int64_t kMaxKeyBlocks = 16000;   // of a call that selects: a CTA holds a query block's scores (of rows_k / block_k
-                                           // full ones and a shorter one, where all are of one sequence)
+constexpr int64_t kNearBlocks = 16000;   // key blocks of a call (rows_k / block_k) whose scores a CTA holds for one query block,
+                                         // all of one sequence at worst, and a shorter one
+constexpr int64_t kFarRows = 1024;       // CTAs that have a row of scores in the workspace where there are more
 cudaError_t launch_select_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k, int64_t ld_k,
                                  int first, int32_t* blocks, float* scores, uint8_t* workspace, cudaStream_t stream);
 cudaError_t launch_attention_blocks(const BlockShape& s, const uint16_t* q, int64_t ld_q, const uint16_t* k,

@@ -56,6 +56,8 @@ struct Sums {
   float* size[2];
   uint4* parts;
   int64_t rows[2];   // block rows
+  uint32_t* far;     // rows of scores that no CTA holds, one for each of kFarRows CTAs at most, or nullptr
+  int64_t far_row;   // scores of such a row
 };
 
 Sums carve(const BlockShape& s, uint8_t* workspace) {
@@ -74,6 +76,10 @@ Sums carve(const BlockShape& s, uint8_t* workspace) {
   for (int t = 0; t < 2; ++t) {
     w.size[t] = at;
     at += w.rows[t] * s.kv_heads;
+  }
+  if (s.rows_k / s.block_k > kNearBlocks) {
+    w.far = reinterpret_cast<uint32_t*>(at);
+    w.far_row = (s.rows_k / s.block_k + 32) / 32 * 32;
   }
   return w;
 }
@@ -350,7 +356,7 @@ constexpr int kRowPad = 8;
 __host__ __device__ constexpr int width_of(int candidates) { return (candidates + 31) / 32 * 32 + kRowPad; }
 // Scores that a CTA holds: 16 query blocks against 1,024 key blocks, or fewer against more.
 constexpr int kScores = kRows * width_of(1024);
-static_assert(width_of(static_cast<int>(kMaxKeyBlocks) + 1) <= kScores, "one query block against the most key blocks");
+static_assert(width_of(static_cast<int>(kNearBlocks) + 1) <= kScores, "one query block against so many");
 
 struct ScoreArgs {
   BlockShape s;
@@ -686,7 +692,9 @@ __device__ __forceinline__ void product(float (&acc)[4], const uint4& x, uint32_
       : "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w), "r"(y0), "r"(y1));
 }
 
-template <int HD, int R>
+// FAR: for calls where a sequence's scores may pass what a CTA holds, which are then in the workspace (an instance of its
+// own: with both ways in one, 16 tokens took 47 us for 43).
+template <int HD, int R, bool FAR>
 __global__ void __launch_bounds__(kScoreThreads<R>, R <= 16 ? 3 : 1) score_kernel(const __grid_constant__ ScoreArgs a) {
   constexpr int kThreads = kScoreThreads<R>, kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t smem[];
@@ -699,203 +707,222 @@ __global__ void __launch_bounds__(kScoreThreads<R>, R <= 16 ? 3 : 1) score_kerne
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t lists = a.sums.rows[0], kb_rows = a.sums.rows[1];
   const int64_t chunks = (lists + a.rows - 1) / a.rows;
-  const int head = static_cast<int>(blockIdx.x / chunks);
-  const int64_t r0 = (blockIdx.x - head * chunks) * a.rows;
-  const int rows = static_cast<int>(lists - r0 < a.rows ? lists - r0 : a.rows);
+  // (a CTA's only one, but where it has a row of the workspace)
+  int64_t block = blockIdx.x;
+  do {
+    const int head = static_cast<int>(block / chunks);
+    const int64_t r0 = (block - head * chunks) * a.rows;
+    const int rows = static_cast<int>(lists - r0 < a.rows ? lists - r0 : a.rows);
 
-  // (the lists of rows are older than the sums: they are looked at before those are there)
-  if (threadIdx.x < rows) {
-    RowPlace p{};
-    p.block = block_at(a.s.cu_q, a.s.batch, a.s.rows_q, a.shift_q, r0 + threadIdx.x);
-    if (p.block.rows > 0) {
-      const int b = p.block.sequence;
-      const int64_t n = rows_of(a.s.cu_q, b, a.s.rows_q), len = rows_of(a.s.cu_k, b, a.s.rows_k);
-      const int64_t from = len - n + (static_cast<int64_t>(p.block.index) << a.shift_q);   // its first query's position
-      int64_t end = len;
-      if (a.s.causal && from + p.block.rows < end) end = from + p.block.rows < 0 ? 0 : from + p.block.rows;
-      p.candidates = static_cast<int>((end + (int64_t{1} << a.shift_k) - 1) >> a.shift_k);
-      p.own = !a.s.causal ? p.candidates : from < 0 ? 0 : static_cast<int>(from >> a.shift_k);
-    }
-    places[threadIdx.x] = p;
-  }
-  if (threadIdx.x == 0) {
-    most_k = 0.0f;
-    odd = 0;
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
-  __syncthreads();
-
-  for (int seg = 0; seg < rows;) {
-    // rows of one sequence, as many as the scores have room for
-    const RowPlace first = places[seg];
-    int most = first.candidates, n = 1, width = width_of(most);
-    while (seg + n < rows && first.block.rows > 0 && places[seg + n].block.rows > 0 &&
-           places[seg + n].block.sequence == first.block.sequence) {
-      const int other = max(places[seg + n].candidates, most);
-      const int w = width_of(other);
-      if ((n + 1) * w > kScores) break;
-      most = other;
-      width = w;
-      ++n;
-    }
-    const int b = first.block.sequence;
-    const int64_t q_at = (static_cast<int64_t>(head) * lists + r0 + seg) * HD;
-    int64_t k_at = 0, len = 0;
-    if (most > 0) {
-      const int64_t kb0 = (a.s.cu_k[b] >> a.shift_k) + static_cast<int64_t>(b);   // the sequence's key block rows
-      len = rows_of(a.s.cu_k, b, a.s.rows_k);
-      const int64_t k_row = static_cast<int64_t>(head) * kb_rows + kb0;   // among all heads'
-      k_at = k_row * HD;
-      const float* const k_size = a.sums.size[1] + k_row;
-      const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
-      auto keys_of = [&](int j) {
-        const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
-        return static_cast<float>(left < a.s.block_k ? left : a.s.block_k);
-      };
-      {
-        float m = 0.0f;
-        for (int i = threadIdx.x; i < most; i += kThreads) {
-          const float size = k_size[i];
-          if (size <= FLT_MAX) {
-            m = fmaxf(m, __fdiv_rn(size, keys_of(i)));
-          } else {
-            odd = 1;
-          }
-        }
-        if (threadIdx.x < n && !(q_size[threadIdx.x] <= FLT_MAX)) odd = 1;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) atomicMax(reinterpret_cast<int*>(&most_k), __float_as_int(m));   // (none is negative)
+    // (the lists of rows are older than the sums: they are looked at before those are there)
+    if (threadIdx.x < rows) {
+      RowPlace p{};
+      p.block = block_at(a.s.cu_q, a.s.batch, a.s.rows_q, a.shift_q, r0 + threadIdx.x);
+      if (p.block.rows > 0) {
+        const int b = p.block.sequence;
+        const int64_t n = rows_of(a.s.cu_q, b, a.s.rows_q), len = rows_of(a.s.cu_k, b, a.s.rows_k);
+        const int64_t from = len - n + (static_cast<int64_t>(p.block.index) << a.shift_q);   // its first query's position
+        int64_t end = len;
+        if (a.s.causal && from + p.block.rows < end) end = from + p.block.rows < 0 ? 0 : from + p.block.rows;
+        p.candidates = static_cast<int>((end + (int64_t{1} << a.shift_k) - 1) >> a.shift_k);
+        p.own = !a.s.causal ? p.candidates : from < 0 ? 0 : static_cast<int>(from >> a.shift_k);
       }
-      // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, which
-      // the warps make together; a warp takes every eighth group of 8 key blocks.
-      float q_down[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int block = lane / 4 + 8 * y;
-        const float size = block < n ? q_size[block] : INFINITY;
-        const bool there = size <= FLT_MAX;
-        const float s = scale_up(there ? size : 1.0f);
-        q_down[y] = scale_down(there ? size : 1.0f);
-        for (int z = warp; z < kSteps; z += kWarps) {
-          const float4 v = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at + block * HD)[4 * z + lane % 4]
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          uint32_t* const to = reinterpret_cast<uint32_t*>(q_parts + 2 * z * 32 + lane) + y;
-          halves_of(make_float2(v.x, v.y), s, to[0], to[32 * 4]);
-          halves_of(make_float2(v.z, v.w), s, to[2], to[32 * 4 + 2]);
-        }
-      }
-      const int last = static_cast<int>((len - 1) >> a.shift_k);   // the sequence's last block, which may be shorter
-      const float per_full = __fdiv_rn(1.0f, static_cast<float>(a.s.block_k)), per_last = __fdiv_rn(1.0f, keys_of(last));
-      const int64_t group0 = k_row / 8;
-      const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
-      const int groups = (before + most + 7) / 8;
-      // Steps whose operands are asked for before the group is begun: half, where there are registers for them.
-      constexpr int kAhead = R > 16 ? kSteps / 2 : 0;
-      const uint4* from = a.sums.parts + (group0 + warp) * (kSteps * 32) + lane;
-      uint4 k[kSteps];
-      if (warp < groups) {
-#pragma unroll
-        for (int z = 0; z < kAhead; ++z) k[z] = from[z * 32];
-      }
-      __syncthreads();
-      uint32_t* const my_scores = scored + lane / 4 * width;
-      for (int g = warp; g < groups; g += kWarps) {
-#pragma unroll
-        for (int z = kAhead; z < kSteps; ++z) k[z] = from[z * 32];
-        if (g + kWarps < groups) from += kWarps * kSteps * 32;
-        const int j = 8 * g - before + lane % 4 * 2;
-        float size[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) size[x] = static_cast<uint32_t>(j + x) < static_cast<uint32_t>(most) ? k_size[j + x] : 0.0f;
-        // (four sums, so that none is long: first parts of even and odd steps, the rest)
-        float even[4] = {}, uneven[4] = {}, rest[4] = {}, other[4] = {};
-#pragma unroll
-        for (int z = 0; z < kSteps; ++z) {
-          const uint4 first = q_parts[2 * z * 32 + lane], second = q_parts[(2 * z + 1) * 32 + lane];
-          product(z & 1 ? uneven : even, first, k[z].x, k[z].y);
-          product(rest, first, k[z].z, k[z].w);
-          product(other, second, k[z].x, k[z].y);
-          if (z < kAhead) k[z] = from[z * 32];   // (after the last group: any)
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (static_cast<uint32_t>(j + x) >= static_cast<uint32_t>(most)) continue;
-          const float per_key = j + x == last ? per_last : per_full, k_down = scale_down(size[x]);
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int i = 2 * y + x;
-            const float sum = __fadd_rn(__fadd_rn(even[i], uneven[i]), __fadd_rn(rest[i], other[i]));
-            // (the smaller factor first: nothing is too large on the way that is not so at the end)
-            const float s = __fmul_rn(__fmul_rn(__fmul_rn(sum, per_key), fminf(q_down[y], k_down)), fmaxf(q_down[y], k_down));
-            if (lane / 4 + 8 * y < n) my_scores[8 * y * width + j + x] = order_of_number(s);
-          }
-        }
-      }
-      __syncthreads();
-      if (odd) {   // scores with sums that are no numbers: as fp32 has them
-        for (int i = threadIdx.x; i < n * most; i += kThreads) {
-          const int y = i / most, j = i - y * most;
-          if (q_size[y] <= FLT_MAX && k_size[j] <= FLT_MAX) continue;
-          const float* const qv = a.sums.hi[0] + q_at + y * HD;
-          const float* const kv = a.sums.hi[1] + k_at + static_cast<int64_t>(j) * HD;
-          float s = 0.0f;
-          for (int d = 0; d < HD; ++d) s = __fmaf_rn(qv[d], kv[d], s);
-          scored[y * width + j] = order_of(__fdiv_rn(s, keys_of(j)));
-        }
-      }
-      if (threadIdx.x < n) {   // (0: queries or keys of zeros, whose scores are exact)
-        const float q_sum = q_size[threadIdx.x];
-        // (2^-145: what scaled sums below 2^-112 may lose)
-        const float off = fmaxf(fmaxf(__fmul_rn(q_sum, fmaxf(__fmul_rn(most_k, 0x1.6p-17f), 0x1p-145f)),
-                                      __fmul_rn(most_k, 0x1p-145f)), 0x1p-140f);
-        places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
-      }
-      __syncthreads();
+      places[threadIdx.x] = p;
     }
     if (threadIdx.x == 0) {
       most_k = 0.0f;
       odd = 0;
     }
-    // the choice: a warp for each query block
-    for (int y = warp; y < n; y += kWarps) {
-      const RowPlace p = places[seg + y];
-      const int64_t list = (static_cast<int64_t>(head) * lists + r0 + seg + y) * a.s.top;
-      uint32_t* const row = scored + y * width;
-      const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
-      if (p.candidates <= 512) {
-        choose<HD, 16>(a, p, row, q_row, k_at, len, list);
-      } else if (R > 16 && p.candidates <= 1024) {
-        choose<HD, (R > 16 ? 32 : 0)>(a, p, row, q_row, k_at, len, list);
-      } else {
-        choose<HD, 0>(a, p, row, q_row, k_at, len, list);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are written
+    __syncthreads();
+
+    for (int seg = 0; seg < rows;) {
+      // rows of one sequence, as many as the scores have room for
+      const RowPlace first = places[seg];
+      const bool far = FAR && width_of(first.candidates) > kScores;   // (one query block, see the loop below)
+      uint32_t* const far_row = a.sums.far + blockIdx.x * a.sums.far_row;
+      int most = first.candidates, n = 1, width = width_of(most);
+      while (seg + n < rows && first.block.rows > 0 && places[seg + n].block.rows > 0 &&
+             places[seg + n].block.sequence == first.block.sequence) {
+        const int other = max(places[seg + n].candidates, most);
+        const int w = width_of(other);
+        if ((n + 1) * w > kScores) break;
+        most = other;
+        width = w;
+        ++n;
       }
+      const int b = first.block.sequence;
+      const int64_t q_at = (static_cast<int64_t>(head) * lists + r0 + seg) * HD;
+      int64_t k_at = 0, len = 0;
+      if (most > 0) {
+        const int64_t kb0 = (a.s.cu_k[b] >> a.shift_k) + static_cast<int64_t>(b);   // the sequence's key block rows
+        len = rows_of(a.s.cu_k, b, a.s.rows_k);
+        const int64_t k_row = static_cast<int64_t>(head) * kb_rows + kb0;   // among all heads'
+        k_at = k_row * HD;
+        const float* const k_size = a.sums.size[1] + k_row;
+        const float* const q_size = a.sums.size[0] + static_cast<int64_t>(head) * lists + r0 + seg;
+        auto keys_of = [&](int j) {
+          const int64_t left = len - (static_cast<int64_t>(j) << a.shift_k);
+          return static_cast<float>(left < a.s.block_k ? left : a.s.block_k);
+        };
+        {
+          float m = 0.0f;
+          for (int i = threadIdx.x; i < most; i += kThreads) {
+            const float size = k_size[i];
+            if (size <= FLT_MAX) {
+              m = fmaxf(m, __fdiv_rn(size, keys_of(i)));
+            } else {
+              odd = 1;
+            }
+          }
+          if (threadIdx.x < n && !(q_size[threadIdx.x] <= FLT_MAX)) odd = 1;
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (lane == 0) atomicMax(reinterpret_cast<int*>(&most_k), __float_as_int(m));   // (none is negative)
+        }
+        // The products: a lane's operand of q is two query blocks (lane / 4 and 8 on), four of 16 dimensions each, which
+        // the warps make together; a warp takes every eighth group of 8 key blocks.
+        float q_down[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int block = lane / 4 + 8 * y;
+          const float size = block < n ? q_size[block] : INFINITY;
+          const bool there = size <= FLT_MAX;
+          const float s = scale_up(there ? size : 1.0f);
+          q_down[y] = scale_down(there ? size : 1.0f);
+          for (int z = warp; z < kSteps; z += kWarps) {
+            const float4 v = there ? reinterpret_cast<const float4*>(a.sums.hi[0] + q_at + block * HD)[4 * z + lane % 4]
+                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            uint32_t* const to = reinterpret_cast<uint32_t*>(q_parts + 2 * z * 32 + lane) + y;
+            halves_of(make_float2(v.x, v.y), s, to[0], to[32 * 4]);
+            halves_of(make_float2(v.z, v.w), s, to[2], to[32 * 4 + 2]);
+          }
+        }
+        const int last = static_cast<int>((len - 1) >> a.shift_k);   // the sequence's last block, which may be shorter
+        const float per_full = __fdiv_rn(1.0f, static_cast<float>(a.s.block_k)), per_last = __fdiv_rn(1.0f, keys_of(last));
+        const int64_t group0 = k_row / 8;
+        const int before = static_cast<int>(k_row - group0 * 8);   // rows of other sequences in the first group
+        const int groups = (before + most + 7) / 8;
+        // Steps whose operands are asked for before the group is begun: half, where there are registers for them.
+        constexpr int kAhead = R > 16 ? kSteps / 2 : 0;
+        const uint4* from = a.sums.parts + (group0 + warp) * (kSteps * 32) + lane;
+        uint4 k[kSteps];
+        if (warp < groups) {
+#pragma unroll
+          for (int z = 0; z < kAhead; ++z) k[z] = from[z * 32];
+        }
+        __syncthreads();
+        uint32_t* const my_scores = scored + lane / 4 * width;
+        for (int g = warp; g < groups; g += kWarps) {
+#pragma unroll
+          for (int z = kAhead; z < kSteps; ++z) k[z] = from[z * 32];
+          if (g + kWarps < groups) from += kWarps * kSteps * 32;
+          const int j = 8 * g - before + lane % 4 * 2;
+          float size[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) size[x] = static_cast<uint32_t>(j + x) < static_cast<uint32_t>(most) ? k_size[j + x] : 0.0f;
+          // (four sums, so that none is long: first parts of even and odd steps, the rest)
+          float even[4] = {}, uneven[4] = {}, rest[4] = {}, other[4] = {};
+#pragma unroll
+          for (int z = 0; z < kSteps; ++z) {
+            const uint4 first = q_parts[2 * z * 32 + lane], second = q_parts[(2 * z + 1) * 32 + lane];
+            product(z & 1 ? uneven : even, first, k[z].x, k[z].y);
+            product(rest, first, k[z].z, k[z].w);
+            product(other, second, k[z].x, k[z].y);
+            if (z < kAhead) k[z] = from[z * 32];   // (after the last group: any)
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (static_cast<uint32_t>(j + x) >= static_cast<uint32_t>(most)) continue;
+            const float per_key = j + x == last ? per_last : per_full, k_down = scale_down(size[x]);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int i = 2 * y + x;
+              const float sum = __fadd_rn(__fadd_rn(even[i], uneven[i]), __fadd_rn(rest[i], other[i]));
+              // (the smaller factor first: nothing is too large on the way that is not so at the end)
+              const float s = __fmul_rn(__fmul_rn(__fmul_rn(sum, per_key), fminf(q_down[y], k_down)), fmaxf(q_down[y], k_down));
+              if (lane / 4 + 8 * y >= n) continue;
+              if (far) {
+                far_row[j + x] = order_of_number(s);
+              } else {
+                my_scores[8 * y * width + j + x] = order_of_number(s);
+              }
+            }
+          }
+        }
+        __syncthreads();
+        if (odd) {   // scores with sums that are no numbers: as fp32 has them
+          for (int i = threadIdx.x; i < n * most; i += kThreads) {
+            const int y = i / most, j = i - y * most;
+            if (q_size[y] <= FLT_MAX && k_size[j] <= FLT_MAX) continue;
+            const float* const qv = a.sums.hi[0] + q_at + y * HD;
+            const float* const kv = a.sums.hi[1] + k_at + static_cast<int64_t>(j) * HD;
+            float s = 0.0f;
+            for (int d = 0; d < HD; ++d) s = __fmaf_rn(qv[d], kv[d], s);
+            if (far) {
+              far_row[j] = order_of(__fdiv_rn(s, keys_of(j)));
+            } else {
+              scored[y * width + j] = order_of(__fdiv_rn(s, keys_of(j)));
+            }
+          }
+        }
+        if (threadIdx.x < n) {   // (0: queries or keys of zeros, whose scores are exact)
+          const float q_sum = q_size[threadIdx.x];
+          // (2^-145: what scaled sums below 2^-112 may lose)
+          const float off = fmaxf(fmaxf(__fmul_rn(q_sum, fmaxf(__fmul_rn(most_k, 0x1.6p-17f), 0x1p-145f)),
+                                        __fmul_rn(most_k, 0x1p-145f)), 0x1p-140f);
+          places[seg + threadIdx.x].delta = q_sum == 0.0f || most_k == 0.0f ? 0.0f : off;
+        }
+        __syncthreads();
+      }
+      if (threadIdx.x == 0) {
+        most_k = 0.0f;
+        odd = 0;
+      }
+      // the choice: a warp for each query block
+      for (int y = warp; y < n; y += kWarps) {
+        const RowPlace p = places[seg + y];
+        const int64_t list = (static_cast<int64_t>(head) * lists + r0 + seg + y) * a.s.top;
+        uint32_t* const row = scored + y * width;
+        const int64_t q_row = q_at + static_cast<int64_t>(y) * HD;
+        if (far) {
+          choose<HD, 0>(a, p, far_row, q_row, k_at, len, list);
+        } else if (p.candidates <= 512) {
+          choose<HD, 16>(a, p, row, q_row, k_at, len, list);
+        } else if (R > 16 && p.candidates <= 1024) {
+          choose<HD, (R > 16 ? 32 : 0)>(a, p, row, q_row, k_at, len, list);
+        } else {
+          choose<HD, 0>(a, p, row, q_row, k_at, len, list);
+        }
+      }
+      seg += n;
+      __syncthreads();   // the scores, and places' deltas, are overwritten
     }
-    seg += n;
-    __syncthreads();   // the scores, and places' deltas, are overwritten
-  }
+    block += gridDim.x;
+  } while (FAR && block < chunks * a.s.kv_heads);
 }
 
 // CTAs of the scores' kernel that the device holds.
 template <int HD>
 constexpr int kScoreSmem = HD / 16 * 2 * 512 + kScores * 4;
-template <int HD, int R>
+template <int HD, int R, bool FAR = false>
 cudaError_t resident(int* blocks) {
-  return persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R>), kScoreThreads<R>, kScoreSmem<HD>,
+  return persistent_blocks(reinterpret_cast<const void*>(&score_kernel<HD, R, FAR>), kScoreThreads<R>, kScoreSmem<HD>,
                            int64_t{1} << 30, blocks);
 }
 
-template <int HD, int R>
+template <int HD, int R, bool FAR = false>
 cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
   int blocks = 0;
-  cudaError_t err = resident<HD, R>(&blocks);
+  cudaError_t err = resident<HD, R, FAR>(&blocks);
   if (err != cudaSuccess) return err;
   // query blocks of a CTA: 16, or fewer where all CTAs run at once all the same
   const int64_t rows = (score.sums.rows[0] * score.s.kv_heads + blocks - 1) / blocks;
   score.rows = static_cast<int>(rows < 1 ? 1 : rows > kRows ? kRows : rows);
-  const int64_t chunks = (score.sums.rows[0] + score.rows - 1) / score.rows;
+  int64_t grid = (score.sums.rows[0] + score.rows - 1) / score.rows * score.s.kv_heads;
+  if (FAR && grid > kFarRows) grid = kFarRows;
   cudaLaunchConfig_t config{};
-  config.gridDim = dim3(static_cast<unsigned>(chunks * score.s.kv_heads));
+  config.gridDim = dim3(static_cast<unsigned>(grid));
   config.blockDim = dim3(kScoreThreads<R>);
   config.dynamicSmemBytes = kScoreSmem<HD>;
   config.stream = stream;
@@ -904,7 +931,7 @@ cudaError_t launch_score(ScoreArgs score, cudaStream_t stream) {
   early.val.programmaticStreamSerializationAllowed = 1;
   config.attrs = &early;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, score_kernel<HD, R>, score);
+  return cudaLaunchKernelEx(&config, score_kernel<HD, R, FAR>, score);
 }
 
 template <int HD>
@@ -921,6 +948,7 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   // hold 1,024 and ask for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
   const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * single * kRows;
+  if (score.sums.far != nullptr) return launch_score<HD, 32, true>(score, stream);
   return many && longest <= 512 * static_cast<int64_t>(score.s.batch) ? launch_score<HD, 16>(score, stream)
                                                                : launch_score<HD, 32>(score, stream);
 }
