@@ -712,8 +712,9 @@ static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
  * lowest numbers) in ascending order, then -1 where there are fewer blocks.  Always among them,
  * whatever their scores: the first `first` blocks, and with `causal` those that hold the query
  * block's own positions (keys - queries + i of query i); causal blocks of later keys alone are
- * not candidates.  The choice is that of the exact scores: where fp32 is too coarse to tell,
- * they are formed again from sums held in pairs of fp32.  (Those are exact where the values
+ * not candidates.  The choice is that of the exact scores, but where two differ by less than 2^-37 of |q| |k|, the
+ * lengths of the means as vectors (k: the longest of the sequence): where fp32 is too coarse to tell, they are formed
+ * again from sums held in pairs of fp32.  (Those are exact where the values
  * of a block's columns lie within a factor of 2^18 of each other, up to 256 of them, and else off by
  * 2^-20 of the largest at most.  The length of a block's sums as a vector and the scores of sums have to fit
  * fp32, not what comes up on the way.)  A score that is no number counts as the lowest.
@@ -722,7 +723,8 @@ static inline int64_t h3q_block_rows(int64_t rows, int64_t batch, int64_t block)
  *                head_dim], row stride ld_k; 32-byte aligned.
  *   first        0 .. top.  With causal, top >= first + ceil(block_q / block_k) + 1.
  *   blocks       out, 4-byte aligned; rows of no query block get -1.
- *   scores       out, fp32 of the same shape: the entries' scores, -inf beside -1; or NULL.
+ *   scores       out, fp32 of the same shape: the entries' scores, off by 176 * 2^-24 of |q| |k| (the entry's own) and
+ *                2^-22 of themselves at most, -inf beside -1; or NULL.
  *   workspace    device memory of h3q_select_blocks_workspace_bytes bytes, 256-byte aligned, any
  *                contents; not touched by other work until the stream has passed this call.
  * rows_q <= 2^31 - 512.  Two launches.  Where rows_k / block_k is above 16,000 (of all sequences together) the

@@ -27,9 +27,11 @@
 // product of 16 values adds 17 terms, of each of which it may cut what is below 2^-23 of the largest, and rounds,
 // 36 * 2^-24 at most: M. Fasi, N. J. Higham, M. Mikaitis and S. Pranesh, "Numerical behavior of NVIDIA tensor
 // cores", PeerJ Comput. Sci. 7, 2021.  Four of them follow each other in each of two sums, 144; in the other two, of
-// second parts, they are 2^-10 of that.  Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the choice is the exact one.  Where it is
-// not (one list in forty for unrelated blocks), the scores within 2 delta of it are formed again from hi + lo in
-// pairs of fp32 (to 2^-40 and better), and the places that are left go to the highest of those.
+// second parts, they are 2^-10 of that.  Sums, mean: 6.)  Where the top-th score is more than 2 delta above the next, the
+// choice is the exact one.  Where it is not (one list in forty for unrelated blocks), the scores within 2 delta of it
+// are formed again from hi + lo in pairs of fp32, and the places that are left go to the highest of those.  What is
+// compared is their distance from the border, 3 delta at most, in fp32: 2^-39 of |q| |k|; the pairs' own error is 2^-40
+// (some 18 sums of rests that come to 10 * 2^-24 at most, each rounded).
 #include <cuda_fp16.h>
 
 #include <cfloat>

@@ -55,9 +55,9 @@ def definition(c, top, block_q, block_k, causal, first):
         mine = score.gather(2, best.clamp(max=nk - 1))
         lists[:, at] = best.masked_fill(none, -1)
         scores[:, at] = mine.masked_fill(none, -torch.inf)
-        # 176 * 2^-24 of |q| |k|, of the longest mean of keys that is a candidate (here: of the sequence), and the
-        # roundings of what is stored
-        off[:, at] = 2.0 ** -24 * (176 * q.norm(dim=2)[:, :, None] * k.norm(dim=2).amax(1)[:, None, None] + 4 * mine.abs())
+        # 176 * 2^-24 of |q| |k| and the roundings of what is stored
+        size = q.norm(dim=2)[:, :, None] * k.norm(dim=2).gather(1, best.clamp(max=nk - 1).flatten(1)).view(best.shape)
+        off[:, at] = 2.0 ** -24 * (176 * size + 4 * mine.abs())
     assert group * kv_heads == c["q"].shape[1]
     return lists, scores, off
 
