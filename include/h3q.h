@@ -630,8 +630,9 @@ int h3q_attention_cache_nvfp4(const void *q, int64_t ld_q, int64_t rows, int64_t
  * The pairs are (j, j + ROT/2), or with `interleaved` (2j, 2j + 1); the axes take them in order,
  * axis_dims[i] / 2 each.  f of pair i of an axis of d values is scale * theta^(-2i/d); with
  * `sections` it is scale * theta^(-2j/ROT) of the pair's number j in all of ROT.  The angle is
- * reduced to a turn in integers before it becomes fp32, so it is as exact for a position of a million
- * as for one of ten (off by at most 2^-46 of the position, and 2^-23 of a turn).
+ * reduced to a turn in integers before it becomes fp32, so a position of a million loses no more than the frequency has
+ * lost, which comes from doubles: the angle is off by at most position * (f * (2 + |log2 theta|) * 2^-51 + 2^-50), and 2^-23
+ * of a turn (theta = 10,000 and frequencies up to one: 2^-46 of the position).
  *
  *   q              bf16 [rows, heads * head_dim], k and v [rows, kv_heads * head_dim], row
  *                  strides ld_q, ld_k, ld_v (multiples of 16), 32-byte aligned.

@@ -8,8 +8,10 @@
 //
 // The angle is taken in turns.  F[j] = f[j] / (2 pi) as a fraction of 2^64: the product of two
 // 64-bit integers that wraps, p * F[j], is the turn's fraction with all whole turns gone, for
-// positive and negative p, off by at most |p| * 2^-53 (F comes from doubles).  So a position of a
-// million is as exact as one of ten; only the fraction, in [-1/2, 1/2), is rounded to fp32.
+// positive and negative p, off by p times what F is.  (F comes from doubles: log2(theta), its quotient and product with the
+// pair's number err by 2^-51 of an exponent of |log2 theta| at most, the power, scale and 2 pi by 2^-50 of f, a negative
+// fraction's distance from a turn by 2^-54.)  So a position of a million is as exact as one of ten; only the fraction, in
+// [-1/2, 1/2), is rounded to fp32.
 //
 // A warp makes the ROT/2 angles of its row once, each lane two of 64, and passes them through
 // shared memory; the weights are folded into them,
