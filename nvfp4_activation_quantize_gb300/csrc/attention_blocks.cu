@@ -14,9 +14,10 @@
 //   with a list each, and every key tile is loaded for one row tile.  That is 64 KB from L2 for 1,024 clocks
 //   of products, 64 bytes a clock of an SM, where copies of 32 KB alone get 80 (23 TB/s) and those in
 //   runs of 64 keys 60.
-// 32,640 tokens, 56 heads of 128, 32 blocks of 128 keys a list: 3.0 to 3.2 ms, 1.25 PFLOP/s, with a list for
-// each 128 tokens, where the loads' latency with 5 tiles in flight is the bound (tensor cores busy 49% of
-// the time); 2.5 ms, 1.53 PFLOP/s, with one for 256 tokens (64%), near what the power limit allows.
+// 32,640 tokens, 56 heads of 128, 32 blocks of 128 keys a list: 3.1 to 3.3 ms, 1.16 to 1.24 PFLOP/s, with a list for
+// each 128 tokens (tensor cores busy 47% of the time).  Of the ring's five tiles two are held, whole, by the products
+// under way, so about three are in flight, and the loads' latency is the bound: 11 TB/s.  2.5 to 2.65 ms, 1.45 to
+// 1.51 PFLOP/s, with a list for 256 tokens (61%), near what the power limit allows.
 //
 //   warps 0..3, 4..7  softmax of tile 0, 1: a thread owns one row of S in TMEM, takes the weights against
 //                     a reference that follows the row's maximum when that has grown by more than

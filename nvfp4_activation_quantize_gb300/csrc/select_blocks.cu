@@ -10,7 +10,7 @@
 //           constant that is larger than all that can come (S. M. Rump, T. Ogita and S. Oishi,
 //           "Accurate floating-point summation part I", SIAM J. Sci. Comput. 31(1), 2008): what its
 //           rounding leaves of each value is exact and goes to a sum of its own, four packed
-//           additions a pair of values (65,280 rows of 56 + 56 heads of 128 in 282 us, 6.8 TB/s with what is
+//           additions a pair of values (65,280 rows of 56 + 56 heads of 128 in 280 us, 6.9 TB/s with what is
 //           written).  A sum of
 //           up to 256 values is exact where they lie within a factor of 2^18 of each other, and else off by
 //           2^-20 of the largest at most (both 2^-1 for each doubling of their number).
@@ -19,7 +19,7 @@
 //           products are as good as fp32's.  q's operands are in shared memory, k's come from L2 in the order
 //           that a lane wants, a load of 16 bytes for three products.  Then a warp per query block takes its
 //           scores into registers and looks for the top-th highest.  65,280 tokens' 510 x 510 scores of 56
-//           heads, of which 64 a row are kept: 140 us (284 with fp32 products from tiles in shared memory).
+//           heads, of which 64 a row are kept: 145 us (284 with fp32 products from tiles in shared memory).
 //           Bound: latency with 24 warps an SM, of the products' loads (80 us) and the choice's steps (55).
 //
 // What these products cannot tell apart is told apart by fp32 pairs: a score is off by at most
@@ -946,8 +946,8 @@ cudaError_t launch(const PoolArgs& pool, const ScoreArgs& score, cudaStream_t st
   pool_kernel<HD><<<static_cast<unsigned>(pool_blocks), kPoolThreads, 0, stream>>>(pool);
   if ((err = cudaGetLastError()) != cudaSuccess) return err;
   // Many lists: three CTAs an SM, whose warps hold 512 scores, which is enough where sequences have so many key
-  // blocks on average (65,280 tokens 486 us against 525 with two).  Else one of twice the threads, whose warps
-  // hold 1,024 and ask for operands ahead (16 single tokens 45.5 us against 49, 4 chunks 61.6 against 63.4).
+  // blocks on average (65,280 tokens 425 us, with the other instance 485).  Else one of twice the threads, whose warps
+  // hold 1,024 and ask for operands ahead (16 single tokens 40.5 us, with the first 43.2; 4 chunks 51.5 and 51.7).
   const int64_t longest = (score.s.rows_k + score.s.block_k - 1) / score.s.block_k;
   const bool many = score.sums.rows[0] * score.s.kv_heads >= int64_t{2} * single * kRows;
   if (score.sums.far != nullptr) return launch_score<HD, 32, true>(score, stream);
